@@ -24,14 +24,18 @@ STATUS = {0: "ok", 1: "invalid argument", 2: "unsupported configuration", 3: "CU
           4: "workspace missing, misaligned or too small", 5: "device-side error recorded"}
 DEVERR = {0: "none", 1: "cu_seqlens mismatch", 2: "slot out of range", 3: "negative position",
           4: "bounded wait timed out", 5: "index range outside a buffer (bounds-checked build)",
-          6: "host positions disagree with the cache (step skipped)"}
+          6: "host positions disagree with the cache (step skipped)",
+          7: "free list or block table too short, or a page outside the cache"}
 
 # every function the header declares (checked by the CPU test suite)
 EXPORTS = ("gdn_cpr_version", "gdn_cpr_status_string", "gdn_cpr_workspace_size",
            "gdn_cpr_prefill", "gdn_cpr_decode_step", "gdn_cpr_fwd", "gdn_cpr_bwd",
            "gdn_cpr_get_device_error", "gdn_cpr_set_profile", "gdn_cpr_decode_step_noalloc",
            "gdn_cpr_policy_digest", "gdn_cpr_prefill_continue", "gdn_cpr_running_state",
-           "gdn_cpr_noalloc_device_error", "gdn_cpr_test_wait_timeout", "gdn_cpr_decode_step_pos")
+           "gdn_cpr_noalloc_device_error", "gdn_cpr_test_wait_timeout", "gdn_cpr_decode_step_pos",
+           "gdn_cpr_qk_norm_rope", "gdn_cpr_qk_norm_rope_bwd", "gdn_cpr_qk_norm_rope_workspace_size",
+           "gdn_cpr_page_map", "gdn_cpr_paged_decode", "gdn_cpr_paged_decode_workspace_size",
+           "gdn_cpr_window_attn", "gdn_cpr_window_attn_bwd", "gdn_cpr_window_attn_workspace_size")
 NOALLOC_SCRATCH_BYTES = 64 * 1024 * 1024
 
 
@@ -99,8 +103,22 @@ def load():
             lib.gdn_cpr_noalloc_device_error.restype = I
             lib.gdn_cpr_test_wait_timeout.argtypes = [ctypes.c_int32]
             lib.gdn_cpr_test_wait_timeout.restype = None
+            N = ctypes.c_int32
+            lib.gdn_cpr_qk_norm_rope.argtypes = [P] * 13 + [N, N, P, P]
+            lib.gdn_cpr_qk_norm_rope_bwd.argtypes = [P] * 15 + [S, P]
+            lib.gdn_cpr_qk_norm_rope_workspace_size.argtypes = [P, ctypes.POINTER(S)]
+            lib.gdn_cpr_page_map.argtypes = [N] * 5 + [P] * 10 + [S, P]
+            lib.gdn_cpr_paged_decode.argtypes = [P, N, N, P, P, P, N, N, P, N, P, P, P, P, S, P]
+            lib.gdn_cpr_paged_decode_workspace_size.argtypes = [P, N, N, ctypes.POINTER(S)]
+            lib.gdn_cpr_window_attn.argtypes = [P, N, N, N] + [P] * 8 + [S, P]
+            lib.gdn_cpr_window_attn_bwd.argtypes = [P, N, N, N] + [P] * 12 + [S, P]
+            lib.gdn_cpr_window_attn_workspace_size.argtypes = [P, N, N, ctypes.POINTER(S)]
             for fn in ("gdn_cpr_workspace_size", "gdn_cpr_prefill", "gdn_cpr_decode_step",
-                       "gdn_cpr_fwd", "gdn_cpr_bwd", "gdn_cpr_get_device_error"):
+                       "gdn_cpr_fwd", "gdn_cpr_bwd", "gdn_cpr_get_device_error",
+                       "gdn_cpr_qk_norm_rope", "gdn_cpr_qk_norm_rope_bwd",
+                       "gdn_cpr_qk_norm_rope_workspace_size", "gdn_cpr_page_map", "gdn_cpr_paged_decode",
+                       "gdn_cpr_paged_decode_workspace_size", "gdn_cpr_window_attn",
+                       "gdn_cpr_window_attn_bwd", "gdn_cpr_window_attn_workspace_size"):
                 getattr(lib, fn).restype = I
             _lib = lib
     return _lib

@@ -1,0 +1,102 @@
+// attn.h -- internal interface of the attention-layer operators: the C-ABI host code
+// (attn_host.cu) checks arguments and calls these launchers.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "../../include/gdn_cpr.h"
+#include "common.cuh"
+
+namespace gdn {
+
+// ------------------------------------------------------------- norms and rotation ----
+struct NormRope {
+  int T, hq, hk, rot, table_rows;
+  int norm, layout;  // gdn_norm, gdn_rope_layout
+  float eps;
+  int64_t q_stride, k_stride, v_stride;
+  const void *q, *k, *v;
+  const float *wq, *wk, *cos, *sin;
+  const int32_t* pos;
+  void *q_out, *k_out, *k_pages, *v_pages;
+  int page_shift;
+  int64_t slots;
+  const int32_t* slot_map;
+  // backward
+  const void *gq, *gk;
+  void *dq, *dk;
+  float* partial;  // [blocks][2][d] sums of the weights' gradients
+  float *dwq, *dwk;
+};
+// launchers return how many kernels they queued where that varies
+void launch_norm_rope(const NormRope& a, int d, bool in_bf16, bool out_bf16, cudaStream_t st);
+int launch_norm_rope_bwd(const NormRope& a, int d, bool in_bf16, bool grad_bf16, cudaStream_t st);
+constexpr int kNormBwdBlocks = 608;  // at most, 4 per SM; fixes the order of the weights' sums
+
+// ------------------------------------------------------------------- page tables ----
+constexpr int kPageMapMaxSeqs = 8192;
+struct PageMap {
+  int N, T, page_shift, max_blocks, num_free;
+  const int32_t *lens, *new_lens, *free_pages;
+  int32_t *block_table, *seq_lens, *cu, *positions, *slot_map, *pages_used;
+  WsHeader* hdr;
+};
+void launch_page_map(const PageMap& a, cudaStream_t st);
+
+// ------------------------------------------------------------------ paged decode ----
+struct PagedDecode {
+  int N, hq, hkv, d, window, sinks, max_len;
+  float scale;
+  const void *q, *k_pages, *v_pages;
+  int num_pages, page_shift, max_blocks;
+  const int32_t *block_table, *seq_lens;
+  void* out;
+  float* lse;
+  float* partial;  // [N, hq, max_splits] records of d + 2 floats
+  int max_splits;
+  WsHeader* hdr;
+};
+// Visible keys of a request with `len` keys (device and host use the same rule).
+__host__ __device__ inline int visible_keys(int len, int window, int sinks) {
+  if (window <= 0 || len <= window) return len;
+  const int behind = len - window;
+  return window + (sinks < behind ? sinks : behind);
+}
+// Keys of one split, from the number of visible keys alone, so that a request's result does not
+// depend on the batch.
+__host__ __device__ inline int split_keys(int n) { return n <= 2048 ? 128 : n <= 8192 ? 256 : 512; }
+__host__ __device__ inline int split_count(int n) { return (n + split_keys(n) - 1) / split_keys(n); }
+int paged_decode_max_splits(int max_visible);
+int launch_paged_decode(const PagedDecode& a, bool bf16, cudaStream_t st);
+
+// -------------------------------------------------------------- window attention ----
+struct WindowAttn {
+  int N, Tq, Tk, hq, hkv, d, window, sinks;
+  float scale;
+  const int32_t *cu_q, *cu_k;
+  const void *q, *k, *v;
+  void* out;
+  float* lse;
+  // backward
+  const void* dout;
+  void *dq, *dk, *dv;
+  float* delta;  // [Tq, hq]: do . o
+  WsHeader* hdr;
+};
+void launch_window_attn(const WindowAttn& a, bool bf16, cudaStream_t st);
+// the gradient: dq (and delta), then dk and dv, which read delta
+void launch_window_dq(const WindowAttn& a, bool bf16, cudaStream_t st);
+void launch_window_dkv(const WindowAttn& a, bool bf16, cudaStream_t st);
+
+// ------------------------------------------------------------------------ device ----
+__device__ __forceinline__ void store4(float* p, float4 x) { *reinterpret_cast<float4*>(p) = x; }
+__device__ __forceinline__ void store4(__nv_bfloat16* p, float4 x) {
+  const __nv_bfloat162 a = __floats2bfloat162_rn(x.x, x.y), b = __floats2bfloat162_rn(x.z, x.w);
+  uint2 u;
+  u.x = *reinterpret_cast<const uint32_t*>(&a);
+  u.y = *reinterpret_cast<const uint32_t*>(&b);
+  *reinterpret_cast<uint2*>(p) = u;
+}
+
+}  // namespace gdn

@@ -2,16 +2,20 @@
 // launch sequence of every mode.  The host never touches tensor data; it only reads the
 // caller's host copy of cu_seqlens to size grids and the workspace.
 #include <cuda_runtime.h>
-#include <nvtx3/nvToolsExt.h>
 #include <stdint.h>
 #include <string.h>
 
 #include <vector>
 
 #include "../../include/gdn_cpr.h"
+#include "hooks.h"
 #include "launch.h"
 
 #define GDN_VERSION_NUM 200  // 0.2.0
+
+namespace gdn {
+thread_local gdn_cpr_profile* t_profile = nullptr;
+}
 
 namespace {
 using namespace gdn;
@@ -130,13 +134,10 @@ gdn_status check_cache(const gdn_cpr_cache* c) {
   return GDN_OK;
 }
 
-thread_local gdn_cpr_profile* t_profile = nullptr;
 // gdn_cpr_test_wait_timeout: calls left that make the tensor-core chain's first CTA give up
 // a wait that nothing completes
 thread_local int32_t t_wait_fault = 0;
 
-// Stage marker of the profiling hook: event `stage` after the stage's kernels, and the
-// count of kernels those stages launched.
 // Continued prefill: the virtual prefill's regions, then the virtual cu_seqlens, tail
 // lengths, base positions, the gathered q, k, v, g, beta and the virtual output.
 struct ContLayout {
@@ -181,52 +182,6 @@ gdn_status virtual_cu(const gdn_cpr_shape* s, const int32_t* cu, const int32_t* 
   }
   return GDN_OK;
 }
-
-// NVTX range over one entry point (host-side markers for profilers such as Nsight; no
-// effect without a tool attached).
-struct NvtxRange {
-  explicit NvtxRange(const char* name) { nvtxRangePushA(name); }
-  ~NvtxRange() { nvtxRangePop(); }
-  NvtxRange(const NvtxRange&) = delete;
-  NvtxRange& operator=(const NvtxRange&) = delete;
-};
-
-// Stage boundaries of one call: the profiling hook's events and kernel counts, and a nested
-// NVTX range per stage (names[i] is stage i + 1; NULL-terminated).
-struct Stages {
-  cudaStream_t st;
-  const char* const* names;
-  int next = 0;
-  bool open = false;
-  Stages(cudaStream_t s, const char* const* stage_names) : st(s), names(stage_names) {
-    if (t_profile) t_profile->stages = 0;
-    mark(0);
-  }
-  ~Stages() {
-    if (open) nvtxRangePop();
-  }
-  Stages(const Stages&) = delete;
-  Stages& operator=(const Stages&) = delete;
-  // a kernel launched at the start of the first stage (counted, no event of its own)
-  void count(int kernels) {
-    if (t_profile) t_profile->kernels += kernels;
-  }
-  void mark(int kernels) {
-    if (open) nvtxRangePop();
-    open = names && names[next] != nullptr;
-    if (open) nvtxRangePushA(names[next]);
-    if (!t_profile) {
-      ++next;
-      return;
-    }
-    t_profile->kernels += kernels;
-    if (next < t_profile->n_events && next < 16 && t_profile->events[next]) {
-      cudaEventRecord(static_cast<cudaEvent_t>(t_profile->events[next]), st);
-      t_profile->stages = next + 1;
-    }
-    ++next;
-  }
-};
 
 const char* const kFwdStages[] = {"work list", "boundary pre-pass", "boundary chain", "intra-chunk recurrence",
                                   "cache tail", nullptr};

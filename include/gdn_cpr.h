@@ -86,8 +86,10 @@ typedef enum {
     GDN_DEVERR_TIMEOUT = 4,    /* a bounded on-device wait gave up */
     GDN_DEVERR_BOUNDS = 5,     /* bounds-checked builds only (GDN_CHECKED): a work item's index
                                   range fell outside its buffer; the item was skipped */
-    GDN_DEVERR_POS_HOST = 6    /* gdn_cpr_decode_step_pos: the host positions said no token
+    GDN_DEVERR_POS_HOST = 6,   /* gdn_cpr_decode_step_pos: the host positions said no token
                                   completes a chunk, the cache says one does; step skipped */
+    GDN_DEVERR_PAGES = 7       /* page operators: free list too short, block table too narrow,
+                                  or a page index outside the cache */
 } gdn_device_error;
 
 typedef enum { GDN_F32 = 0, GDN_BF16 = 1 } gdn_dtype;
@@ -358,6 +360,159 @@ void gdn_cpr_test_wait_timeout(int32_t calls);
  * last call queued with it) into *code (a gdn_device_error).  Returns GDN_OK when the
  * word is clear, GDN_ERR_DEVICE when it is set, GDN_ERR_CUDA if the sync or copy fails. */
 gdn_status gdn_cpr_get_device_error(const void *ws, gdn_stream_t stream, int32_t *code);
+
+/* =====================================================================================
+ * Attention-layer operators
+ *
+ * A hybrid model interleaves Gated DeltaNet layers with softmax-attention layers.  These are
+ * the operators such layers need beside the recurrence above (this library's own addition;
+ * the pages describe CPR only): the per-head norms and rotation of queries and keys, the
+ * paged cache's bookkeeping, decode attention over that cache, and sliding-window attention
+ * for prefill and training with its gradient.  The conventions above hold (caller-owned
+ * memory, work only queued on `stream`, argument errors returned before anything is queued,
+ * fixed reduction orders and no atomics in any arithmetic) with these additions:
+ *
+ * Layouts:  q, out [T, H_q, d];  k, v [T, H_kv, d];  query head h reads key head
+ * h / (H_q / H_kv).  Cache pages: k_pages, v_pages [pages, H_kv, page_size, d] -- the rows of
+ * one head of a page are contiguous.  block_table [N, max_blocks] int32: page of positions
+ * b * page_size .. of request n.  A slot is page * page_size + offset.
+ * Claims: d in {32, 64, 128}; dtypes fp32 and bf16; H_q % H_kv == 0; page_size a power of two
+ * in [16, 256]; tensors 16-byte aligned.
+ *
+ * Visibility: a query at position p of its request sees key j when j <= p and (window == 0 or
+ * p - j < window or j < sinks).  A query that sees no key gives a row of zeros (and a
+ * log-sum-exp of -infinity), and its gradient is zero.
+ *
+ * Results for a request depend on that request alone: not on the batch it is in, its place in
+ * the packing, the pages it lies on, or what lies in other requests' rows or in the unused
+ * part of a page (infinities and NaN there included).
+ * ===================================================================================== */
+typedef enum { GDN_NORM_NONE = 0, GDN_NORM_RMS = 1, GDN_NORM_L2 = 2 } gdn_norm;
+typedef enum { GDN_ROPE_HALF = 0, GDN_ROPE_INTERLEAVED = 1 } gdn_rope_layout;
+
+typedef struct {
+    int32_t tokens;      /* T */
+    int32_t h_q, h_k;    /* heads of q and of k (and v) */
+    int32_t d;
+    int32_t rot;         /* rotated entries at the front of every head: 0 or a multiple of 8, <= d */
+    int32_t table_rows;  /* rows of cos and sin */
+    gdn_norm norm;
+    gdn_rope_layout layout;
+    float eps;
+    gdn_dtype in_dtype;   /* q, k, v, and the gradients dq, dk */
+    gdn_dtype out_dtype;  /* q_out, k_out and the cache */
+    gdn_dtype grad_dtype; /* dq_out, dk_out (backward) */
+    int64_t q_stride, k_stride, v_stride; /* elements from one token of q, k, v to the next, so that
+                                             they may be parts of one projection's rows; multiples
+                                             of 16 bytes.  Everything else is dense. */
+} gdn_cpr_norm_rope;
+
+/* Norm and rotation of queries and keys, one pass:  y = R(pos) (x * r * w) per (token, head),
+ *   r = 1, 1 / sqrt(mean x^2 + eps) (RMS) or 1 / sqrt(sum x^2 + eps) (L2; what gdn_cpr_prefill
+ *   and gdn_cpr_fwd expect of q and k);  w [d] fp32 or NULL (ones);
+ *   R turns the pairs (x_i, x_{i + rot/2}) (half) or (x_{2i}, x_{2i+1}) (interleaved), i < rot/2,
+ *   by (cos, sin)[pos][i]:  (a, b) -> (a c - b s, b c + a s).
+ *   q_weight, k_weight  [d] fp32 or NULL
+ *   cos, sin            [table_rows, rot / 2] fp32, positions [T] int32 (all NULL if rot == 0);
+ *                       a token whose position lies outside the tables gets rows of NaN
+ *   q_out, k_out        [T, H, d]; either may be NULL (that output is not wanted)
+ *   k_pages, v_pages    NULL, or the paged cache: k_out's rows and v's rows (unchanged but for
+ *                       the conversion to out_dtype) are written at slot_map [T] int32; a slot
+ *                       outside [0, num_pages * page_size) is skipped (-1: a token not kept)  */
+gdn_status gdn_cpr_qk_norm_rope(const gdn_cpr_norm_rope *cfg, const void *q, const void *k,
+                                const void *v, const float *q_weight, const float *k_weight,
+                                const float *cos, const float *sin, const int32_t *positions,
+                                void *q_out, void *k_out, void *k_pages, void *v_pages,
+                                int32_t num_pages, int32_t page_size, const int32_t *slot_map,
+                                gdn_stream_t stream);
+
+/* Its gradient.  With g = R^T dy and g' = g w:  dx = r g' - c r^3 (x . g') x, c = 1 / d (RMS),
+ * 1 (L2) or 0;  dw = sum over tokens and heads of g x r, in a fixed order (fp32).
+ *   dq_out, dk_out  [T, H, d] in grad_dtype;  dq, dk [T, H, d] in in_dtype
+ *   dq_weight, dk_weight  [d] fp32, or both NULL; then no workspace is needed
+ *   A token whose position lies outside the tables gives NaN in dq and dk and is left out of
+ *   the weights' gradients.                                                                 */
+gdn_status gdn_cpr_qk_norm_rope_bwd(const gdn_cpr_norm_rope *cfg, const void *q, const void *k,
+                                    const float *q_weight, const float *k_weight, const float *cos,
+                                    const float *sin, const int32_t *positions, const void *dq_out,
+                                    const void *dk_out, void *dq, void *dk, float *dq_weight,
+                                    float *dk_weight, void *ws, size_t ws_bytes,
+                                    gdn_stream_t stream);
+gdn_status gdn_cpr_qk_norm_rope_workspace_size(const gdn_cpr_norm_rope *cfg, size_t *bytes);
+
+/* The paged cache's bookkeeping for one step, on the device, from request lengths.  Request n
+ * has lens[n] cached tokens and appends new_lens[n]; it owns ceil(lens[n] / page_size) pages,
+ * listed at the front of its block-table row, and takes those it lacks from free_pages, in
+ * request order from the list's front.
+ *   lens, new_lens [N] int32; free_pages [num_free] int32
+ *   block_table [N, max_blocks] int32   updated: the new pages' entries, nothing else
+ *   seq_lens [N] int32                  lens + new_lens
+ *   cu_seqlens [N + 1] int32            offsets of the new tokens, packed
+ *   positions, slot_map [total_tokens] int32  of every new token; total_tokens = sum new_lens
+ *   pages_used [1] int32                how many entries of free_pages were taken
+ * Nothing is taken off the list here, so a call may be repeated.  If total_tokens is not the
+ * sum (GDN_DEVERR_CU_SEQLENS), a length is negative or their sum does not fit 32 bits
+ * (GDN_DEVERR_POS), or the free list or a block-table row is too short (GDN_DEVERR_PAGES), the
+ * error word says so, positions and slot_map are -1, seq_lens and cu_seqlens are zeros,
+ * pages_used is 0 and the block table keeps its contents.  A page whose index is negative or
+ * whose slots do not fit 32 bits sets GDN_DEVERR_PAGES too, and its tokens' slots are -1.
+ * N <= 8192.
+ *   ws: GDN_CPR_ATTN_HEADER_BYTES, 256-byte aligned (the error word)                         */
+#define GDN_CPR_ATTN_HEADER_BYTES 256u
+gdn_status gdn_cpr_page_map(int32_t num_seqs, int32_t total_tokens, int32_t page_size,
+                            int32_t max_blocks, int32_t num_free, const int32_t *lens,
+                            const int32_t *new_lens, const int32_t *free_pages,
+                            int32_t *block_table, int32_t *seq_lens, int32_t *cu_seqlens,
+                            int32_t *positions, int32_t *slot_map, int32_t *pages_used, void *ws,
+                            size_t ws_bytes, gdn_stream_t stream);
+
+typedef struct {
+    int32_t h_q, h_kv, d;
+    int32_t window; /* keys a query sees behind it, itself included; 0 = all */
+    int32_t sinks;  /* first keys that stay visible outside the window */
+    float scale;    /* of the scores; 0 = 1 / sqrt(d) */
+    gdn_dtype dtype; /* q, k, v, out and their gradients */
+} gdn_cpr_attn;
+
+/* Attention of one new token per request over the paged cache: q [N, H_q, d] is the token at
+ * position seq_lens[n] - 1, whose key and value are already in the cache.  seq_lens[n] = 0
+ * gives zeros.  The visible keys are split over their count and joined in a fixed order.
+ *   seq_lens [N] int32; max_len >= every seq_lens (sizes the grid; a longer or negative one
+ *   sets GDN_DEVERR_POS and gives NaN for that request); a page index outside [0, num_pages)
+ *   sets GDN_DEVERR_PAGES, NaN likewise
+ *   out [N, H_q, d];  lse NULL or [N, H_q] fp32: the log-sum-exp of the scaled scores
+ *   ws: gdn_cpr_paged_decode_workspace_size bytes; its error word is set by every call      */
+gdn_status gdn_cpr_paged_decode(const gdn_cpr_attn *attn, int32_t num_seqs, int32_t max_len,
+                                const void *q, const void *k_pages, const void *v_pages,
+                                int32_t num_pages, int32_t page_size, const int32_t *block_table,
+                                int32_t max_blocks, const int32_t *seq_lens, void *out, float *lse,
+                                void *ws, size_t ws_bytes, gdn_stream_t stream);
+gdn_status gdn_cpr_paged_decode_workspace_size(const gdn_cpr_attn *attn, int32_t num_seqs,
+                                               int32_t max_len, size_t *bytes);
+
+/* Causal attention over packed sequences with a sliding window and first keys that stay
+ * visible (prefill and trainer forward).  Sequence n has queries cu_q[n] .. and keys cu_k[n]
+ * ..; the last query is at the last key's position, so fewer queries than keys continue a
+ * sequence, and with more the first rows see nothing.
+ *   total_q, total_k  rows of q and of k, v: cu_q[N], cu_k[N]; at most 2^30
+ *   cu_q, cu_k        [N + 1] int32 on the device only; a table that is not non-decreasing from
+ *                     0 to its total sets GDN_DEVERR_CU_SEQLENS (outputs are then not valid)
+ *   out [total_q, H_q, d];  lse [total_q, H_q] fp32, natural logarithm
+ *   ws: gdn_cpr_window_attn_workspace_size bytes; its error word is set by every call       */
+gdn_status gdn_cpr_window_attn(const gdn_cpr_attn *attn, int32_t num_seqs, int32_t total_q,
+                               int32_t total_k, const int32_t *cu_q, const int32_t *cu_k,
+                               const void *q, const void *k, const void *v, void *out, float *lse,
+                               void *ws, size_t ws_bytes, gdn_stream_t stream);
+
+/* Its gradient, from the forward's out and lse.  dq [total_q, H_q, d]; dk, dv [total_k, H_kv,
+ * d], summed over a group's heads in ascending order; deterministic.                       */
+gdn_status gdn_cpr_window_attn_bwd(const gdn_cpr_attn *attn, int32_t num_seqs, int32_t total_q,
+                                   int32_t total_k, const int32_t *cu_q, const int32_t *cu_k,
+                                   const void *q, const void *k, const void *v, const void *out,
+                                   const float *lse, const void *dout, void *dq, void *dk, void *dv,
+                                   void *ws, size_t ws_bytes, gdn_stream_t stream);
+gdn_status gdn_cpr_window_attn_workspace_size(const gdn_cpr_attn *attn, int32_t total_q,
+                                              int32_t backward, size_t *bytes);
 
 #ifdef __cplusplus
 }
