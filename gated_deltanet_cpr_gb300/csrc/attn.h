@@ -84,7 +84,14 @@ struct WindowAttn {
   float* delta;  // [Tq, hq]: do . o
   WsHeader* hdr;
 };
-void launch_window_attn(const WindowAttn& a, bool bf16, cudaStream_t st);
+// false: nothing was queued
+bool launch_window_attn(const WindowAttn& a, bool bf16, cudaStream_t st);
+// tensor-core kernels: bf16, d = 64 or 128, some queries and keys (a tensor map has no empty
+// dimension); false if the tensor maps cannot be made
+inline bool window_on_tensor_cores(const WindowAttn& a, bool bf16) {
+  return bf16 && a.d != 32 && a.Tq > 0 && a.Tk > 0;
+}
+bool launch_window_fwd_tc(const WindowAttn& a, cudaStream_t st);
 // the gradient: dq (and delta), then dk and dv, which read delta
 void launch_window_dq(const WindowAttn& a, bool bf16, cudaStream_t st);
 void launch_window_dkv(const WindowAttn& a, bool bf16, cudaStream_t st);

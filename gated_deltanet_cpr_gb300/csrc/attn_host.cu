@@ -344,7 +344,7 @@ gdn_status gdn_cpr_window_attn(const gdn_cpr_attn* attn, int32_t num_seqs, int32
   w.lse = lse;
   w.hdr = static_cast<WsHeader*>(ws);
   Stages stg(stream, kWindowStages);
-  launch_window_attn(w, attn->dtype == GDN_BF16, stream);
+  if (!launch_window_attn(w, attn->dtype == GDN_BF16, stream)) return GDN_ERR_CUDA;
   stg.mark(1);
   return finish();
 }
