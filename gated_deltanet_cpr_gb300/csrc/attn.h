@@ -81,7 +81,8 @@ struct WindowAttn {
   // backward
   const void* dout;
   void *dq, *dk, *dv;
-  float* delta;  // [Tq, hq]: do . o
+  float* delta;  // 2 Tq hq floats that dq leaves for dk, dv: do . o [Tq, hq] (fp32 SIMT), or
+                 // lse log2 e [hq, Tq] (infinite for a row that sees nothing) and do . o [hq, Tq]
   WsHeader* hdr;
 };
 // false: nothing was queued
@@ -92,9 +93,11 @@ inline bool window_on_tensor_cores(const WindowAttn& a, bool bf16) {
   return bf16 && a.d != 32 && a.Tq > 0 && a.Tk > 0;
 }
 bool launch_window_fwd_tc(const WindowAttn& a, cudaStream_t st);
+bool launch_window_dq_tc(const WindowAttn& a, cudaStream_t st);
+bool launch_window_dkv_tc(const WindowAttn& a, cudaStream_t st);
 // the gradient: dq (and delta), then dk and dv, which read delta
-void launch_window_dq(const WindowAttn& a, bool bf16, cudaStream_t st);
-void launch_window_dkv(const WindowAttn& a, bool bf16, cudaStream_t st);
+bool launch_window_dq(const WindowAttn& a, bool bf16, cudaStream_t st);
+bool launch_window_dkv(const WindowAttn& a, bool bf16, cudaStream_t st);
 
 // ------------------------------------------------------------------------ device ----
 __device__ __forceinline__ void store4(float* p, float4 x) { *reinterpret_cast<float4*>(p) = x; }

@@ -133,7 +133,7 @@ gdn_status window_args(const gdn_cpr_attn* attn, int32_t N, int32_t Tq, int32_t 
 }
 
 size_t window_bytes(const gdn_cpr_attn* a, int32_t Tq, bool backward) {
-  return align_up(GDN_CPR_ATTN_HEADER_BYTES + (backward ? (size_t)Tq * a->h_q * sizeof(float) : 0));
+  return align_up(GDN_CPR_ATTN_HEADER_BYTES + (backward ? 2 * (size_t)Tq * a->h_q * sizeof(float) : 0));
 }
 
 }  // namespace
@@ -371,9 +371,9 @@ gdn_status gdn_cpr_window_attn_bwd(const gdn_cpr_attn* attn, int32_t num_seqs, i
   w.delta = reinterpret_cast<float*>(at(ws, GDN_CPR_ATTN_HEADER_BYTES));
   w.hdr = static_cast<WsHeader*>(ws);
   Stages stg(stream, kWindowBwdStages);
-  launch_window_dq(w, attn->dtype == GDN_BF16, stream);
+  if (!launch_window_dq(w, attn->dtype == GDN_BF16, stream)) return GDN_ERR_CUDA;
   stg.mark(1);
-  launch_window_dkv(w, attn->dtype == GDN_BF16, stream);
+  if (!launch_window_dkv(w, attn->dtype == GDN_BF16, stream)) return GDN_ERR_CUDA;
   stg.mark(1);
   return finish();
 }

@@ -381,7 +381,15 @@ bool launch_window_attn(const WindowAttn& a, bool bf16, cudaStream_t st) {
   GDN_BY_TYPE(fwd_t)
   return true;
 }
-void launch_window_dq(const WindowAttn& a, bool bf16, cudaStream_t st) { GDN_BY_TYPE(dq_t) }
-void launch_window_dkv(const WindowAttn& a, bool bf16, cudaStream_t st) { GDN_BY_TYPE(dkv_t) }
+bool launch_window_dq(const WindowAttn& a, bool bf16, cudaStream_t st) {
+  if (window_on_tensor_cores(a, bf16)) return launch_window_dq_tc(a, st);
+  GDN_BY_TYPE(dq_t)
+  return true;
+}
+bool launch_window_dkv(const WindowAttn& a, bool bf16, cudaStream_t st) {
+  if (window_on_tensor_cores(a, bf16)) return launch_window_dkv_tc(a, st);
+  GDN_BY_TYPE(dkv_t)
+  return true;
+}
 
 }  // namespace gdn
