@@ -63,12 +63,27 @@ __host__ __device__ inline int visible_keys(int len, int window, int sinks) {
   const int behind = len - window;
   return window + (sinks < behind ? sinks : behind);
 }
-// Keys of one split, from the number of visible keys alone, so that a request's result does not
-// depend on the batch.
-__host__ __device__ inline int split_keys(int n) { return n <= 2048 ? 128 : n <= 8192 ? 256 : 512; }
-__host__ __device__ inline int split_count(int n) { return (n + split_keys(n) - 1) / split_keys(n); }
-int paged_decode_max_splits(int max_visible);
-int launch_paged_decode(const PagedDecode& a, bool bf16, cudaStream_t st);
+// Keys of one run, from the request's visible keys and the number of key heads alone, so that a
+// request's result does not depend on the batch: about kRunsPerRequest runs over a request's heads,
+// of 64 to 512 keys, evened out and a multiple of 32 (a tile).
+constexpr int kRunsPerRequest = 32;
+__host__ __device__ inline int target_keys(int n, int hkv) {
+  const int64_t x = (int64_t)n * hkv / kRunsPerRequest;
+  return x < 128 ? 64 : x < 256 ? 128 : x < 512 ? 256 : 512;
+}
+__host__ __device__ inline int target_runs(int n, int hkv) {
+  const int t = target_keys(n, hkv), r = (n + t / 2) / t;
+  return r < 1 ? 1 : r;
+}
+__host__ __device__ inline int split_keys(int n, int hkv) {
+  const int r = target_runs(n, hkv);
+  return ((n + r - 1) / r + 31) / 32 * 32;
+}
+__host__ __device__ inline int split_count(int n, int hkv) {
+  return n == 0 ? 0 : (n + split_keys(n, hkv) - 1) / split_keys(n, hkv);
+}
+int paged_decode_max_splits(int max_visible, int hkv);
+void launch_paged_decode(const PagedDecode& a, bool bf16, cudaStream_t st);
 
 // -------------------------------------------------------------- window attention ----
 struct WindowAttn {

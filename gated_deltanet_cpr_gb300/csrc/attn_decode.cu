@@ -2,20 +2,28 @@
 //
 // A request's visible keys (the first `sinks` and the last `window`, or all) are numbered
 // u = 0 .. n - 1 in key order, so that masks never cut a tile: only its end is short.  They are
-// split into runs of split_keys(n), a function of n alone, and each CTA takes one run of one
-// key head for up to 16 query heads:
+// split into runs of split_keys(n, key heads); one warp takes a run of one key head for up to 16
+// of its query heads in one pass with a running maximum (scores in units of log2 e, so that
+// e^x is one exp2):
 //     s_u = scale q . k_u,  m = max s,  l = sum e^(s - m),  a = sum e^(s - m) v_u
-// in one pass with a running maximum (scores in units of log2 e, so that e^x is one exp2).
-// With one run the CTA writes the output a / l; otherwise it leaves (m, l, a) in the workspace
-// and k_decode_join adds a request's runs in ascending order.
+// and writes the output a / l, or, where a request has several runs, leaves (m, l, a) in the
+// workspace for k_decode_join, which adds them in ascending order.
+//
+// The kernel is bound by the cache's bytes, so what matters is that loads never pause.  A warp
+// works alone: it walks over runs (the grid fills the SMs once), and copies keys and values
+// asynchronously into its own ring, two tiles ahead and across the end of a run.  A
+// kernel of one CTA of four warps per run, which waits for its first keys and joins its warps at
+// the end, reached 72% (runs of 256 keys) to 94% (1024 keys) of the copy bandwidth on 256 requests
+// of about 2112 tokens.
 #include "attn.h"
+#include "tc.cuh"
 
 namespace gdn {
 
 namespace {
 
-constexpr int kDecThreads = 128, kDecWarps = kDecThreads / 32;
-constexpr int kHeadsPerCta = 16;
+constexpr int kHeadsPerRun = 16;
+constexpr int kSms = 152;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ float exp2_approx(float x) {
@@ -24,13 +32,13 @@ __device__ __forceinline__ float exp2_approx(float x) {
   return y;
 }
 
-// What a CTA needs to know of its request.
+// What a warp needs to know of a request.
 struct Request {
   int len, n;        // cached tokens (0 if the length is not valid), visible keys
   int head, skip;    // key of visible index u: u < head ? u : u + skip
   bool bad;
-  __device__ __forceinline__ Request(const PagedDecode& a, int i) {
-    len = a.seq_lens[i];
+  __device__ __forceinline__ Request(const PagedDecode& a, int length) {
+    len = length;
     bad = len < 0 || len > a.max_len;
     if (bad) len = 0;
     n = visible_keys(len, a.window, a.sinks);
@@ -40,156 +48,98 @@ struct Request {
   __device__ __forceinline__ int key(int u) const { return u < head ? u : u + skip; }
 };
 
-// Row (page, key head) of key j, or -1 for a page outside the cache.
-__device__ __forceinline__ int64_t key_row(const PagedDecode& a, const int32_t* bt, int kvh, int j) {
-  const int b = j >> a.page_shift;
-  const int page = b < a.max_blocks ? bt[b] : -1;
-  if (page < 0 || page >= a.num_pages) return -1;
-  return ((((int64_t)page * a.hkv + kvh) << a.page_shift) + (j & ((1 << a.page_shift) - 1)));
+__device__ __forceinline__ void cp_async16_or_zero(uint32_t smem, const void* gmem, bool load) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem), "l"(gmem), "r"(load ? 16 : 0) : "memory");
 }
 
-// Error word: every visible key of request i lies on a page of the cache.  All threads call it.
-__device__ int check_request(const PagedDecode& a, int i) {
-  const Request rq(a, i);
-  if (rq.bad) return GDN_DEVERR_POS;
-  const int32_t* bt = a.block_table + (int64_t)i * a.max_blocks;
-  const int first = rq.n ? rq.key(rq.head) >> a.page_shift : 0, last = rq.n ? (rq.len - 1) >> a.page_shift : -1;
-  const int head_pages = rq.head ? ((rq.head - 1) >> a.page_shift) + 1 : 0;
-  bool bad = false;
-  for (int b = threadIdx.x; b < head_pages + (last - first + 1); b += blockDim.x) {
-    const int p = b < head_pages ? b : first + b - head_pages;
-    const int page = p < a.max_blocks ? bt[p] : -1;
-    bad |= page < 0 || page >= a.num_pages;
-  }
-  return __syncthreads_or(bad) ? GDN_DEVERR_PAGES : 0;
-}
+// One run: request i, key head and part of its query heads, which run, and its keys [u, end); bad:
+// a key's page is outside the cache.
+struct Run {
+  int i, y, run, runs, u, end, head, skip, bad;
+  __device__ __forceinline__ int key(int x) const { return x < head ? x : x + skip; }
+};
 
-// The warps' (m, l, a) of one CTA joined in warp order and written: as the output when the
-// request has one run, else as the run's record.  sm, sl: [heads][warps]; sa: [warps][heads][D].
-template <int D, typename T>
-__device__ __forceinline__ void finish_run(const PagedDecode& a, int i, int h0, int heads, int run, bool single,
-                                           const float* sm, const float* sl, const float* sa, int sa_heads) {
-  for (int e = threadIdx.x; e < heads * D; e += kDecThreads) {
-    const int h = e / D, c = e % D;
-    float m = sm[h * kDecWarps];
-#pragma unroll
-    for (int w = 1; w < kDecWarps; ++w) m = fmaxf(m, sm[h * kDecWarps + w]);
-    float l = 0.f, acc = 0.f;
-#pragma unroll
-    for (int w = 0; w < kDecWarps; ++w) {
-      const float mw = sm[h * kDecWarps + w];
-      const float f = mw == -INFINITY ? 0.f : exp2_approx(__fsub_rn(mw, m));
-      l = __fmaf_rn(f, sl[h * kDecWarps + w], l);
-      acc = __fmaf_rn(f, sa[(w * sa_heads + h) * D + c], acc);
-    }
-    const int64_t row = (int64_t)i * a.hq + h0 + h;
-    if (single) {
-      store_out(static_cast<T*>(a.out) + row * D + c, __fdiv_rn(acc, l));
-      if (a.lse && c == 0) a.lse[row] = __fmul_rn(__fadd_rn(m, log2f(l)), kLn2);
-    } else {
-      const int64_t rec = row * a.max_splits + run;
-      a.partial[rec * D + c] = acc;
-      if (c == 0) {
-        float* ml = a.partial + (int64_t)a.N * a.hq * a.max_splits * D + rec * 2;
-        ml[0] = m;
-        ml[1] = l;
-      }
+// Where a run's (m, l, a) or output goes: rows of its heads.
+struct Sink {
+  float* acc;   // record of head 0's run, or NULL: the run is the whole request
+  float2* ml;
+  int64_t acc_step, ml_step;  // from one head to the next
+  void* out;                  // row of head 0
+  float* lse;
+  int heads;
+  __device__ __forceinline__ Sink(const PagedDecode& a, const Run& r, int h0, int heads_, int elem) : heads(heads_) {
+    const int64_t row = (int64_t)r.i * a.hq + h0;
+    out = static_cast<char*>(a.out) + row * a.d * elem;
+    lse = a.lse ? a.lse + row : nullptr;
+    acc = nullptr;
+    ml = nullptr;
+    acc_step = ml_step = 0;
+    if (r.runs > 1) {
+      const int64_t rec = row * a.max_splits + r.run;
+      acc = a.partial + rec * a.d;
+      ml = reinterpret_cast<float2*>(a.partial + (int64_t)a.N * a.hq * a.max_splits * a.d) + rec;
+      acc_step = (int64_t)a.max_splits * a.d;
+      ml_step = a.max_splits;
     }
   }
-}
-
-// Rows of a request without keys (zeros) or with a length that is not valid (NaN).
-template <int D, typename T>
-__device__ __forceinline__ void write_empty(const PagedDecode& a, int i, int h0, int heads, bool bad) {
-  const float x = bad ? __builtin_nanf("") : 0.f;
-  for (int e = threadIdx.x; e < heads * D; e += kDecThreads) {
-    const int64_t row = (int64_t)i * a.hq + h0 + e / D;
-    store_out(static_cast<T*>(a.out) + row * D + e % D, x);
-    if (a.lse && e % D == 0) a.lse[row] = bad ? x : -INFINITY;
+  __device__ __forceinline__ void stats(int h, float m, float l) const {
+    if (ml) ml[h * ml_step] = make_float2(m, l);
+    else if (lse) lse[h] = __fmul_rn(__fadd_rn(m, log2f(l)), kLn2);
   }
-}
-
-// The error word of a call: set by the join kernel's CTAs, after this kernel's first CTA has
-// cleared it; without a join kernel that CTA looks at every request itself.
-__device__ __forceinline__ void error_word(const PagedDecode& a) {
-  if (blockIdx.x || blockIdx.y || blockIdx.z) return;
-  int err = 0;
-  if (a.max_splits == 1)
-    for (int i = 0; i < a.N && !err; ++i) err = check_request(a, i);
-  if (threadIdx.x == 0) a.hdr->err = err;
-}
+};
 
 // ---------------------------------------------------------------------------- SIMT ----
-// fp32 caches, and bf16 ones with d = 32.  A lane holds 4 columns, LPR = D / 4 lanes a key, and a warp takes 8 keys
-// at a time.  Per lane group the partial dots of 8 / KPW keys with 4 heads are LPR values, which
-// one halving exchange turns into one whole score per lane (LPR - 1 shuffles instead of
-// log2(LPR) per score), where its exponential is formed.
-template <int D, typename T, int NC>
-__global__ void __launch_bounds__(kDecThreads) k_decode_simt(const PagedDecode a) {
-  constexpr int LPR = D / 4, KPW = 32 / LPR, KT = 8 / KPW;
-  static_assert(KT * 4 == LPR, "one score per lane");
-  __shared__ float qs[NC * 4][D];
-  __shared__ float sm[NC * 4][kDecWarps], sl[NC * 4][kDecWarps];
-  __shared__ float sa[kDecWarps][NC * 4][D];
-  error_word(a);
-  const int i = blockIdx.z, run = blockIdx.x, group = a.hq / a.hkv;
-  const int parts = (group + kHeadsPerCta - 1) / kHeadsPerCta, kvh = blockIdx.y / parts;
-  const int g0 = (blockIdx.y % parts) * kHeadsPerCta, heads = min(kHeadsPerCta, group - g0);
-  const int h0 = kvh * group + g0;
-  const Request rq(a, i);
-  const int runs = split_count(rq.n);
-  if (run >= runs) {
-    if (run == 0) write_empty<D, T>(a, i, h0, heads, rq.bad);
-    return;
-  }
-  const float qscale = __fmul_rn(a.scale, kLog2e);
-  for (int e = threadIdx.x; e < NC * 4 * D; e += kDecThreads) {
-    const int h = e / D;
-    qs[h][e % D] =
-        h < heads ? __fmul_rn(to_f32(static_cast<const T*>(a.q)[((int64_t)i * a.hq + h0 + h) * D + e % D]), qscale) : 0.f;
-  }
-  __syncthreads();
-  const int per = split_keys(rq.n), u_end = min(rq.n, (run + 1) * per);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, grp = lane / LPR, b = lane % LPR;
-  const int32_t* bt = a.block_table + (int64_t)i * a.max_blocks;
-  const T *kp = static_cast<const T*>(a.k_pages) + 4 * b, *vp = static_cast<const T*>(a.v_pages) + 4 * b;
+// fp32 caches, and bf16 ones with d = 32.  A lane holds 4 columns, LPR = D / 4 lanes a key, and a
+// tile is 32 / H keys.  Per lane group the partial dots of its KT keys with H heads (2 or 4) are LPR
+// values, which one halving exchange turns into one whole score per lane (LPR - 1 shuffles
+// instead of log2(LPR) per score), where its exponential is formed.  NC chunks of H heads.
+template <int D, typename T, int H, int NC>
+struct SimtEngine {
+  using Elem = T;
+  static constexpr int DIM = D, KEYS = 32 / H, ROWB = D * sizeof(T), EXTRA = NC * H * D * 4;
+  static constexpr int RING = KEYS * ROWB > 4096 ? 2 : 3, WARPS = KEYS * ROWB > 4096 ? 6 : 4;
+  static constexpr int LPR = D / 4, KPW = 32 / LPR, KT = KEYS / KPW;
+  static_assert(KT * H == LPR, "one score per lane");
+  const float* qs;  // [NC * H][D], scaled
   float m[NC], l[NC];
-  float4 acc[NC][4];
+  float4 acc[NC][H];
+
+  __device__ __forceinline__ static uint32_t place(int r, int c) { return r * ROWB + c * 16; }
+
+  __device__ __forceinline__ void start(const PagedDecode& a, int64_t row, int heads, unsigned char* extra, int lane) {
+    float* q = reinterpret_cast<float*>(extra);
+    const float scale = __fmul_rn(a.scale, kLog2e);
+    const T* src = static_cast<const T*>(a.q) + row * D;
+    __syncwarp();
+#pragma unroll 4
+    for (int e = lane; e < NC * H * D; e += 32) q[e] = e < heads * D ? __fmul_rn(to_f32(src[e]), scale) : 0.f;
+    __syncwarp();
+    qs = q;
 #pragma unroll
-  for (int c = 0; c < NC; ++c) {
-    m[c] = -INFINITY;
-    l[c] = 0.f;
+    for (int c = 0; c < NC; ++c) {
+      m[c] = -INFINITY;
+      l[c] = 0.f;
 #pragma unroll
-    for (int h = 0; h < 4; ++h) acc[c][h] = make_float4(0.f, 0.f, 0.f, 0.f);
-  }
-  bool bad = false;
-  for (int u0 = run * per + warp * 8; u0 < u_end; u0 += kDecWarps * 8) {
-    float4 kk[KT], vv[KT];
-#pragma unroll
-    for (int t = 0; t < KT; ++t) {
-      const int u = u0 + grp * KT + t;
-      kk[t] = vv[t] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (u < u_end) {
-        const int64_t row = key_row(a, bt, kvh, rq.key(u));
-        if (row >= 0) {
-          kk[t] = load4(kp + row * D);
-          vv[t] = load4(vp + row * D);
-        } else {
-          bad = true;
-        }
-      }
+      for (int h = 0; h < H; ++h) acc[c][h] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
-    const bool live = u0 + grp * KT + (b >> 2) < u_end;  // the key of this lane's score
+  }
+
+  __device__ __forceinline__ void tile(const PagedDecode&, const unsigned char* st, int keys, int lane) {
+    const int grp = lane / LPR, b = lane % LPR;
+    const T* p0 = reinterpret_cast<const T*>(st) + grp * KT * D + 4 * b;
+    const bool live = grp * KT + b / H < keys;  // the key of this lane's score
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
       float val[LPR];
 #pragma unroll
-      for (int h = 0; h < 4; ++h) {
-        const float4 q4 = *reinterpret_cast<const float4*>(&qs[c * 4 + h][4 * b]);
+      for (int t = 0; t < KT; ++t) {
+        const float4 k4 = load4(p0 + t * D);
 #pragma unroll
-        for (int t = 0; t < KT; ++t)
-          val[t * 4 + h] = __fmaf_rn(
-              q4.w, kk[t].w, __fmaf_rn(q4.z, kk[t].z, __fmaf_rn(q4.y, kk[t].y, __fmul_rn(q4.x, kk[t].x))));
+        for (int h = 0; h < H; ++h) {
+          const float4 q4 = *reinterpret_cast<const float4*>(qs + (c * H + h) * D + 4 * b);
+          val[t * H + h] =
+              __fmaf_rn(q4.w, k4.w, __fmaf_rn(q4.z, k4.z, __fmaf_rn(q4.y, k4.y, __fmul_rn(q4.x, k4.x))));
+        }
       }
 #pragma unroll
       for (int o = LPR / 2; o > 0; o >>= 1) {
@@ -200,123 +150,550 @@ __global__ void __launch_bounds__(kDecThreads) k_decode_simt(const PagedDecode a
           val[j] = __fadd_rn(keep, __shfl_xor_sync(0xffffffffu, send, o));
         }
       }
-      const float s = live ? val[0] : -INFINITY;  // head b & 3
+      const float s = live ? val[0] : -INFINITY;  // head b % H
       float mx = s;
 #pragma unroll
-      for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      for (int o = H; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
       mx = fmaxf(mx, m[c]);
       const float base = mx == -INFINITY ? 0.f : mx;
       const float alpha = exp2_approx(__fsub_rn(m[c], base)), p = exp2_approx(__fsub_rn(s, base));
       m[c] = mx;
       l[c] = __fmaf_rn(l[c], alpha, p);
 #pragma unroll
-      for (int h = 0; h < 4; ++h) {
+      for (int h = 0; h < H; ++h) {
         const float al = __shfl_sync(0xffffffffu, alpha, h);
-        float4 x = acc[c][h];
+        float4& x = acc[c][h];
         x = make_float4(__fmul_rn(x.x, al), __fmul_rn(x.y, al), __fmul_rn(x.z, al), __fmul_rn(x.w, al));
+      }
 #pragma unroll
-        for (int t = 0; t < KT; ++t) {
-          const float ph = __shfl_sync(0xffffffffu, p, grp * LPR + t * 4 + h);
-          x = make_float4(__fmaf_rn(ph, vv[t].x, x.x), __fmaf_rn(ph, vv[t].y, x.y), __fmaf_rn(ph, vv[t].z, x.z),
-                          __fmaf_rn(ph, vv[t].w, x.w));
+      for (int t = 0; t < KT; ++t) {
+        const float4 v4 = load4(p0 + (KEYS + t) * D);
+#pragma unroll
+        for (int h = 0; h < H; ++h) {
+          const float ph = __shfl_sync(0xffffffffu, p, grp * LPR + t * H + h);
+          float4& x = acc[c][h];
+          x = make_float4(__fmaf_rn(ph, v4.x, x.x), __fmaf_rn(ph, v4.y, x.y), __fmaf_rn(ph, v4.z, x.z),
+                          __fmaf_rn(ph, v4.w, x.w));
         }
-        acc[c][h] = x;
       }
     }
   }
-  bad = __any_sync(0xffffffffu, bad);
+
+  __device__ __forceinline__ void finish(const Sink& k, bool bad, int lane) {
+    const int grp = lane / LPR, b = lane % LPR;
 #pragma unroll
-  for (int c = 0; c < NC; ++c) {
-    float lc = l[c];
+    for (int c = 0; c < NC; ++c) {
+      float lc = l[c];
 #pragma unroll
-    for (int o = 4; o < 32; o <<= 1) lc = __fadd_rn(lc, __shfl_xor_sync(0xffffffffu, lc, o));
-    if (lane < 4) {
-      sm[c * 4 + lane][warp] = m[c];
-      sl[c * 4 + lane][warp] = bad ? __builtin_nanf("") : lc;
-    }
+      for (int o = H; o < 32; o <<= 1) lc = __fadd_rn(lc, __shfl_xor_sync(0xffffffffu, lc, o));
+      if (bad) lc = __builtin_nanf("");
+      if (lane < H && c * H + lane < k.heads) k.stats(c * H + lane, m[c], lc);
 #pragma unroll
-    for (int h = 0; h < 4; ++h) {
-      float4 x = acc[c][h];
+      for (int h = 0; h < H; ++h) {
+        float4 x = acc[c][h];
 #pragma unroll
-      for (int o = LPR; o < 32; o <<= 1) {
-        x.x = __fadd_rn(x.x, __shfl_xor_sync(0xffffffffu, x.x, o));
-        x.y = __fadd_rn(x.y, __shfl_xor_sync(0xffffffffu, x.y, o));
-        x.z = __fadd_rn(x.z, __shfl_xor_sync(0xffffffffu, x.z, o));
-        x.w = __fadd_rn(x.w, __shfl_xor_sync(0xffffffffu, x.w, o));
+        for (int o = LPR; o < 32; o <<= 1) {
+          x.x = __fadd_rn(x.x, __shfl_xor_sync(0xffffffffu, x.x, o));
+          x.y = __fadd_rn(x.y, __shfl_xor_sync(0xffffffffu, x.y, o));
+          x.z = __fadd_rn(x.z, __shfl_xor_sync(0xffffffffu, x.z, o));
+          x.w = __fadd_rn(x.w, __shfl_xor_sync(0xffffffffu, x.w, o));
+        }
+        const float lh = __shfl_sync(0xffffffffu, lc, h);
+        if (grp || c * H + h >= k.heads) continue;
+        if (k.acc)
+          store4(k.acc + (c * H + h) * k.acc_step + 4 * b, x);
+        else
+          store4(static_cast<T*>(k.out) + (c * H + h) * D + 4 * b,
+                 make_float4(__fdiv_rn(x.x, lh), __fdiv_rn(x.y, lh), __fdiv_rn(x.z, lh), __fdiv_rn(x.w, lh)));
       }
-      if (grp == 0) *reinterpret_cast<float4*>(&sa[warp][c * 4 + h][4 * b]) = x;
     }
   }
-  __syncthreads();
-  finish_run<D, T>(a, i, h0, heads, run, runs == 1, &sm[0][0], &sl[0][0], &sa[0][0][0], NC * 4);
+};
+
+// ----------------------------------------------------------------------- tensor cores ----
+// bf16 caches with d = 64 or 128.  fp32 lanes would spend 4 FMA per byte on 16 heads, more than
+// they have, so the products run on warp-level MMAs (m16n8k16), far below their rate.  A tile is
+// 32 keys: scores [16 heads x 32 keys], the running maximum and sum, then P V with P as the sum of
+// two bf16 (so that its rounding does not show in the output).  Rows are swizzled so that the 8
+// rows of a matrix load lie in 8 bank groups: piece c of row r at c ^ (r & 7).
+__device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  const __nv_bfloat162 x = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&x);
+}
+// the part of (lo, hi) that pack2 lost
+__device__ __forceinline__ uint32_t pack2_rest(float lo, float hi, uint32_t packed) {
+  return pack2(__fsub_rn(lo, __uint_as_float(packed << 16)), __fsub_rn(hi, __uint_as_float(packed & 0xffff0000u)));
+}
+
+template <int D>
+struct MmaEngine {
+  using Elem = __nv_bfloat16;
+  static constexpr int DIM = D, KEYS = 32, ROWB = D * 2, RING = 2, WARPS = D == 128 ? 7 : 4, EXTRA = 0, KS = D / 16, NT = KEYS / 8;
+  uint32_t q[KS][4];
+  float m[2], l[2], o[D / 8][4];
+
+  __device__ __forceinline__ static uint32_t place(int r, int c) { return r * ROWB + ((c ^ (r & 7)) << 4); }
+
+  __device__ __forceinline__ void start(const PagedDecode& a, int64_t row, int heads, unsigned char*, int lane) {
+    // query fragments: rows = heads lane / 4 and + 8, columns 16 k + 2 (lane % 4) and + 8
+    const Elem* qp = static_cast<const Elem*>(a.q) + row * D + 2 * (lane & 3);
+    const int r0 = lane >> 2, r1 = r0 + 8;
+#pragma unroll
+    for (int k = 0; k < KS; ++k)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        q[k][2 * e] = r0 < heads ? *reinterpret_cast<const uint32_t*>(qp + r0 * D + 16 * k + 8 * e) : 0u;
+        q[k][2 * e + 1] = r1 < heads ? *reinterpret_cast<const uint32_t*>(qp + r1 * D + 16 * k + 8 * e) : 0u;
+      }
+#pragma unroll
+    for (int r = 0; r < 2; ++r) m[r] = -INFINITY, l[r] = 0.f;
+#pragma unroll
+    for (int j = 0; j < D / 8; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
+  }
+
+  __device__ __forceinline__ void tile(const PagedDecode& a, const unsigned char* stage, int keys, int lane) {
+    const uint32_t st = tc::smem_u32(stage);
+    // matrix-load addresses: row of the tile, and which 16-byte piece of a pair
+    const int kr = (lane & 7) + ((lane >> 4) << 3), kc = (lane >> 3) & 1, vr = lane & 15, vc = lane >> 4;
+    const float sc = __fmul_rn(a.scale, kLog2e);
+    float x[NT][4];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[n][e] = 0.f;
+#pragma unroll
+    for (int k = 0; k < KS; ++k)
+#pragma unroll
+      for (int n = 0; n < NT; n += 2) {
+        uint32_t b[4];
+        ldsm_x4(st + place(kr + 8 * n, 2 * k + kc), b);
+        mma16816(x[n], q[k], b[0], b[1]);
+        mma16816(x[n + 1], q[k], b[2], b[3]);
+      }
+    if (keys < KEYS) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (2 * (lane & 3) + 8 * n + (e & 1) >= keys) x[n][e] = -INFINITY;
+    }
+    float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) mx[e >> 1] = fmaxf(mx[e >> 1], x[n][e]);
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
+      mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
+      mx[r] = fmaxf(m[r], __fmul_rn(mx[r], sc));
+    }
+    if (__any_sync(0xffffffffu, mx[0] > m[0] || mx[1] > m[1])) {
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const float f = m[r] == -INFINITY ? 0.f : exp2_approx(__fsub_rn(m[r], mx[r]));
+        m[r] = mx[r];
+        l[r] = __fmul_rn(l[r], f);
+#pragma unroll
+        for (int j = 0; j < D / 8; ++j) {
+          o[j][2 * r] = __fmul_rn(o[j][2 * r], f);
+          o[j][2 * r + 1] = __fmul_rn(o[j][2 * r + 1], f);
+        }
+      }
+    }
+    const float base[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        x[n][e] = exp2_approx(__fmaf_rn(x[n][e], sc, -base[e >> 1]));
+        l[e >> 1] = __fadd_rn(l[e >> 1], x[n][e]);
+      }
+#pragma unroll
+    for (int n = 0; n < NT; n += 2) {  // 16 keys
+      const uint32_t hi[4] = {pack2(x[n][0], x[n][1]), pack2(x[n][2], x[n][3]), pack2(x[n + 1][0], x[n + 1][1]),
+                              pack2(x[n + 1][2], x[n + 1][3])};
+      const uint32_t lo[4] = {pack2_rest(x[n][0], x[n][1], hi[0]), pack2_rest(x[n][2], x[n][3], hi[1]),
+                              pack2_rest(x[n + 1][0], x[n + 1][1], hi[2]), pack2_rest(x[n + 1][2], x[n + 1][3], hi[3])};
+#pragma unroll
+      for (int j = 0; j < D / 16; ++j) {
+        uint32_t b[4];
+        tc::ldsm_x4_trans(st + KEYS * ROWB + place(vr + 8 * n, 2 * j + vc), b);
+        mma16816(o[2 * j], hi, b[0], b[1]);
+        mma16816(o[2 * j + 1], hi, b[2], b[3]);
+        mma16816(o[2 * j], lo, b[0], b[1]);
+        mma16816(o[2 * j + 1], lo, b[2], b[3]);
+      }
+    }
+  }
+
+  __device__ __forceinline__ void finish(const Sink& k, bool bad, int lane) {
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      l[r] = __fadd_rn(l[r], __shfl_xor_sync(0xffffffffu, l[r], 1));
+      l[r] = __fadd_rn(l[r], __shfl_xor_sync(0xffffffffu, l[r], 2));
+      if (bad) l[r] = __builtin_nanf("");
+      const int h = (lane >> 2) + 8 * r;
+      if (h >= k.heads) continue;
+      if ((lane & 3) == 0) k.stats(h, m[r], l[r]);
+#pragma unroll
+      for (int j = 0; j < D / 8; ++j) {
+        const int c = 8 * j + 2 * (lane & 3);
+        if (k.acc)
+          *reinterpret_cast<float2*>(k.acc + h * k.acc_step + c) = make_float2(o[j][2 * r], o[j][2 * r + 1]);
+        else
+          *reinterpret_cast<uint32_t*>(static_cast<Elem*>(k.out) + h * D + c) =
+              pack2(__fdiv_rn(o[j][2 * r], l[r]), __fdiv_rn(o[j][2 * r + 1], l[r]));
+      }
+    }
+  }
+};
+
+// ---------------------------------------------------------------------------- walk ----
+// The fetching side of a warp: which tile comes next, and where its keys lie.
+template <typename E>
+struct Walk {
+  static constexpr int STAGE = 2 * E::KEYS * E::ROWB;
+  int64_t next, total;  // where the search for the next run goes on; all (request, part, run)
+  int cand_len;         // length of the request of candidate next + lane * (warps of the grid)
+  Run r;                // the run being fetched
+  bool live;            // there is one
+  uint32_t row;         // lane < KEYS: row of key r.u + lane (~0: none, or past the run's end)
+
+  __device__ __forceinline__ int64_t candidate(int lane) const {
+    return next + (int64_t)lane * (gridDim.x * E::WARPS);
+  }
+  // the candidates' lengths, read a run ahead of their use
+  __device__ __forceinline__ void look_ahead(const PagedDecode& a, int64_t rows, int parts, int lane) {
+    const int64_t w = candidate(lane);
+    if (w < total) cand_len = a.seq_lens[(int)(w % rows / (a.hkv * parts))];
+  }
+
+  // The next run of this warp from `next` on, 32 candidates at a time.  Requests without keys have
+  // their rows written here.
+  __device__ void seek(const PagedDecode& a, int parts, int lane) {
+    const int64_t rows = (int64_t)a.N * a.hkv * parts;
+    live = false;
+    while (next < total) {
+      const int64_t w = candidate(lane);
+      bool have = false;
+      Run c{};
+      if (w < total) {
+        c.run = (int)(w / rows);  // slowest, so that the places short requests leave empty come last
+        c.y = (int)(w % rows % (a.hkv * parts));
+        c.i = (int)(w % rows / (a.hkv * parts));
+        const Request rq(a, cand_len);
+        c.runs = split_count(rq.n, a.hkv);
+        if (c.run < c.runs) {
+          const int per = split_keys(rq.n, a.hkv);
+          c.u = c.run * per;
+          c.end = min(rq.n, c.u + per);
+          c.head = rq.head;
+          c.skip = rq.skip;
+          have = true;
+        } else if (c.runs == 0 && c.run == 0) {
+          write_empty(a, c, parts, rq.bad);
+        }
+      }
+      const uint32_t any = __ballot_sync(0xffffffffu, have);
+      if (any) {
+        const int src = __ffs(any) - 1;
+        r.i = __shfl_sync(0xffffffffu, c.i, src);
+        r.y = __shfl_sync(0xffffffffu, c.y, src);
+        r.run = __shfl_sync(0xffffffffu, c.run, src);
+        r.runs = __shfl_sync(0xffffffffu, c.runs, src);
+        r.u = __shfl_sync(0xffffffffu, c.u, src);
+        r.end = __shfl_sync(0xffffffffu, c.end, src);
+        r.head = __shfl_sync(0xffffffffu, c.head, src);
+        r.skip = __shfl_sync(0xffffffffu, c.skip, src);
+        next += (int64_t)(src + 1) * (gridDim.x * E::WARPS);
+        live = true;
+        look_ahead(a, rows, parts, lane);
+        return;
+      }
+      next += 32 * (int64_t)(gridDim.x * E::WARPS);
+      look_ahead(a, rows, parts, lane);
+    }
+  }
+
+  // zeros for a request without keys, NaN for a length that is not valid; one lane
+  __device__ static void write_empty(const PagedDecode& a, const Run& c, int parts, bool bad) {
+    const int group = a.hq / a.hkv, g0 = (c.y % parts) * kHeadsPerRun, heads = min(kHeadsPerRun, group - g0);
+    const int64_t row = (int64_t)c.i * a.hq + (c.y / parts) * group + g0;
+    const float x = bad ? __builtin_nanf("") : 0.f;
+    for (int e = 0; e < heads * E::DIM; e += 4)
+      store4(static_cast<typename E::Elem*>(a.out) + row * E::DIM + e, make_float4(x, x, x, x));
+    if (a.lse)
+      for (int h = 0; h < heads; ++h) a.lse[row + h] = bad ? x : -INFINITY;
+  }
+
+  __device__ __forceinline__ void look_up(const PagedDecode& a, int parts, int lane, Run* queue, int tail) {
+    row = ~0u;
+    if (!live) return;
+    bool lost = false;
+    if (lane < E::KEYS && r.u + lane < r.end) {
+      const int j = r.key(r.u + lane), b = j >> a.page_shift;
+      const int page = b < a.max_blocks ? a.block_table[(int64_t)r.i * a.max_blocks + b] : -1;
+      lost = page < 0 || page >= a.num_pages;
+      if (!lost)
+        row = (uint32_t)((((int64_t)page * a.hkv + r.y / parts) << a.page_shift) + (j & ((1 << a.page_shift) - 1)));
+    }
+    if (__any_sync(0xffffffffu, lost) && lane == 0) queue[(tail - 1) & 3].bad = 1;
+  }
+
+  // The current tile into `stage`, then on to the next one (its rows are looked up meanwhile).
+  // Eight lanes copy 128 bytes of a row (its last 64 or 128 at smaller rows); a lane meets the
+  // rows G, G + step, ..., so that one shuffle and one address serve all of a row's pieces.
+  __device__ __forceinline__ void fetch(const PagedDecode& a, int parts, uint32_t stage, int lane, Run* queue, int& tail) {
+    if (live) {
+      constexpr int PIECES = E::ROWB / 16, LANES = PIECES < 8 ? PIECES : 8;  // lanes of a row
+      constexpr int ROWS = 32 / LANES, PARTS = PIECES / LANES;                // rows at a time, pieces of a lane
+      const int g = lane / LANES, c = lane % LANES;
+#pragma unroll
+      for (int r0 = 0; r0 < E::KEYS; r0 += ROWS) {
+        const uint32_t at = __shfl_sync(0xffffffffu, row, (r0 + g) % E::KEYS);
+        if (ROWS > E::KEYS && g >= E::KEYS) break;
+        const bool load = at != ~0u;
+        const int64_t off = load ? (int64_t)at * E::ROWB + 16 * c : 0;
+        const char *kp = static_cast<const char*>(a.k_pages) + off, *vp = static_cast<const char*>(a.v_pages) + off;
+        const uint32_t dst = stage + E::place(r0 + g, c);
+#pragma unroll
+        for (int e = 0; e < PARTS; ++e) {  // place() moves by 128 bytes from piece c to c + 8
+          cp_async16_or_zero(dst + 128 * e, kp + 128 * e, load);
+          cp_async16_or_zero(dst + E::KEYS * E::ROWB + 128 * e, vp + 128 * e, load);
+        }
+      }
+      step(a, parts, lane, queue, tail);
+    }
+    tc::cp_async_commit();
+  }
+
+  __device__ __forceinline__ void step(const PagedDecode& a, int parts, int lane, Run* queue, int& tail) {
+    r.u += E::KEYS;
+    if (r.u >= r.end) {
+      seek(a, parts, lane);
+      if (live) push(a, parts, queue, tail, lane);
+    }
+    look_up(a, parts, lane, queue, tail);
+  }
+  // a run that is fetched from here on: at most the computed one, two fetched tiles' and the next are open
+  __device__ __forceinline__ void push(const PagedDecode& a, int parts, Run* queue, int& tail, int lane) {
+    r.bad = 0;
+    if (lane == 0) queue[tail & 3] = r;
+    const int group = a.hq / a.hkv, g0 = (r.y % parts) * kHeadsPerRun, heads = min(kHeadsPerRun, group - g0);
+    const char* q = static_cast<const char*>(a.q) + ((int64_t)r.i * a.hq + (r.y / parts) * group + g0) * E::ROWB;
+    for (int e = lane * 128; e < heads * E::ROWB; e += 32 * 128) tc::prefetch_l2(q + e);
+    ++tail;
+  }
+};
+
+template <typename E>
+struct DecodeSmem {
+  static constexpr int STAGE = Walk<E>::STAGE, RING = E::RING * STAGE, EXTRA = RING, QUEUE = EXTRA + E::EXTRA;
+  static constexpr int WARP = (QUEUE + 4 * (int)sizeof(Run) + 127) / 128 * 128, BYTES = E::WARPS * WARP;
+};
+
+template <typename E>
+__global__ void __launch_bounds__(32 * E::WARPS) k_decode(const PagedDecode a, const int parts) {
+  using L = DecodeSmem<E>;
+  extern __shared__ __align__(128) unsigned char all[];
+  unsigned char* sh = all + (threadIdx.x >> 5) * L::WARP;
+  asm volatile("griddepcontrol.launch_dependents;");  // the join kernel may get ready
+  const int lane = threadIdx.x & 31, group = a.hq / a.hkv;
+  if (blockIdx.x == 0 && threadIdx.x == 0) a.hdr->err = 0;  // set by the join kernel
+  Run* queue = reinterpret_cast<Run*>(sh + L::QUEUE);
+  const uint32_t ring = tc::smem_u32(sh);
+  Walk<E> f;
+  f.next = (int64_t)blockIdx.x * E::WARPS + (threadIdx.x >> 5);
+  f.total = (int64_t)a.N * a.hkv * parts * a.max_splits;
+  int head = 0, tail = 0, put = 0, get = 0;
+  f.look_ahead(a, (int64_t)a.N * a.hkv * parts, parts, lane);
+  f.seek(a, parts, lane);
+  if (f.live) f.push(a, parts, queue, tail, lane);
+  f.look_up(a, parts, lane, queue, tail);
+#pragma unroll
+  for (int s = 0; s < E::RING - 1; ++s) {
+    f.fetch(a, parts, ring + put * L::STAGE, lane, queue, tail);
+    put = put + 1 == E::RING ? 0 : put + 1;
+  }
+  E eng;
+  while (head != tail) {
+    __syncwarp();
+    Run r = queue[head & 3];
+    const int g0 = (r.y % parts) * kHeadsPerRun, heads = min(kHeadsPerRun, group - g0);
+    const int h0 = (r.y / parts) * group + g0;
+    eng.start(a, (int64_t)r.i * a.hq + h0, heads, sh + L::EXTRA, lane);
+    for (; r.u < r.end; r.u += E::KEYS) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(E::RING - 2) : "memory");
+      __syncwarp();
+      eng.tile(a, sh + get * L::STAGE, r.end - r.u, lane);
+      get = get + 1 == E::RING ? 0 : get + 1;
+      __syncwarp();  // every lane has read the ring place that is filled next
+      f.fetch(a, parts, ring + put * L::STAGE, lane, queue, tail);
+      put = put + 1 == E::RING ? 0 : put + 1;
+    }
+    __syncwarp();
+    eng.finish(Sink(a, r, h0, heads, sizeof(typename E::Elem)), queue[head & 3].bad != 0, lane);
+    ++head;
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 // ---------------------------------------------------------------------------- join ----
-// One warp per (request, head): adds the runs' records in ascending order.  The first head's
-// CTA of a request also checks it for the error word.
+// D / 4 lanes per (request, head) add the runs' records in ascending order, 8 at a time so that their
+// loads are in flight together; more than 32 runs are shared out to the block's groups of lanes,
+// whose sums are added in order (`split`: the blocks have one head each).  How a request's runs are added
+// depends on their number alone.  A request's CTAs also check its length and the pages of its
+// visible keys for the error word.
 template <int D, typename T>
-__global__ void __launch_bounds__(128) k_decode_join(const PagedDecode a) {
-  constexpr int V = D / 32;
-  const int i = blockIdx.y, h = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  const Request rq(a, i);
-  const int runs = split_count(rq.n);
-  if (h < a.hq && runs > 1) {
+__global__ void __launch_bounds__(128) k_decode_join(const PagedDecode a, const bool split) {
+  constexpr int LANES = D / 4, GROUPS = 128 / LANES, B = 8;
+  __shared__ float4 so[GROUPS][LANES];
+  __shared__ float2 sml[GROUPS];
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the runs' kernel has finished
+  const int g = threadIdx.x / LANES, lane = threadIdx.x % LANES, c = 4 * lane;
+  const int i = blockIdx.y, h = split ? blockIdx.x : blockIdx.x * GROUPS + g;
+  const Request rq(a, a.seq_lens[i]);
+  const int runs = split_count(rq.n, a.hkv);
+  const bool shared = runs > 32;  // only with `split`
+  const int per = shared ? (runs + GROUPS - 1) / GROUPS : runs;
+  const int begin = shared ? min(runs, g * per) : 0, end = shared ? min(runs, begin + per) : runs;
+  if (runs > 1 && h < a.hq && (shared || !split || g == 0)) {
     const int64_t row = (int64_t)i * a.hq + h;
-    const float* rec = a.partial + row * a.max_splits * D;
-    const float* ml = a.partial + ((int64_t)a.N * a.hq * D + row * 2) * a.max_splits;
-    float m = -INFINITY;
-    for (int r = lane; r < runs; r += 32) m = fmaxf(m, ml[2 * r]);
+    const float* rec = a.partial + row * a.max_splits * D + c;
+    const float2* mls =
+        reinterpret_cast<const float2*>(a.partial + (int64_t)a.N * a.hq * a.max_splits * D) + row * a.max_splits;
+    float m = -INFINITY, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto add = [&](const float2 (&ml)[B], const float4 (&x)[B]) {
+      float mx = m;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    float l = 0.f, acc[V];
+      for (int r = 0; r < B; ++r) mx = fmaxf(mx, ml[r].x);
+      const float base = mx == -INFINITY ? 0.f : mx, f0 = exp2_approx(__fsub_rn(m, base));
+      m = mx;
+      l = __fmul_rn(l, f0);
+      o = make_float4(__fmul_rn(o.x, f0), __fmul_rn(o.y, f0), __fmul_rn(o.z, f0), __fmul_rn(o.w, f0));
 #pragma unroll
-    for (int v = 0; v < V; ++v) acc[v] = 0.f;
-#pragma unroll 4
-    for (int r = 0; r < runs; ++r) {
-      const float f = exp2_approx(__fsub_rn(ml[2 * r], m));
-      l = __fmaf_rn(f, ml[2 * r + 1], l);
+      for (int r = 0; r < B; ++r) {
+        const float f = exp2_approx(__fsub_rn(ml[r].x, base));
+        l = __fmaf_rn(f, ml[r].y, l);
+        o = make_float4(__fmaf_rn(f, x[r].x, o.x), __fmaf_rn(f, x[r].y, o.y), __fmaf_rn(f, x[r].z, o.z),
+                        __fmaf_rn(f, x[r].w, o.w));
+      }
+    };
+    float2 ml[B];
+    float4 x[B];
+    for (int r0 = begin; r0 < end; r0 += B) {
 #pragma unroll
-      for (int v = 0; v < V; ++v) acc[v] = __fmaf_rn(f, rec[(int64_t)r * D + v * 32 + lane], acc[v]);
+      for (int r = 0; r < B; ++r) {
+        ml[r] = make_float2(-INFINITY, 0.f);
+        x[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (r0 + r < end) {
+          ml[r] = mls[r0 + r];
+          x[r] = *reinterpret_cast<const float4*>(rec + (int64_t)(r0 + r) * D);
+        }
+      }
+      add(ml, x);
     }
+    if (shared) {
+      so[g][lane] = o;
+      if (lane == 0) sml[g] = make_float2(m, l);
+      __syncthreads();  // every thread of the block is here: `shared` is the request's
+      m = -INFINITY, l = 0.f, o = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int g0 = 0; g0 < GROUPS; g0 += B) {
 #pragma unroll
-    for (int v = 0; v < V; ++v)
-      store_out(static_cast<T*>(a.out) + row * D + v * 32 + lane, __fdiv_rn(acc[v], l));
-    if (a.lse && lane == 0) a.lse[row] = __fmul_rn(__fadd_rn(m, log2f(l)), kLn2);
+        for (int r = 0; r < B; ++r) {
+          ml[r] = g0 + r < GROUPS ? sml[g0 + r] : make_float2(-INFINITY, 0.f);
+          x[r] = g0 + r < GROUPS ? so[g0 + r][lane] : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        add(ml, x);
+      }
+    }
+    if (g == 0 || !split) {
+      store4(static_cast<T*>(a.out) + row * D + c,
+             make_float4(__fdiv_rn(o.x, l), __fdiv_rn(o.y, l), __fdiv_rn(o.z, l), __fdiv_rn(o.w, l)));
+      if (a.lse && c == 0) a.lse[row] = __fmul_rn(__fadd_rn(m, log2f(l)), kLn2);
+    }
   }
-  if (blockIdx.x == 0) {
-    const int err = check_request(a, i);
-    if (err && threadIdx.x == 0) set_error(a.hdr, err);
+  if (rq.bad && threadIdx.x == 0) set_error(a.hdr, GDN_DEVERR_POS);
+  if (rq.n == 0) return;
+  const int first = rq.key(rq.head) >> a.page_shift, last = (rq.len - 1) >> a.page_shift;
+  const int head_pages = rq.head ? ((rq.head - 1) >> a.page_shift) + 1 : 0;
+  for (int b = blockIdx.x * 128 + threadIdx.x; b < head_pages + last - first + 1; b += gridDim.x * 128) {
+    const int p = b < head_pages ? b : first + b - head_pages;
+    const int page = p < a.max_blocks ? a.block_table[(int64_t)i * a.max_blocks + p] : -1;
+    if (page < 0 || page >= a.num_pages) set_error(a.hdr, GDN_DEVERR_PAGES);
   }
+}
+
+template <typename E>
+void launch_decode(const PagedDecode& a, cudaStream_t st) {
+  constexpr int D = E::DIM, BYTES = DecodeSmem<E>::BYTES;
+  cudaFuncSetAttribute(k_decode<E>, cudaFuncAttributeMaxDynamicSharedMemorySize, BYTES);
+  static const int per_sm = [] {  // CTAs an SM holds
+    int n = 1;
+    cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, k_decode<E>, 32 * E::WARPS, BYTES);
+    return n < 1 ? 1 : n;
+  }();
+  const int group = a.hq / a.hkv, parts = (group + kHeadsPerRun - 1) / kHeadsPerRun;
+  const int64_t total = (int64_t)a.N * a.hkv * parts * a.max_splits, most = (int64_t)kSms * per_sm;
+  const int64_t need = (total + E::WARPS - 1) / E::WARPS;
+  k_decode<E><<<(unsigned)(need < most ? need : most), 32 * E::WARPS, BYTES, st>>>(a, parts);
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t c{};
+  const bool split = a.max_splits > 32;
+  c.gridDim = dim3(split ? a.hq : (a.hq + 512 / D - 1) / (512 / D), a.N);
+  c.blockDim = dim3(128);
+  c.stream = st;
+  c.attrs = &attr;
+  c.numAttrs = 1;
+  cudaLaunchKernelEx(&c, k_decode_join<D, typename E::Elem>, a, split);
 }
 
 template <int D, typename T>
 void decode_t(const PagedDecode& a, cudaStream_t st) {
-  const int group = a.hq / a.hkv, parts = (group + kHeadsPerCta - 1) / kHeadsPerCta;
-  const dim3 grid(a.max_splits, a.hkv * parts, a.N);
-  const int nc = group <= 4 ? 1 : group <= 8 ? 2 : 4;
-  if (nc == 1)
-    k_decode_simt<D, T, 1><<<grid, kDecThreads, 0, st>>>(a);
-  else if (nc == 2)
-    k_decode_simt<D, T, 2><<<grid, kDecThreads, 0, st>>>(a);
-  else
-    k_decode_simt<D, T, 4><<<grid, kDecThreads, 0, st>>>(a);
-  if (a.max_splits > 1) k_decode_join<D, T><<<dim3((a.hq + 3) / 4, a.N), 128, 0, st>>>(a);
+  const int group = a.hq / a.hkv;
+  if constexpr (D >= 64 && sizeof(T) == 2) {
+    launch_decode<MmaEngine<D>>(a, st);
+  } else {
+    if (group <= 2) launch_decode<SimtEngine<D, T, 2, 1>>(a, st);
+    else if (group <= 4) launch_decode<SimtEngine<D, T, 4, 1>>(a, st);
+    else if (group <= 8) launch_decode<SimtEngine<D, T, 4, 2>>(a, st);
+    else launch_decode<SimtEngine<D, T, 4, 4>>(a, st);
+  }
 }
 
 }  // namespace
 
-// The largest number of runs of any request that sees at most `max_visible` keys.
-int paged_decode_max_splits(int max_visible) {
+// A bound on the runs of any request that sees at most `max_visible` keys: target_runs grows with n
+// between the lengths where target_keys changes, and split_count is at most target_runs.
+int paged_decode_max_splits(int max_visible, int hkv) {
   int best = 1;
-  for (const int edge : {2048, 8192}) {
-    const int n = max_visible < edge ? max_visible : edge;
-    if (n > 0 && split_count(n) > best) best = split_count(n);
+  for (const int64_t x : {128, 256, 512, 0}) {
+    const int64_t last = x ? (kRunsPerRequest * x - 1) / hkv : max_visible;  // the last n before the next length
+    const int n = (int)(last < max_visible ? last : max_visible);
+    if (n > 0 && target_runs(n, hkv) > best) best = target_runs(n, hkv);
   }
-  if (max_visible > 0 && split_count(max_visible) > best) best = split_count(max_visible);
   return best;
 }
 
-int launch_paged_decode(const PagedDecode& a, bool bf16, cudaStream_t st) {
+void launch_paged_decode(const PagedDecode& a, bool bf16, cudaStream_t st) {
   if (bf16) {
     if (a.d == 32) decode_t<32, __nv_bfloat16>(a, st);
     else if (a.d == 64) decode_t<64, __nv_bfloat16>(a, st);
@@ -326,7 +703,6 @@ int launch_paged_decode(const PagedDecode& a, bool bf16, cudaStream_t st) {
     else if (a.d == 64) decode_t<64, float>(a, st);
     else decode_t<128, float>(a, st);
   }
-  return a.max_splits > 1 ? 2 : 1;
 }
 
 }  // namespace gdn

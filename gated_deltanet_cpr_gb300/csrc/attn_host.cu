@@ -91,7 +91,7 @@ size_t decode_bytes(const gdn_cpr_attn* a, int32_t N, int splits) {
 }
 
 int decode_splits(const gdn_cpr_attn* a, int32_t max_len) {
-  return paged_decode_max_splits(visible_keys(max_len, a->window, a->sinks));
+  return paged_decode_max_splits(visible_keys(max_len, a->window, a->sinks), a->h_kv);
 }
 
 gdn_status finish() { return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA; }
@@ -286,6 +286,8 @@ gdn_status gdn_cpr_paged_decode(const gdn_cpr_attn* attn, int32_t num_seqs, int3
   if (num_seqs < 0 || max_len < 0 || num_pages < 0 || page_size <= 0 || max_blocks < 0) return GDN_ERR_INVALID_ARG;
   const int shift = page_shift_of(page_size);
   if (shift < 0 || num_seqs > 65535) return GDN_ERR_UNSUPPORTED;
+  // the kernels keep a key's row (page, head, offset) in 32 bits
+  if ((((int64_t)num_pages * attn->h_kv) << shift) >= (int64_t)UINT32_MAX) return GDN_ERR_UNSUPPORTED;
   if (num_seqs > 0 && (!ok_ptr(q, 16) || !ok_ptr(out, 16) || !ok_ptr(seq_lens, 4) || !aligned(lse, 4)))
     return GDN_ERR_INVALID_ARG;
   if (num_seqs > 0 && num_pages > 0 && (!ok_ptr(k_pages, 16) || !ok_ptr(v_pages, 16))) return GDN_ERR_INVALID_ARG;
@@ -316,7 +318,8 @@ gdn_status gdn_cpr_paged_decode(const gdn_cpr_attn* attn, int32_t num_seqs, int3
   a.max_splits = splits;
   a.hdr = static_cast<WsHeader*>(ws);
   Stages stg(stream, kPagedStages);
-  stg.mark(launch_paged_decode(a, attn->dtype == GDN_BF16, stream));
+  launch_paged_decode(a, attn->dtype == GDN_BF16, stream);
+  stg.mark(2);
   return finish();
 }
 

@@ -481,6 +481,7 @@ typedef struct {
  *   sets GDN_DEVERR_POS and gives NaN for that request); a page index outside [0, num_pages)
  *   sets GDN_DEVERR_PAGES, NaN likewise
  *   out [N, H_q, d];  lse NULL or [N, H_q] fp32: the log-sum-exp of the scaled scores
+ *   num_pages * H_kv * page_size < 2^32 - 1
  *   ws: gdn_cpr_paged_decode_workspace_size bytes; its error word is set by every call      */
 gdn_status gdn_cpr_paged_decode(const gdn_cpr_attn *attn, int32_t num_seqs, int32_t max_len,
                                 const void *q, const void *k_pages, const void *v_pages,
