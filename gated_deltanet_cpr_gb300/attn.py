@@ -11,7 +11,7 @@ import ctypes
 import torch
 
 from . import api
-from .api import _check, _dt, _p, _stream
+from .api import GdnError, _dt
 
 NORMS = {"none": 0, "rms": 1, "l2": 2}
 LAYOUTS = {"half": 0, "interleaved": 1}
@@ -51,7 +51,8 @@ class PagedCache:
         self.pages, self.h_kv, self.page_size, self.d = k.shape
 
     def pointers(self):
-        return _want(self.k, self.k.shape, self.k.dtype, "k pages"), _want(self.v, self.v.shape, self.v.dtype, "v pages")
+        k, v = self.k, self.v
+        return _want(k, v.shape, v.dtype, "k pages"), _want(v, k.shape, k.dtype, "v pages")
 
 
 def rope_tables(rows, rot, base=10000.0, scale=1.0, device="cuda"):
@@ -62,27 +63,45 @@ def rope_tables(rows, rot, base=10000.0, scale=1.0, device="cuda"):
     return ang.cos().float().to(device), ang.sin().float().to(device)
 
 
+# The calls below run once or more per layer of a decode step, so the wrappers keep their own cost
+# low: one check per tensor, the raw stream handle, one allocation where several results go together.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _check(fn, rc):
+    if rc:
+        raise GdnError(fn, rc)
+
+
+def _want(x, shape, dtype, name):
+    """Pointer of a contiguous GPU tensor of that shape and dtype."""
+    if x.dtype is not dtype or x.shape != shape or not x.is_cuda or not x.is_contiguous():
+        raise ValueError(f"{name} is {x.dtype} {tuple(x.shape)} on {x.device}"
+                         f"{'' if x.is_contiguous() else ', not contiguous'}; expected {dtype} {tuple(shape)} on the GPU")
+    return x.data_ptr()
+
+
+def _opt(x, shape, dtype, name):
+    return None if x is None else _want(x, shape, dtype, name)
+
+
 def _rows(x, heads, d, name):
     """(pointer, token stride) of [T, heads, d] whose heads are dense; tokens may be strided."""
-    if x.dim() != 3 or x.shape[1] != heads or x.shape[2] != d:
-        raise ValueError(f"{name} has shape {tuple(x.shape)}, expected [T, {heads}, {d}]")
-    if not x.is_cuda:
-        raise ValueError(f"{name} is not on the GPU")
+    if x.dim() != 3 or x.shape[1] != heads or x.shape[2] != d or not x.is_cuda:
+        raise ValueError(f"{name} is {tuple(x.shape)} on {x.device}, expected [T, {heads}, {d}] on the GPU")
     if x.numel() and (x.stride(2) != 1 or x.stride(1) != d):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
     return x.data_ptr(), (x.stride(0) if x.shape[0] > 1 else heads * d)
 
 
-def _want(x, shape, dtype, name):
-    if tuple(x.shape) != tuple(shape) or x.dtype != dtype:
-        raise ValueError(f"{name} is {x.dtype} {tuple(x.shape)}, expected {dtype} {tuple(shape)}")
-    if not x.is_cuda:
-        raise ValueError(f"{name} is not on the GPU")
-    return _p(x)
+def _bytes(fn, *args):
+    n = ctypes.c_size_t(0)
+    _check(fn, getattr(api.load(), fn)(*args, ctypes.byref(n)))
+    return n.value
 
 
-def _opt(x, shape, dtype, name):
-    return None if x is None else _want(x, shape, dtype, name)
+def _workspace(x, nbytes):
+    return torch.empty(nbytes, dtype=torch.uint8, device=x.device)
 
 
 def _norm_rope_struct(q, k, v, norm, eps, cos, sin, positions, layout, out_dtype, grad_dtype):
@@ -90,11 +109,12 @@ def _norm_rope_struct(q, k, v, norm, eps, cos, sin, positions, layout, out_dtype
     hk = k.shape[1]
     if k.shape[0] != T or k.dtype != q.dtype or (v is not None and v.dtype != q.dtype):
         raise ValueError("q, k and v have the same tokens and dtype")
-    rot, rows = (0, 0) if cos is None else (2 * cos.shape[1], cos.shape[0])
-    if rot:
-        _want(sin, cos.shape, torch.float32, "sin")
-        _want(cos, cos.shape, torch.float32, "cos")
-        _want(positions, (T,), torch.int32, "positions")
+    rot = rows = 0
+    cp = sp = pp = None
+    if cos is not None:
+        rot, rows = 2 * cos.shape[1], cos.shape[0]
+        cp, sp = _want(cos, cos.shape, torch.float32, "cos"), _want(sin, cos.shape, torch.float32, "sin")
+        pp = _want(positions, (T,), torch.int32, "positions")
     qp, qs = _rows(q, hq, d, "q")
     kp, ks = _rows(k, hk, d, "k")
     vp, vs = (None, hk * d) if v is None else _rows(v, hk, d, "v")
@@ -102,7 +122,7 @@ def _norm_rope_struct(q, k, v, norm, eps, cos, sin, positions, layout, out_dtype
         raise ValueError("q, k and v have the same tokens and dtype")
     st = NormRopeStruct(T, hq, hk, d, rot, rows, NORMS[norm], LAYOUTS[layout], eps, _dt(q.dtype), _dt(out_dtype),
                         _dt(grad_dtype), qs, ks, vs)
-    return st, qp, kp, vp
+    return st, qp, kp, vp, cp, sp, pp
 
 
 def qk_norm_rope(q, k, v=None, *, norm="rms", q_weight=None, k_weight=None, eps=1e-6, cos=None, sin=None,
@@ -111,27 +131,24 @@ def qk_norm_rope(q, k, v=None, *, norm="rms", q_weight=None, k_weight=None, eps=
     """gdn_cpr_qk_norm_rope: norms of q [T, Hq, d] and k [T, Hk, d] per head and the rotation by
     cos, sin [rows, rot / 2] at positions [T].  With a cache, k's results and v go to the cache
     at slot_map [T] as well.  Returns (q_out, k_out); want_q / want_k leave one out."""
-    lib = api.load()
     od = out_dtype or (cache.k.dtype if cache is not None else q.dtype)
-    st, qp, kp, vp = _norm_rope_struct(q, k, v, norm, eps, cos, sin, positions, layout, od, od)
+    st, qp, kp, vp, cp, sp, pp = _norm_rope_struct(q, k, v, norm, eps, cos, sin, positions, layout, od, od)
     T, d = st.tokens, st.d
-    dev = q.device
     if q_out is None and want_q:
-        q_out = torch.empty((T, st.h_q, d), dtype=od, device=dev)
+        q_out = torch.empty((T, st.h_q, d), dtype=od, device=q.device)
     if k_out is None and want_k:
-        k_out = torch.empty((T, st.h_k, d), dtype=od, device=dev)
-    kc = vc = sp = None
+        k_out = torch.empty((T, st.h_k, d), dtype=od, device=q.device)
+    kc = vc = slots = None
     pages = page = 0
     if cache is not None:
         if cache.h_kv != st.h_k or cache.d != d or cache.k.dtype != od or v is None:
             raise ValueError("the cache holds heads, size and dtype of k_out, and needs v")
-        kc, vc, pages, page = *cache.pointers(), cache.pages, cache.page_size
-        sp = _want(slot_map, (T,), torch.int32, "slot_map")
-    _check("gdn_cpr_qk_norm_rope", lib.gdn_cpr_qk_norm_rope(
+        (kc, vc), pages, page = cache.pointers(), cache.pages, cache.page_size
+        slots = _want(slot_map, (T,), torch.int32, "slot_map")
+    _check("gdn_cpr_qk_norm_rope", api.load().gdn_cpr_qk_norm_rope(
         ctypes.byref(st), qp, kp, vp, _opt(q_weight, (d,), torch.float32, "q_weight"),
-        _opt(k_weight, (d,), torch.float32, "k_weight"), _p(cos), _p(sin), _p(positions),
-        _opt(q_out, (T, st.h_q, d), od, "q_out"), _opt(k_out, (T, st.h_k, d), od, "k_out"), kc, vc, pages, page, sp,
-        _stream(dev)))
+        _opt(k_weight, (d,), torch.float32, "k_weight"), cp, sp, pp, _opt(q_out, (T, st.h_q, d), od, "q_out"),
+        _opt(k_out, (T, st.h_k, d), od, "k_out"), kc, vc, pages, page, slots, _raw_stream(q.device.index)))
     return q_out, k_out
 
 
@@ -139,60 +156,55 @@ def qk_norm_rope_bwd(q, k, dq_out, dk_out, *, norm="rms", q_weight=None, k_weigh
                      positions=None, layout="half", ws=None):
     """gdn_cpr_qk_norm_rope_bwd.  Returns dict dq, dk (q's dtype) and, when a weight is given,
     dq_weight, dk_weight [d] fp32."""
-    lib = api.load()
-    if dq_out.dtype != dk_out.dtype:
-        raise ValueError("dq_out and dk_out have the same dtype")
-    st, qp, kp, _ = _norm_rope_struct(q, k, None, norm, eps, cos, sin, positions, layout, q.dtype, dq_out.dtype)
-    T, d = st.tokens, st.d
+    gd = dq_out.dtype
+    st, qp, kp, _, cp, sp, pp = _norm_rope_struct(q, k, None, norm, eps, cos, sin, positions, layout, q.dtype, gd)
+    T, hq, hk, d = st.tokens, st.h_q, st.h_k, st.d
     dev = q.device
-    out = dict(dq=torch.empty((T, st.h_q, d), dtype=q.dtype, device=dev),
-               dk=torch.empty((T, st.h_k, d), dtype=q.dtype, device=dev), dq_weight=None, dk_weight=None)
+    dq, dk = torch.empty((T, hq, d), dtype=q.dtype, device=dev), torch.empty((T, hk, d), dtype=q.dtype, device=dev)
+    out = dict(dq=dq, dk=dk, dq_weight=None, dk_weight=None)
+    dwq = dwk = wp = None
+    nbytes = 0
     if q_weight is not None or k_weight is not None:
-        out["dq_weight"] = torch.empty(d, dtype=torch.float32, device=dev)
-        out["dk_weight"] = torch.empty(d, dtype=torch.float32, device=dev)
+        out["dq_weight"], out["dk_weight"] = torch.empty((2, d), dtype=torch.float32, device=dev).unbind()
+        dwq, dwk = out["dq_weight"].data_ptr(), out["dk_weight"].data_ptr()
         if ws is None:
-            n = ctypes.c_size_t(0)
-            _check("gdn_cpr_qk_norm_rope_workspace_size",
-                   lib.gdn_cpr_qk_norm_rope_workspace_size(ctypes.byref(st), ctypes.byref(n)))
-            ws = api.alloc_workspace(n.value, dev)
-    _check("gdn_cpr_qk_norm_rope_bwd", lib.gdn_cpr_qk_norm_rope_bwd(
+            ws = _workspace(q, _bytes("gdn_cpr_qk_norm_rope_workspace_size", ctypes.byref(st)))
+        wp, nbytes = ws.data_ptr(), ws.numel()
+    _check("gdn_cpr_qk_norm_rope_bwd", api.load().gdn_cpr_qk_norm_rope_bwd(
         ctypes.byref(st), qp, kp, _opt(q_weight, (d,), torch.float32, "q_weight"),
-        _opt(k_weight, (d,), torch.float32, "k_weight"), _p(cos), _p(sin), _p(positions),
-        _want(dq_out, (T, st.h_q, d), dq_out.dtype, "dq_out"), _want(dk_out, (T, st.h_k, d), dq_out.dtype, "dk_out"),
-        _p(out["dq"]), _p(out["dk"]), _p(out["dq_weight"]), _p(out["dk_weight"]), _p(ws),
-        0 if ws is None else ws.numel(), _stream(dev)))
+        _opt(k_weight, (d,), torch.float32, "k_weight"), cp, sp, pp, _want(dq_out, (T, hq, d), gd, "dq_out"),
+        _want(dk_out, (T, hk, d), gd, "dk_out"), dq.data_ptr(), dk.data_ptr(), dwq, dwk, wp, nbytes,
+        _raw_stream(dev.index)))
     return out
 
 
-def page_map(lens, new_lens, free_pages, block_table, page_size, total_tokens, *, ws=None):
+def page_map(lens, new_lens, free_pages, block_table, page_size, total_tokens):
     """gdn_cpr_page_map: extends block_table [N, max_blocks] (in place) for new_lens [N] tokens
     after lens [N] cached ones with pages from the front of free_pages.  Returns dict seq_lens,
-    cu_seqlens, positions, slot_map, pages_used, and ws, whose error word says what was wrong."""
-    lib = api.load()
-    N = lens.numel()
-    dev = lens.device
+    cu_seqlens, positions, slot_map, pages_used, and ws, whose error word says what was wrong
+    (api.device_error)."""
+    N, T = lens.numel(), int(total_tokens)
     i32 = torch.int32
-    # one allocation for the five results: parts of it start on 16-byte boundaries
-    T4, N4 = -(-int(total_tokens) // 4) * 4, -(-(N + 1) // 4) * 4
-    buf = torch.empty(2 * T4 + 2 * N4 + 4, dtype=i32, device=dev)
-    positions, slots, seq, cu, used = buf.split([T4, T4, N4, N4, 4])
-    out = dict(seq_lens=seq[:N], cu_seqlens=cu[:N + 1], positions=positions[:total_tokens],
-               slot_map=slots[:total_tokens], pages_used=used[:1])
-    if ws is None:
-        ws = api.alloc_workspace(HEADER_BYTES, dev)
+    # one allocation: the header, then the results, positions and slots on 16-byte boundaries
+    pad = -T % 4
+    buf = torch.empty(HEADER_BYTES // 4 + 2 * (T + pad) + 2 * N + 2, dtype=i32, device=lens.device)
+    ws, pos, _, slots, _, seq, cu, used = buf.split_with_sizes([HEADER_BYTES // 4, T, pad, T, pad, N, N + 1, 1])
+    at = buf.data_ptr()
+    a_pos = at + HEADER_BYTES
+    a_slots = a_pos + 4 * (T + pad)
+    a_seq = a_slots + 4 * (T + pad)
     if block_table.dim() != 2 or block_table.shape[0] != N:
         raise ValueError("block_table is [N, max_blocks]")
-    _check("gdn_cpr_page_map", lib.gdn_cpr_page_map(
-        N, total_tokens, page_size, block_table.shape[1], free_pages.numel(), _want(lens, (N,), i32, "lens"),
+    _check("gdn_cpr_page_map", api.load().gdn_cpr_page_map(
+        N, T, page_size, block_table.shape[1], free_pages.numel(), _want(lens, (N,), i32, "lens"),
         _want(new_lens, (N,), i32, "new_lens"), _want(free_pages, free_pages.shape, i32, "free_pages"),
-        _want(block_table, block_table.shape, i32, "block_table"), _p(seq), _p(cu), _p(positions), _p(slots), _p(used),
-        _p(ws), ws.numel(), _stream(dev)))
-    out["ws"] = ws
-    return out
+        _want(block_table, block_table.shape, i32, "block_table"), a_seq, a_seq + 4 * N, a_pos, a_slots,
+        a_seq + 8 * N + 4, at, HEADER_BYTES, _raw_stream(lens.device.index)))
+    return dict(seq_lens=seq, cu_seqlens=cu, positions=pos, slot_map=slots, pages_used=used, ws=ws)
 
 
 def _attn_struct(hq, hkv, d, window, sinks, scale, dtype):
-    return AttnStruct(hq, hkv, d, int(window or 0), int(sinks), 0.0 if scale is None else float(scale), _dt(dtype))
+    return AttnStruct(hq, hkv, d, window, sinks, scale or 0.0, _dt(dtype))
 
 
 def paged_decode(q, cache: PagedCache, block_table, seq_lens, *, window=0, sinks=0, scale=None, max_len=None, out=None,
@@ -200,47 +212,41 @@ def paged_decode(q, cache: PagedCache, block_table, seq_lens, *, window=0, sinks
     """gdn_cpr_paged_decode: attention of one token per request, q [N, Hq, d], over the cache's
     first seq_lens[n] tokens.  max_len bounds seq_lens (default: what block_table can hold).
     Returns out [N, Hq, d], or (out, lse) with want_lse."""
-    lib = api.load()
     N, hq, d = q.shape
-    dev = q.device
-    if cache.d != d or cache.k.dtype != q.dtype:
+    if cache.d != d or cache.k.dtype is not q.dtype:
         raise ValueError("q and the cache have the same d and dtype")
     if block_table.dim() != 2 or block_table.shape[0] != N:
         raise ValueError("block_table is [N, max_blocks]")
     if max_len is None:
         max_len = block_table.shape[1] * cache.page_size
     st = _attn_struct(hq, cache.h_kv, d, window, sinks, scale, q.dtype)
+    qp = _want(q, q.shape, q.dtype, "q")
     if out is None:
-        out = torch.empty((N, hq, d), dtype=q.dtype, device=dev)
-    lse = torch.empty((N, hq), dtype=torch.float32, device=dev) if want_lse else None
+        out = torch.empty_like(q)
+    lse = torch.empty((N, hq), dtype=torch.float32, device=q.device) if want_lse else None
     if ws is None:
-        n = ctypes.c_size_t(0)
-        _check("gdn_cpr_paged_decode_workspace_size",
-               lib.gdn_cpr_paged_decode_workspace_size(ctypes.byref(st), N, max_len, ctypes.byref(n)))
-        ws = api.alloc_workspace(n.value, dev)
-    _check("gdn_cpr_paged_decode", lib.gdn_cpr_paged_decode(
-        ctypes.byref(st), N, max_len, _want(q, q.shape, q.dtype, "q"), *cache.pointers(), cache.pages,
-        cache.page_size, _want(block_table, block_table.shape, torch.int32, "block_table"), block_table.shape[1],
-        _want(seq_lens, (N,), torch.int32, "seq_lens"), _want(out, (N, hq, d), q.dtype, "out"), _p(lse), _p(ws),
-        ws.numel(), _stream(dev)))
+        ws = _workspace(q, _bytes("gdn_cpr_paged_decode_workspace_size", ctypes.byref(st), N, max_len))
+    kp, vp = cache.pointers()
+    _check("gdn_cpr_paged_decode", api.load().gdn_cpr_paged_decode(
+        ctypes.byref(st), N, max_len, qp, kp, vp, cache.pages, cache.page_size,
+        _want(block_table, block_table.shape, torch.int32, "block_table"), block_table.shape[1],
+        _want(seq_lens, (N,), torch.int32, "seq_lens"), _want(out, q.shape, q.dtype, "out"),
+        None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.numel(), _raw_stream(q.device.index)))
     return (out, lse) if want_lse else out
 
 
-def _window_setup(lib, q, k, v, cu_q, cu_k, window, sinks, scale, backward, ws):
+def _window_setup(q, k, v, cu_q, cu_k, window, sinks, scale, backward, ws):
     Tq, hq, d = q.shape
     Tk, hkv, _ = k.shape
     N = cu_q.numel() - 1
     cu_k = cu_q if cu_k is None else cu_k
     st = _attn_struct(hq, hkv, d, window, sinks, scale, q.dtype)
+    args = (ctypes.byref(st), N, Tq, Tk, _want(cu_q, (N + 1,), torch.int32, "cu_seqlens"),
+            _want(cu_k, (N + 1,), torch.int32, "cu_seqlens_k"), _want(q, q.shape, q.dtype, "q"),
+            _want(k, (Tk, hkv, d), q.dtype, "k"), _want(v, (Tk, hkv, d), q.dtype, "v"))
     if ws is None:
-        n = ctypes.c_size_t(0)
-        _check("gdn_cpr_window_attn_workspace_size",
-               lib.gdn_cpr_window_attn_workspace_size(ctypes.byref(st), Tq, int(backward), ctypes.byref(n)))
-        ws = api.alloc_workspace(n.value, q.device)
-    args = [ctypes.byref(st), N, Tq, Tk, _want(cu_q, (N + 1,), torch.int32, "cu_seqlens"),
-            _want(cu_k, (N + 1,), torch.int32, "cu_seqlens_k"), _want(q, q.shape, q.dtype, "q"), _want(k, (Tk, hkv, d), q.dtype, "k"),
-            _want(v, (Tk, hkv, d), q.dtype, "v")]
-    return st, args, ws
+        ws = _workspace(q, _bytes("gdn_cpr_window_attn_workspace_size", args[0], Tq, int(backward)))
+    return args, ws
 
 
 def window_attn(q, k, v, cu_seqlens, *, cu_seqlens_k=None, window=0, sinks=0, scale=None, out=None, lse=None, ws=None):
@@ -248,25 +254,23 @@ def window_attn(q, k, v, cu_seqlens, *, cu_seqlens_k=None, window=0, sinks=0, sc
     [Tk, Hkv, d]; a query sees the last `window` keys (0: all) and the first `sinks`.
     cu_seqlens_k (default cu_seqlens) gives sequences more keys than queries.  Returns
     (out [Tq, Hq, d], lse [Tq, Hq] fp32)."""
-    lib = api.load()
-    _, args, ws = _window_setup(lib, q, k, v, cu_seqlens, cu_seqlens_k, window, sinks, scale, False, ws)
+    args, ws = _window_setup(q, k, v, cu_seqlens, cu_seqlens_k, window, sinks, scale, False, ws)
     if out is None:
         out = torch.empty_like(q)
     if lse is None:
         lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
-    _check("gdn_cpr_window_attn", lib.gdn_cpr_window_attn(
-        *args, _want(out, q.shape, q.dtype, "out"), _want(lse, q.shape[:2], torch.float32, "lse"), _p(ws), ws.numel(),
-        _stream(q.device)))
+    _check("gdn_cpr_window_attn", api.load().gdn_cpr_window_attn(
+        *args, _want(out, q.shape, q.dtype, "out"), _want(lse, q.shape[:2], torch.float32, "lse"), ws.data_ptr(),
+        ws.numel(), _raw_stream(q.device.index)))
     return out, lse
 
 
 def window_attn_bwd(q, k, v, out, lse, dout, cu_seqlens, *, cu_seqlens_k=None, window=0, sinks=0, scale=None, ws=None):
     """gdn_cpr_window_attn_bwd from window_attn's out and lse.  Returns dict dq, dk, dv in q's dtype."""
-    lib = api.load()
-    _, args, ws = _window_setup(lib, q, k, v, cu_seqlens, cu_seqlens_k, window, sinks, scale, True, ws)
+    args, ws = _window_setup(q, k, v, cu_seqlens, cu_seqlens_k, window, sinks, scale, True, ws)
     g = dict(dq=torch.empty_like(q), dk=torch.empty_like(k), dv=torch.empty_like(v))
-    _check("gdn_cpr_window_attn_bwd", lib.gdn_cpr_window_attn_bwd(
+    _check("gdn_cpr_window_attn_bwd", api.load().gdn_cpr_window_attn_bwd(
         *args, _want(out, q.shape, q.dtype, "out"), _want(lse, q.shape[:2], torch.float32, "lse"),
-        _want(dout, q.shape, q.dtype, "dout"), _p(g["dq"]), _p(g["dk"]), _p(g["dv"]), _p(ws), ws.numel(),
-        _stream(q.device)))
+        _want(dout, q.shape, q.dtype, "dout"), g["dq"].data_ptr(), g["dk"].data_ptr(), g["dv"].data_ptr(),
+        ws.data_ptr(), ws.numel(), _raw_stream(q.device.index)))
     return g

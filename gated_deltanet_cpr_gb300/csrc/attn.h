@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/gdn_cpr.h"
 #include "common.cuh"
 
@@ -113,6 +115,18 @@ bool launch_window_dkv_tc(const WindowAttn& a, cudaStream_t st);
 // the gradient: dq (and delta), then dk and dv, which read delta
 bool launch_window_dq(const WindowAttn& a, bool bf16, cudaStream_t st);
 bool launch_window_dkv(const WindowAttn& a, bool bf16, cudaStream_t st);
+
+// Opts a kernel into `bytes` of dynamic shared memory, once per (kernel, device): a call of the
+// runtime costs as much as a launch.  `done` is the kernel's own flag word.
+template <typename F>
+inline void ensure_smem(F* fn, int bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  cudaGetDevice(&dev);
+  const uint64_t bit = 1ull << (dev & 63);
+  if (done.load(std::memory_order_acquire) & bit) return;
+  if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess)
+    done.fetch_or(bit, std::memory_order_release);
+}
 
 // ------------------------------------------------------------------------ device ----
 __device__ __forceinline__ void store4(float* p, float4 x) { *reinterpret_cast<float4*>(p) = x; }

@@ -643,7 +643,8 @@ __global__ void __launch_bounds__(128) k_decode_join(const PagedDecode a, const 
 template <typename E>
 void launch_decode(const PagedDecode& a, cudaStream_t st) {
   constexpr int D = E::DIM, BYTES = DecodeSmem<E>::BYTES;
-  cudaFuncSetAttribute(k_decode<E>, cudaFuncAttributeMaxDynamicSharedMemorySize, BYTES);
+  static std::atomic<uint64_t> ready{0};
+  ensure_smem(k_decode<E>, BYTES, ready);
   static const int per_sm = [] {  // CTAs an SM holds
     int n = 1;
     cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, k_decode<E>, 32 * E::WARPS, BYTES);

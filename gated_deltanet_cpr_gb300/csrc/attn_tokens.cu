@@ -436,8 +436,8 @@ int launch_norm_rope_bwd(const NormRope& a, int d, bool in_bf16, bool grad_bf16,
 
 void launch_page_map(const PageMap& a, cudaStream_t st) {
   const size_t smem = 2 * sizeof(int32_t) * ((size_t)a.N + 1);
-  // once per device in effect: setting the same value again costs well under a microsecond
-  if (smem > 48 * 1024) cudaFuncSetAttribute(k_page_map, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  static std::atomic<uint64_t> ready{0};
+  ensure_smem(k_page_map, 2 * (int)sizeof(int32_t) * (kPageMapMaxSeqs + 1), ready);
   int64_t blocks = ((int64_t)a.T + 4 * kMapThreads - 1) / (4 * kMapThreads);
   blocks = blocks < 1 ? 1 : blocks > 152 ? 152 : blocks;
   k_page_map<<<(unsigned)blocks, kMapThreads, smem, st>>>(a);

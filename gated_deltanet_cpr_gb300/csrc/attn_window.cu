@@ -342,24 +342,24 @@ __global__ void __launch_bounds__(kThreads) k_window_dkv(const WindowAttn a) {
   dk.template store<T>(a.dk, q.k0, j0, q.Lk, a.hkv, kvh, ty, tx, f);
 }
 
-template <typename F>
-void launch(F* fn, dim3 grid, size_t floats, const WindowAttn& a, cudaStream_t st) {
-  // set on every call: it costs well under a microsecond and needs no state
-  cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(floats * sizeof(float)));
-  fn<<<grid, kThreads, floats * sizeof(float), st>>>(a);
+template <void (*FN)(WindowAttn)>
+void launch(dim3 grid, size_t floats, const WindowAttn& a, cudaStream_t st) {
+  static std::atomic<uint64_t> ready{0};
+  ensure_smem(FN, (int)(floats * sizeof(float)), ready);
+  FN<<<grid, kThreads, floats * sizeof(float), st>>>(a);
 }
 
 template <int D, typename T>
 void fwd_t(const WindowAttn& a, cudaStream_t st) {
-  launch(k_window_fwd<D, T>, dim3((unsigned)item_count(a.Tq, BM, a.N), a.hq), 3 * 64 * pitch<D>() + 64 * PS, a, st);
+  launch<k_window_fwd<D, T>>(dim3((unsigned)item_count(a.Tq, BM, a.N), a.hq), 3 * 64 * pitch<D>() + 64 * PS, a, st);
 }
 template <int D, typename T>
 void dq_t(const WindowAttn& a, cudaStream_t st) {
-  launch(k_window_dq<D, T>, dim3((unsigned)item_count(a.Tq, BM, a.N), a.hq), 4 * 64 * pitch<D>() + 64 * PS, a, st);
+  launch<k_window_dq<D, T>>(dim3((unsigned)item_count(a.Tq, BM, a.N), a.hq), 4 * 64 * pitch<D>() + 64 * PS, a, st);
 }
 template <int D, typename T>
 void dkv_t(const WindowAttn& a, cudaStream_t st) {
-  launch(k_window_dkv<D, T>, dim3((unsigned)item_count(a.Tk, BN, a.N), a.hkv), 4 * 64 * pitch<D>() + 2 * 64 * PS, a,
+  launch<k_window_dkv<D, T>>(dim3((unsigned)item_count(a.Tk, BN, a.N), a.hkv), 4 * 64 * pitch<D>() + 2 * 64 * PS, a,
          st);
 }
 

@@ -463,7 +463,8 @@ bool bwd_tc(const WindowAttn& a, cudaStream_t st) {
   // dk, dv: N more items, the sequences' first blocks ahead of the others
   const int64_t blocks = item_count(DKV ? a.Tk : a.Tq, BR, a.N);
   const int64_t work = DKV ? (blocks + a.N) * a.hkv : blocks * a.hq;
-  cudaFuncSetAttribute(k_window_bwd_tc<D, DKV>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::BYTES);
+  static std::atomic<uint64_t> ready{0};
+  ensure_smem(k_window_bwd_tc<D, DKV>, Smem<D>::BYTES, ready);
   k_window_bwd_tc<D, DKV><<<(unsigned)(work < kSms ? work : kSms), kThreads, Smem<D>::BYTES, st>>>(
       a, blocks, work, a.hdr->pad + (DKV ? 1 : 0), a.delta, mx, my, mu, mw);
   return true;

@@ -397,11 +397,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kMmaWarp) tmem_dealloc(tm, 512);
 }
 
-template <typename F>
-void set_smem(F* fn, int bytes) {
-  cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-}
-
 template <int D>
 bool fwd_tc(const WindowAttn& a, cudaStream_t st) {
   CUtensorMap mq, mk, mv;
@@ -409,7 +404,8 @@ bool fwd_tc(const WindowAttn& a, cudaStream_t st) {
       !make_rows_map(&mv, a.v, a.Tk, a.hkv, D, BN))
     return false;
   const int64_t items = item_count(a.Tq, 2 * BM, a.N), work = items * a.hq;
-  set_smem(k_window_fwd_tc<D>, FwdSmem<D>::BYTES);
+  static std::atomic<uint64_t> ready{0};
+  ensure_smem(k_window_fwd_tc<D>, FwdSmem<D>::BYTES, ready);
   k_window_fwd_tc<D><<<(unsigned)(work < kSms ? work : kSms), kThreads, FwdSmem<D>::BYTES, st>>>(a, items, mq, mk, mv);
   return true;
 }
