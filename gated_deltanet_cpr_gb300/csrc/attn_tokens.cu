@@ -7,16 +7,22 @@ namespace gdn {
 namespace {
 
 // =====================================================================================
-// Norm and rotation.  One row is one head of one token; LPR = D / 4 lanes hold 4 consecutive
-// entries each, a warp holds 32 / LPR rows at a time and U of these at once (their loads are
-// issued together).  A work item is one token and a run of U * 32 / LPR of its rows, so that
-// the few rows of a decode step spread over warps.
+// Norm and rotation.  One row is one head of one token; LPR = D / 8 lanes hold two pieces of 4
+// consecutive entries each, chosen so that the half layout's pairs (i, i + rot / 2) lie in one lane:
+// a lane of the rotated part holds pieces at A and A + rot / 2, one of the rest at A and
+// A + (D - rot) / 2.  The interleaved layout's pairs lie within a piece.  So the rotation needs no
+// exchange, and the norm log2(LPR) shuffles.  A warp holds GPW = 32 / LPR rows at a time and U of
+// these at once (their loads are issued together).  A work item is one token and U * GPW heads of
+// q, of k or of v, so that nothing inside depends on which it is, and the few rows of a decode step
+// spread over warps.  With two pieces a lane the kernel issues half the instructions per row that one
+// piece costs, and packed pairs halve the arithmetic again; before both it was bound by issue
+// (202 us for 16384 tokens of 32 / 8 heads, d = 128, with the cache written).
 // =====================================================================================
-constexpr int kNormThreads = 256;
+constexpr int kNormThreads = 128;
 
 template <int D>
 struct RowLanes {
-  static constexpr int LPR = D / 4, GPW = 32 / LPR;
+  static constexpr int LPR = D / 8, GPW = 32 / LPR;
 };
 
 template <int LPR>
@@ -26,191 +32,265 @@ __device__ __forceinline__ float row_sum(float x) {
   return x;
 }
 
-__device__ __forceinline__ float dot4(float4 a, float4 b) {
-  return __fmaf_rn(a.w, b.w, __fmaf_rn(a.z, b.z, __fmaf_rn(a.y, b.y, __fmul_rn(a.x, b.x))));
+struct Row8 {  // a lane's two pieces of a row: pairs 0, 1 of the first, 2, 3 of the second
+  float2 p[4];
+};
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(d)
+      : "l"(*reinterpret_cast<const uint64_t*>(&a)), "l"(*reinterpret_cast<const uint64_t*>(&b)));
+  return *reinterpret_cast<const float2*>(&d);
 }
-__device__ __forceinline__ float4 mul4(float4 a, float4 b) {
-  return make_float4(__fmul_rn(a.x, b.x), __fmul_rn(a.y, b.y), __fmul_rn(a.z, b.z), __fmul_rn(a.w, b.w));
+__device__ __forceinline__ Row8 all8(float x) {
+  Row8 r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r.p[i] = make_float2(x, x);
+  return r;
 }
-__device__ __forceinline__ float4 scale4(float4 a, float b) { return mul4(a, make_float4(b, b, b, b)); }
+__device__ __forceinline__ Row8 mul8(const Row8& x, const Row8& y) {
+  Row8 r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r.p[i] = mul2(x.p[i], y.p[i]);
+  return r;
+}
+__device__ __forceinline__ Row8 fma8(const Row8& x, const Row8& y, const Row8& z) {
+  Row8 r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r.p[i] = fma2(x.p[i], y.p[i], z.p[i]);
+  return r;
+}
+__device__ __forceinline__ float dot8(const Row8& x, const Row8& y) {
+  const float2 s = add2(fma2(x.p[1], y.p[1], mul2(x.p[0], y.p[0])), fma2(x.p[3], y.p[3], mul2(x.p[2], y.p[2])));
+  return __fadd_rn(s.x, s.y);
+}
+// the entries that a rotation adds to each: the other piece (half), the pair's other one (interleaved)
+__device__ __forceinline__ Row8 partners(const Row8& x, bool half) {
+  Row8 r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r.p[i] = half ? x.p[i ^ 2] : make_float2(x.p[i].y, x.p[i].x);
+  return r;
+}
+__device__ __forceinline__ Row8 pick8(bool first, const Row8& x, const Row8& y) {
+  Row8 r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    r.p[i] = make_float2(first ? x.p[i].x : y.p[i].x, first ? x.p[i].y : y.p[i].y);
+  return r;
+}
+constexpr float kNan = __builtin_nanf("");
+template <typename T>
+__device__ __forceinline__ Row8 load8p(const T* p, int gap) {
+  const float4 a = load4(p), b = load4(p + gap);
+  Row8 r;
+  r.p[0] = make_float2(a.x, a.y), r.p[1] = make_float2(a.z, a.w);
+  r.p[2] = make_float2(b.x, b.y), r.p[3] = make_float2(b.z, b.w);
+  return r;
+}
+template <typename T>
+__device__ __forceinline__ void store8p(T* p, int gap, const Row8& x) {
+  store4(p, make_float4(x.p[0].x, x.p[0].y, x.p[1].x, x.p[1].y));
+  store4(p + gap, make_float4(x.p[2].x, x.p[2].y, x.p[3].x, x.p[3].y));
+}
 
-// 1 / sqrt of the norm's sum of squares (plus eps); 1 without a norm.  The square root and the
-// reciprocal are the correctly rounded ones: they run once per row.
+// 1 / sqrt of the norm's sum of squares (plus eps); 1 without a norm
 __device__ __forceinline__ float inverse_norm(int norm, float sumsq, float inv_d, float eps) {
   if (norm == GDN_NORM_NONE) return 1.f;
-  const float m = norm == GDN_NORM_RMS ? __fmul_rn(sumsq, inv_d) : sumsq;
-  return __frcp_rn(__fsqrt_rn(__fadd_rn(m, eps)));
+  return rsqrtf(__fadd_rn(norm == GDN_NORM_RMS ? __fmul_rn(sumsq, inv_d) : sumsq, eps));
 }
 
-// The angles that a lane's 4 entries use, and where its partners are.
-struct Turn {
-  float4 c, s;   // half: of entries i .. i + 3; interleaved: (c0, c0, c1, c1)
-  int src;       // half: the lane that holds the partners
-  bool on, low;  // whether these entries turn; half: whether they are the first of their pairs
+// Where a lane's pieces start, and whether they turn.
+struct Pieces {
+  int at, gap;  // at `at` and at + gap
+  bool on;
 };
-
-template <int LPR>
-__device__ __forceinline__ Turn turn_of(const NormRope& a, int64_t p, int lane, float sign) {
-  Turn t;
-  const int i = 4 * (lane % LPR), half = a.rot / 2;
-  t.on = i < a.rot;
-  t.low = i < half;
-  t.src = t.on && a.layout == GDN_ROPE_HALF ? (t.low ? lane + a.rot / 8 : lane - a.rot / 8) : lane;
-  t.c = make_float4(1.f, 1.f, 1.f, 1.f);
-  t.s = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (t.on) {
-    if (a.layout == GDN_ROPE_HALF) {
-      const int64_t at = p * half + (t.low ? i : i - half);
-      t.c = *reinterpret_cast<const float4*>(a.cos + at);
-      t.s = *reinterpret_cast<const float4*>(a.sin + at);
-    } else {
-      const float2 c = *reinterpret_cast<const float2*>(a.cos + p * half + i / 2);
-      const float2 s = *reinterpret_cast<const float2*>(a.sin + p * half + i / 2);
-      t.c = make_float4(c.x, c.x, c.y, c.y);
-      t.s = make_float4(s.x, s.x, s.y, s.y);
-    }
-    t.s = scale4(t.s, sign);
-  }
+template <int D>
+__device__ __forceinline__ Pieces pieces_of(const NormRope& a, int lane) {
+  const int l = lane % (D / 8);
+  Pieces t;
+  t.on = l < a.rot / 8;
+  t.at = t.on ? 4 * l : a.rot + 4 * (l - a.rot / 8);
+  t.gap = t.on ? a.rot / 2 : (D - a.rot) / 2;
   return t;
 }
-
-// x c + (partner) s with the sign of the pair's place: the first takes -s, the second +s.
-// All lanes of the warp call it together.
-__device__ __forceinline__ float4 turn(const Turn& t, int layout, float4 x) {
-  float4 y;
-  if (layout == GDN_ROPE_HALF) {
-    y.x = __shfl_sync(0xffffffffu, x.x, t.src);
-    y.y = __shfl_sync(0xffffffffu, x.y, t.src);
-    y.z = __shfl_sync(0xffffffffu, x.z, t.src);
-    y.w = __shfl_sync(0xffffffffu, x.w, t.src);
-    if (t.low) y = make_float4(-y.x, -y.y, -y.z, -y.w);
+// cos, and sin with the sign of the entry's place in its pair (-, +) times `sign`; 1 and 0 where
+// nothing turns
+__device__ __forceinline__ void angles_of(const NormRope& a, int64_t row, float sign, const Pieces& t, bool half, Row8& c,
+                                          Row8& s) {
+  c = all8(1.f);
+  s = all8(0.f);
+  if (!t.on) return;
+  const float *cp = a.cos + row * (a.rot / 2), *sp = a.sin + row * (a.rot / 2);
+  if (half) {
+    const float4 c4 = *reinterpret_cast<const float4*>(cp + t.at), s4 = *reinterpret_cast<const float4*>(sp + t.at);
+    c.p[0] = c.p[2] = make_float2(c4.x, c4.y);
+    c.p[1] = c.p[3] = make_float2(c4.z, c4.w);
+    s.p[2] = make_float2(__fmul_rn(sign, s4.x), __fmul_rn(sign, s4.y));
+    s.p[3] = make_float2(__fmul_rn(sign, s4.z), __fmul_rn(sign, s4.w));
+    s.p[0] = make_float2(-s.p[2].x, -s.p[2].y);
+    s.p[1] = make_float2(-s.p[3].x, -s.p[3].y);
   } else {
-    y = make_float4(-x.y, x.x, -x.w, x.z);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float2 cc = *reinterpret_cast<const float2*>(cp + (t.at + i * t.gap) / 2);
+      const float2 ss = *reinterpret_cast<const float2*>(sp + (t.at + i * t.gap) / 2);
+      c.p[2 * i] = make_float2(cc.x, cc.x);
+      c.p[2 * i + 1] = make_float2(cc.y, cc.y);
+      s.p[2 * i] = make_float2(-__fmul_rn(sign, ss.x), __fmul_rn(sign, ss.x));
+      s.p[2 * i + 1] = make_float2(-__fmul_rn(sign, ss.y), __fmul_rn(sign, ss.y));
+    }
   }
-  if (!t.on) return x;
-  return make_float4(__fmaf_rn(y.x, t.s.x, __fmul_rn(x.x, t.c.x)), __fmaf_rn(y.y, t.s.y, __fmul_rn(x.y, t.c.y)),
-                     __fmaf_rn(y.z, t.s.z, __fmul_rn(x.z, t.c.z)), __fmaf_rn(y.w, t.s.w, __fmul_rn(x.w, t.c.w)));
 }
 
-constexpr float kNan = __builtin_nanf("");
+// Item -> token, which of q (0), k (1), v (2), and the first head.
+struct NormItem {
+  int64_t t;
+  int kind, h0, heads;
+};
+template <int RUN>
+__host__ __device__ __forceinline__ int norm_items(int hq, int hk, int hv) {
+  return (hq + RUN - 1) / RUN + (hk + RUN - 1) / RUN + (hv + RUN - 1) / RUN;
+}
+template <int RUN>
+__device__ __forceinline__ NormItem norm_item(const NormRope& a, int64_t item, int per) {
+  NormItem r;
+  r.t = item / per;
+  int c = (int)(item - r.t * per);
+  const int nq = (a.hq + RUN - 1) / RUN, nk = (a.hk + RUN - 1) / RUN;
+  r.kind = c < nq ? 0 : c < nq + nk ? 1 : 2;
+  c -= r.kind == 0 ? 0 : r.kind == 1 ? nq : nq + nk;
+  r.h0 = c * RUN;
+  r.heads = r.kind == 0 ? a.hq : a.hk;
+  return r;
+}
 
 template <int D, typename TI, typename TO, int U>
-__global__ void __launch_bounds__(kNormThreads) k_norm_rope(const NormRope a) {
+__global__ void __launch_bounds__(kNormThreads, U > 1 ? 8 : 1) k_norm_rope(const NormRope a, const int per) {
   constexpr int LPR = RowLanes<D>::LPR, GPW = RowLanes<D>::GPW;
-  const int lane = threadIdx.x & 31, i = 4 * (lane % LPR), grp = lane / LPR;
-  const int rows = a.hq + a.hk + (a.v_pages ? a.hk : 0);
-  const int per = (rows + U * GPW - 1) / (U * GPW);
+  const int lane = threadIdx.x & 31;
   const int64_t item = (int64_t)blockIdx.x * (kNormThreads / 32) + (threadIdx.x >> 5);
   if (item >= (int64_t)a.T * per) return;
-  const int64_t t = item / per;
-  const int row0 = (int)(item % per) * U * GPW + grp;
-
-  float4 x[U];
+  const NormItem it = norm_item<U * GPW>(a, item, per);
+  const int64_t t = it.t;
+  const int h = it.h0 + lane / LPR;
+  const Pieces pc = pieces_of<D>(a, lane);
+  // what other loads wait for comes first
+  const int64_t p = a.rot && it.kind < 2 ? a.pos[t] : 0;
+  const int64_t slot = it.kind && a.slot_map ? a.slot_map[t] : -1;
+  const TI* src = (it.kind == 0 ? static_cast<const TI*>(a.q) + t * a.q_stride
+                   : it.kind == 1 ? static_cast<const TI*>(a.k) + t * a.k_stride
+                                  : static_cast<const TI*>(a.v) + t * a.v_stride) + h * D + pc.at;
+  Row8 x[U];
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int r = row0 + u * GPW;
-    x[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (r < a.hq)
-      x[u] = load4(static_cast<const TI*>(a.q) + t * a.q_stride + (int64_t)r * D + i);
-    else if (r < a.hq + a.hk)
-      x[u] = load4(static_cast<const TI*>(a.k) + t * a.k_stride + (int64_t)(r - a.hq) * D + i);
-    else if (r < rows)
-      x[u] = load4(static_cast<const TI*>(a.v) + t * a.v_stride + (int64_t)(r - a.hq - a.hk) * D + i);
+  for (int u = 0; u < U; ++u) x[u] = h + u * GPW < it.heads ? load8p(src + u * GPW * D, pc.gap) : all8(0.f);
+  const bool bad = a.rot && (p < 0 || p >= a.table_rows), half = a.layout == GDN_ROPE_HALF;
+  Row8 c, s;
+  angles_of(a, bad ? 0 : p, 1.f, pc, half, c, s);
+  // the cache's cell of head h
+  TO* cell = nullptr;
+  const int64_t ps = (int64_t)1 << a.page_shift;
+  if (it.kind) {
+    if (slot >= 0 && slot < a.slots)
+      cell = static_cast<TO*>(it.kind == 1 ? a.k_pages : a.v_pages) +
+             (((slot >> a.page_shift) * a.hk + h) * ps + (slot & (ps - 1))) * D + pc.at;
   }
-  const int64_t p = a.rot ? a.pos[t] : 0;
-  const bool bad = a.rot && (p < 0 || p >= a.table_rows);
-  const Turn tn = turn_of<LPR>(a, bad ? 0 : p, lane, 1.f);
-  const float4 one = make_float4(1.f, 1.f, 1.f, 1.f);
-  const float4 wq = a.wq ? load4(a.wq + i) : one, wk = a.wk ? load4(a.wk + i) : one;
-  const int64_t slot = a.slot_map ? a.slot_map[t] : -1;
-  const bool keep = slot >= 0 && slot < a.slots;
-  const int64_t ps = (int64_t)1 << a.page_shift, page = slot >> a.page_shift, off = slot & (ps - 1);
+  if (it.kind == 2) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (cell && h + u * GPW < it.heads) store8p(cell + u * GPW * ps * D, pc.gap, x[u]);
+    return;
+  }
+  const float* wp = it.kind ? a.wk : a.wq;
+  const Row8 w = wp ? load8p(wp + pc.at, pc.gap) : all8(1.f);
+  // y = r (x (w c) + partner (w' s)), w' the partner's weight
+  c = mul8(w, c);
+  s = mul8(partners(w, half), s);
+  const bool some_off = a.rot < D;
+  TO* dst = static_cast<TO*>(it.kind ? a.k_out : a.q_out);
+  if (dst) dst += (t * it.heads + h) * D + pc.at;
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const int r = row0 + u * GPW;
-    const float ss = row_sum<LPR>(dot4(x[u], x[u]));
-    const float4 w = r < a.hq ? wq : wk;
-    float4 y = turn(tn, a.layout, mul4(scale4(x[u], inverse_norm(a.norm, ss, 1.f / D, a.eps)), w));
-    if (bad) y = make_float4(kNan, kNan, kNan, kNan);
-    if (r < a.hq) {
-      if (a.q_out) store4(static_cast<TO*>(a.q_out) + (t * a.hq + r) * D + i, y);
-    } else if (r < a.hq + a.hk) {
-      const int h = r - a.hq;
-      if (a.k_out) store4(static_cast<TO*>(a.k_out) + (t * a.hk + h) * D + i, y);
-      if (keep) store4(static_cast<TO*>(a.k_pages) + ((page * a.hk + h) * ps + off) * D + i, y);
-    } else if (r < rows && keep) {
-      const int h = r - a.hq - a.hk;
-      store4(static_cast<TO*>(a.v_pages) + ((page * a.hk + h) * ps + off) * D + i, x[u]);
+    const float r = inverse_norm(a.norm, row_sum<LPR>(dot8(x[u], x[u])), 1.f / D, a.eps);
+    Row8 y = mul8(x[u], c);
+    if (a.rot) {
+      const Row8 z = fma8(partners(x[u], half), s, y);
+      y = some_off ? pick8(pc.on, z, y) : z;  // 0 x infinity stays out of what does not turn
+    }
+    y = mul8(y, all8(r));
+    if (bad) y = all8(kNan);
+    if (h + u * GPW < it.heads) {
+      if (dst) store8p(dst + u * GPW * D, pc.gap, y);
+      if (cell) store8p(cell + u * GPW * ps * D, pc.gap, y);
     }
   }
 }
 
 // Backward: dx per row, and with weights the sums of g x r over this block's items: each lane
-// adds its 4 columns in the order of the items it meets, then the block's rows of lanes in
+// adds its 8 columns in the order of the items it meets, then the block's rows of lanes in
 // ascending order; k_norm_rope_dw adds the blocks.
-template <int D, typename TI, typename TG, int U>
-__global__ void __launch_bounds__(kNormThreads) k_norm_rope_bwd(const NormRope a) {
+template <int D, typename TI, typename TG, int U, bool W>
+__global__ void __launch_bounds__(kNormThreads, 8) k_norm_rope_bwd(const NormRope a, const int per) {
   constexpr int LPR = RowLanes<D>::LPR, GPW = RowLanes<D>::GPW;
-  const int lane = threadIdx.x & 31, i = 4 * (lane % LPR), grp = lane / LPR;
-  const int rows = a.hq + a.hk, per = (rows + U * GPW - 1) / (U * GPW);
+  const int lane = threadIdx.x & 31;
   const int64_t items = (int64_t)a.T * per, step = (int64_t)gridDim.x * (kNormThreads / 32);
-  const float4 one = make_float4(1.f, 1.f, 1.f, 1.f), zero = make_float4(0.f, 0.f, 0.f, 0.f);
-  const float4 wq = a.wq ? load4(a.wq + i) : one, wk = a.wk ? load4(a.wk + i) : one;
+  const Pieces pc = pieces_of<D>(a, lane);
+  const bool half = a.layout == GDN_ROPE_HALF, some_off = a.rot < D;
+  const Row8 wq = W && a.wq ? load8p(a.wq + pc.at, pc.gap) : all8(1.f);
+  const Row8 wk = W && a.wk ? load8p(a.wk + pc.at, pc.gap) : all8(1.f);
   const float cn = a.norm == GDN_NORM_RMS ? 1.f / D : a.norm == GDN_NORM_L2 ? 1.f : 0.f;
-  float4 accq = zero, acck = zero;
+  Row8 acc[2] = {all8(0.f), all8(0.f)};
   for (int64_t item = (int64_t)blockIdx.x * (kNormThreads / 32) + (threadIdx.x >> 5); item < items; item += step) {
-    const int64_t t = item / per;
-    const int row0 = (int)(item % per) * U * GPW + grp;
-    float4 x[U], g[U];
+    const NormItem it = norm_item<U * GPW>(a, item, per);
+    const int h = it.h0 + lane / LPR;
+    const int64_t at = (it.t * it.heads + h) * D + pc.at;
+    const TI* src = (it.kind ? static_cast<const TI*>(a.k) + it.t * a.k_stride
+                             : static_cast<const TI*>(a.q) + it.t * a.q_stride) + h * D + pc.at;
+    const TG* gsrc = static_cast<const TG*>(it.kind ? a.gk : a.gq) + at;
+    TI* dst = static_cast<TI*>(it.kind ? a.dk : a.dq) + at;
+    Row8 x[U], g[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int r = row0 + u * GPW;
-      x[u] = g[u] = zero;
-      if (r < a.hq) {
-        x[u] = load4(static_cast<const TI*>(a.q) + t * a.q_stride + (int64_t)r * D + i);
-        g[u] = load4(static_cast<const TG*>(a.gq) + (t * a.hq + r) * D + i);
-      } else if (r < rows) {
-        x[u] = load4(static_cast<const TI*>(a.k) + t * a.k_stride + (int64_t)(r - a.hq) * D + i);
-        g[u] = load4(static_cast<const TG*>(a.gk) + (t * a.hk + (r - a.hq)) * D + i);
-      }
+      const bool in = h + u * GPW < it.heads;
+      x[u] = in ? load8p(src + u * GPW * D, pc.gap) : all8(0.f);
+      g[u] = in ? load8p(gsrc + u * GPW * D, pc.gap) : all8(0.f);
     }
-    const int64_t p = a.rot ? a.pos[t] : 0;
+    const int64_t p = a.rot ? a.pos[it.t] : 0;
     const bool bad = a.rot && (p < 0 || p >= a.table_rows);
-    const Turn tn = turn_of<LPR>(a, bad ? 0 : p, lane, -1.f);
+    Row8 c, s;
+    angles_of(a, bad ? 0 : p, -1.f, pc, half, c, s);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int r = row0 + u * GPW;
-      const float4 gr = turn(tn, a.layout, g[u]);
-      const float4 gw = mul4(gr, r < a.hq ? wq : wk);
-      const float rn = inverse_norm(a.norm, row_sum<LPR>(dot4(x[u], x[u])), 1.f / D, a.eps);
-      const float xg = row_sum<LPR>(dot4(x[u], gw));
-      const float f = -__fmul_rn(__fmul_rn(cn, __fmul_rn(rn, __fmul_rn(rn, rn))), xg);
-      float4 dx = make_float4(__fmaf_rn(f, x[u].x, __fmul_rn(rn, gw.x)), __fmaf_rn(f, x[u].y, __fmul_rn(rn, gw.y)),
-                              __fmaf_rn(f, x[u].z, __fmul_rn(rn, gw.z)), __fmaf_rn(f, x[u].w, __fmul_rn(rn, gw.w)));
-      if (bad) dx = make_float4(kNan, kNan, kNan, kNan);
-      if (r < a.hq)
-        store4(static_cast<TI*>(a.dq) + (t * a.hq + r) * D + i, dx);
-      else if (r < rows)
-        store4(static_cast<TI*>(a.dk) + (t * a.hk + (r - a.hq)) * D + i, dx);
-      if (a.partial && r < rows && !bad) {
-        const float4 y = mul4(gr, scale4(x[u], rn));
-        float4& acc = r < a.hq ? accq : acck;
-        acc = make_float4(__fadd_rn(acc.x, y.x), __fadd_rn(acc.y, y.y), __fadd_rn(acc.z, y.z), __fadd_rn(acc.w, y.w));
+      if (a.rot) {
+        const Row8 z = fma8(partners(g[u], half), s, mul8(g[u], c));
+        g[u] = some_off ? pick8(pc.on, z, g[u]) : z;
+      }
+      const Row8 gw = W ? mul8(g[u], it.kind ? wk : wq) : g[u];
+      const float r = inverse_norm(a.norm, row_sum<LPR>(dot8(x[u], x[u])), 1.f / D, a.eps);
+      const float xg = row_sum<LPR>(dot8(x[u], gw));
+      const float f = -__fmul_rn(__fmul_rn(cn, __fmul_rn(r, __fmul_rn(r, r))), xg);
+      Row8 dx = fma8(all8(f), x[u], mul8(gw, all8(r)));
+      if (bad) dx = all8(kNan);
+      if (h + u * GPW < it.heads) {
+        store8p(dst + u * GPW * D, pc.gap, dx);
+        if (W && !bad) {
+          const Row8 xr = mul8(x[u], all8(r));
+          if (it.kind) acc[1] = fma8(g[u], xr, acc[1]); else acc[0] = fma8(g[u], xr, acc[0]);
+        }
       }
     }
   }
-  if (!a.partial) return;
+  if (!W || !a.partial) return;
   constexpr int NR = kNormThreads / LPR;  // rows of lanes in the block
   __shared__ float sh[2][NR][D];
   const int rr = threadIdx.x / LPR;
-  store4(&sh[0][rr][i], accq);
-  store4(&sh[1][rr][i], acck);
+  store8p(&sh[0][rr][pc.at], pc.gap, acc[0]);
+  store8p(&sh[1][rr][pc.at], pc.gap, acc[1]);
   __syncthreads();
   for (int e = threadIdx.x; e < 2 * D; e += kNormThreads) {
-    float s = 0.f;
-#pragma unroll
-    for (int r = 0; r < NR; ++r) s = __fadd_rn(s, sh[e / D][r][e % D]);
-    a.partial[(int64_t)blockIdx.x * 2 * D + e] = s;
+    float sum = 0.f;
+#pragma unroll 8
+    for (int r = 0; r < NR; ++r) sum = __fadd_rn(sum, sh[e / D][r][e % D]);
+    a.partial[(int64_t)blockIdx.x * 2 * D + e] = sum;
   }
 }
 
@@ -235,20 +315,31 @@ __global__ void __launch_bounds__(256) k_norm_rope_dw(const float* __restrict__ 
 
 template <int D, typename TI, typename TO>
 void norm_rope_t(const NormRope& a, cudaStream_t st) {
-  constexpr int U = 4, GPW = RowLanes<D>::GPW;
-  const int rows = a.hq + a.hk + (a.v_pages ? a.hk : 0);
-  const int64_t items = (int64_t)a.T * ((rows + U * GPW - 1) / (U * GPW));
-  const int64_t blocks = (items + kNormThreads / 32 - 1) / (kNormThreads / 32);
-  k_norm_rope<D, TI, TO, U><<<(unsigned)blocks, kNormThreads, 0, st>>>(a);
+  // Few rows: one row set per warp, which ends sooner (4 tokens of 16 / 2 heads: 2.0 us against 2.8);
+  // from about 8 warps a scheduler on, four at once keep more loads in flight (16384 tokens: 96 us
+  // against 140).
+  constexpr int GPW = RowLanes<D>::GPW;
+  const int hv = a.v_pages ? a.hk : 0;
+  const auto blocks = [&](int per) { return (unsigned)(((int64_t)a.T * per + kNormThreads / 32 - 1) / (kNormThreads / 32)); };
+  if ((int64_t)a.T * norm_items<GPW>(a.hq, a.hk, hv) <= 152 * 32) {
+    const int per = norm_items<GPW>(a.hq, a.hk, hv);
+    k_norm_rope<D, TI, TO, 1><<<blocks(per), kNormThreads, 0, st>>>(a, per);
+  } else {
+    const int per = norm_items<4 * GPW>(a.hq, a.hk, hv);
+    k_norm_rope<D, TI, TO, 4><<<blocks(per), kNormThreads, 0, st>>>(a, per);
+  }
 }
 
 template <int D, typename TI, typename TG>
 void norm_rope_bwd_t(const NormRope& a, cudaStream_t st) {
-  constexpr int U = 4, GPW = RowLanes<D>::GPW;
-  const int64_t items = (int64_t)a.T * ((a.hq + a.hk + U * GPW - 1) / (U * GPW));
-  int64_t blocks = (items + kNormThreads / 32 - 1) / (kNormThreads / 32);
+  constexpr int U = 2, RUN = U * RowLanes<D>::GPW;
+  const int per = norm_items<RUN>(a.hq, a.hk, 0);
+  int64_t blocks = ((int64_t)a.T * per + kNormThreads / 32 - 1) / (kNormThreads / 32);
   if (a.partial && blocks > kNormBwdBlocks) blocks = kNormBwdBlocks;
-  k_norm_rope_bwd<D, TI, TG, U><<<(unsigned)blocks, kNormThreads, 0, st>>>(a);
+  if (a.wq || a.wk || a.partial)
+    k_norm_rope_bwd<D, TI, TG, U, true><<<(unsigned)blocks, kNormThreads, 0, st>>>(a, per);
+  else
+    k_norm_rope_bwd<D, TI, TG, U, false><<<(unsigned)blocks, kNormThreads, 0, st>>>(a, per);
   if (a.partial) k_norm_rope_dw<<<2 * D / 8, 256, 0, st>>>(a.partial, (int)blocks, D, a.dwq, a.dwk);
 }
 
