@@ -7,9 +7,10 @@
 // with P = exp2(c Q K^T - lse log2 e) and dS = P (dO V^T - delta) formed anew in both (7 products of
 // 128 x 64 x d where one kernel that adds dQ across CTAs would need 5).  The row tiles X, Y (Q and
 // dO, or K and V) stay in shared memory; column tiles U, W come by TMA.  S = X U^T and T = Y W^T go
-// to one of two buffers in TMEM, a group of four warps (a thread per row) turns them into dS
-// and P as bf16 in place, and the accumulating products read those from TMEM.  The two groups
-// take the column blocks in turn, so that one's arithmetic runs beside the other's products.
+// to TMEM; a group of four warps (a thread per row) takes them into registers, which frees their
+// place for the next block's, and leaves dS and P as bf16 in a place of its own, from which the
+// accumulating products read them.  The two groups take the column blocks in turn, so that one's
+// arithmetic runs beside the other's and the products.
 // P and dS are rounded to bf16 for their products; everything else stays in 32 bits.
 // A 128 x 64 block costs 128 x 64 x d MACs per product at 4096 a clock, and S and T read 48 KB of
 // shared memory each at 128 bytes a clock: the two limits lie together.
@@ -76,9 +77,18 @@ struct Smem {
   static constexpr int BYTES = BARS + 1024 + 1024;
 };
 
+// TMEM columns: buffers of S and T (128 columns), dS and P of each group as bf16 (32 columns each),
+// the accumulators.
+template <int D, bool DKV>
+struct Tmem {
+  static constexpr int ST_BUFS = DKV && D == 128 ? 1 : 2, PD_STEP = DKV ? 64 : 32;
+  static constexpr int PD = 128 * ST_BUFS, ACC = PD + 2 * PD_STEP;
+  static_assert(ACC + (DKV ? 2 : 1) * D <= 512, "TMEM has 512 columns");
+};
+
 struct Bars {
-  uint64_t item_full[2], item_empty[2], x_full, x_empty, st_full[STAGES], st_empty[STAGES], s_full[2], p_full[2],
-      acc_full, acc_empty, aux;
+  uint64_t item_full[2], item_empty[2], x_full, x_empty, st_full[STAGES], st_empty[STAGES], s_full[2], s_free[2],
+      p_full[2], p_free[2], acc_full, acc_empty, aux;
   uint32_t tmem;
   Item item[2];
 };
@@ -116,6 +126,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap my,
                     const __grid_constant__ CUtensorMap mu, const __grid_constant__ CUtensorMap mw) {
   using L = Smem<D>;
+  using M = Tmem<D, DKV>;
   extern __shared__ unsigned char raw[];
   unsigned char* sm = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
   Bars& B = *reinterpret_cast<Bars*>(sm + L::BARS);
@@ -127,7 +138,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&B.item_full[i], 1);
       mbar_init(&B.item_empty[i], 9);  // the MMA thread and eight row warps
       mbar_init(&B.s_full[i], 1);
+      mbar_init(&B.s_free[i], 4);
       mbar_init(&B.p_full[i], 4);
+      mbar_init(&B.p_free[i], 1);
     }
     for (int i = 0; i < STAGES; ++i) {
       mbar_init(&B.st_full[i], DKV ? 33 : 1);  // tiles; the loader's lanes' vectors
@@ -225,54 +238,66 @@ __global__ void __launch_bounds__(kThreads, 1)
       cp_async_wait_all();
     } else if (warp == kMmaWarp) {
       // ------------------------------------------------------------------- MMA ----
-      if (lane == 0) {
+      {
+        // The warp stays converged, and each group of MMAs is issued by its elected lane: the compiler
+        // then knows that there is one, and keeps descriptors in uniform registers.
         const uint32_t iS = idesc_bf16(BR, BC), iA = idesc_bf16(BR, D) | IDESC_B_MN;
-        const uint32_t sX = smem_u32(sm + L::X), sY = smem_u32(sm + L::Y), sT = smem_u32(sm + L::ST);
-        uint32_t n = 0, stage = 0, round = 0, xn = 0, np[2] = {0, 0}, an = 0;
+        const uint64_t dX = desc_k_sw128(smem_u32(sm + L::X)), dY = desc_k_sw128(smem_u32(sm + L::Y));
+        const uint64_t dU = desc_k_sw128(smem_u32(sm + L::ST)), dUt = desc_mn_sw128(smem_u32(sm + L::ST), BC * 128);
+        constexpr int STEP = L::COLS / 16;  // of a descriptor, from U to W of a stage
+        uint32_t n = 0, xn = 0, an = 0;
+        uint32_t stage = 0, is = 0, ir = 0;            // stage of the block accumulated and formed next
+        uint32_t buf = 0, bn = 0, np[2] = {0, 0};      // S, T buffer and its use; P, dS
         while (ok) {
           const uint32_t slot = n & 1;
-          ok = mbar_wait(&B.item_full[slot], (n >> 1) & 1);
+          ok = warp_wait(&B.item_full[slot], (n >> 1) & 1);
           if (!ok) break;
-          const Item it = B.item[slot];
-          mbar_arrive(&B.item_empty[slot]);
+          Item it = B.item[slot];
+          __syncwarp();
+          if (elect_one()) mbar_arrive(&B.item_empty[slot]);
           ++n;
-          if (!it.ok) break;
-          const int cnt = Cols<DKV>(a, it).cnt;
+          if (!uniform(it.ok)) break;
+          const int cnt = uniform(Cols<DKV>(a, it).cnt);
           if (!cnt) continue;
-          ok = mbar_wait(&B.x_full, xn & 1);
+          ok = warp_wait(&B.x_full, xn & 1);
           ++xn;
-          uint32_t is = stage, ir = round;  // stage of the next block whose S and T are issued
-          for (int i = -2; i < cnt && ok; ++i) {  // accumulate block i, then issue S, T of i + 2
-            const int b = i & 1;
-            if (i >= 0) {
-              ok = mbar_wait(&B.p_full[b], np[b] & 1);
+          for (int i = 0; i <= cnt && ok; ++i) {
+            if (i < cnt) {  // S, T of block i
+              ok = warp_wait(&B.st_full[is], ir & 1);
+              ok = ok && warp_wait(&B.s_free[buf], (bn & 1) ^ 1);
+              if (!ok) break;
+              fence_after_sync();
+              if (elect_one()) {
+                const uint64_t u = dU + is * (2 * STEP);
+                mma_rows<D, BR, BC>(tm + 128 * buf, dX, u, iS);
+                mma_rows<D, BR, BC>(tm + 128 * buf + 64, dY, u + STEP, iS);
+                mma_commit(&B.s_full[i & 1]);
+                if (i + 1 == cnt) mma_commit(&B.x_empty);
+              }
+              if (++is == STAGES) is = 0, ++ir;
+              if (++buf == M::ST_BUFS) buf = 0, ++bn;
+            }
+            if (i > 0) {  // accumulate block i - 1
+              const int b = (i - 1) & 1;
+              ok = warp_wait(&B.p_full[b], np[b] & 1);
               ++np[b];
-              if (i == 0) {  // the last item's results have left TMEM
-                ok = ok && mbar_wait(&B.acc_empty, (an & 1) ^ 1);
+              if (i == 1) {  // the last item's results have left TMEM
+                ok = ok && warp_wait(&B.acc_empty, (an & 1) ^ 1);
                 ++an;
               }
               if (!ok) break;
               fence_after_sync();
-              const uint32_t u = sT + stage * 2 * L::COLS;
-              mma_ts_cols<BC>(tm + 256, tm + 128 * b, u, iA, i > 0);
-              if (DKV) mma_ts_cols<BC>(tm + 256 + D, tm + 128 * b + 64, u + L::COLS, iA, i > 0);
-              mma_commit(&B.st_empty[stage]);
-              if (++stage == STAGES) stage = 0, ++round;
-            }
-            if (i + 2 < cnt) {
-              ok = mbar_wait(&B.st_full[is], ir & 1);
-              if (!ok) break;
-              fence_after_sync();
-              const uint32_t u = sT + is * 2 * L::COLS;
-              mma_rows<D, BR, BC>(tm + 128 * b, sX, u, iS);
-              mma_rows<D, BR, BC>(tm + 128 * b + 64, sY, u + L::COLS, iS);
-              mma_commit(&B.s_full[b]);
-              if (++is == STAGES) is = 0, ++ir;
-              if (i + 3 == cnt) mma_commit(&B.x_empty);
+              if (elect_one()) {
+                const uint64_t u = dUt + stage * (2 * STEP);
+                mma_ts_cols<BC>(tm + M::ACC, tm + M::PD + M::PD_STEP * b, u, iA, i > 1);
+                if (DKV) mma_ts_cols<BC>(tm + M::ACC + D, tm + M::PD + M::PD_STEP * b + 32, u + STEP, iA, i > 1);
+                mma_commit(&B.p_free[b]);
+                mma_commit(&B.st_empty[stage]);
+                if (i == cnt) mma_commit(&B.acc_full);
+              }
+              if (++stage == STAGES) stage = 0;
             }
           }
-          if (!ok) break;
-          mma_commit(&B.acc_full);
         }
       }
     }
@@ -280,10 +305,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     // -------------------------------------------------------------------- rows ----
     regs_more<kRowRegs>();
     const int wg = warp >> 2, row = (warp & 3) * 32 + lane;
-    const uint32_t tS = tmem_lane_addr(tm + 128 * wg, warp, 0), tT = tS + 64;
+    const uint32_t tP = tmem_lane_addr(tm + M::PD + M::PD_STEP * wg, warp, 0);
     const float sc = __fmul_rn(a.scale, kLog2e);
     const float2 sc2 = make_float2(sc, sc);
-    uint32_t n = 0, ns = 0, an = 0, stage = 0, round = 0;  // stage of the item's block 0
+    uint32_t n = 0, ns = 0, an = 0;
+    uint32_t stage = 0, round = 0, blk = 0;  // stage of the item's block 0, and the S, T buffer's block count
     while (ok) {
       const uint32_t slot = n & 1;
       ok = mbar_wait(&B.item_full[slot], (n >> 1) & 1);
@@ -356,8 +382,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!cut) see[0] = see[1] = ~0u;
         float s[BC], t[BC];
+        const uint32_t tS = tmem_lane_addr(tm + 128 * ((blk + i) % M::ST_BUFS), warp, 0);
         tmem_ld64(tS, s);
-        tmem_ld64(tT, t);
+        tmem_ld64(tS + 64, t);
+        fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&B.s_free[(blk + i) % M::ST_BUFS]);  // S, T are in registers
+        if (ns > 1) {  // the group's last P and dS have been read
+          ok = mbar_wait(&B.p_free[wg], ns & 1);
+          if (!ok) break;
+        }
         const float4* lv = reinterpret_cast<const float4*>(sm + L::VEC) + st * (2 * BC / 4);
         const float4* dv = lv + BC / 4;
 #pragma unroll
@@ -388,8 +422,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (DKV) pp[k] &= keep;
             }
           }
-          tmem_st16u(tS + 16 * g, pd);
-          if (DKV) tmem_st16u(tT + 16 * g, pp);
+          tmem_st16u(tP + 16 * g, pd);
+          if (DKV) tmem_st16u(tP + 32 + 16 * g, pp);
         }
         tmem_st_wait();
         fence_before_sync();
@@ -400,6 +434,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (!ok) break;
+      blk += c.cnt;
       stage += c.cnt;
       round += stage / STAGES;
       stage %= STAGES;
@@ -413,7 +448,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr int W = DKV ? D : D / 2;  // columns of this group
       const int heads = DKV ? a.hkv : a.hq, col = DKV ? 0 : wg * W;
       const float f = DKV && wg == 1 ? 1.f : a.scale;
-      const uint32_t tA = tmem_lane_addr(tm + 256, warp, DKV ? D * wg : W * wg);
+      const uint32_t tA = tmem_lane_addr(tm + M::ACC, warp, DKV ? D * wg : W * wg);
       __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(DKV ? (wg ? a.dv : a.dk) : a.dq) +
                            ((int64_t)((DKV ? it.q.k0 : it.q.q0) + it.row0 + row) * heads + it.h) * D + col;
 #pragma unroll
