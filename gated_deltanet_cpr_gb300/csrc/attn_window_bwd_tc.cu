@@ -25,7 +25,7 @@ using namespace win;
 using namespace tc;
 
 constexpr int BR = 128, BC = 64, STAGES = 4;  // rows, columns of a block
-constexpr int kThreads = 384, kMmaWarp = 8, kLoadWarp = 9;
+constexpr int kThreads = 384, kScoreWarp = 8, kLoadWarp = 9, kAccWarp = 10;
 // 384 threads x 168 registers at launch = 256 x 208 + 128 x 88
 constexpr int kRowRegs = 208, kOtherRegs = 88;
 constexpr int kSms = 152;
@@ -132,11 +132,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   Bars& B = *reinterpret_cast<Bars*>(sm + L::BARS);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (!DKV && blockIdx.x == 0) check_tables(a);
-  if (warp == kMmaWarp) tmem_alloc(&B.tmem, 512);
+  if (warp == kScoreWarp) tmem_alloc(&B.tmem, 512);
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&B.item_full[i], 1);
-      mbar_init(&B.item_empty[i], 9);  // the MMA thread and eight row warps
+      mbar_init(&B.item_empty[i], 10);  // all warps but the loader and the idle one
       mbar_init(&B.s_full[i], 1);
       mbar_init(&B.s_free[i], 4);
       mbar_init(&B.p_full[i], 4);
@@ -236,68 +236,68 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       cp_async_wait_all();
-    } else if (warp == kMmaWarp) {
+    } else if (warp == kScoreWarp || warp == kAccWarp) {
       // ------------------------------------------------------------------- MMA ----
-      {
-        // The warp stays converged, and each group of MMAs is issued by its elected lane: the compiler
-        // then knows that there is one, and keeps descriptors in uniform registers.
-        const uint32_t iS = idesc_bf16(BR, BC), iA = idesc_bf16(BR, D) | IDESC_B_MN;
-        const uint64_t dX = desc_k_sw128(smem_u32(sm + L::X)), dY = desc_k_sw128(smem_u32(sm + L::Y));
-        const uint64_t dU = desc_k_sw128(smem_u32(sm + L::ST)), dUt = desc_mn_sw128(smem_u32(sm + L::ST), BC * 128);
-        constexpr int STEP = L::COLS / 16;  // of a descriptor, from U to W of a stage
-        uint32_t n = 0, xn = 0, an = 0;
-        uint32_t stage = 0, is = 0, ir = 0;            // stage of the block accumulated and formed next
-        uint32_t buf = 0, bn = 0, np[2] = {0, 0};      // S, T buffer and its use; P, dS
-        while (ok) {
-          const uint32_t slot = n & 1;
-          ok = warp_wait(&B.item_full[slot], (n >> 1) & 1);
-          if (!ok) break;
-          Item it = B.item[slot];
-          __syncwarp();
-          if (elect_one()) mbar_arrive(&B.item_empty[slot]);
-          ++n;
-          if (!uniform(it.ok)) break;
-          const int cnt = uniform(Cols<DKV>(a, it).cnt);
-          if (!cnt) continue;
+      // One warp issues S and T, another the accumulating products: an issuing thread stands still
+      // while its products run, and each wait costs it a few hundred cycles.  The warps stay
+      // converged, and each group of MMAs is issued by its elected lane: the compiler then knows that
+      // there is one, and keeps descriptors in uniform registers.
+      const bool scores = warp == kScoreWarp;
+      const uint32_t iS = idesc_bf16(BR, BC), iA = idesc_bf16(BR, D) | IDESC_B_MN;
+      const uint64_t dX = desc_k_sw128(smem_u32(sm + L::X)), dY = desc_k_sw128(smem_u32(sm + L::Y));
+      const uint64_t dU = desc_k_sw128(smem_u32(sm + L::ST)), dUt = desc_mn_sw128(smem_u32(sm + L::ST), BC * 128);
+      constexpr int STEP = L::COLS / 16;  // of a descriptor, from U to W of a stage
+      uint32_t n = 0, xn = 0, an = 0, stage = 0, round = 0;
+      uint32_t buf = 0, bn = 0, np[2] = {0, 0};  // S, T buffer and its use; P, dS
+      while (ok) {
+        const uint32_t slot = n & 1;
+        ok = warp_wait(&B.item_full[slot], (n >> 1) & 1);
+        if (!ok) break;
+        Item it = B.item[slot];
+        __syncwarp();
+        if (elect_one()) mbar_arrive(&B.item_empty[slot]);
+        ++n;
+        if (!uniform(it.ok)) break;
+        const int cnt = uniform(Cols<DKV>(a, it).cnt);
+        if (!cnt) continue;
+        if (scores) {
           ok = warp_wait(&B.x_full, xn & 1);
           ++xn;
-          for (int i = 0; i <= cnt && ok; ++i) {
-            if (i < cnt) {  // S, T of block i
-              ok = warp_wait(&B.st_full[is], ir & 1);
-              ok = ok && warp_wait(&B.s_free[buf], (bn & 1) ^ 1);
-              if (!ok) break;
-              fence_after_sync();
-              if (elect_one()) {
-                const uint64_t u = dU + is * (2 * STEP);
-                mma_rows<D, BR, BC>(tm + 128 * buf, dX, u, iS);
-                mma_rows<D, BR, BC>(tm + 128 * buf + 64, dY, u + STEP, iS);
-                mma_commit(&B.s_full[i & 1]);
-                if (i + 1 == cnt) mma_commit(&B.x_empty);
-              }
-              if (++is == STAGES) is = 0, ++ir;
-              if (++buf == M::ST_BUFS) buf = 0, ++bn;
+        }
+        for (int i = 0; i < cnt && ok; ++i) {
+          ok = warp_wait(&B.st_full[stage], round & 1);
+          if (scores) {
+            ok = ok && warp_wait(&B.s_free[buf], (bn & 1) ^ 1);  // the buffer's last S, T are in registers
+            if (!ok) break;
+            fence_after_sync();
+            if (elect_one()) {
+              const uint64_t u = dU + stage * (2 * STEP);
+              mma_rows<D, BR, BC>(tm + 128 * buf, dX, u, iS);
+              mma_rows<D, BR, BC>(tm + 128 * buf + 64, dY, u + STEP, iS);
+              mma_commit(&B.s_full[i & 1]);
+              if (i + 1 == cnt) mma_commit(&B.x_empty);
             }
-            if (i > 0) {  // accumulate block i - 1
-              const int b = (i - 1) & 1;
-              ok = warp_wait(&B.p_full[b], np[b] & 1);
-              ++np[b];
-              if (i == 1) {  // the last item's results have left TMEM
-                ok = ok && warp_wait(&B.acc_empty, (an & 1) ^ 1);
-                ++an;
-              }
-              if (!ok) break;
-              fence_after_sync();
-              if (elect_one()) {
-                const uint64_t u = dUt + stage * (2 * STEP);
-                mma_ts_cols<BC>(tm + M::ACC, tm + M::PD + M::PD_STEP * b, u, iA, i > 1);
-                if (DKV) mma_ts_cols<BC>(tm + M::ACC + D, tm + M::PD + M::PD_STEP * b + 32, u + STEP, iA, i > 1);
-                mma_commit(&B.p_free[b]);
-                mma_commit(&B.st_empty[stage]);
-                if (i == cnt) mma_commit(&B.acc_full);
-              }
-              if (++stage == STAGES) stage = 0;
+            if (++buf == M::ST_BUFS) buf = 0, ++bn;
+          } else {
+            const int b = i & 1;
+            ok = ok && warp_wait(&B.p_full[b], np[b] & 1);
+            ++np[b];
+            if (i == 0) {  // the last item's results have left TMEM
+              ok = ok && warp_wait(&B.acc_empty, (an & 1) ^ 1);
+              ++an;
+            }
+            if (!ok) break;
+            fence_after_sync();
+            if (elect_one()) {
+              const uint64_t u = dUt + stage * (2 * STEP);
+              mma_ts_cols<BC>(tm + M::ACC, tm + M::PD + M::PD_STEP * b, u, iA, i > 0);
+              if (DKV) mma_ts_cols<BC>(tm + M::ACC + D, tm + M::PD + M::PD_STEP * b + 32, u + STEP, iA, i > 0);
+              mma_commit(&B.p_free[b]);
+              mma_commit(&B.st_empty[stage]);
+              if (i + 1 == cnt) mma_commit(&B.acc_full);
             }
           }
+          if (++stage == STAGES) stage = 0, ++round;
         }
       }
     }
@@ -484,7 +484,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; i < STAGES; ++i) mbar_wait(&B.st_full[i], 0, 1u << 12);
   }
   __syncthreads();
-  if (warp == kMmaWarp) tmem_dealloc(tm, 512);
+  if (warp == kScoreWarp) tmem_dealloc(tm, 512);
 }
 
 template <int D, bool DKV>

@@ -14,8 +14,8 @@
 // bf16 and fp32 are as exact as below 1, and the rescaling (a TMEM round trip) is rare.  Blocks
 // that no row of a tile sees are skipped tile by tile.
 //
-// Warps: 0-3 softmax of tile 0, 4-7 of tile 1, 8 issues the MMAs, 9 loads (TMA), 10 and 11 only
-// complete the warpgroup whose registers the softmax warps take over.  The loader
+// Warps: 0-3 softmax of tile 0, 4-7 of tile 1, 8 issues the scores' products, 9 loads (TMA), 10
+// issues P V, 11 only completes the warpgroup whose registers the softmax warps take over.  The loader
 // publishes the items, runs ahead by the ring of key and value blocks, and zeroes the rows of a
 // value block that lie past the sequence's end (they belong to another sequence, may hold NaN,
 // and 0 x NaN is not 0).
@@ -32,7 +32,7 @@ using namespace win;
 using namespace tc;
 
 constexpr int BM = 128, BN = 128;  // rows of a query tile, keys of a block
-constexpr int kWarps = 12, kThreads = 32 * kWarps, kMmaWarp = 8, kLoadWarp = 9;
+constexpr int kWarps = 12, kThreads = 32 * kWarps, kScoreWarp = 8, kLoadWarp = 9, kAccWarp = 10;
 // 384 threads x 168 registers at launch = 256 x 208 + 128 x 88: a softmax thread holds a row's 128
 // scores
 constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
@@ -106,11 +106,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   FwdBars& B = *reinterpret_cast<FwdBars*>(sm + L::BARS);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (blockIdx.x == 0) check_tables(a);
-  if (warp == kMmaWarp) tmem_alloc(&B.tmem, 512);
+  if (warp == kScoreWarp) tmem_alloc(&B.tmem, 512);
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&B.item_full[i], 1);
-      mbar_init(&B.item_empty[i], 9);  // the MMA thread and eight softmax warps
+      mbar_init(&B.item_empty[i], 10);  // all warps but the loader and the idle one
       mbar_init(&B.s_full[i], 1);
       mbar_init(&B.p_full[i], 4);
       mbar_init(&B.pv_done[i], 1);
@@ -198,16 +198,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-    } else if (warp == kMmaWarp) {
-    // --------------------------------------------------------------------- MMA ----
-    {
-      // The warp stays converged, and each group of MMAs is issued by its elected lane: the compiler then
-      // knows that there is one, and keeps descriptors in uniform registers.
+    } else if (warp == kScoreWarp || warp == kAccWarp) {
+      // --------------------------------------------------------------------- MMA ----
+      // One warp issues the scores' products, another P V: an issuing thread stands still while its
+      // products run, and each wait costs it a few hundred cycles.  The warps stay converged, and
+      // each group of MMAs is issued by its elected lane: the compiler then knows that there is one,
+      // and keeps descriptors in uniform registers.
+      const bool scores = warp == kScoreWarp;
       const uint32_t iS = idesc_bf16(BM, BN), iO = idesc_bf16(BM, D) | IDESC_B_MN;
       const uint64_t dQ = desc_k_sw128(smem_u32(sm + L::Q)), dK = desc_k_sw128(smem_u32(sm + L::KV));
       const uint64_t dV = desc_mn_sw128(smem_u32(sm + L::KV), BN * 128);
       constexpr int STEP = L::TILE / 16;  // of a descriptor, from one tile to the next
-      uint32_t n = 0, stage = 0, round = 0, qn = 0, sn = 0, np[2] = {0, 0}, no[2] = {0, 0};
+      uint32_t n = 0, qn = 0, sn = 0, np[2] = {0, 0}, no[2] = {0, 0};
+      uint32_t stage = scores ? 0 : 1, round = 0;  // of the next key or value block
       while (ok) {
         const uint32_t slot = n & 1;
         ok = warp_wait(&B.item_full[slot], (n >> 1) & 1);
@@ -215,83 +218,57 @@ __global__ void __launch_bounds__(kThreads, 1)
         Item it = B.item[slot];
         __syncwarp();
         if (elect_one()) mbar_arrive(&B.item_empty[slot]);
-        it.ok = uniform(it.ok);
         ++n;
-        if (!it.ok) break;
+        if (!uniform(it.ok)) break;
         Plan p(a, it);
         p.uniform_all();
         const int cnt = p.count();
         if (!cnt) continue;
-        ok = warp_wait(&B.q_full, qn & 1);
-        ++qn;
-        if (!ok) break;
+        if (scores) {
+          ok = warp_wait(&B.q_full, qn & 1);
+          ++qn;
+        }
         bool started[2] = {false, false};
-        // stage of K(i) is `ks` at step i's start; V(i) the next one
-        uint32_t ks = stage, kr = round;
-        ok = warp_wait(&B.kv_full[ks], kr & 1);
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-          if (ok && p.need(t, p.block(0))) {
-            ok = warp_wait(&B.s_free, (sn & 1) ^ 1);  // the last scores are in registers
-            ++sn;
-            fence_after_sync();
-            if (elect_one()) {
-              mma_rows<D, BM, BN>(tS, dQ + t * STEP, dK + ks * STEP, iS);
-              mma_commit(&B.s_full[t]);
-            }
-          }
-        if (!ok) break;
-        if (elect_one()) mma_commit(&B.kv_empty[ks]);
-        if (cnt == 1 && elect_one()) mma_commit(&B.q_empty);
         for (int i = 0; i < cnt && ok; ++i) {
-          uint32_t vs = ks + 1, vr = kr;
-          if (vs == L::STAGES) vs = 0, ++vr;
-          uint32_t ns = vs + 1, nr = vr;
-          if (ns == L::STAGES) ns = 0, ++nr;
           const int b = p.block(i);
-          if (i + 1 < cnt) ok = warp_wait(&B.kv_full[ns], nr & 1);
-          ok = ok && warp_wait(&B.kv_full[vs], vr & 1);
+          ok = warp_wait(&B.kv_full[stage], round & 1);
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
-            if (ok && i + 1 < cnt && p.need(t, p.block(i + 1))) {
-              ok = warp_wait(&B.s_free, (sn & 1) ^ 1);
+            if (!ok || !p.need(t, b)) continue;
+            if (scores) {
+              ok = warp_wait(&B.s_free, (sn & 1) ^ 1);  // the last scores are in registers
               ++sn;
-              if (ok) {
-                fence_after_sync();
-                if (elect_one()) {
-                  mma_rows<D, BM, BN>(tS, dQ + t * STEP, dK + ns * STEP, iS);
-                  mma_commit(&B.s_full[t]);
-                }
+              if (!ok) continue;
+              fence_after_sync();
+              if (elect_one()) {
+                mma_rows<D, BM, BN>(tS, dQ + t * STEP, dK + stage * STEP, iS);
+                mma_commit(&B.s_full[t]);
               }
-            }
-            if (ok && p.need(t, b)) {
+            } else {
               ok = warp_wait(&B.p_full[t], np[t] & 1);
               ++np[t];
               if (!started[t]) {  // the last item's output has left TMEM
                 ok = ok && warp_wait(&B.o_empty[t], (no[t] & 1) ^ 1);
                 ++no[t];
               }
-              if (ok) {
-                fence_after_sync();
-                if (elect_one()) {
-                  mma_ts_cols<BN>(tO[t], tP[t], dV + vs * STEP, iO, started[t]);
-                  mma_commit(&B.pv_done[t]);
-                }
+              if (!ok) continue;
+              fence_after_sync();
+              if (elect_one()) {
+                mma_ts_cols<BN>(tO[t], tP[t], dV + stage * STEP, iO, started[t]);
+                mma_commit(&B.pv_done[t]);
               }
               started[t] = true;
             }
           }
           if (!ok) break;
           if (elect_one()) {
-            mma_commit(&B.kv_empty[vs]);
-            if (i + 1 < cnt) mma_commit(&B.kv_empty[ns]);
-            if (i + 2 == cnt) mma_commit(&B.q_empty);  // the item's last scores are issued
+            mma_commit(&B.kv_empty[stage]);
+            if (scores && i + 1 == cnt) mma_commit(&B.q_empty);
           }
-          ks = ns, kr = nr;
+          stage += 2;
+          if (stage >= L::STAGES) stage -= L::STAGES, ++round;
         }
-        stage = ks, round = kr;
       }
-    }
     }
   } else {
     // ----------------------------------------------------------------- softmax ----
@@ -431,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; i < L::STAGES; ++i) mbar_wait(&B.kv_full[i], 0, 1u << 12);
   }
   __syncthreads();
-  if (warp == kMmaWarp) tmem_dealloc(tm, 512);
+  if (warp == kScoreWarp) tmem_dealloc(tm, 512);
 }
 
 template <int D>
