@@ -6,14 +6,16 @@
 //           ascending order:   dK += dS^T Q,  dV += P^T dO
 // with P = exp2(c Q K^T - lse log2 e) and dS = P (dO V^T - delta) formed anew in both (7 products of
 // 128 x 64 x d where one kernel that adds dQ across CTAs would need 5).  The row tiles X, Y (Q and
-// dO, or K and V) stay in shared memory; column tiles U, W come by TMA.  S = X U^T and T = Y W^T go
+// dO, or K and V) stay on chip: Q and dO in TMEM, as the first operand of their products, K and V,
+// for which TMEM has no room, in shared memory; column tiles U, W come by TMA.  S = X U^T and T = Y W^T go
 // to TMEM; a group of four warps (a thread per row) takes them into registers, which frees their
 // place for the next block's, and leaves dS and P as bf16 in a place of its own, from which the
 // accumulating products read them.  The two groups take the column blocks in turn, so that one's
 // arithmetic runs beside the other's and the products.
 // P and dS are rounded to bf16 for their products; everything else stays in 32 bits.
-// A 128 x 64 block costs 128 x 64 x d MACs per product at 4096 a clock, and S and T read 48 KB of
-// shared memory each at 128 bytes a clock: the two limits lie together.
+// A 128 x 64 block costs 128 x 64 x d MACs per product at 4096 a clock; an operand from shared memory
+// is read at 128 bytes a clock, so that with both operands there S and T (48 KB each at d = 128) take
+// half as long again, and with the rows in TMEM they do not.
 #include "attn_tc.cuh"
 #include "attn_window.cuh"
 
@@ -24,7 +26,7 @@ namespace {
 using namespace win;
 using namespace tc;
 
-constexpr int BR = 128, BC = 64, STAGES = 4;  // rows, columns of a block
+constexpr int BR = 128, BC = 64;  // rows, columns of a block
 constexpr int kThreads = 384, kScoreWarp = 8, kLoadWarp = 9, kAccWarp = 10;
 // 384 threads x 168 registers at launch = 256 x 208 + 128 x 88
 constexpr int kRowRegs = 208, kOtherRegs = 88;
@@ -69,26 +71,26 @@ struct Cols {
   __device__ __forceinline__ int group_head(int i) const { return DKV ? i / nb : 0; }
 };
 
-template <int D>
+template <int D, bool DKV>
 struct Smem {
-  static constexpr int ROWS = BR * D * 2, COLS = BC * D * 2;
+  static constexpr int ROWS = DKV ? BR * D * 2 : 0, COLS = BC * D * 2, STAGES = DKV ? 4 : 6;
   static constexpr int X = 0, Y = ROWS, ST = 2 * ROWS, VEC = ST + STAGES * 2 * COLS;
-  static constexpr int BARS = VEC + STAGES * 2 * BC * 4;
+  static constexpr int BARS = VEC + (DKV ? STAGES * 2 * BC * 4 : 2 * BR * 4);
   static constexpr int BYTES = BARS + 1024 + 1024;
 };
 
 // TMEM columns: buffers of S and T (128 columns), dS and P of each group as bf16 (32 columns each),
-// the accumulators.
+// the accumulators, and for dq the rows X, Y (see above).
 template <int D, bool DKV>
 struct Tmem {
-  static constexpr int ST_BUFS = DKV && D == 128 ? 1 : 2, PD_STEP = DKV ? 64 : 32;
-  static constexpr int PD = 128 * ST_BUFS, ACC = PD + 2 * PD_STEP;
-  static_assert(ACC + (DKV ? 2 : 1) * D <= 512, "TMEM has 512 columns");
+  static constexpr int ST_BUFS = D == 128 ? 1 : 2, PD_STEP = DKV ? 64 : 32;
+  static constexpr int PD = 128 * ST_BUFS, ACC = PD + 2 * PD_STEP, X = ACC + (DKV ? 2 : 1) * D, Y = X + D / 2;
+  static_assert(X + (DKV ? 0 : D) <= 512, "TMEM has 512 columns");
 };
 
 struct Bars {
-  uint64_t item_full[2], item_empty[2], x_full, x_empty, st_full[STAGES], st_empty[STAGES], s_full[2], s_free[2],
-      p_full[2], p_free[2], acc_full, acc_empty, aux;
+  uint64_t item_full[2], item_empty[2], x_full, x_empty, st_full[6], st_empty[6], s_full[2], s_free[2],
+      p_full[2], p_free[2], acc_full, acc_empty, vec_full, vec_free, aux;
   uint32_t tmem;
   Item item[2];
 };
@@ -125,7 +127,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     k_window_bwd_tc(const WindowAttn a, const int64_t blocks, const int64_t work, int* next_item, float* vec,
                     const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap my,
                     const __grid_constant__ CUtensorMap mu, const __grid_constant__ CUtensorMap mw) {
-  using L = Smem<D>;
+  using L = Smem<D, DKV>;
+  constexpr int STAGES = L::STAGES;
   using M = Tmem<D, DKV>;
   extern __shared__ unsigned char raw[];
   unsigned char* sm = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
@@ -146,8 +149,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&B.st_full[i], DKV ? 33 : 1);  // tiles; the loader's lanes' vectors
       mbar_init(&B.st_empty[i], DKV ? 5 : 1);  // MMA; the four warps that read the vectors
     }
-    mbar_init(&B.x_full, 1);
+    mbar_init(&B.x_full, DKV ? 1 : 8);  // TMA, or the row warps
     mbar_init(&B.x_empty, 1);
+    mbar_init(&B.vec_full, 4);
+    mbar_init(&B.vec_free, 4);
     mbar_init(&B.acc_full, 1);
     mbar_init(&B.acc_empty, 8);
     mbar_init(&B.aux, 1);
@@ -184,15 +189,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!it.ok) break;
         const Cols<DKV> c(a, it);
         if (!c.cnt) continue;
-        ok = mbar_wait(&B.x_empty, (xn & 1) ^ 1);
-        if (!ok) break;
-        ++xn;
-        if (lane == 0) {
-          mbar_expect_tx(&B.x_full, 2 * L::ROWS);
-          const int row = (DKV ? it.q.k0 : it.q.q0) + it.row0;
-          for (int e = 0; e < D / 64; ++e) {
-            tma_load_3d(sm + L::X + e * BR * 128, &mx, 64 * e, it.h, row, &B.x_full);
-            tma_load_3d(sm + L::Y + e * BR * 128, &my, 64 * e, it.h, row, &B.x_full);
+        if (DKV) {
+          ok = mbar_wait(&B.x_empty, (xn & 1) ^ 1);
+          if (!ok) break;
+          ++xn;
+          if (lane == 0) {
+            mbar_expect_tx(&B.x_full, 2 * L::ROWS);
+            const int row = it.q.k0 + it.row0;
+            for (int e = 0; e < D / 64; ++e) {
+              tma_load_3d(sm + L::X + e * BR * 128, &mx, 64 * e, it.h, row, &B.x_full);
+              tma_load_3d(sm + L::Y + e * BR * 128, &my, 64 * e, it.h, row, &B.x_full);
+            }
           }
         }
         const int group = a.hq / a.hkv, len = DKV ? it.q.Lq : it.q.Lk;
@@ -272,8 +279,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             fence_after_sync();
             if (elect_one()) {
               const uint64_t u = dU + stage * (2 * STEP);
-              mma_rows<D, BR, BC>(tm + 128 * buf, dX, u, iS);
-              mma_rows<D, BR, BC>(tm + 128 * buf + 64, dY, u + STEP, iS);
+              if (DKV) {
+                mma_rows<D, BR, BC>(tm + 128 * buf, dX, u, iS);
+                mma_rows<D, BR, BC>(tm + 128 * buf + 64, dY, u + STEP, iS);
+              } else {
+                mma_ts_rows<D, BC>(tm + 128 * buf, tm + M::X, u, iS);
+                mma_ts_rows<D, BC>(tm + 128 * buf + 64, tm + M::Y, u + STEP, iS);
+              }
               mma_commit(&B.s_full[i & 1]);
               if (i + 1 == cnt) mma_commit(&B.x_empty);
             }
@@ -308,7 +320,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tP = tmem_lane_addr(tm + M::PD + M::PD_STEP * wg, warp, 0);
     const float sc = __fmul_rn(a.scale, kLog2e);
     const float2 sc2 = make_float2(sc, sc);
-    uint32_t n = 0, ns = 0, an = 0;
+    uint32_t n = 0, ns = 0, an = 0, xn = 0;
     uint32_t stage = 0, round = 0, blk = 0;  // stage of the item's block 0, and the S, T buffer's block count
     while (ok) {
       const uint32_t slot = n & 1;
@@ -324,28 +336,62 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int at = it.row0 + row + (DKV ? 0 : c.off);  // key, or the query's position
       float2 nl2, nd2;                                   // dq: -lse log2 e and -delta of the row
       if (!DKV) {
-        float dl = 0.f, ls = INFINITY;
-        if (live) {
-          const int64_t r = (int64_t)(it.q.q0 + it.row0 + row) * a.hq + it.h;
-          const __nv_bfloat16* o = static_cast<const __nv_bfloat16*>(a.out) + r * D;
-          const __nv_bfloat16* g = static_cast<const __nv_bfloat16*>(a.dout) + r * D;
-          float x0 = 0.f, x1 = 0.f;
-#pragma unroll 4
-          for (int e = 0; e < D; e += 8) {
-            float x[8], y[8];
-            load8(o + e, x);
-            load8(g + e, y);
+        // Group 0 brings Q's rows to TMEM, group 1 dO's, with which it forms delta = do . o.
+        const int64_t r = (int64_t)(it.q.q0 + it.row0 + row) * a.hq + it.h;
+        const uint4* xp = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(wg ? a.dout : a.q) + r * D);
+        uint4 x[D / 8];
 #pragma unroll
-            for (int k = 0; k < 8; k += 2) x0 = __fmaf_rn(x[k], y[k], x0), x1 = __fmaf_rn(x[k + 1], y[k + 1], x1);
-          }
-          dl = __fadd_rn(x0, x1);
-          const float l = a.lse[r];
-          if (l != -INFINITY) ls = __fmul_rn(l, kLog2e);  // a row that sees nothing: P = exp2(-inf) = 0
-          if (wg == 0) {
+        for (int e = 0; e < D / 8; ++e) x[e] = live ? xp[e] : make_uint4(0, 0, 0, 0);
+        float dl = 0.f, ls = INFINITY;
+        float* sh = reinterpret_cast<float*>(sm + L::VEC);
+        if (wg) {
+          if (live) {
+            const __nv_bfloat16* o = static_cast<const __nv_bfloat16*>(a.out) + r * D;
+            float x0 = 0.f, x1 = 0.f;
+#pragma unroll
+            for (int e = 0; e < D / 8; ++e) {
+              float y[8];
+              load8(o + 8 * e, y);
+              const uint32_t g[4] = {x[e].x, x[e].y, x[e].z, x[e].w};
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                x0 = __fmaf_rn(__uint_as_float(g[k] << 16), y[2 * k], x0);
+                x1 = __fmaf_rn(__uint_as_float(g[k] & 0xffff0000u), y[2 * k + 1], x1);
+              }
+            }
+            dl = __fadd_rn(x0, x1);
+            const float l = a.lse[r];
+            if (l != -INFINITY) ls = __fmul_rn(l, kLog2e);  // a row that sees nothing: P = exp2(-inf) = 0
             float* v = vec + (int64_t)it.h * a.Tq + it.q.q0 + it.row0 + row;
             v[0] = ls;
             v[(int64_t)a.hq * a.Tq] = dl;
           }
+          ok = mbar_wait(&B.vec_free, (n & 1));  // group 0 has the last item's (n counts from 1 here)
+          if (!ok) break;
+          sh[row] = ls;
+          sh[BR + row] = dl;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&B.vec_full);
+        }
+        if (c.cnt) {
+          ok = mbar_wait(&B.x_empty, (xn & 1) ^ 1);  // the last item's scores are done
+          ++xn;
+          if (!ok) break;
+          const uint32_t tX = tmem_lane_addr(tm + (wg ? M::Y : M::X), warp, 0);
+#pragma unroll
+          for (int e = 0; e < D / 8; e += 4) tmem_st16u(tX + 4 * e, reinterpret_cast<const uint32_t*>(&x[e]));
+          tmem_st_wait();
+          fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&B.x_full);
+        }
+        if (!wg) {
+          ok = mbar_wait(&B.vec_full, (n & 1) ^ 1);
+          if (!ok) break;
+          ls = sh[row];
+          dl = sh[BR + row];
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&B.vec_free);
         }
         nl2 = make_float2(-ls, -ls);
         nd2 = make_float2(-dl, -dl);
@@ -499,8 +545,8 @@ bool bwd_tc(const WindowAttn& a, cudaStream_t st) {
   const int64_t blocks = item_count(DKV ? a.Tk : a.Tq, BR, a.N);
   const int64_t work = DKV ? (blocks + a.N) * a.hkv : blocks * a.hq;
   static std::atomic<uint64_t> ready{0};
-  ensure_smem(k_window_bwd_tc<D, DKV>, Smem<D>::BYTES, ready);
-  k_window_bwd_tc<D, DKV><<<(unsigned)(work < kSms ? work : kSms), kThreads, Smem<D>::BYTES, st>>>(
+  ensure_smem(k_window_bwd_tc<D, DKV>, (Smem<D, DKV>::BYTES), ready);
+  k_window_bwd_tc<D, DKV><<<(unsigned)(work < kSms ? work : kSms), kThreads, (Smem<D, DKV>::BYTES), st>>>(
       a, blocks, work, a.hdr->pad + (DKV ? 1 : 0), a.delta, mx, my, mu, mw);
   return true;
 }

@@ -98,7 +98,7 @@ static_assert(sizeof(FwdBars) <= 1024, "fits its place");
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
-    k_window_fwd_tc(const WindowAttn a, const int64_t items, const __grid_constant__ CUtensorMap mq,
+    k_window_fwd_tc(const WindowAttn a, const int64_t items, int* next_item, const __grid_constant__ CUtensorMap mq,
                     const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
   using L = FwdSmem<D>;
   extern __shared__ unsigned char raw[];
@@ -136,12 +136,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kLoadWarp) {
     // ------------------------------------------------------------------ loader ----
     uint32_t n = 0, stage = 0, round = 0, aux = 0, qn = 0;
-    for (int64_t w = blockIdx.x; ok; w += gridDim.x) {
+    int64_t w = blockIdx.x;
+    while (ok) {
       Item it;
       it.ok = w < items * a.hq;
       if (it.ok) {
         it.h = (int)(w % a.hq);
-        it.q = find_seq(a, items - 1 - w / a.hq, 2 * BM, false, it.row0);
+        it.q = find_seq(a, items - 1 - w / a.hq, 2 * BM, false, it.row0);  // a sequence's last blocks see most
+        int nx = 0;
+        if (lane == 0 && next_item) nx = atomicAdd(next_item, 1);
+        w = next_item ? (int64_t)gridDim.x + __shfl_sync(0xffffffffu, nx, 0) : items * a.hq;
         if (!it.q.ok) continue;
       }
       const uint32_t slot = n & 1;
@@ -420,7 +424,13 @@ bool fwd_tc(const WindowAttn& a, cudaStream_t st) {
   const int64_t items = item_count(a.Tq, 2 * BM, a.N), work = items * a.hq;
   static std::atomic<uint64_t> ready{0};
   ensure_smem(k_window_fwd_tc<D>, FwdSmem<D>::BYTES, ready);
-  k_window_fwd_tc<D><<<(unsigned)(work < kSms ? work : kSms), kThreads, FwdSmem<D>::BYTES, st>>>(a, items, mq, mk, mv);
+  // more items than CTAs: they take the next one from a counter, as sequences' blocks differ in work
+  int* next_item = nullptr;
+  if (work > kSms) {
+    if (cudaMemsetAsync(a.hdr, 0, sizeof(WsHeader), st) != cudaSuccess) return false;
+    next_item = a.hdr->pad;
+  }
+  k_window_fwd_tc<D><<<(unsigned)(work < kSms ? work : kSms), kThreads, FwdSmem<D>::BYTES, st>>>(a, items, next_item, mq, mk, mv);
   return true;
 }
 
