@@ -104,11 +104,7 @@ struct WindowAttn {
 };
 // false: nothing was queued
 bool launch_window_attn(const WindowAttn& a, bool bf16, cudaStream_t st);
-// tensor-core kernels: bf16, d = 64 or 128, some queries and keys (a tensor map has no empty
-// dimension); false if the tensor maps cannot be made
-inline bool window_on_tensor_cores(const WindowAttn& a, bool bf16) {
-  return bf16 && a.d != 32 && a.Tq > 0 && a.Tk > 0;
-}
+// tensor-core kernels: bf16, d = 64 or 128; false if a tensor map cannot be made
 bool launch_window_fwd_tc(const WindowAttn& a, cudaStream_t st);
 bool launch_window_dq_tc(const WindowAttn& a, cudaStream_t st);
 bool launch_window_dkv_tc(const WindowAttn& a, cudaStream_t st);

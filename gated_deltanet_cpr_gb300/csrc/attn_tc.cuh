@@ -158,7 +158,8 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 }  // namespace tc
 
 // Host: tensor map of a packed [T, H, d] bf16 tensor whose boxes are 64 columns x one head x
-// `rows` rows in the 128-byte swizzle; rows past T read as zeros.  False if it cannot be made.
-bool make_rows_map(CUtensorMap* map, const void* base, int T, int H, int d, int rows);
+// `rows` rows in the 128-byte swizzle; rows past T read as zeros.  False if it cannot be made.  An
+// empty tensor, of which nothing is ever loaded, gets a map of one row of `any`.
+bool make_rows_map(CUtensorMap* map, const void* base, int T, int H, int d, int rows, const void* any);
 
 }  // namespace gdn

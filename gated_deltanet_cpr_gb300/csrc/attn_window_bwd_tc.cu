@@ -536,10 +536,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <int D, bool DKV>
 bool bwd_tc(const WindowAttn& a, cudaStream_t st) {
   CUtensorMap mx, my, mu, mw;
-  const bool ok = DKV ? make_rows_map(&mx, a.k, a.Tk, a.hkv, D, BR) && make_rows_map(&my, a.v, a.Tk, a.hkv, D, BR) &&
-                            make_rows_map(&mu, a.q, a.Tq, a.hq, D, BC) && make_rows_map(&mw, a.dout, a.Tq, a.hq, D, BC)
-                      : make_rows_map(&mx, a.q, a.Tq, a.hq, D, BR) && make_rows_map(&my, a.dout, a.Tq, a.hq, D, BR) &&
-                            make_rows_map(&mu, a.k, a.Tk, a.hkv, D, BC) && make_rows_map(&mw, a.v, a.Tk, a.hkv, D, BC);
+  const bool ok = DKV ? make_rows_map(&mx, a.k, a.Tk, a.hkv, D, BR, a.hdr) && make_rows_map(&my, a.v, a.Tk, a.hkv, D, BR, a.hdr) &&
+                            make_rows_map(&mu, a.q, a.Tq, a.hq, D, BC, a.hdr) && make_rows_map(&mw, a.dout, a.Tq, a.hq, D, BC, a.hdr)
+                      : make_rows_map(&mx, a.q, a.Tq, a.hq, D, BR, a.hdr) && make_rows_map(&my, a.dout, a.Tq, a.hq, D, BR, a.hdr) &&
+                            make_rows_map(&mu, a.k, a.Tk, a.hkv, D, BC, a.hdr) && make_rows_map(&mw, a.v, a.Tk, a.hkv, D, BC, a.hdr);
   if (!ok) return false;
   // dk, dv: N more items, the sequences' first blocks ahead of the others
   const int64_t blocks = item_count(DKV ? a.Tk : a.Tq, BR, a.N);

@@ -418,8 +418,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <int D>
 bool fwd_tc(const WindowAttn& a, cudaStream_t st) {
   CUtensorMap mq, mk, mv;
-  if (!make_rows_map(&mq, a.q, a.Tq, a.hq, D, BM) || !make_rows_map(&mk, a.k, a.Tk, a.hkv, D, BN) ||
-      !make_rows_map(&mv, a.v, a.Tk, a.hkv, D, BN))
+  if (!make_rows_map(&mq, a.q, a.Tq, a.hq, D, BM, a.hdr) || !make_rows_map(&mk, a.k, a.Tk, a.hkv, D, BN, a.hdr) ||
+      !make_rows_map(&mv, a.v, a.Tk, a.hkv, D, BN, a.hdr))
     return false;
   const int64_t items = item_count(a.Tq, 2 * BM, a.N), work = items * a.hq;
   static std::atomic<uint64_t> ready{0};
@@ -436,7 +436,7 @@ bool fwd_tc(const WindowAttn& a, cudaStream_t st) {
 
 }  // namespace
 
-bool make_rows_map(CUtensorMap* map, const void* base, int T, int H, int d, int rows) {
+bool make_rows_map(CUtensorMap* map, const void* base, int T, int H, int d, int rows, const void* any) {
   using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
                               const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
                               CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -450,6 +450,7 @@ bool make_rows_map(CUtensorMap* map, const void* base, int T, int H, int d, int 
       encode = reinterpret_cast<Encode>(f);
   });
   if (!encode) return false;
+  if (T == 0) base = any, T = 1;
   const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)H, (cuuint64_t)T};
   const cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)H * d * 2};
   const cuuint32_t box[3] = {64, 1, (cuuint32_t)rows}, step[3] = {1, 1, 1};

@@ -110,6 +110,19 @@ def test_other_sequences_do_not_matter(attn, dtype, d):
             assert torch.equal(alone[n], dirty[n][a:b]), (n, junk)
 
 
+@pytest.mark.parametrize("dtype,d", [(BF, 128), (BF, 64), (BF, 32), (F32, 128), (F32, 32)])
+def test_batch_size_does_not_change_bits(attn, dtype, d):
+    """A sequence alone and among many (which may choose other tiles and schedules)."""
+    lens = [150] * 20 + [333] * 40
+    x = make(lens, lens, 4, 2, d, dtype)
+    got = run(attn, x, window=90, sinks=3)
+    for s, (a, b) in {3: (450, 600), 30: (3000 + 10 * 333, 3000 + 11 * 333)}.items():
+        one = {n: x[n][a:b] for n in ("q", "k", "v", "do")} | dict(cq=cu([b - a]), ck=cu([b - a]))
+        alone = run(attn, one, window=90, sinks=3)
+        for n in alone:
+            assert torch.equal(alone[n], got[n][a:b]), (n, s)
+
+
 @pytest.mark.parametrize("dtype,d", [(BF, 128), (F32, 64)])
 def test_repeatable_and_on_another_stream(attn, dtype, d):
     x = make([500, 260], [500, 260], 6, 2, d, dtype)
@@ -163,3 +176,5 @@ def test_nothing_to_do(attn, gdn):
         assert got["out"].numel() == 0 and got["dk"].numel() == 0
         got = run(attn, make([0, 0], [10, 0], 2, 1, d, dtype))
         assert (got["dk"] == 0).all() and (got["dv"] == 0).all()
+        got = run(attn, make([5, 0], [0, 0], 2, 1, d, dtype))
+        assert (got["out"] == 0).all() and (got["dq"] == 0).all() and (got["lse"] == -float("inf")).all()
