@@ -69,23 +69,26 @@ __host__ __device__ inline int visible_keys(int len, int window, int sinks) {
 // request's result does not depend on the batch: about kRunsPerRequest runs over a request's heads,
 // of 64 to 512 keys, evened out and a multiple of 32 (a tile).
 constexpr int kRunsPerRequest = 32;
-__host__ __device__ inline int target_keys(int n, int hkv) {
-  const int64_t x = (int64_t)n * hkv / kRunsPerRequest;
-  return x < 128 ? 64 : x < 256 ? 128 : x < 512 ? 256 : 512;
+__host__ __device__ inline int target_shift(int n, int hkv) {
+  const int64_t x = (int64_t)n * hkv;
+  return x < 128 * kRunsPerRequest ? 6 : x < 256 * kRunsPerRequest ? 7 : x < 512 * kRunsPerRequest ? 8 : 9;
 }
 __host__ __device__ inline int target_runs(int n, int hkv) {
-  const int t = target_keys(n, hkv), r = (n + t / 2) / t;
+  const int s = target_shift(n, hkv), r = (n + (1 << s >> 1)) >> s;
   return r < 1 ? 1 : r;
 }
-__host__ __device__ inline int split_keys(int n, int hkv) {
-  const int r = target_runs(n, hkv);
-  return ((n + r - 1) / r + 31) / 32 * 32;
-}
-__host__ __device__ inline int split_count(int n, int hkv) {
-  return n == 0 ? 0 : (n + split_keys(n, hkv) - 1) / split_keys(n, hkv);
+struct Split {
+  int keys, runs;  // of a run, of a request
+};
+__host__ __device__ inline Split split_of(int n, int hkv) {
+  const unsigned r = (unsigned)target_runs(n, hkv);
+  Split s;
+  s.keys = (int)((((unsigned)n + r - 1) / r + 31) / 32 * 32);
+  s.runs = n == 0 ? 0 : (int)(((unsigned)n + s.keys - 1) / (unsigned)s.keys);
+  return s;
 }
 int paged_decode_max_splits(int max_visible, int hkv);
-void launch_paged_decode(const PagedDecode& a, bool bf16, cudaStream_t st);
+int launch_paged_decode(const PagedDecode& a, bool bf16, cudaStream_t st);
 
 // -------------------------------------------------------------- window attention ----
 struct WindowAttn {

@@ -2,7 +2,7 @@
 //
 // A request's visible keys (the first `sinks` and the last `window`, or all) are numbered
 // u = 0 .. n - 1 in key order, so that masks never cut a tile: only its end is short.  They are
-// split into runs of split_keys(n, key heads); one warp takes a run of one key head for up to 16
+// split into runs of split_of(n, key heads); one warp takes a run of one key head for up to 16
 // of its query heads in one pass with a running maximum (scores in units of log2 e, so that
 // e^x is one exp2):
 //     s_u = scale q . k_u,  m = max s,  l = sum e^(s - m),  a = sum e^(s - m) v_u
@@ -368,66 +368,69 @@ struct MmaEngine {
 template <typename E>
 struct Walk {
   static constexpr int STAGE = 2 * E::KEYS * E::ROWB;
-  int64_t next, total;  // where the search for the next run goes on; all (request, part, run)
-  int cand_len;         // length of the request of candidate next + lane * (warps of the grid)
-  Run r;                // the run being fetched
-  bool live;            // there is one
-  uint32_t row;         // lane < KEYS: row of key r.u + lane (~0: none, or past the run's end)
+  // (run, request, part) slots are numbered with the run slowest and dealt out in chunks of `chunk`
+  // <= 32 consecutive ones, one per lane: the first by the warp's number, further ones from a
+  // counter, as runs differ in length and many slots of short requests are empty.
+  uint32_t total, chunk;
+  int32_t* counter;
+  uint32_t base;                 // the chunk after the present one, looked up a run ahead of its use:
+  int next_i, next_y, next_run;  // this lane's slot of it (next_run < 0: none)
+  int next_len;                  // and its request's length
+  uint32_t left;                 // slots of the present chunk that hold a run and are still to come
+  Run mine;                      // this lane's run of it
+  Run r;                         // the run being fetched
+  bool live;                     // there is one
+  uint32_t row;                  // lane < KEYS: row of key r.u + lane (~0: none, or past the run's end)
 
-  __device__ __forceinline__ int64_t candidate(int lane) const {
-    return next + (int64_t)lane * (gridDim.x * E::WARPS);
-  }
-  // the candidates' lengths, read a run ahead of their use
-  __device__ __forceinline__ void look_ahead(const PagedDecode& a, int64_t rows, int parts, int lane) {
-    const int64_t w = candidate(lane);
-    if (w < total) cand_len = a.seq_lens[(int)(w % rows / (a.hkv * parts))];
+  __device__ __forceinline__ void look_ahead(const PagedDecode& a, int parts, int lane) {
+    const uint32_t w = base + (uint32_t)lane, ny = (uint32_t)(a.hkv * parts), rows = (uint32_t)a.N * ny;
+    next_run = -1;
+    if (w >= total || lane >= (int)chunk) return;
+    next_run = (int)(w / rows);
+    const uint32_t v = w - (uint32_t)next_run * rows;
+    next_i = (int)(v / ny);
+    next_y = (int)(v - (uint32_t)next_i * ny);
+    next_len = a.seq_lens[next_i];
   }
 
-  // The next run of this warp from `next` on, 32 candidates at a time.  Requests without keys have
-  // their rows written here.
+  // The next run of this warp.  Requests without keys have their rows written here.
   __device__ void seek(const PagedDecode& a, int parts, int lane) {
-    const int64_t rows = (int64_t)a.N * a.hkv * parts;
     live = false;
-    while (next < total) {
-      const int64_t w = candidate(lane);
+    while (!left) {
+      if (base >= total) return;
       bool have = false;
-      Run c{};
-      if (w < total) {
-        c.run = (int)(w / rows);  // slowest, so that the places short requests leave empty come last
-        c.y = (int)(w % rows % (a.hkv * parts));
-        c.i = (int)(w % rows / (a.hkv * parts));
-        const Request rq(a, cand_len);
-        c.runs = split_count(rq.n, a.hkv);
-        if (c.run < c.runs) {
-          const int per = split_keys(rq.n, a.hkv);
-          c.u = c.run * per;
-          c.end = min(rq.n, c.u + per);
-          c.head = rq.head;
-          c.skip = rq.skip;
-          have = true;
-        } else if (c.runs == 0 && c.run == 0) {
-          write_empty(a, c, parts, rq.bad);
-        }
+      if (next_run >= 0) {
+        const Request rq(a, next_len);
+        const Split s = split_of(rq.n, a.hkv);
+        mine.i = next_i;
+        mine.y = next_y;
+        mine.run = next_run;
+        mine.runs = s.runs;
+        have = next_run < s.runs;
+        mine.u = next_run * s.keys;
+        mine.end = min(rq.n, mine.u + s.keys);
+        mine.head = rq.head;
+        mine.skip = rq.skip;
+        if (s.runs == 0 && next_run == 0) write_empty(a, mine, parts, rq.bad);
       }
-      const uint32_t any = __ballot_sync(0xffffffffu, have);
-      if (any) {
-        const int src = __ffs(any) - 1;
-        r.i = __shfl_sync(0xffffffffu, c.i, src);
-        r.y = __shfl_sync(0xffffffffu, c.y, src);
-        r.run = __shfl_sync(0xffffffffu, c.run, src);
-        r.runs = __shfl_sync(0xffffffffu, c.runs, src);
-        r.u = __shfl_sync(0xffffffffu, c.u, src);
-        r.end = __shfl_sync(0xffffffffu, c.end, src);
-        r.head = __shfl_sync(0xffffffffu, c.head, src);
-        r.skip = __shfl_sync(0xffffffffu, c.skip, src);
-        next += (int64_t)(src + 1) * (gridDim.x * E::WARPS);
-        live = true;
-        look_ahead(a, rows, parts, lane);
-        return;
-      }
-      next += 32 * (int64_t)(gridDim.x * E::WARPS);
-      look_ahead(a, rows, parts, lane);
+      left = __ballot_sync(0xffffffffu, have);
+      int n = 0;
+      if (!counter) base = total;
+      else if (lane == 0) n = atomicAdd(counter, 1);
+      if (counter) base = (gridDim.x * E::WARPS + (uint32_t)__shfl_sync(0xffffffffu, n, 0)) * chunk;
+      look_ahead(a, parts, lane);
     }
+    const int src = __ffs(left) - 1;
+    left &= left - 1;
+    r.i = __shfl_sync(0xffffffffu, mine.i, src);
+    r.y = __shfl_sync(0xffffffffu, mine.y, src);
+    r.run = __shfl_sync(0xffffffffu, mine.run, src);
+    r.runs = __shfl_sync(0xffffffffu, mine.runs, src);
+    r.u = __shfl_sync(0xffffffffu, mine.u, src);
+    r.end = __shfl_sync(0xffffffffu, mine.end, src);
+    r.head = __shfl_sync(0xffffffffu, mine.head, src);
+    r.skip = __shfl_sync(0xffffffffu, mine.skip, src);
+    live = true;
   }
 
   // zeros for a request without keys, NaN for a length that is not valid; one lane
@@ -508,7 +511,7 @@ struct DecodeSmem {
 };
 
 template <typename E>
-__global__ void __launch_bounds__(32 * E::WARPS) k_decode(const PagedDecode a, const int parts) {
+__global__ void __launch_bounds__(32 * E::WARPS) k_decode(const PagedDecode a, const int parts, const uint32_t chunk, int32_t* counter) {
   using L = DecodeSmem<E>;
   extern __shared__ __align__(128) unsigned char all[];
   unsigned char* sh = all + (threadIdx.x >> 5) * L::WARP;
@@ -518,10 +521,14 @@ __global__ void __launch_bounds__(32 * E::WARPS) k_decode(const PagedDecode a, c
   Run* queue = reinterpret_cast<Run*>(sh + L::QUEUE);
   const uint32_t ring = tc::smem_u32(sh);
   Walk<E> f;
-  f.next = (int64_t)blockIdx.x * E::WARPS + (threadIdx.x >> 5);
-  f.total = (int64_t)a.N * a.hkv * parts * a.max_splits;
+  f.total = (uint32_t)(a.N * a.hkv * parts * a.max_splits);
+  f.chunk = chunk;
+  f.counter = counter;
+  f.base = (blockIdx.x * E::WARPS + (threadIdx.x >> 5)) * chunk;
+  f.left = 0;
   int head = 0, tail = 0, put = 0, get = 0;
-  f.look_ahead(a, (int64_t)a.N * a.hkv * parts, parts, lane);
+  f.look_ahead(a, parts, lane);
+  if (counter) asm volatile("griddepcontrol.wait;" ::: "memory");  // it has been cleared
   f.seek(a, parts, lane);
   if (f.live) f.push(a, parts, queue, tail, lane);
   f.look_up(a, parts, lane, queue, tail);
@@ -538,13 +545,14 @@ __global__ void __launch_bounds__(32 * E::WARPS) k_decode(const PagedDecode a, c
     const int h0 = (r.y / parts) * group + g0;
     eng.start(a, (int64_t)r.i * a.hq + h0, heads, sh + L::EXTRA, lane);
     for (; r.u < r.end; r.u += E::KEYS) {
-      asm volatile("cp.async.wait_group %0;" ::"n"(E::RING - 2) : "memory");
+      // the next tile on its way first, into the place that every lane has read
+      f.fetch(a, parts, ring + put * L::STAGE, lane, queue, tail);
+      put = put + 1 == E::RING ? 0 : put + 1;
+      asm volatile("cp.async.wait_group %0;" ::"n"(E::RING - 1) : "memory");
       __syncwarp();
       eng.tile(a, sh + get * L::STAGE, r.end - r.u, lane);
       get = get + 1 == E::RING ? 0 : get + 1;
-      __syncwarp();  // every lane has read the ring place that is filled next
-      f.fetch(a, parts, ring + put * L::STAGE, lane, queue, tail);
-      put = put + 1 == E::RING ? 0 : put + 1;
+      __syncwarp();
     }
     __syncwarp();
     eng.finish(Sink(a, r, h0, heads, sizeof(typename E::Elem)), queue[head & 3].bad != 0, lane);
@@ -564,14 +572,27 @@ __global__ void __launch_bounds__(128) k_decode_join(const PagedDecode a, const 
   constexpr int LANES = D / 4, GROUPS = 128 / LANES, B = 8;
   __shared__ float4 so[GROUPS][LANES];
   __shared__ float2 sml[GROUPS];
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the runs' kernel has finished
+  // what does not come from the runs' kernel is read while that still runs
   const int g = threadIdx.x / LANES, lane = threadIdx.x % LANES, c = 4 * lane;
   const int i = blockIdx.y, h = split ? blockIdx.x : blockIdx.x * GROUPS + g;
   const Request rq(a, a.seq_lens[i]);
-  const int runs = split_count(rq.n, a.hkv);
+  const int runs = split_of(rq.n, a.hkv).runs;
   const bool shared = runs > 32;  // only with `split`
   const int per = shared ? (runs + GROUPS - 1) / GROUPS : runs;
   const int begin = shared ? min(runs, g * per) : 0, end = shared ? min(runs, begin + per) : runs;
+  bool lost = false;  // a page of the request's visible keys is outside the cache
+  if (rq.n) {
+    const int first = rq.key(rq.head) >> a.page_shift, last = (rq.len - 1) >> a.page_shift;
+    const int head_pages = rq.head ? ((rq.head - 1) >> a.page_shift) + 1 : 0;
+    for (int b = blockIdx.x * 128 + threadIdx.x; b < head_pages + last - first + 1; b += gridDim.x * 128) {
+      const int p = b < head_pages ? b : first + b - head_pages;
+      const int page = p < a.max_blocks ? a.block_table[(int64_t)i * a.max_blocks + p] : -1;
+      lost |= page < 0 || page >= a.num_pages;
+    }
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the runs' kernel has finished
+  if (rq.bad && threadIdx.x == 0) set_error(a.hdr, GDN_DEVERR_POS);
+  if (lost) set_error(a.hdr, GDN_DEVERR_PAGES);
   if (runs > 1 && h < a.hq && (shared || !split || g == 0)) {
     const int64_t row = (int64_t)i * a.hq + h;
     const float* rec = a.partial + row * a.max_splits * D + c;
@@ -629,19 +650,16 @@ __global__ void __launch_bounds__(128) k_decode_join(const PagedDecode a, const 
       if (a.lse && c == 0) a.lse[row] = __fmul_rn(__fadd_rn(m, log2f(l)), kLn2);
     }
   }
-  if (rq.bad && threadIdx.x == 0) set_error(a.hdr, GDN_DEVERR_POS);
-  if (rq.n == 0) return;
-  const int first = rq.key(rq.head) >> a.page_shift, last = (rq.len - 1) >> a.page_shift;
-  const int head_pages = rq.head ? ((rq.head - 1) >> a.page_shift) + 1 : 0;
-  for (int b = blockIdx.x * 128 + threadIdx.x; b < head_pages + last - first + 1; b += gridDim.x * 128) {
-    const int p = b < head_pages ? b : first + b - head_pages;
-    const int page = p < a.max_blocks ? a.block_table[(int64_t)i * a.max_blocks + p] : -1;
-    if (page < 0 || page >= a.num_pages) set_error(a.hdr, GDN_DEVERR_PAGES);
-  }
+}
+
+// The counter of a call whose warps take more than one chunk; the runs' kernel starts beside this.
+__global__ void k_decode_clear(int32_t* counter) {
+  asm volatile("griddepcontrol.launch_dependents;");
+  *counter = 0;
 }
 
 template <typename E>
-void launch_decode(const PagedDecode& a, cudaStream_t st) {
+int launch_decode(const PagedDecode& a, cudaStream_t st) {
   constexpr int D = E::DIM, BYTES = DecodeSmem<E>::BYTES;
   static std::atomic<uint64_t> ready{0};
   ensure_smem(k_decode<E>, BYTES, ready);
@@ -652,38 +670,52 @@ void launch_decode(const PagedDecode& a, cudaStream_t st) {
   }();
   const int group = a.hq / a.hkv, parts = (group + kHeadsPerRun - 1) / kHeadsPerRun;
   const int64_t total = (int64_t)a.N * a.hkv * parts * a.max_splits, most = (int64_t)kSms * per_sm;
-  const int64_t need = (total + E::WARPS - 1) / E::WARPS;
-  k_decode<E><<<(unsigned)(need < most ? need : most), 32 * E::WARPS, BYTES, st>>>(a, parts);
+  const int64_t need = (total + E::WARPS - 1) / E::WARPS, ctas = need < most ? need : most, warps = ctas * E::WARPS;
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t c{};
+  c.stream = st;
+  c.attrs = &attr;
+  c.numAttrs = 0;
+  int32_t* counter = nullptr;
+  if (total > warps) {
+    counter = a.hdr->pad;
+    k_decode_clear<<<1, 1, 0, st>>>(counter);
+    c.numAttrs = 1;
+  }
+  // about eight chunks a warp, of single slots unless there are many
+  const int64_t chunk = total / (8 * warps);
+  c.gridDim = dim3((unsigned)ctas);
+  c.blockDim = dim3(32 * E::WARPS);
+  c.dynamicSmemBytes = BYTES;
+  cudaLaunchKernelEx(&c, k_decode<E>, a, parts, (uint32_t)(chunk < 1 ? 1 : chunk > 32 ? 32 : chunk), counter);
   const bool split = a.max_splits > 32;
   c.gridDim = dim3(split ? a.hq : (a.hq + 512 / D - 1) / (512 / D), a.N);
   c.blockDim = dim3(128);
-  c.stream = st;
-  c.attrs = &attr;
+  c.dynamicSmemBytes = 0;
   c.numAttrs = 1;
   cudaLaunchKernelEx(&c, k_decode_join<D, typename E::Elem>, a, split);
+  return counter ? 3 : 2;
 }
 
 template <int D, typename T>
-void decode_t(const PagedDecode& a, cudaStream_t st) {
+int decode_t(const PagedDecode& a, cudaStream_t st) {
   const int group = a.hq / a.hkv;
   if constexpr (D >= 64 && sizeof(T) == 2) {
-    launch_decode<MmaEngine<D>>(a, st);
+    return launch_decode<MmaEngine<D>>(a, st);
   } else {
-    if (group <= 2) launch_decode<SimtEngine<D, T, 2, 1>>(a, st);
-    else if (group <= 4) launch_decode<SimtEngine<D, T, 4, 1>>(a, st);
-    else if (group <= 8) launch_decode<SimtEngine<D, T, 4, 2>>(a, st);
-    else launch_decode<SimtEngine<D, T, 4, 4>>(a, st);
+    if (group <= 2) return launch_decode<SimtEngine<D, T, 2, 1>>(a, st);
+    if (group <= 4) return launch_decode<SimtEngine<D, T, 4, 1>>(a, st);
+    if (group <= 8) return launch_decode<SimtEngine<D, T, 4, 2>>(a, st);
+    return launch_decode<SimtEngine<D, T, 4, 4>>(a, st);
   }
 }
 
 }  // namespace
 
 // A bound on the runs of any request that sees at most `max_visible` keys: target_runs grows with n
-// between the lengths where target_keys changes, and split_count is at most target_runs.
+// between the lengths where target_shift changes, and a request has at most target_runs runs.
 int paged_decode_max_splits(int max_visible, int hkv) {
   int best = 1;
   for (const int64_t x : {128, 256, 512, 0}) {
@@ -694,15 +726,15 @@ int paged_decode_max_splits(int max_visible, int hkv) {
   return best;
 }
 
-void launch_paged_decode(const PagedDecode& a, bool bf16, cudaStream_t st) {
+int launch_paged_decode(const PagedDecode& a, bool bf16, cudaStream_t st) {
   if (bf16) {
-    if (a.d == 32) decode_t<32, __nv_bfloat16>(a, st);
-    else if (a.d == 64) decode_t<64, __nv_bfloat16>(a, st);
-    else decode_t<128, __nv_bfloat16>(a, st);
+    if (a.d == 32) return decode_t<32, __nv_bfloat16>(a, st);
+    if (a.d == 64) return decode_t<64, __nv_bfloat16>(a, st);
+    return decode_t<128, __nv_bfloat16>(a, st);
   } else {
-    if (a.d == 32) decode_t<32, float>(a, st);
-    else if (a.d == 64) decode_t<64, float>(a, st);
-    else decode_t<128, float>(a, st);
+    if (a.d == 32) return decode_t<32, float>(a, st);
+    if (a.d == 64) return decode_t<64, float>(a, st);
+    return decode_t<128, float>(a, st);
   }
 }
 

@@ -293,6 +293,9 @@ gdn_status gdn_cpr_paged_decode(const gdn_cpr_attn* attn, int32_t num_seqs, int3
   if (num_seqs > 0 && num_pages > 0 && (!ok_ptr(k_pages, 16) || !ok_ptr(v_pages, 16))) return GDN_ERR_INVALID_ARG;
   if (num_seqs > 0 && max_blocks > 0 && !ok_ptr(block_table, 4)) return GDN_ERR_INVALID_ARG;
   const int splits = decode_splits(attn, max_len);
+  // runs are numbered in 32 bits (at most 16 query heads of a key head to one)
+  const int64_t parts = (attn->h_q / attn->h_kv + 15) / 16;
+  if ((double)num_seqs * attn->h_kv * parts * splits >= (double)(1 << 30)) return GDN_ERR_UNSUPPORTED;
   if (!ok_ws(ws, ws_bytes, decode_bytes(attn, num_seqs, splits))) return GDN_ERR_WORKSPACE;
   if (num_seqs == 0) return GDN_OK;
   PagedDecode a{};
@@ -318,8 +321,7 @@ gdn_status gdn_cpr_paged_decode(const gdn_cpr_attn* attn, int32_t num_seqs, int3
   a.max_splits = splits;
   a.hdr = static_cast<WsHeader*>(ws);
   Stages stg(stream, kPagedStages);
-  launch_paged_decode(a, attn->dtype == GDN_BF16, stream);
-  stg.mark(2);
+  stg.mark(launch_paged_decode(a, attn->dtype == GDN_BF16, stream));
   return finish();
 }
 
