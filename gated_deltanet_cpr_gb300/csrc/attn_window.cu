@@ -46,6 +46,28 @@ __device__ __forceinline__ void load_tile(float* tile, const void* src, int64_t 
   }
 }
 
+// The next column tile on its way in registers while the present one is worked on.
+template <int D, typename T>
+struct NextTile {
+  static constexpr int V = D / 4, N = 64 * V / kThreads;
+  float4 x[N];
+  __device__ __forceinline__ void fetch(const void* src, int64_t base, int row0, int end, int H, int h) {
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const int e = k * kThreads + threadIdx.x, r = e / V, c = 4 * (e % V);
+      x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (row0 + r < end) x[k] = load4(static_cast<const T*>(src) + ((base + row0 + r) * H + h) * D + c);
+    }
+  }
+  __device__ __forceinline__ void put(float* tile) const {
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const int e = k * kThreads + threadIdx.x;
+      *reinterpret_cast<float4*>(tile + (e / V) * pitch<D>() + 4 * (e % V)) = x[k];
+    }
+  }
+};
+
 // x[r][c] = a_row(R ty + r) . b_row(16 c + tx)
 template <int D, int R>
 __device__ __forceinline__ void rows_dot(const float* A, const float* B, int ty, int tx, float (&x)[R][4]) {
@@ -170,12 +192,21 @@ __global__ void __launch_bounds__(kThreads) k_window_fwd(const WindowAttn a) {
   o.zero();
 #pragma unroll
   for (int r = 0; r < R; ++r) m[r] = -INFINITY, l[r] = 0.f;
+  NextTile<D, T> kn, vn;
+  if (kb.count()) {
+    kn.fetch(a.k, q.k0, kb.block(0) * BN, q.Lk, a.hkv, kvh);
+    vn.fetch(a.v, q.k0, kb.block(0) * BN, q.Lk, a.hkv, kvh);
+  }
   for (int b = 0; b < kb.count(); ++b) {
     const int j0 = kb.block(b) * BN;
     __syncthreads();
-    load_tile<D, T, BN>(Ks, a.k, q.k0, j0, q.Lk, a.hkv, kvh);
-    load_tile<D, T, BN>(Vs, a.v, q.k0, j0, q.Lk, a.hkv, kvh);
+    kn.put(Ks);
+    vn.put(Vs);
     __syncthreads();
+    if (b + 1 < kb.count()) {
+      kn.fetch(a.k, q.k0, kb.block(b + 1) * BN, q.Lk, a.hkv, kvh);
+      vn.fetch(a.v, q.k0, kb.block(b + 1) * BN, q.Lk, a.hkv, kvh);
+    }
     float x[R][4];
     rows_dot<D, R>(Qs, Ks, ty, tx, x);
 #pragma unroll
@@ -279,12 +310,21 @@ __global__ void __launch_bounds__(kThreads) k_window_dq(const WindowAttn a) {
       if (tx == 0) a.delta[at] = delta[r];
     }
   }
+  NextTile<D, T> kn, vn;
+  if (kb.count()) {
+    kn.fetch(a.k, q.k0, kb.block(0) * BN, q.Lk, a.hkv, kvh);
+    vn.fetch(a.v, q.k0, kb.block(0) * BN, q.Lk, a.hkv, kvh);
+  }
   for (int b = 0; b < kb.count(); ++b) {
     const int j0 = kb.block(b) * BN;
     __syncthreads();
-    load_tile<D, T, BN>(Ks, a.k, q.k0, j0, q.Lk, a.hkv, kvh);
-    load_tile<D, T, BN>(Vs, a.v, q.k0, j0, q.Lk, a.hkv, kvh);
+    kn.put(Ks);
+    vn.put(Vs);
     __syncthreads();
+    if (b + 1 < kb.count()) {
+      kn.fetch(a.k, q.k0, kb.block(b + 1) * BN, q.Lk, a.hkv, kvh);
+      vn.fetch(a.v, q.k0, kb.block(b + 1) * BN, q.Lk, a.hkv, kvh);
+    }
     float x[R][4], y[R][4];
     rows_dot<D, R>(Qs, Ks, ty, tx, x);
     rows_dot<D, R>(Os, Vs, ty, tx, y);
@@ -320,37 +360,50 @@ __global__ void __launch_bounds__(kThreads) k_window_dkv(const WindowAttn a) {
   Acc<D, R> dk, dv;
   dk.zero();
   dv.zero();
-  for (int g = 0; g < group; ++g) {
-    const int h = kvh * group + g;
-    for (int b = b0; b < b1; ++b) {
-      const int row0 = b * BN;
-      __syncthreads();
-      load_tile<D, T, BN>(Qs, a.q, q.q0, row0, q.Lq, a.hq, h);
-      load_tile<D, T, BN>(Os, a.dout, q.q0, row0, q.Lq, a.hq, h);
-      __syncthreads();
-      int pos[4];
-      float lse2[4], delta[4], x[R][4], y[R][4];
+  // column tiles: the query blocks of the group's heads, one head after the other
+  const int nb = b1 - b0, tiles = nb * group;
+  NextTile<D, T> qn, on;
+  float lse_n[4], delta_n[4];  // of the thread's columns
+  auto fetch = [&](int i) {
+    const int h = kvh * group + i / nb, row0 = (b0 + i % nb) * BN;
+    qn.fetch(a.q, q.q0, row0, q.Lq, a.hq, h);
+    on.fetch(a.dout, q.q0, row0, q.Lq, a.hq, h);
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const int row = row0 + 16 * c + tx;
-        pos[c] = row + off;
-        lse2[c] = -INFINITY;
-        delta[c] = 0.f;
-        if (row < q.Lq) {
-          const int64_t at = (int64_t)(q.q0 + row) * a.hq + h;
-          lse2[c] = __fmul_rn(a.lse[at], kLog2e);
-          delta[c] = a.delta[at];
-        }
+    for (int c = 0; c < 4; ++c) {
+      const int row = row0 + 16 * c + tx;
+      lse_n[c] = -INFINITY;
+      delta_n[c] = 0.f;
+      if (row < q.Lq) {
+        const int64_t at = (int64_t)(q.q0 + row) * a.hq + h;
+        lse_n[c] = a.lse[at];
+        delta_n[c] = a.delta[at];
       }
-      rows_dot<D, R>(Ks, Qs, ty, tx, x);  // transposed: rows are keys
-      rows_dot<D, R>(Vs, Os, ty, tx, y);
-      grad_scores<R>(a, sc, pos, key, lse2, delta, false, x, y);
-      put_doubled<R>(Ps, ty, tx, x);
-      put_doubled<R>(Ds, ty, tx, y);
-      __syncwarp();
-      dv.add(Ps, Os, ty, tx);
-      dk.add(Ds, Qs, ty, tx);
     }
+  };
+  if (tiles) fetch(0);
+  for (int i = 0; i < tiles; ++i) {
+    const int row0 = (b0 + i % nb) * BN;
+    __syncthreads();
+    qn.put(Qs);
+    on.put(Os);
+    int pos[4];
+    float lse2[4], delta[4], x[R][4], y[R][4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      pos[c] = row0 + 16 * c + tx + off;
+      lse2[c] = __fmul_rn(lse_n[c], kLog2e);
+      delta[c] = delta_n[c];
+    }
+    __syncthreads();
+    if (i + 1 < tiles) fetch(i + 1);
+    rows_dot<D, R>(Ks, Qs, ty, tx, x);  // transposed: rows are keys
+    rows_dot<D, R>(Vs, Os, ty, tx, y);
+    grad_scores<R>(a, sc, pos, key, lse2, delta, false, x, y);
+    put_doubled<R>(Ps, ty, tx, x);
+    put_doubled<R>(Ds, ty, tx, y);
+    __syncwarp();
+    dv.add(Ps, Os, ty, tx);
+    dk.add(Ds, Qs, ty, tx);
   }
   float one[R], f[R];
 #pragma unroll
