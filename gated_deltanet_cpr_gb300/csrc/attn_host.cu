@@ -33,6 +33,8 @@ gdn_status check_norm(const gdn_cpr_norm_rope* c) {
     return GDN_ERR_INVALID_ARG;
   if (!(c->eps >= 0.f) || !isfinite(c->eps)) return GDN_ERR_INVALID_ARG;
   if (c->h_q > 65535 || c->h_k > 65535 || !ok_d(c->d)) return GDN_ERR_UNSUPPORTED;
+  // blocks are numbered in 31 bits
+  if ((int64_t)c->tokens * (c->h_q + 2 * (int64_t)c->h_k) > (int64_t)INT32_MAX) return GDN_ERR_UNSUPPORTED;
   if (c->rot > c->d || c->rot % 8 != 0) return GDN_ERR_UNSUPPORTED;
   if (c->norm != GDN_NORM_NONE && c->norm != GDN_NORM_RMS && c->norm != GDN_NORM_L2) return GDN_ERR_UNSUPPORTED;
   if (c->layout != GDN_ROPE_HALF && c->layout != GDN_ROPE_INTERLEAVED) return GDN_ERR_UNSUPPORTED;
@@ -183,7 +185,9 @@ gdn_status gdn_cpr_qk_norm_rope_workspace_size(const gdn_cpr_norm_rope* cfg, siz
   if (!bytes) return GDN_ERR_INVALID_ARG;
   const gdn_status rc = check_norm(cfg);
   if (rc != GDN_OK) return rc;
-  *bytes = align_up((size_t)kNormBwdBlocks * 2 * cfg->d * sizeof(float));
+  // one row of d sums per block: at most kNormBwdBlocks, or one per run of heads (of 8 or more)
+  const size_t runs = (size_t)(cfg->h_q + 3) / 4 + (size_t)(cfg->h_k + 3) / 4;
+  *bytes = align_up((runs > kNormBwdBlocks ? runs : kNormBwdBlocks) * cfg->d * sizeof(float));
   return GDN_OK;
 }
 

@@ -12,9 +12,9 @@ namespace {
 // a lane of the rotated part holds pieces at A and A + rot / 2, one of the rest at A and
 // A + (D - rot) / 2.  The interleaved layout's pairs lie within a piece.  So the rotation needs no
 // exchange, and the norm log2(LPR) shuffles.  A warp holds GPW = 32 / LPR rows at a time and U of
-// these at once (their loads are issued together).  A work item is one token and U * GPW heads of
-// q, of k or of v, so that nothing inside depends on which it is, and the few rows of a decode step
-// spread over warps.  With two pieces a lane the kernel issues half the instructions per row that one
+// these at once (their loads are issued together).  A warp takes one token's U * GPW heads of q, of
+// k or of v, so that nothing inside depends on which it is, and the few rows of
+// a decode step spread over warps.  With two pieces a lane the kernel issues half the instructions per row that one
 // piece costs, and packed pairs halve the arithmetic again; before both it was bound by issue
 // (202 us for 16384 tokens of 32 / 8 heads, d = 128, with the cache written).
 // =====================================================================================
@@ -142,36 +142,32 @@ __device__ __forceinline__ void angles_of(const NormRope& a, int64_t row, float 
   }
 }
 
-// Item -> token, which of q (0), k (1), v (2), and the first head.
-struct NormItem {
-  int64_t t;
+// A run of RUN heads: which of q (0), k (1), v (2), and its first head.
+struct HeadRun {
   int kind, h0, heads;
 };
 template <int RUN>
-__host__ __device__ __forceinline__ int norm_items(int hq, int hk, int hv) {
+int head_runs(int hq, int hk, int hv) {
   return (hq + RUN - 1) / RUN + (hk + RUN - 1) / RUN + (hv + RUN - 1) / RUN;
 }
 template <int RUN>
-__device__ __forceinline__ NormItem norm_item(const NormRope& a, int64_t item, int per) {
-  NormItem r;
-  r.t = item / per;
-  int c = (int)(item - r.t * per);
+__device__ __forceinline__ HeadRun head_run(const NormRope& a, int c) {
   const int nq = (a.hq + RUN - 1) / RUN, nk = (a.hk + RUN - 1) / RUN;
+  HeadRun r;
   r.kind = c < nq ? 0 : c < nq + nk ? 1 : 2;
-  c -= r.kind == 0 ? 0 : r.kind == 1 ? nq : nq + nk;
-  r.h0 = c * RUN;
+  r.h0 = (c - (r.kind == 0 ? 0 : r.kind == 1 ? nq : nq + nk)) * RUN;
   r.heads = r.kind == 0 ? a.hq : a.hk;
   return r;
 }
 
 template <int D, typename TI, typename TO, int U>
-__global__ void __launch_bounds__(kNormThreads, U > 1 ? 8 : 1) k_norm_rope(const NormRope a, const int per) {
+__global__ void __launch_bounds__(kNormThreads, U > 1 ? 8 : 1) k_norm_rope(const NormRope a, const int runs) {
   constexpr int LPR = RowLanes<D>::LPR, GPW = RowLanes<D>::GPW;
   const int lane = threadIdx.x & 31;
-  const int64_t item = (int64_t)blockIdx.x * (kNormThreads / 32) + (threadIdx.x >> 5);
-  if (item >= (int64_t)a.T * per) return;
-  const NormItem it = norm_item<U * GPW>(a, item, per);
-  const int64_t t = it.t;
+  // a token's runs of heads in neighbouring blocks: their rows are neighbours in memory
+  const int64_t t = (int64_t)(blockIdx.x / runs) * (kNormThreads / 32) + (threadIdx.x >> 5);
+  if (t >= a.T) return;
+  const HeadRun it = head_run<U * GPW>(a, blockIdx.x % runs);
   const int h = it.h0 + lane / LPR;
   const Pieces pc = pieces_of<D>(a, lane);
   // what other loads wait for comes first
@@ -226,25 +222,27 @@ __global__ void __launch_bounds__(kNormThreads, U > 1 ? 8 : 1) k_norm_rope(const
 }
 
 // Backward: dx per row, and with weights the sums of g x r over this block's items: each lane
-// adds its 8 columns in the order of the items it meets, then the block's rows of lanes in
+// adds its 8 columns in the order of the tokens it meets, then the block's rows of lanes in
 // ascending order; k_norm_rope_dw adds the blocks.
 template <int D, typename TI, typename TG, int U, bool W>
-__global__ void __launch_bounds__(kNormThreads, 8) k_norm_rope_bwd(const NormRope a, const int per) {
+__global__ void __launch_bounds__(kNormThreads, W ? 5 : 8) k_norm_rope_bwd(const NormRope a, const int runs) {
   constexpr int LPR = RowLanes<D>::LPR, GPW = RowLanes<D>::GPW;
   const int lane = threadIdx.x & 31;
-  const int64_t items = (int64_t)a.T * per, step = (int64_t)gridDim.x * (kNormThreads / 32);
+  const int block = blockIdx.x / runs, blocks = gridDim.x / runs;  // of this run of heads
+  const HeadRun it = head_run<U * GPW>(a, blockIdx.x % runs);
+  const int h = it.h0 + lane / LPR;
   const Pieces pc = pieces_of<D>(a, lane);
   const bool half = a.layout == GDN_ROPE_HALF, some_off = a.rot < D;
-  const Row8 wq = W && a.wq ? load8p(a.wq + pc.at, pc.gap) : all8(1.f);
-  const Row8 wk = W && a.wk ? load8p(a.wk + pc.at, pc.gap) : all8(1.f);
+  const float* wp = it.kind ? a.wk : a.wq;
+  const Row8 w = W && wp ? load8p(wp + pc.at, pc.gap) : all8(1.f);
   const float cn = a.norm == GDN_NORM_RMS ? 1.f / D : a.norm == GDN_NORM_L2 ? 1.f : 0.f;
-  Row8 acc[2] = {all8(0.f), all8(0.f)};
-  for (int64_t item = (int64_t)blockIdx.x * (kNormThreads / 32) + (threadIdx.x >> 5); item < items; item += step) {
-    const NormItem it = norm_item<U * GPW>(a, item, per);
-    const int h = it.h0 + lane / LPR;
-    const int64_t at = (it.t * it.heads + h) * D + pc.at;
-    const TI* src = (it.kind ? static_cast<const TI*>(a.k) + it.t * a.k_stride
-                             : static_cast<const TI*>(a.q) + it.t * a.q_stride) + h * D + pc.at;
+  Row8 acc = all8(0.f);
+  for (int64_t t = (int64_t)block * (kNormThreads / 32) + (threadIdx.x >> 5); t < a.T;
+       t += (int64_t)blocks * (kNormThreads / 32)) {
+    const int64_t p = a.rot ? a.pos[t] : 0;
+    const int64_t at = (t * it.heads + h) * D + pc.at;
+    const TI* src = (it.kind ? static_cast<const TI*>(a.k) + t * a.k_stride
+                             : static_cast<const TI*>(a.q) + t * a.q_stride) + h * D + pc.at;
     const TG* gsrc = static_cast<const TG*>(it.kind ? a.gk : a.gq) + at;
     TI* dst = static_cast<TI*>(it.kind ? a.dk : a.dq) + at;
     Row8 x[U], g[U];
@@ -254,7 +252,6 @@ __global__ void __launch_bounds__(kNormThreads, 8) k_norm_rope_bwd(const NormRop
       x[u] = in ? load8p(src + u * GPW * D, pc.gap) : all8(0.f);
       g[u] = in ? load8p(gsrc + u * GPW * D, pc.gap) : all8(0.f);
     }
-    const int64_t p = a.rot ? a.pos[it.t] : 0;
     const bool bad = a.rot && (p < 0 || p >= a.table_rows);
     Row8 c, s;
     angles_of(a, bad ? 0 : p, -1.f, pc, half, c, s);
@@ -264,7 +261,7 @@ __global__ void __launch_bounds__(kNormThreads, 8) k_norm_rope_bwd(const NormRop
         const Row8 z = fma8(partners(g[u], half), s, mul8(g[u], c));
         g[u] = some_off ? pick8(pc.on, z, g[u]) : z;
       }
-      const Row8 gw = W ? mul8(g[u], it.kind ? wk : wq) : g[u];
+      const Row8 gw = W ? mul8(g[u], w) : g[u];
       const float r = inverse_norm(a.norm, row_sum<LPR>(dot8(x[u], x[u])), 1.f / D, a.eps);
       const float xg = row_sum<LPR>(dot8(x[u], gw));
       const float f = -__fmul_rn(__fmul_rn(cn, __fmul_rn(r, __fmul_rn(r, r))), xg);
@@ -272,45 +269,39 @@ __global__ void __launch_bounds__(kNormThreads, 8) k_norm_rope_bwd(const NormRop
       if (bad) dx = all8(kNan);
       if (h + u * GPW < it.heads) {
         store8p(dst + u * GPW * D, pc.gap, dx);
-        if (W && !bad) {
-          const Row8 xr = mul8(x[u], all8(r));
-          if (it.kind) acc[1] = fma8(g[u], xr, acc[1]); else acc[0] = fma8(g[u], xr, acc[0]);
-        }
+        if (W && !bad) acc = fma8(g[u], mul8(x[u], all8(r)), acc);
       }
     }
   }
   if (!W || !a.partial) return;
   constexpr int NR = kNormThreads / LPR;  // rows of lanes in the block
-  __shared__ float sh[2][NR][D];
-  const int rr = threadIdx.x / LPR;
-  store8p(&sh[0][rr][pc.at], pc.gap, acc[0]);
-  store8p(&sh[1][rr][pc.at], pc.gap, acc[1]);
+  __shared__ float sh[NR][D];
+  store8p(&sh[threadIdx.x / LPR][pc.at], pc.gap, acc);
   __syncthreads();
-  for (int e = threadIdx.x; e < 2 * D; e += kNormThreads) {
+  for (int e = threadIdx.x; e < D; e += kNormThreads) {
     float sum = 0.f;
 #pragma unroll 8
-    for (int r = 0; r < NR; ++r) sum = __fadd_rn(sum, sh[e / D][r][e % D]);
-    a.partial[(int64_t)blockIdx.x * 2 * D + e] = sum;
+    for (int r = 0; r < NR; ++r) sum = __fadd_rn(sum, sh[r][e]);
+    a.partial[((int64_t)(blockIdx.x % runs) * blocks + block) * D + e] = sum;
   }
 }
 
-// dw[e] = sum over blocks of partial[block][e], e < 2 D: 8 columns per CTA, 32 threads a column
-// with ascending strided sums, then a fixed tree.
-__global__ void __launch_bounds__(256) k_norm_rope_dw(const float* __restrict__ partial, int blocks, int D,
+// dw[e] = sum over blocks of partial[block][e]: those of q's runs come first, then k's (blockIdx.y).  8 columns per
+// CTA, 32 threads a column with ascending strided sums, then a fixed tree.
+__global__ void __launch_bounds__(256) k_norm_rope_dw(const float* __restrict__ partial, int q_blocks, int k_blocks, int D,
                                                       float* __restrict__ dwq, float* __restrict__ dwk) {
   __shared__ float sh[8][33];
   const int c = threadIdx.x & 7, r = threadIdx.x >> 3, e = blockIdx.x * 8 + c;
+  const int first = blockIdx.y ? q_blocks : 0, blocks = blockIdx.y ? k_blocks : q_blocks;
   float s = 0.f;
-  for (int b = r; b < blocks; b += 32) s = __fadd_rn(s, partial[(int64_t)b * 2 * D + e]);
+#pragma unroll 4
+  for (int b = r; b < blocks; b += 32) s = __fadd_rn(s, partial[(int64_t)(first + b) * D + e]);
   sh[c][r] = s;
   __syncthreads();
   float x = sh[threadIdx.x >> 5][threadIdx.x & 31];
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) x = __fadd_rn(x, __shfl_xor_sync(0xffffffffu, x, o));
-  if ((threadIdx.x & 31) == 0) {
-    const int col = blockIdx.x * 8 + (threadIdx.x >> 5);
-    (col < D ? dwq : dwk)[col % D] = x;
-  }
+  if ((threadIdx.x & 31) == 0) (blockIdx.y ? dwk : dwq)[blockIdx.x * 8 + (threadIdx.x >> 5)] = x;
 }
 
 template <int D, typename TI, typename TO>
@@ -318,29 +309,34 @@ void norm_rope_t(const NormRope& a, cudaStream_t st) {
   // Few rows: one row set per warp, which ends sooner (4 tokens of 16 / 2 heads: 2.0 us against 2.8);
   // from about 8 warps a scheduler on, four at once keep more loads in flight (16384 tokens: 96 us
   // against 140).
-  constexpr int GPW = RowLanes<D>::GPW;
+  constexpr int GPW = RowLanes<D>::GPW, WARPS = kNormThreads / 32;
   const int hv = a.v_pages ? a.hk : 0;
-  const auto blocks = [&](int per) { return (unsigned)(((int64_t)a.T * per + kNormThreads / 32 - 1) / (kNormThreads / 32)); };
-  if ((int64_t)a.T * norm_items<GPW>(a.hq, a.hk, hv) <= 152 * 32) {
-    const int per = norm_items<GPW>(a.hq, a.hk, hv);
-    k_norm_rope<D, TI, TO, 1><<<blocks(per), kNormThreads, 0, st>>>(a, per);
-  } else {
-    const int per = norm_items<4 * GPW>(a.hq, a.hk, hv);
-    k_norm_rope<D, TI, TO, 4><<<blocks(per), kNormThreads, 0, st>>>(a, per);
+  const unsigned x = (unsigned)(((int64_t)a.T + WARPS - 1) / WARPS);
+  const int runs = head_runs<GPW>(a.hq, a.hk, hv);
+  if ((int64_t)a.T * runs <= 152 * 32)
+    k_norm_rope<D, TI, TO, 1><<<x * runs, kNormThreads, 0, st>>>(a, runs);
+  else {
+    const int r4 = head_runs<4 * GPW>(a.hq, a.hk, hv);
+    k_norm_rope<D, TI, TO, 4><<<x * r4, kNormThreads, 0, st>>>(a, r4);
   }
 }
 
 template <int D, typename TI, typename TG>
 void norm_rope_bwd_t(const NormRope& a, cudaStream_t st) {
-  constexpr int U = 2, RUN = U * RowLanes<D>::GPW;
-  const int per = norm_items<RUN>(a.hq, a.hk, 0);
-  int64_t blocks = ((int64_t)a.T * per + kNormThreads / 32 - 1) / (kNormThreads / 32);
-  if (a.partial && blocks > kNormBwdBlocks) blocks = kNormBwdBlocks;
+  constexpr int U = 2, RUN = U * RowLanes<D>::GPW, WARPS = kNormThreads / 32;
+  const int nq = head_runs<RUN>(a.hq, 0, 0), runs = head_runs<RUN>(a.hq, a.hk, 0);
+  int64_t x = ((int64_t)a.T + WARPS - 1) / WARPS;
+  if (a.partial) {
+    const int64_t most = kNormBwdBlocks / runs > 1 ? kNormBwdBlocks / runs : 1;
+    if (x > most) x = most;
+  }
+  const unsigned grid = (unsigned)(x * runs);
   if (a.wq || a.wk || a.partial)
-    k_norm_rope_bwd<D, TI, TG, U, true><<<(unsigned)blocks, kNormThreads, 0, st>>>(a, per);
+    k_norm_rope_bwd<D, TI, TG, U, true><<<grid, kNormThreads, 0, st>>>(a, runs);
   else
-    k_norm_rope_bwd<D, TI, TG, U, false><<<(unsigned)blocks, kNormThreads, 0, st>>>(a, per);
-  if (a.partial) k_norm_rope_dw<<<2 * D / 8, 256, 0, st>>>(a.partial, (int)blocks, D, a.dwq, a.dwk);
+    k_norm_rope_bwd<D, TI, TG, U, false><<<grid, kNormThreads, 0, st>>>(a, runs);
+  if (a.partial)
+    k_norm_rope_dw<<<dim3(D / 8, 2), 256, 0, st>>>(a.partial, nq * (int)x, (runs - nq) * (int)x, D, a.dwq, a.dwk);
 }
 
 #define GDN_BY_D(d, CALL)              \

@@ -392,7 +392,7 @@ typedef enum { GDN_ROPE_HALF = 0, GDN_ROPE_INTERLEAVED = 1 } gdn_rope_layout;
 
 typedef struct {
     int32_t tokens;      /* T */
-    int32_t h_q, h_k;    /* heads of q and of k (and v) */
+    int32_t h_q, h_k;    /* heads of q and of k (and v); T (h_q + 2 h_k) < 2^31 */
     int32_t d;
     int32_t rot;         /* rotated entries at the front of every head: 0 or a multiple of 8, <= d */
     int32_t table_rows;  /* rows of cos and sin */
