@@ -49,13 +49,6 @@ __device__ __forceinline__ void mma_rows(uint32_t d, uint64_t a, uint64_t b, uin
     mma_bf16(d, a + ((kk / 4) * RA * 128 + (kk % 4) * 32) / 16, b + ((kk / 4) * RB * 128 + (kk % 4) * 32) / 16, idesc,
              kk > 0);
 }
-// The same with A in TMEM: COLS packed bf16 columns from `a`
-template <int COLS, int RB>
-__device__ __forceinline__ void mma_ts_rows(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc) {
-#pragma unroll
-  for (int kk = 0; kk < COLS / 16; ++kk)
-    mma_bf16_ts(d, a + kk * 8, b + ((kk / 4) * RB * 128 + (kk % 4) * 32) / 16, idesc, kk > 0);
-}
 // D (+)= P B, P [128 x RB] in TMEM, B a tile of RB rows (K) read MN-major
 template <int RB>
 __device__ __forceinline__ void mma_ts_cols(uint32_t d, uint32_t p, uint64_t b, uint32_t idesc, bool accumulate) {

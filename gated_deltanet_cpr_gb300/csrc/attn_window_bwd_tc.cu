@@ -1,21 +1,26 @@
 // attn_window_bwd_tc.cu -- gradient of sliding-window attention for bf16 with d = 64 or 128 on the
 // tensor cores.  Two kernels of one form, so that nothing is added across CTAs and the result
 // does not depend on their order:
-//   dq      rows = 128 queries of a head, columns = blocks of 64 keys:   dQ += dS K
+//   dq      rows = 128 queries of a head, columns = blocks of 128 keys:   dQ += dS K
 //   dk, dv  rows = 128 keys of a key head, columns = blocks of 64 queries of each head of the group in
 //           ascending order:   dK += dS^T Q,  dV += P^T dO
-// with P = exp2(c Q K^T - lse log2 e) and dS = P (dO V^T - delta) formed anew in both (7 products of
-// 128 x 64 x d where one kernel that adds dQ across CTAs would need 5).  The row tiles X, Y (Q and
-// dO, or K and V) stay on chip: Q and dO in TMEM, as the first operand of their products, K and V,
-// for which TMEM has no room, in shared memory; column tiles U, W come by TMA.  S = X U^T and T = Y W^T go
-// to TMEM; a group of four warps (a thread per row) takes them into registers, which frees their
-// place for the next block's, and leaves dS and P as bf16 in a place of its own, from which the
-// accumulating products read them.  The two groups take the column blocks in turn, so that one's
-// arithmetic runs beside the other's and the products.
-// P and dS are rounded to bf16 for their products; everything else stays in 32 bits.
-// A 128 x 64 block costs 128 x 64 x d MACs per product at 4096 a clock; an operand from shared memory
-// is read at 128 bytes a clock, so that with both operands there S and T (48 KB each at d = 128) take
-// half as long again, and with the rows in TMEM they do not.
+// with P = exp2(c Q K^T - lse log2 e) and dS = P (dO V^T - delta) formed anew in both (7 products
+// where one kernel that adds dQ across CTAs would need 5).  The row tiles X, Y (Q and dO, or K and
+// V) stay in shared memory; column tiles U, W come by TMA.  S = X U^T and T = Y W^T go to TMEM; two
+// groups of four warps, a thread per row, take them into registers, which frees their place for
+// the next block's, and leave dS and P as bf16 in one of two places of their own, from which the
+// accumulating products read them while the groups are at the next block.  In dq the groups share
+// a block's columns, in dk, dv they take alternate blocks.
+// P and dS are rounded to bf16 for their products, as their other operands are; everything else
+// stays in 32 bits.
+// What bounds them: a 128 x 128 block needs 512 clocks of the tensor core per product at d = 128, and
+// shared memory, at 128 bytes a clock, 512 for S and T each, 256 for an accumulating product and
+// 512 to take in U and W: 1792 against 1536 in dq.  At 128 x 64 (dk, dv, whose accumulators leave
+// TMEM no room for more) it is 1280 against 1024.  Packed training case (32387 tokens of 16/4 heads,
+// window 2048): dq 531 us at 54% tensor activity, dk and dv 619 us at 61%.  With the rows in TMEM and
+// 64 columns dq took 599 us; with one ring for U and W 627; with S and T issued by two warps 521,
+// but dk and dv then 764; with one loading warp for both rings dq 636 and dk, dv 754; with four groups
+// of 32 columns dq 539.
 #include "attn_tc.cuh"
 #include "attn_window.cuh"
 
@@ -26,8 +31,10 @@ namespace {
 using namespace win;
 using namespace tc;
 
-constexpr int BR = 128, BC = 64;  // rows, columns of a block
-constexpr int kThreads = 384, kScoreWarp = 8, kLoadWarp = 9, kAccWarp = 10;
+constexpr int BR = 128;  // rows of a block
+template <bool DKV>
+constexpr int kCols = DKV ? 64 : 128;  // its columns
+constexpr int kThreads = 384, kScoreWarp = 8, kLoadWarp = 9, kAccWarp = 10, kLoadWarp2 = 11;
 // 384 threads x 168 registers at launch = 256 x 208 + 128 x 88
 constexpr int kRowRegs = 208, kOtherRegs = 88;
 constexpr int kSms = 152;
@@ -44,6 +51,7 @@ __device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : n >= 32 
 // The column blocks of an item: for dq key blocks, for dk and dv the query blocks of each head.
 template <bool DKV>
 struct Cols {
+  static constexpr int BC = kCols<DKV>;
   int rows, cnt, head, from, nb, off;
   __device__ __forceinline__ Cols(const WindowAttn& a, const Item& it) {
     off = it.q.Lk - it.q.Lq;
@@ -71,26 +79,35 @@ struct Cols {
   __device__ __forceinline__ int group_head(int i) const { return DKV ? i / nb : 0; }
 };
 
+// Tiles U and W have rings of their own: dq's W is free as soon as T is formed.
 template <int D, bool DKV>
 struct Smem {
-  static constexpr int ROWS = DKV ? BR * D * 2 : 0, COLS = BC * D * 2, STAGES = DKV ? 4 : 6;
-  static constexpr int X = 0, Y = ROWS, ST = 2 * ROWS, VEC = ST + STAGES * 2 * COLS;
-  static constexpr int BARS = VEC + (DKV ? STAGES * 2 * BC * 4 : 2 * BR * 4);
+  static constexpr int BC = kCols<DKV>, ROWS = BR * D * 2, COLS = BC * D * 2;
+  static constexpr int NU = DKV ? 4 : D == 128 ? 3 : 4, NW = DKV ? 4 : D == 128 ? 2 : 3;
+  static constexpr int X = 0, Y = ROWS, U = 2 * ROWS, W = U + NU * COLS, VEC = W + NW * COLS;
+  static constexpr int BARS = VEC + (DKV ? NU * 2 * BC * 4 : 2 * BR * 4);
   static constexpr int BYTES = BARS + 1024 + 1024;
 };
 
-// TMEM columns: buffers of S and T (128 columns), dS and P of each group as bf16 (32 columns each),
-// the accumulators, and for dq the rows X, Y (see above).
+// Place in a ring of N tiles.
+template <int N>
+struct Ring {
+  uint32_t at = 0, round = 0;
+  __device__ __forceinline__ void next() {
+    if (++at == N) at = 0, ++round;
+  }
+};
+
+// TMEM columns: S and T, two places of dS (and P) as bf16, the accumulators.
 template <int D, bool DKV>
 struct Tmem {
-  static constexpr int ST_BUFS = D == 128 ? 1 : 2, PD_STEP = DKV ? 64 : 32;
-  static constexpr int PD = 128 * ST_BUFS, ACC = PD + 2 * PD_STEP, X = ACC + (DKV ? 2 : 1) * D, Y = X + D / 2;
-  static_assert(X + (DKV ? 0 : D) <= 512, "TMEM has 512 columns");
+  static constexpr int BC = kCols<DKV>, PD = 2 * BC, PD_STEP = (DKV ? 2 : 1) * BC / 2, ACC = PD + 2 * PD_STEP;
+  static_assert(ACC + (DKV ? 2 : 1) * D <= 512, "TMEM has 512 columns");
 };
 
 struct Bars {
-  uint64_t item_full[2], item_empty[2], x_full, x_empty, st_full[6], st_empty[6], s_full[2], s_free[2],
-      p_full[2], p_free[2], acc_full, acc_empty, vec_full, vec_free, aux;
+  uint64_t item_full[2], item_empty[2], x_full, x_empty, u_full[4], u_empty[4], w_full[4], w_empty[4], s_full[2], s_free,
+      p_full[2], p_free[2], acc_full, acc_empty, vec_full, vec_free, aux[2];
   uint32_t tmem;
   Item item[2];
 };
@@ -128,7 +145,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap my,
                     const __grid_constant__ CUtensorMap mu, const __grid_constant__ CUtensorMap mw) {
   using L = Smem<D, DKV>;
-  constexpr int STAGES = L::STAGES;
+  constexpr int BC = L::BC, HB = 64;  // HB: columns of a group: half of dq's block, every second block of dk, dv
+  constexpr int WARPS = DKV ? 4 : 8;  // row warps at a block
   using M = Tmem<D, DKV>;
   extern __shared__ unsigned char raw[];
   unsigned char* sm = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
@@ -139,23 +157,27 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&B.item_full[i], 1);
-      mbar_init(&B.item_empty[i], 10);  // all warps but the loader and the idle one
+      mbar_init(&B.item_empty[i], 11);  // all warps but the one that hands them out
+      mbar_init(&B.aux[i], 1);
       mbar_init(&B.s_full[i], 1);
-      mbar_init(&B.s_free[i], 4);
-      mbar_init(&B.p_full[i], 4);
+      mbar_init(&B.p_full[i], WARPS);
       mbar_init(&B.p_free[i], 1);
     }
-    for (int i = 0; i < STAGES; ++i) {
-      mbar_init(&B.st_full[i], DKV ? 33 : 1);  // tiles; the loader's lanes' vectors
-      mbar_init(&B.st_empty[i], DKV ? 5 : 1);  // MMA; the four warps that read the vectors
+    for (int i = 0; i < L::NU; ++i) {
+      mbar_init(&B.u_full[i], DKV ? 33 : 1);  // the tile; the loader's lanes' vectors
+      mbar_init(&B.u_empty[i], DKV ? 5 : 1);  // MMA; the row warps, which read the vectors
     }
-    mbar_init(&B.x_full, DKV ? 1 : 8);  // TMA, or the row warps
+    for (int i = 0; i < L::NW; ++i) {
+      mbar_init(&B.w_full[i], 1);
+      mbar_init(&B.w_empty[i], 1);
+    }
+    mbar_init(&B.s_free, WARPS);
+    mbar_init(&B.x_full, 1);
     mbar_init(&B.x_empty, 1);
     mbar_init(&B.vec_full, 4);
     mbar_init(&B.vec_free, 4);
     mbar_init(&B.acc_full, 1);
     mbar_init(&B.acc_empty, 8);
-    mbar_init(&B.aux, 1);
     fence_mbar_init();
   }
   __syncthreads();
@@ -164,38 +186,53 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp >= 8) {
     regs_less<kOtherRegs>();
-    if (warp == kLoadWarp) {
-      // ---------------------------------------------------------------- loader ----
-      uint32_t n = 0, stage = 0, round = 0, aux = 0, xn = 0;
+    if (warp == kLoadWarp || warp == kLoadWarp2) {
+      // --------------------------------------------------------------- loaders ----
+      // One hands out the items and loads the row tiles, the tiles U and the vectors, the other the tiles W.
+      const bool first = warp == kLoadWarp;
+      const uint32_t N = first ? L::NU : L::NW;
+      uint64_t *const full = first ? B.u_full : B.w_full, *const empty = first ? B.u_empty : B.w_empty;
+      uint64_t* const aux = &B.aux[first ? 0 : 1];
+      const CUtensorMap* const map = first ? &mu : &mw;
+      unsigned char* const tiles = sm + (first ? L::U : L::W);
+      uint32_t n = 0, tails = 0, xn = 0, at = 0, round = 0;
       int64_t w = blockIdx.x;
       while (ok) {
         Item it;
-        it.ok = w < work;
-        if (it.ok) {
-          const bool have = find_item<DKV>(a, w, blocks, it);
-          int nx = 0;
-          if (lane == 0) nx = atomicAdd(next_item, 1);
-          w = (int64_t)gridDim.x + __shfl_sync(0xffffffffu, nx, 0);
-          if (!have) continue;
-        }
         const uint32_t slot = n & 1;
-        ok = mbar_wait(&B.item_empty[slot], ((n >> 1) & 1) ^ 1);
-        if (!ok) break;
-        if (lane == 0) {
-          B.item[slot] = it;
-          mbar_arrive(&B.item_full[slot]);
+        if (first) {
+          it.ok = w < work;
+          if (it.ok) {
+            const bool have = find_item<DKV>(a, w, blocks, it);
+            int nx = 0;
+            if (lane == 0) nx = atomicAdd(next_item, 1);
+            w = (int64_t)gridDim.x + __shfl_sync(0xffffffffu, nx, 0);
+            if (!have) continue;
+          }
+          ok = mbar_wait(&B.item_empty[slot], ((n >> 1) & 1) ^ 1);
+          if (!ok) break;
+          if (lane == 0) {
+            B.item[slot] = it;
+            mbar_arrive(&B.item_full[slot]);
+          }
+        } else {
+          ok = mbar_wait(&B.item_full[slot], (n >> 1) & 1);
+          if (!ok) break;
+          it = B.item[slot];
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&B.item_empty[slot]);
         }
         ++n;
         if (!it.ok) break;
         const Cols<DKV> c(a, it);
         if (!c.cnt) continue;
-        if (DKV) {
+        if (first) {
           ok = mbar_wait(&B.x_empty, (xn & 1) ^ 1);
           if (!ok) break;
           ++xn;
           if (lane == 0) {
             mbar_expect_tx(&B.x_full, 2 * L::ROWS);
-            const int row = it.q.k0 + it.row0;
+            const int row = (DKV ? it.q.k0 : it.q.q0) + it.row0;
             for (int e = 0; e < D / 64; ++e) {
               tma_load_3d(sm + L::X + e * BR * 128, &mx, 64 * e, it.h, row, &B.x_full);
               tma_load_3d(sm + L::Y + e * BR * 128, &my, 64 * e, it.h, row, &B.x_full);
@@ -203,43 +240,42 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         const int group = a.hq / a.hkv, len = DKV ? it.q.Lq : it.q.Lk;
+        int blk = 0, gh = 0;  // dk, dv: block of the head, head of the group
         for (int i = 0; i < c.cnt; ++i) {
-          ok = mbar_wait(&B.st_empty[stage], (round & 1) ^ 1);
+          const int c0 = DKV ? (c.from + blk) * BC : c.col0(i), head = DKV ? it.h * group + gh : it.h / group;
+          if (DKV && ++blk == c.nb) blk = 0, ++gh;
+          const int left = len - c0;  // rows of this sequence in the tile
+          ok = mbar_wait(&empty[at], (round & 1) ^ 1);
           if (!ok) break;
-          const int c0 = c.col0(i), head = DKV ? it.h * group + c.group_head(i) : it.h / group;
-          const int left = len - c0;  // rows of this sequence in the tiles
-          unsigned char* dst = sm + L::ST + stage * 2 * L::COLS;
-          uint64_t* bar = left < BC ? &B.aux : &B.st_full[stage];
+          unsigned char* dst = tiles + at * L::COLS;
+          uint64_t* bar = left < BC ? aux : &full[at];
           if (lane == 0) {
-            mbar_expect_tx(bar, 2 * L::COLS);
+            mbar_expect_tx(bar, L::COLS);
             const int row = (DKV ? it.q.q0 : it.q.k0) + c0;
-            for (int e = 0; e < D / 64; ++e) {
-              tma_load_3d(dst + e * BC * 128, &mu, 64 * e, head, row, bar);
-              tma_load_3d(dst + L::COLS + e * BC * 128, &mw, 64 * e, head, row, bar);
-            }
+            for (int e = 0; e < D / 64; ++e) tma_load_3d(dst + e * BC * 128, map, 64 * e, head, row, bar);
           }
-          if (DKV) {
-            float* v = reinterpret_cast<float*>(sm + L::VEC) + stage * 2 * BC;
+          if (DKV && first) {
+            float* v = reinterpret_cast<float*>(sm + L::VEC) + at * 2 * BC;
             const float* src = vec + (int64_t)head * a.Tq + it.q.q0 + c0;
             for (int e = lane; e < BC; e += 32)
               if (e < left) {
                 cp_async4(v + e, src + e);
                 cp_async4(v + BC + e, src + (int64_t)a.hq * a.Tq + e);
               }
-            cp_async_arrive(&B.st_full[stage]);
+            cp_async_arrive(&full[at]);
           }
           if (left < BC) {  // the rows past the sequence's end are another's: zeros instead
-            ok = mbar_wait(&B.aux, aux & 1);
-            ++aux;
+            ok = mbar_wait(aux, tails & 1);
+            ++tails;
             if (!ok) break;
             const int per = (BC - left) * 8;
-            for (int e = lane; e < per * 2 * (D / 64); e += 32)
+            for (int e = lane; e < per * (D / 64); e += 32)
               *reinterpret_cast<uint4*>(dst + (e / per) * BC * 128 + left * 128 + (e % per) * 16) = make_uint4(0, 0, 0, 0);
             fence_proxy_async();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&B.st_full[stage]);
+            if (lane == 0) mbar_arrive(&full[at]);
           }
-          if (++stage == STAGES) stage = 0, ++round;
+          if (++at == N) at = 0, ++round;
         }
       }
       cp_async_wait_all();
@@ -252,10 +288,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool scores = warp == kScoreWarp;
       const uint32_t iS = idesc_bf16(BR, BC), iA = idesc_bf16(BR, D) | IDESC_B_MN;
       const uint64_t dX = desc_k_sw128(smem_u32(sm + L::X)), dY = desc_k_sw128(smem_u32(sm + L::Y));
-      const uint64_t dU = desc_k_sw128(smem_u32(sm + L::ST)), dUt = desc_mn_sw128(smem_u32(sm + L::ST), BC * 128);
-      constexpr int STEP = L::COLS / 16;  // of a descriptor, from U to W of a stage
-      uint32_t n = 0, xn = 0, an = 0, stage = 0, round = 0;
-      uint32_t buf = 0, bn = 0, np[2] = {0, 0};  // S, T buffer and its use; P, dS
+      const uint64_t dU = desc_k_sw128(smem_u32(sm + L::U)), dUt = desc_mn_sw128(smem_u32(sm + L::U), BC * 128);
+      constexpr int STEP = L::COLS / 16, UW = (L::W - L::U) / 16;  // of a descriptor: to the next tile, to W
+      uint32_t n = 0, xn = 0, an = 0;
+      Ring<L::NU> ru;
+      Ring<L::NW> rw;
+      uint32_t gb = 0;  // blocks so far
       while (ok) {
         const uint32_t slot = n & 1;
         ok = warp_wait(&B.item_full[slot], (n >> 1) & 1);
@@ -272,28 +310,24 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++xn;
         }
         for (int i = 0; i < cnt && ok; ++i) {
-          ok = warp_wait(&B.st_full[stage], round & 1);
           if (scores) {
-            ok = ok && warp_wait(&B.s_free[buf], (bn & 1) ^ 1);  // the buffer's last S, T are in registers
+            ok = warp_wait(&B.u_full[ru.at], ru.round & 1);
+            ok = ok && warp_wait(&B.w_full[rw.at], rw.round & 1);
+            ok = ok && warp_wait(&B.s_free, (gb & 1) ^ 1);  // the last S, T are in registers
             if (!ok) break;
             fence_after_sync();
             if (elect_one()) {
-              const uint64_t u = dU + stage * (2 * STEP);
-              if (DKV) {
-                mma_rows<D, BR, BC>(tm + 128 * buf, dX, u, iS);
-                mma_rows<D, BR, BC>(tm + 128 * buf + 64, dY, u + STEP, iS);
-              } else {
-                mma_ts_rows<D, BC>(tm + 128 * buf, tm + M::X, u, iS);
-                mma_ts_rows<D, BC>(tm + 128 * buf + 64, tm + M::Y, u + STEP, iS);
-              }
-              mma_commit(&B.s_full[i & 1]);
+              mma_rows<D, BR, BC>(tm, dX, dU + ru.at * STEP, iS);
+              mma_rows<D, BR, BC>(tm + BC, dY, dU + UW + rw.at * STEP, iS);
+              mma_commit(&B.s_full[gb & 1]);
+              if (!DKV) mma_commit(&B.w_empty[rw.at]);
               if (i + 1 == cnt) mma_commit(&B.x_empty);
             }
-            if (++buf == M::ST_BUFS) buf = 0, ++bn;
           } else {
-            const int b = i & 1;
-            ok = ok && warp_wait(&B.p_full[b], np[b] & 1);
-            ++np[b];
+            const uint32_t b = gb & 1, pd = tm + M::PD + M::PD_STEP * b;
+            ok = warp_wait(&B.u_full[ru.at], ru.round & 1);
+            if (DKV) ok = ok && warp_wait(&B.w_full[rw.at], rw.round & 1);
+            ok = ok && warp_wait(&B.p_full[b], (gb >> 1) & 1);
             if (i == 0) {  // the last item's results have left TMEM
               ok = ok && warp_wait(&B.acc_empty, (an & 1) ^ 1);
               ++an;
@@ -301,15 +335,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok) break;
             fence_after_sync();
             if (elect_one()) {
-              const uint64_t u = dUt + stage * (2 * STEP);
-              mma_ts_cols<BC>(tm + M::ACC, tm + M::PD + M::PD_STEP * b, u, iA, i > 0);
-              if (DKV) mma_ts_cols<BC>(tm + M::ACC + D, tm + M::PD + M::PD_STEP * b + 32, u + STEP, iA, i > 0);
+              mma_ts_cols<BC>(tm + M::ACC, pd, dUt + ru.at * STEP, iA, i > 0);
+              if (DKV) mma_ts_cols<BC>(tm + M::ACC + D, pd + BC / 2, dUt + UW + rw.at * STEP, iA, i > 0);
               mma_commit(&B.p_free[b]);
-              mma_commit(&B.st_empty[stage]);
+              mma_commit(&B.u_empty[ru.at]);
+              if (DKV) mma_commit(&B.w_empty[rw.at]);
               if (i + 1 == cnt) mma_commit(&B.acc_full);
             }
           }
-          if (++stage == STAGES) stage = 0, ++round;
+          ++gb;
+          ru.next();
+          rw.next();
         }
       }
     }
@@ -317,11 +353,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     // -------------------------------------------------------------------- rows ----
     regs_more<kRowRegs>();
     const int wg = warp >> 2, row = (warp & 3) * 32 + lane;
-    const uint32_t tP = tmem_lane_addr(tm + M::PD + M::PD_STEP * wg, warp, 0);
+    const uint32_t tS = tmem_lane_addr(tm + (DKV ? 0 : HB * wg), warp, 0);
+    const uint32_t tP = tmem_lane_addr(tm + M::PD + (DKV ? 0 : HB / 2 * wg), warp, 0);
     const float sc = __fmul_rn(a.scale, kLog2e);
     const float2 sc2 = make_float2(sc, sc);
-    uint32_t n = 0, ns = 0, an = 0, xn = 0;
-    uint32_t stage = 0, round = 0, blk = 0;  // stage of the item's block 0, and the S, T buffer's block count
+    uint32_t n = 0, an = 0, gb = 0;  // gb: blocks so far
+    Ring<L::NU> ru;
     while (ok) {
       const uint32_t slot = n & 1;
       ok = mbar_wait(&B.item_full[slot], (n >> 1) & 1);
@@ -336,28 +373,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int at = it.row0 + row + (DKV ? 0 : c.off);  // key, or the query's position
       float2 nl2, nd2;                                   // dq: -lse log2 e and -delta of the row
       if (!DKV) {
-        // Group 0 brings Q's rows to TMEM, group 1 dO's, with which it forms delta = do . o.
-        const int64_t r = (int64_t)(it.q.q0 + it.row0 + row) * a.hq + it.h;
-        const uint4* xp = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(wg ? a.dout : a.q) + r * D);
-        uint4 x[D / 8];
-#pragma unroll
-        for (int e = 0; e < D / 8; ++e) x[e] = live ? xp[e] : make_uint4(0, 0, 0, 0);
+        // Group 1 forms delta = do . o of its rows and hands it and lse to group 0.
         float dl = 0.f, ls = INFINITY;
         float* sh = reinterpret_cast<float*>(sm + L::VEC);
         if (wg) {
           if (live) {
+            const int64_t r = (int64_t)(it.q.q0 + it.row0 + row) * a.hq + it.h;
             const __nv_bfloat16* o = static_cast<const __nv_bfloat16*>(a.out) + r * D;
+            const __nv_bfloat16* g = static_cast<const __nv_bfloat16*>(a.dout) + r * D;
             float x0 = 0.f, x1 = 0.f;
+#pragma unroll 8
+            for (int e = 0; e < D; e += 8) {
+              float x[8], y[8];
+              load8(o + e, x);
+              load8(g + e, y);
 #pragma unroll
-            for (int e = 0; e < D / 8; ++e) {
-              float y[8];
-              load8(o + 8 * e, y);
-              const uint32_t g[4] = {x[e].x, x[e].y, x[e].z, x[e].w};
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                x0 = __fmaf_rn(__uint_as_float(g[k] << 16), y[2 * k], x0);
-                x1 = __fmaf_rn(__uint_as_float(g[k] & 0xffff0000u), y[2 * k + 1], x1);
-              }
+              for (int k = 0; k < 8; k += 2) x0 = __fmaf_rn(x[k], y[k], x0), x1 = __fmaf_rn(x[k + 1], y[k + 1], x1);
             }
             dl = __fadd_rn(x0, x1);
             const float l = a.lse[r];
@@ -373,18 +404,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(&B.vec_full);
         }
-        if (c.cnt) {
-          ok = mbar_wait(&B.x_empty, (xn & 1) ^ 1);  // the last item's scores are done
-          ++xn;
-          if (!ok) break;
-          const uint32_t tX = tmem_lane_addr(tm + (wg ? M::Y : M::X), warp, 0);
-#pragma unroll
-          for (int e = 0; e < D / 8; e += 4) tmem_st16u(tX + 4 * e, reinterpret_cast<const uint32_t*>(&x[e]));
-          tmem_st_wait();
-          fence_before_sync();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&B.x_full);
-        }
         if (!wg) {
           ok = mbar_wait(&B.vec_full, (n & 1) ^ 1);
           if (!ok) break;
@@ -396,52 +415,47 @@ __global__ void __launch_bounds__(kThreads, 1)
         nl2 = make_float2(-ls, -ls);
         nd2 = make_float2(-dl, -dl);
       }
-      for (int i = wg; i < c.cnt; i += 2) {
-        const int c0 = c.col0(i);
-        uint32_t st = stage + i, sr = round + st / STAGES;
-        st %= STAGES;
+      for (int i = 0; i < c.cnt; ++i, ++gb, ru.next()) {
+        if (DKV && (gb & 1) != wg) continue;
+        const int c0 = c.col0(i), cg = c0 + (DKV ? 0 : HB * wg);  // the block's first column, and the group's
         if (DKV) {
-          ok = mbar_wait(&B.st_full[st], sr & 1);  // the vectors
+          ok = mbar_wait(&B.u_full[ru.at], ru.round & 1);  // the vectors
           if (!ok) break;
         }
-        ok = mbar_wait(&B.s_full[wg], ns & 1);
-        ++ns;
+        ok = mbar_wait(&B.s_full[gb & 1], (gb >> 1) & 1);
         if (!ok) break;
         fence_after_sync();
         // which entries are visible, where not all are
         bool cut;
-        uint32_t see[2];
+        uint32_t see[HB / 32];
         if (DKV) {
-          const int p0 = c0 + c.off;  // position of column 0
+          const int p0 = c0 + c.off, pg = cg + c.off;  // positions of those columns
           cut = it.row0 + BR - 1 > p0 || c0 + BC > it.q.Lq ||
                 (a.window > 0 && p0 + BC - 1 - it.row0 >= a.window && it.row0 + BR > a.sinks);
-          const int end = (a.window > 0 && at >= a.sinks) ? min(it.q.Lq - c0, at + a.window - p0) : it.q.Lq - c0;
+          const int end = (a.window > 0 && at >= a.sinks) ? min(it.q.Lq - cg, at + a.window - pg) : it.q.Lq - cg;
 #pragma unroll
-          for (int g = 0; g < 2; ++g) see[g] = ~below(at - p0 - 32 * g) & below(end - 32 * g);
+          for (int g = 0; g < HB / 32; ++g) see[g] = ~below(at - pg - 32 * g) & below(end - 32 * g);
         } else {
           const int p0 = it.row0 + c.off;
           cut = c0 + BC - 1 > p0 || (a.window > 0 && p0 + BR - 1 - c0 >= a.window && c0 + BC > a.sinks);
           const int lo = a.window > 0 ? at - a.window + 1 : 0;
 #pragma unroll
-          for (int g = 0; g < 2; ++g)
-            see[g] = below(at + 1 - c0 - 32 * g) & (~below(lo - c0 - 32 * g) | below(a.sinks - c0 - 32 * g));
+          for (int g = 0; g < HB / 32; ++g)
+            see[g] = below(at + 1 - cg - 32 * g) & (~below(lo - cg - 32 * g) | below(a.sinks - cg - 32 * g));
         }
-        if (!cut) see[0] = see[1] = ~0u;
-        float s[BC], t[BC];
-        const uint32_t tS = tmem_lane_addr(tm + 128 * ((blk + i) % M::ST_BUFS), warp, 0);
+        float s[HB], t[HB];
         tmem_ld64(tS, s);
-        tmem_ld64(tS + 64, t);
+        tmem_ld64(tS + BC, t);
         fence_before_sync();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&B.s_free[(blk + i) % M::ST_BUFS]);  // S, T are in registers
-        if (ns > 1) {  // the group's last P and dS have been read
-          ok = mbar_wait(&B.p_free[wg], ns & 1);
-          if (!ok) break;
-        }
-        const float4* lv = reinterpret_cast<const float4*>(sm + L::VEC) + st * (2 * BC / 4);
+        if (lane == 0) mbar_arrive(&B.s_free);  // S, T are in registers
+        const uint32_t b = gb & 1, tD = tP + M::PD_STEP * b;
+        ok = mbar_wait(&B.p_free[b], ((gb >> 1) & 1) ^ 1);  // what was there two blocks ago has been read
+        if (!ok) break;
+        const float4* lv = reinterpret_cast<const float4*>(sm + L::VEC) + ru.at * (2 * BC / 4);
         const float4* dv = lv + BC / 4;
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
+        for (int g = 0; g < HB / 32; ++g) {
           uint32_t pp[16], pd[16];
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
@@ -468,22 +482,18 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (DKV) pp[k] &= keep;
             }
           }
-          tmem_st16u(tP + 16 * g, pd);
-          if (DKV) tmem_st16u(tP + 32 + 16 * g, pp);
+          tmem_st16u(tD + 16 * g, pd);
+          if (DKV) tmem_st16u(tD + BC / 2 + 16 * g, pp);
         }
         tmem_st_wait();
         fence_before_sync();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(&B.p_full[wg]);
-          if (DKV) mbar_arrive(&B.st_empty[st]);
+          mbar_arrive(&B.p_full[b]);
+          if (DKV) mbar_arrive(&B.u_empty[ru.at]);
         }
       }
       if (!ok) break;
-      blk += c.cnt;
-      stage += c.cnt;
-      round += stage / STAGES;
-      stage %= STAGES;
       // results: dq's columns are shared between the groups; dk goes to group 0, dv to group 1
       if (c.cnt) {
         ok = mbar_wait(&B.acc_full, an & 1);
@@ -526,8 +536,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (!ok) set_error(a.hdr, GDN_DEVERR_TIMEOUT);
   if (__syncthreads_or(!ok)) {
     // something gave up: copies that were issued land before the memory is given back
-    if (warp == kLoadWarp && lane == 0)
-      for (int i = 0; i < STAGES; ++i) mbar_wait(&B.st_full[i], 0, 1u << 12);
+    if (warp == kLoadWarp && lane == 0) {
+      for (int i = 0; i < L::NU; ++i) mbar_wait(&B.u_full[i], 0, 1u << 12);
+      for (int i = 0; i < L::NW; ++i) mbar_wait(&B.w_full[i], 0, 1u << 12);
+    }
   }
   __syncthreads();
   if (warp == kScoreWarp) tmem_dealloc(tm, 512);
@@ -536,10 +548,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <int D, bool DKV>
 bool bwd_tc(const WindowAttn& a, cudaStream_t st) {
   CUtensorMap mx, my, mu, mw;
-  const bool ok = DKV ? make_rows_map(&mx, a.k, a.Tk, a.hkv, D, BR, a.hdr) && make_rows_map(&my, a.v, a.Tk, a.hkv, D, BR, a.hdr) &&
-                            make_rows_map(&mu, a.q, a.Tq, a.hq, D, BC, a.hdr) && make_rows_map(&mw, a.dout, a.Tq, a.hq, D, BC, a.hdr)
-                      : make_rows_map(&mx, a.q, a.Tq, a.hq, D, BR, a.hdr) && make_rows_map(&my, a.dout, a.Tq, a.hq, D, BR, a.hdr) &&
-                            make_rows_map(&mu, a.k, a.Tk, a.hkv, D, BC, a.hdr) && make_rows_map(&mw, a.v, a.Tk, a.hkv, D, BC, a.hdr);
+  constexpr int BC = kCols<DKV>;
+  const bool ok = DKV ? make_rows_map(&mx, a.k, a.Tk, a.hkv, D, BR, a.hdr) &&
+                            make_rows_map(&my, a.v, a.Tk, a.hkv, D, BR, a.hdr) &&
+                            make_rows_map(&mu, a.q, a.Tq, a.hq, D, BC, a.hdr) &&
+                            make_rows_map(&mw, a.dout, a.Tq, a.hq, D, BC, a.hdr)
+                      : make_rows_map(&mx, a.q, a.Tq, a.hq, D, BR, a.hdr) &&
+                            make_rows_map(&my, a.dout, a.Tq, a.hq, D, BR, a.hdr) &&
+                            make_rows_map(&mu, a.k, a.Tk, a.hkv, D, BC, a.hdr) &&
+                            make_rows_map(&mw, a.v, a.Tk, a.hkv, D, BC, a.hdr);
   if (!ok) return false;
   // dk, dv: N more items, the sequences' first blocks ahead of the others
   const int64_t blocks = item_count(DKV ? a.Tk : a.Tq, BR, a.N);
