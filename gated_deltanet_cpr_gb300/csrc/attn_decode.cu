@@ -11,10 +11,12 @@
 //
 // The kernel is bound by the cache's bytes, so what matters is that loads never pause.  A warp
 // works alone: it walks over runs (the grid fills the SMs once), and copies keys and values
-// asynchronously into its own ring, two tiles ahead and across the end of a run.  A
-// kernel of one CTA of four warps per run, which waits for its first keys and joins its warps at
-// the end, reached 72% (runs of 256 keys) to 94% (1024 keys) of the copy bandwidth on 256 requests
-// of about 2112 tokens.
+// asynchronously into its own ring, a tile or two ahead and across the end of a run, with the next
+// tile's pages looked up meanwhile.  256 requests of about 2112 tokens, 32 / 8 heads, d = 128: 328 us,
+// 6.8 TB/s of the cache, which is a copy's rate.  A kernel of one CTA of four warps per run,
+// which waits for its first keys and joins its warps at the end, reached 72% (runs of 256 keys) to
+// 94% (1024 keys) of it.  Few requests are bound by the latency of one run, the launch and the join:
+// 4 of about 700 tokens take 9.0 us.
 #include "attn.h"
 #include "tc.cuh"
 
@@ -97,8 +99,9 @@ template <int D, typename T, int H, int NC>
 struct SimtEngine {
   using Elem = T;
   static constexpr int DIM = D, KEYS = 32 / H, ROWB = D * sizeof(T), EXTRA = NC * H * D * 4;
-  static constexpr int RING = KEYS * ROWB > 4096 ? 2 : 3, WARPS = KEYS * ROWB > 4096 ? 6 : 4;
+  static constexpr int RING = KEYS * ROWB > 4096 ? 2 : 3;
   static constexpr int LPR = D / 4, KPW = 32 / LPR, KT = KEYS / KPW;
+  static constexpr bool MANY_REGS = NC == 4;  // more than 168 a thread
   static_assert(KT * H == LPR, "one score per lane");
   const float* qs;  // [NC * H][D], scaled
   float m[NC], l[NC];
@@ -240,7 +243,8 @@ __device__ __forceinline__ uint32_t pack2_rest(float lo, float hi, uint32_t pack
 template <int D>
 struct MmaEngine {
   using Elem = __nv_bfloat16;
-  static constexpr int DIM = D, KEYS = 32, ROWB = D * 2, RING = 2, WARPS = D == 128 ? 7 : 4, EXTRA = 0, KS = D / 16, NT = KEYS / 8;
+  static constexpr int DIM = D, KEYS = 32, ROWB = D * 2, RING = 2, EXTRA = 0, KS = D / 16, NT = KEYS / 8;
+  static constexpr bool MANY_REGS = false;
   uint32_t q[KS][4];
   float m[2], l[2], o[D / 8][4];
 
@@ -364,10 +368,22 @@ struct MmaEngine {
 };
 
 // ---------------------------------------------------------------------------- walk ----
+// One CTA per SM with as many warps as its shared memory has rings for (7, or as many on each
+// scheduler: 13 warps instead of 12 at d = 64 cost 200 requests 249 us against 225).  First slots are
+// dealt out across the SMs before a second warp of any gets one, so that a few runs spread over
+// all of them: with several smaller CTAs an SM, some SMs got three busy ones and some none (7 requests
+// of 4 to 22 thousand tokens, d = 64: 28.1 us against 23.9; 4 of about 700: 10.2 against 9.0).
+template <typename E>
+struct DecodeSmem {
+  static constexpr int STAGE = 2 * E::KEYS * E::ROWB, RING = E::RING * STAGE, EXTRA = RING, QUEUE = EXTRA + E::EXTRA;
+  static constexpr int WARP = (QUEUE + 4 * (int)sizeof(Run) + 127) / 128 * 128, MOST = 227 * 1024 / WARP;
+  static constexpr int WARPS = MOST < 8 ? MOST : MOST < 12 || E::MANY_REGS ? 8 : 12, HALF = 116 * 1024;
+  static constexpr int BYTES = WARPS * WARP > HALF ? WARPS * WARP : HALF;  // more than half: one CTA per SM
+};
+
 // The fetching side of a warp: which tile comes next, and where its keys lie.
 template <typename E>
 struct Walk {
-  static constexpr int STAGE = 2 * E::KEYS * E::ROWB;
   // (run, request, part) slots are numbered with the run slowest and dealt out in chunks of `chunk`
   // <= 32 consecutive ones, one per lane: the first by the warp's number, further ones from a
   // counter, as runs differ in length and many slots of short requests are empty.
@@ -380,7 +396,7 @@ struct Walk {
   Run mine;                      // this lane's run of it
   Run r;                         // the run being fetched
   bool live;                     // there is one
-  uint32_t row;                  // lane < KEYS: row of key r.u + lane (~0: none, or past the run's end)
+  int page;                      // lane < KEYS: page of key r.u + lane, on its way during the tile before
 
   __device__ __forceinline__ void look_ahead(const PagedDecode& a, int parts, int lane) {
     const uint32_t w = base + (uint32_t)lane, ny = (uint32_t)(a.hkv * parts), rows = (uint32_t)a.N * ny;
@@ -417,7 +433,7 @@ struct Walk {
       int n = 0;
       if (!counter) base = total;
       else if (lane == 0) n = atomicAdd(counter, 1);
-      if (counter) base = (gridDim.x * E::WARPS + (uint32_t)__shfl_sync(0xffffffffu, n, 0)) * chunk;
+      if (counter) base = (gridDim.x * DecodeSmem<E>::WARPS + (uint32_t)__shfl_sync(0xffffffffu, n, 0)) * chunk;
       look_ahead(a, parts, lane);
     }
     const int src = __ffs(left) - 1;
@@ -444,18 +460,13 @@ struct Walk {
       for (int h = 0; h < heads; ++h) a.lse[row + h] = bad ? x : -INFINITY;
   }
 
-  __device__ __forceinline__ void look_up(const PagedDecode& a, int parts, int lane, Run* queue, int tail) {
-    row = ~0u;
-    if (!live) return;
-    bool lost = false;
-    if (lane < E::KEYS && r.u + lane < r.end) {
-      const int j = r.key(r.u + lane), b = j >> a.page_shift;
-      const int page = b < a.max_blocks ? a.block_table[(int64_t)r.i * a.max_blocks + b] : -1;
-      lost = page < 0 || page >= a.num_pages;
-      if (!lost)
-        row = (uint32_t)((((int64_t)page * a.hkv + r.y / parts) << a.page_shift) + (j & ((1 << a.page_shift) - 1)));
-    }
-    if (__any_sync(0xffffffffu, lost) && lane == 0) queue[(tail - 1) & 3].bad = 1;
+  __device__ __forceinline__ bool has_key(int lane) const { return lane < E::KEYS && r.u + lane < r.end; }
+
+  __device__ __forceinline__ void look_up(const PagedDecode& a, int lane) {
+    page = -1;
+    if (!live || !has_key(lane)) return;
+    const int b = r.key(r.u + lane) >> a.page_shift;
+    if (b < a.max_blocks) page = a.block_table[(int64_t)r.i * a.max_blocks + b];
   }
 
   // The current tile into `stage`, then on to the next one (its rows are looked up meanwhile).
@@ -463,6 +474,12 @@ struct Walk {
   // rows G, G + step, ..., so that one shuffle and one address serve all of a row's pieces.
   __device__ __forceinline__ void fetch(const PagedDecode& a, int parts, uint32_t stage, int lane, Run* queue, int& tail) {
     if (live) {
+      uint32_t row = ~0u;  // of this lane's key in the pages: none, or its page is outside the cache
+      const bool lost = has_key(lane) && (page < 0 || page >= a.num_pages);
+      if (has_key(lane) && !lost)
+        row = (uint32_t)((((int64_t)page * a.hkv + r.y / parts) << a.page_shift) +
+                         (r.key(r.u + lane) & ((1 << a.page_shift) - 1)));
+      if (__any_sync(0xffffffffu, lost) && lane == 0) queue[(tail - 1) & 3].bad = 1;
       constexpr int PIECES = E::ROWB / 16, LANES = PIECES < 8 ? PIECES : 8;  // lanes of a row
       constexpr int ROWS = 32 / LANES, PARTS = PIECES / LANES;                // rows at a time, pieces of a lane
       const int g = lane / LANES, c = lane % LANES;
@@ -491,7 +508,7 @@ struct Walk {
       seek(a, parts, lane);
       if (live) push(a, parts, queue, tail, lane);
     }
-    look_up(a, parts, lane, queue, tail);
+    look_up(a, lane);
   }
   // a run that is fetched from here on: at most the computed one, two fetched tiles' and the next are open
   __device__ __forceinline__ void push(const PagedDecode& a, int parts, Run* queue, int& tail, int lane) {
@@ -505,13 +522,7 @@ struct Walk {
 };
 
 template <typename E>
-struct DecodeSmem {
-  static constexpr int STAGE = Walk<E>::STAGE, RING = E::RING * STAGE, EXTRA = RING, QUEUE = EXTRA + E::EXTRA;
-  static constexpr int WARP = (QUEUE + 4 * (int)sizeof(Run) + 127) / 128 * 128, BYTES = E::WARPS * WARP;
-};
-
-template <typename E>
-__global__ void __launch_bounds__(32 * E::WARPS) k_decode(const PagedDecode a, const int parts, const uint32_t chunk, int32_t* counter) {
+__global__ void __launch_bounds__(32 * DecodeSmem<E>::WARPS, 1) k_decode(const PagedDecode a, const int parts, const uint32_t chunk, int32_t* counter) {
   using L = DecodeSmem<E>;
   extern __shared__ __align__(128) unsigned char all[];
   unsigned char* sh = all + (threadIdx.x >> 5) * L::WARP;
@@ -524,14 +535,14 @@ __global__ void __launch_bounds__(32 * E::WARPS) k_decode(const PagedDecode a, c
   f.total = (uint32_t)(a.N * a.hkv * parts * a.max_splits);
   f.chunk = chunk;
   f.counter = counter;
-  f.base = (blockIdx.x * E::WARPS + (threadIdx.x >> 5)) * chunk;
+  f.base = ((threadIdx.x >> 5) * gridDim.x + blockIdx.x) * chunk;
   f.left = 0;
   int head = 0, tail = 0, put = 0, get = 0;
   f.look_ahead(a, parts, lane);
   if (counter) asm volatile("griddepcontrol.wait;" ::: "memory");  // it has been cleared
   f.seek(a, parts, lane);
   if (f.live) f.push(a, parts, queue, tail, lane);
-  f.look_up(a, parts, lane, queue, tail);
+  f.look_up(a, lane);
 #pragma unroll
   for (int s = 0; s < E::RING - 1; ++s) {
     f.fetch(a, parts, ring + put * L::STAGE, lane, queue, tail);
@@ -562,29 +573,30 @@ __global__ void __launch_bounds__(32 * E::WARPS) k_decode(const PagedDecode a, c
 }
 
 // ---------------------------------------------------------------------------- join ----
-// D / 4 lanes per (request, head) add the runs' records in ascending order, 8 at a time so that their
-// loads are in flight together; more than 32 runs are shared out to the block's groups of lanes,
-// whose sums are added in order (`split`: the blocks have one head each).  How a request's runs are added
+// D / 4 lanes per (request, head) add the runs' records in ascending order, 16 at a time so that their
+// loads are in flight together; more than 16 runs are shared out to the groups of lanes of a
+// block that has the head to itself (SPLIT), whose sums are added in order.  How a request's runs are added
 // depends on their number alone.  A request's CTAs also check its length and the pages of its
 // visible keys for the error word.
-template <int D, typename T>
-__global__ void __launch_bounds__(128) k_decode_join(const PagedDecode a, const bool split) {
-  constexpr int LANES = D / 4, GROUPS = 128 / LANES, B = 8;
-  __shared__ float4 so[GROUPS][LANES];
-  __shared__ float2 sml[GROUPS];
+constexpr int kJoinAtOnce = 16;
+template <int D, typename T, bool SPLIT>
+__global__ void __launch_bounds__(SPLIT ? 256 : 128) k_decode_join(const PagedDecode a) {
+  constexpr int THREADS = SPLIT ? 256 : 128, LANES = D / 4, GROUPS = THREADS / LANES, B = kJoinAtOnce;
+  __shared__ float4 so[SPLIT ? GROUPS : 1][LANES];
+  __shared__ float2 sml[SPLIT ? GROUPS : 1];
   // what does not come from the runs' kernel is read while that still runs
   const int g = threadIdx.x / LANES, lane = threadIdx.x % LANES, c = 4 * lane;
-  const int i = blockIdx.y, h = split ? blockIdx.x : blockIdx.x * GROUPS + g;
+  const int i = blockIdx.y, h = SPLIT ? blockIdx.x : blockIdx.x * GROUPS + g;
   const Request rq(a, a.seq_lens[i]);
   const int runs = split_of(rq.n, a.hkv).runs;
-  const bool shared = runs > 32;  // only with `split`
+  const bool shared = SPLIT && runs > B;
   const int per = shared ? (runs + GROUPS - 1) / GROUPS : runs;
   const int begin = shared ? min(runs, g * per) : 0, end = shared ? min(runs, begin + per) : runs;
   bool lost = false;  // a page of the request's visible keys is outside the cache
   if (rq.n) {
     const int first = rq.key(rq.head) >> a.page_shift, last = (rq.len - 1) >> a.page_shift;
     const int head_pages = rq.head ? ((rq.head - 1) >> a.page_shift) + 1 : 0;
-    for (int b = blockIdx.x * 128 + threadIdx.x; b < head_pages + last - first + 1; b += gridDim.x * 128) {
+    for (int b = blockIdx.x * THREADS + threadIdx.x; b < head_pages + last - first + 1; b += gridDim.x * THREADS) {
       const int p = b < head_pages ? b : first + b - head_pages;
       const int page = p < a.max_blocks ? a.block_table[(int64_t)i * a.max_blocks + p] : -1;
       lost |= page < 0 || page >= a.num_pages;
@@ -593,7 +605,7 @@ __global__ void __launch_bounds__(128) k_decode_join(const PagedDecode a, const 
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the runs' kernel has finished
   if (rq.bad && threadIdx.x == 0) set_error(a.hdr, GDN_DEVERR_POS);
   if (lost) set_error(a.hdr, GDN_DEVERR_PAGES);
-  if (runs > 1 && h < a.hq && (shared || !split || g == 0)) {
+  if (runs > 1 && h < a.hq && (shared || !SPLIT || g == 0)) {
     const int64_t row = (int64_t)i * a.hq + h;
     const float* rec = a.partial + row * a.max_splits * D + c;
     const float2* mls =
@@ -644,7 +656,7 @@ __global__ void __launch_bounds__(128) k_decode_join(const PagedDecode a, const 
         add(ml, x);
       }
     }
-    if (g == 0 || !split) {
+    if (g == 0 || !SPLIT) {
       store4(static_cast<T*>(a.out) + row * D + c,
              make_float4(__fdiv_rn(o.x, l), __fdiv_rn(o.y, l), __fdiv_rn(o.z, l), __fdiv_rn(o.w, l)));
       if (a.lse && c == 0) a.lse[row] = __fmul_rn(__fadd_rn(m, log2f(l)), kLn2);
@@ -663,14 +675,9 @@ int launch_decode(const PagedDecode& a, cudaStream_t st) {
   constexpr int D = E::DIM, BYTES = DecodeSmem<E>::BYTES;
   static std::atomic<uint64_t> ready{0};
   ensure_smem(k_decode<E>, BYTES, ready);
-  static const int per_sm = [] {  // CTAs an SM holds
-    int n = 1;
-    cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, k_decode<E>, 32 * E::WARPS, BYTES);
-    return n < 1 ? 1 : n;
-  }();
   const int group = a.hq / a.hkv, parts = (group + kHeadsPerRun - 1) / kHeadsPerRun;
-  const int64_t total = (int64_t)a.N * a.hkv * parts * a.max_splits, most = (int64_t)kSms * per_sm;
-  const int64_t need = (total + E::WARPS - 1) / E::WARPS, ctas = need < most ? need : most, warps = ctas * E::WARPS;
+  const int64_t total = (int64_t)a.N * a.hkv * parts * a.max_splits, ctas = total < kSms ? total : kSms;
+  const int64_t warps = ctas * DecodeSmem<E>::WARPS;
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
@@ -687,15 +694,18 @@ int launch_decode(const PagedDecode& a, cudaStream_t st) {
   // about eight chunks a warp, of single slots unless there are many
   const int64_t chunk = total / (8 * warps);
   c.gridDim = dim3((unsigned)ctas);
-  c.blockDim = dim3(32 * E::WARPS);
+  c.blockDim = dim3(32 * DecodeSmem<E>::WARPS);
   c.dynamicSmemBytes = BYTES;
   cudaLaunchKernelEx(&c, k_decode<E>, a, parts, (uint32_t)(chunk < 1 ? 1 : chunk > 32 ? 32 : chunk), counter);
-  const bool split = a.max_splits > 32;
+  const bool split = a.max_splits > kJoinAtOnce;
   c.gridDim = dim3(split ? a.hq : (a.hq + 512 / D - 1) / (512 / D), a.N);
-  c.blockDim = dim3(128);
+  c.blockDim = dim3(split ? 256 : 128);
   c.dynamicSmemBytes = 0;
   c.numAttrs = 1;
-  cudaLaunchKernelEx(&c, k_decode_join<D, typename E::Elem>, a, split);
+  if (split)
+    cudaLaunchKernelEx(&c, k_decode_join<D, typename E::Elem, true>, a);
+  else
+    cudaLaunchKernelEx(&c, k_decode_join<D, typename E::Elem, false>, a);
   return counter ? 3 : 2;
 }
 
