@@ -15,8 +15,9 @@ namespace {
 // these at once (their loads are issued together).  A warp takes one token's U * GPW heads of q, of
 // k or of v, so that nothing inside depends on which it is, and the few rows of
 // a decode step spread over warps.  With two pieces a lane the kernel issues half the instructions per row that one
-// piece costs, and packed pairs halve the arithmetic again; before both it was bound by issue
-// (202 us for 16384 tokens of 32 / 8 heads, d = 128, with the cache written).
+// piece costs, and packed pairs halve the arithmetic again; before both it was bound by issue.
+// 16384 tokens of 32 / 8 heads, d = 128, with the cache written: 202 us before, 85.5 now, 5.15 TB/s
+// (77% of a copy's rate), bound by the bytes and what is left of their latency.
 // =====================================================================================
 constexpr int kNormThreads = 128;
 
@@ -223,9 +224,12 @@ __global__ void __launch_bounds__(kNormThreads, U > 1 ? 8 : 1) k_norm_rope(const
 
 // Backward: dx per row, and with weights the sums of g x r over this block's items: each lane
 // adds its 8 columns in the order of the tokens it meets, then the block's rows of lanes in
-// ascending order; k_norm_rope_dw adds the blocks.
+// ascending order; k_norm_rope_dw adds the blocks.  Forward and gradient of 16384 tokens of 32 / 8 heads,
+// d = 128, rotated, with weights, bf16: 183 us (3.7 TB/s), 213 with two row sets at a time on five blocks an
+// SM instead of four on four: what bounds it is how many loads are in flight, and registers bound
+// those.
 template <int D, typename TI, typename TG, int U, bool W>
-__global__ void __launch_bounds__(kNormThreads, W ? 5 : 8) k_norm_rope_bwd(const NormRope a, const int runs) {
+__global__ void __launch_bounds__(kNormThreads, W ? 4 : 4) k_norm_rope_bwd(const NormRope a, const int runs) {
   constexpr int LPR = RowLanes<D>::LPR, GPW = RowLanes<D>::GPW;
   const int lane = threadIdx.x & 31;
   const int block = blockIdx.x / runs, blocks = gridDim.x / runs;  // of this run of heads
@@ -237,9 +241,12 @@ __global__ void __launch_bounds__(kNormThreads, W ? 5 : 8) k_norm_rope_bwd(const
   const Row8 w = W && wp ? load8p(wp + pc.at, pc.gap) : all8(1.f);
   const float cn = a.norm == GDN_NORM_RMS ? 1.f / D : a.norm == GDN_NORM_L2 ? 1.f : 0.f;
   Row8 acc = all8(0.f);
-  for (int64_t t = (int64_t)block * (kNormThreads / 32) + (threadIdx.x >> 5); t < a.T;
-       t += (int64_t)blocks * (kNormThreads / 32)) {
-    const int64_t p = a.rot ? a.pos[t] : 0;
+  const int64_t step = (int64_t)blocks * (kNormThreads / 32);
+  int64_t t = (int64_t)block * (kNormThreads / 32) + (threadIdx.x >> 5);
+  int next_p = a.rot && t < a.T ? a.pos[t] : 0;
+  for (; t < a.T; t += step) {
+    const int p = next_p;
+    if (a.rot && t + step < a.T) next_p = a.pos[t + step];  // a turn ahead: the angles wait for it
     const int64_t at = (t * it.heads + h) * D + pc.at;
     const TI* src = (it.kind ? static_cast<const TI*>(a.k) + t * a.k_stride
                              : static_cast<const TI*>(a.q) + t * a.q_stride) + h * D + pc.at;
@@ -306,9 +313,9 @@ __global__ void __launch_bounds__(256) k_norm_rope_dw(const float* __restrict__ 
 
 template <int D, typename TI, typename TO>
 void norm_rope_t(const NormRope& a, cudaStream_t st) {
-  // Few rows: one row set per warp, which ends sooner (4 tokens of 16 / 2 heads: 2.0 us against 2.8);
-  // from about 8 warps a scheduler on, four at once keep more loads in flight (16384 tokens: 96 us
-  // against 140).
+  // Few rows: one row set per warp, which ends sooner (4 tokens of 16 / 2 heads: 2.1 us against 2.8; 256 of
+  // 16 / 4: 2.6 against 3.2); from about 8 warps a scheduler on, four at once keep more loads in
+  // flight (1024 tokens of 16 / 4 heads: 4.2 us against 5.2; 16384 of 32 / 8: 85.6 against 158).
   constexpr int GPW = RowLanes<D>::GPW, WARPS = kNormThreads / 32;
   const int hv = a.v_pages ? a.hk : 0;
   const unsigned x = (unsigned)(((int64_t)a.T + WARPS - 1) / WARPS);
@@ -323,7 +330,7 @@ void norm_rope_t(const NormRope& a, cudaStream_t st) {
 
 template <int D, typename TI, typename TG>
 void norm_rope_bwd_t(const NormRope& a, cudaStream_t st) {
-  constexpr int U = 2, RUN = U * RowLanes<D>::GPW, WARPS = kNormThreads / 32;
+  constexpr int U = 4, RUN = U * RowLanes<D>::GPW, WARPS = kNormThreads / 32;
   const int nq = head_runs<RUN>(a.hq, 0, 0), runs = head_runs<RUN>(a.hq, a.hk, 0);
   int64_t x = ((int64_t)a.T + WARPS - 1) / WARPS;
   if (a.partial) {

@@ -13,6 +13,10 @@
 // other needs), per key block dk and dv over the group's heads in ascending order.
 // R is 4, or 2 where 64-row tiles would leave SMs without work: a row's arithmetic is the same in
 // both (the column blocks do not move), so its bits do not depend on the choice.
+// Forward and gradient, fp32, d = 64: 7 sequences of 54 to 271 tokens, 4 / 2 heads, 115 us with R = 2, 160
+// with 4; 4 of 512, 8 / 2 heads, 415 against 495; 8 of 2048, window 512, 3.99 ms against 3.67 with R = 4.
+// The short cases are bound by the latency of a tile's chain of products, barriers and exchanges,
+// the long ones by shared memory's reads beside the fp32 units.
 #include "attn_window.cuh"
 
 namespace gdn {
