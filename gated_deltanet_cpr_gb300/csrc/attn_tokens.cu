@@ -229,7 +229,7 @@ __global__ void __launch_bounds__(kNormThreads, U > 1 ? 8 : 1) k_norm_rope(const
 // SM instead of four on four: what bounds it is how many loads are in flight, and registers bound
 // those.
 template <int D, typename TI, typename TG, int U, bool W>
-__global__ void __launch_bounds__(kNormThreads, W ? 4 : 4) k_norm_rope_bwd(const NormRope a, const int runs) {
+__global__ void __launch_bounds__(kNormThreads, 4) k_norm_rope_bwd(const NormRope a, const int runs) {
   constexpr int LPR = RowLanes<D>::LPR, GPW = RowLanes<D>::GPW;
   const int lane = threadIdx.x & 31;
   const int block = blockIdx.x / runs, blocks = gridDim.x / runs;  // of this run of heads

@@ -10,7 +10,10 @@
 // the probabilities lie doubled and transposed in shared memory, so that one 16-byte read gives
 // the multipliers of two rows.  One pass over the keys with a running maximum and sum per row.
 // The gradient is two kernels, each deterministic: per query block dq (and do . o, which the
-// other needs), per key block dk and dv over the group's heads in ascending order.
+// other needs), per key block dk and dv.  There a cluster of CTAs shares out the group's heads and
+// adds its sums in ascending order through its shared memory (one CTA per key block, head after
+// head, took 77 us in the first case below, whose 39 blocks of 2 key heads leave half of the SMs
+// without one).
 // R is 4, or 2 where 64-row tiles would leave SMs without work: a row's arithmetic is the same in
 // both (the column blocks do not move), so its bits do not depend on the choice.
 // Forward and gradient, fp32, d = 64: 7 sequences of 54 to 271 tokens, 4 / 2 heads, 115 us with R = 2, 160
@@ -344,15 +347,33 @@ __global__ void __launch_bounds__(kThreads) k_window_dq(const WindowAttn a) {
   dq.template store<T>(a.dq, q.q0, row0, q.Lq, a.hq, h, ty, tx, f);
 }
 
+// CTAs of a key block: a power of two, from the group alone, so that it fixes the order of the sums
+inline int dkv_cluster(int group) { return group >= 8 ? 8 : group >= 4 ? 4 : group >= 2 ? 2 : 1; }
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float4 load4_of(uint32_t smem, int rank) {
+  float4 x;
+  asm volatile(
+      "{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %4, %5;\n ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [a];\n}"
+      : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
+      : "r"(smem), "r"(rank)
+      : "memory");
+  return x;
+}
+
 template <int D, typename T, int R>
-__global__ void __launch_bounds__(kThreads) k_window_dkv(const WindowAttn a) {
+__global__ void __launch_bounds__(kThreads) k_window_dkv(const WindowAttn a, const int ctas) {
   extern __shared__ float sh[];
   constexpr int BM = 16 * R, ROWS = BM * pitch<D>(), COLS = BN * pitch<D>();
   float *Ks = sh, *Vs = Ks + ROWS, *Qs = Vs + ROWS, *Os = Qs + COLS, *Ps = Os + COLS, *Ds = Ps + 64 * pp<R>();
   int j0;
   const Seq q = find_seq(a, blockIdx.x, BM, true, j0);
   if (!q.ok) return;
-  const int kvh = blockIdx.y, group = a.hq / a.hkv, ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+  const int kvh = blockIdx.y / ctas, rank = blockIdx.y % ctas, group = a.hq / a.hkv;
+  const int per = (group + ctas - 1) / ctas, h0 = rank * per, heads = max(0, min(per, group - h0));  // of this CTA
+  const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
   load_tile<D, T, BM>(Ks, a.k, q.k0, j0, q.Lk, a.hkv, kvh);
   load_tile<D, T, BM>(Vs, a.v, q.k0, j0, q.Lk, a.hkv, kvh);
   const QueryRange qr(q, j0, min(j0 + BM, q.Lk), a.window, a.sinks);
@@ -364,12 +385,12 @@ __global__ void __launch_bounds__(kThreads) k_window_dkv(const WindowAttn a) {
   Acc<D, R> dk, dv;
   dk.zero();
   dv.zero();
-  // column tiles: the query blocks of the group's heads, one head after the other
-  const int nb = b1 - b0, tiles = nb * group;
+  // column tiles: the query blocks of the heads, one head after the other
+  const int nb = b1 - b0, tiles = nb * heads;
   NextTile<D, T> qn, on;
   float lse_n[4], delta_n[4];  // of the thread's columns
   auto fetch = [&](int i) {
-    const int h = kvh * group + i / nb, row0 = (b0 + i % nb) * BN;
+    const int h = kvh * group + h0 + i / nb, row0 = (b0 + i % nb) * BN;
     qn.fetch(a.q, q.q0, row0, q.Lq, a.hq, h);
     on.fetch(a.dout, q.q0, row0, q.Lq, a.hq, h);
 #pragma unroll
@@ -409,11 +430,33 @@ __global__ void __launch_bounds__(kThreads) k_window_dkv(const WindowAttn a) {
     dv.add(Ps, Os, ty, tx);
     dk.add(Ds, Qs, ty, tx);
   }
-  float one[R], f[R];
+  // the cluster's sums meet in its shared memory; each CTA adds and stores its share of them
+  using A = Acc<D, R>;
+  float4* mine = reinterpret_cast<float4*>(Qs);
+  __syncthreads();
 #pragma unroll
-  for (int r = 0; r < R; ++r) one[r] = 1.f, f[r] = a.scale;
-  dv.template store<T>(a.dv, q.k0, j0, q.Lk, a.hkv, kvh, ty, tx, one);
-  dk.template store<T>(a.dk, q.k0, j0, q.Lk, a.hkv, kvh, ty, tx, f);
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int c = 0; c < A::C; ++c) {
+      mine[(r * A::C + c) * kThreads + threadIdx.x] = dk.v[r][c];
+      mine[((R + r) * A::C + c) * kThreads + threadIdx.x] = dv.v[r][c];
+    }
+  cluster_sync();
+  const uint32_t at = (uint32_t)__cvta_generic_to_shared(mine + threadIdx.x);
+  for (int s = rank; s < 2 * R * A::C; s += ctas) {
+    const int r = s / A::C % R, c = s % A::C, row = j0 + R * ty + r;
+    const bool k = s < R * A::C;
+    float4 x = load4_of(at + s * kThreads * 16, 0);
+    for (int o = 1; o < ctas && o * per < group; ++o) {
+      const float4 y = load4_of(at + s * kThreads * 16, o);
+      x = make_float4(__fadd_rn(x.x, y.x), __fadd_rn(x.y, y.y), __fadd_rn(x.z, y.z), __fadd_rn(x.w, y.w));
+    }
+    const float f = k ? a.scale : 1.f;
+    if (A::mine(tx) && row < q.Lk)
+      store4(static_cast<T*>(k ? a.dk : a.dv) + ((int64_t)(q.k0 + row) * a.hkv + kvh) * D + 4 * tx + 64 * c,
+             make_float4(__fmul_rn(x.x, f), __fmul_rn(x.y, f), __fmul_rn(x.z, f), __fmul_rn(x.w, f)));
+  }
+  cluster_sync();  // until all have read
 }
 
 template <void (*FN)(WindowAttn)>
@@ -438,8 +481,23 @@ void dq_r(const WindowAttn& a, cudaStream_t st) {
 }
 template <int D, typename T, int R>
 void dkv_r(const WindowAttn& a, cudaStream_t st) {
-  launch<k_window_dkv<D, T, R>>(dim3((unsigned)item_count(a.Tk, 16 * R, a.N), a.hkv),
-                                (2 * 16 * R + 2 * 64) * pitch<D>() + 2 * 64 * pp<R>(), a, st);
+  constexpr size_t BYTES = ((2 * 16 * R + 2 * 64) * pitch<D>() + 2 * 64 * pp<R>()) * sizeof(float);
+  static std::atomic<uint64_t> ready{0};
+  ensure_smem(k_window_dkv<D, T, R>, (int)BYTES, ready);
+  const int ctas = dkv_cluster(a.hq / a.hkv);
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = 1;
+  attr.val.clusterDim.y = (unsigned)ctas;
+  attr.val.clusterDim.z = 1;
+  cudaLaunchConfig_t c{};
+  c.gridDim = dim3((unsigned)item_count(a.Tk, 16 * R, a.N), a.hkv * ctas);
+  c.blockDim = dim3(kThreads);
+  c.dynamicSmemBytes = BYTES;
+  c.stream = st;
+  c.attrs = &attr;
+  c.numAttrs = 1;
+  cudaLaunchKernelEx(&c, k_window_dkv<D, T, R>, a, ctas);
 }
 template <int D, typename T>
 void fwd_t(const WindowAttn& a, cudaStream_t st) {
@@ -451,7 +509,7 @@ void dq_t(const WindowAttn& a, cudaStream_t st) {
 }
 template <int D, typename T>
 void dkv_t(const WindowAttn& a, cudaStream_t st) {
-  if (small_tiles(a.Tk, a.N, a.hkv)) dkv_r<D, T, 2>(a, st); else dkv_r<D, T, 4>(a, st);
+  if (small_tiles(a.Tk, a.N, a.hkv * dkv_cluster(a.hq / a.hkv))) dkv_r<D, T, 2>(a, st); else dkv_r<D, T, 4>(a, st);
 }
 
 }  // namespace

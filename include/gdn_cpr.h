@@ -506,7 +506,9 @@ gdn_status gdn_cpr_window_attn(const gdn_cpr_attn *attn, int32_t num_seqs, int32
                                void *ws, size_t ws_bytes, gdn_stream_t stream);
 
 /* Its gradient, from the forward's out and lse.  dq [total_q, H_q, d]; dk, dv [total_k, H_kv,
- * d], summed over a group's heads in ascending order; deterministic.                       */
+ * d], summed over a group's heads in a fixed order; deterministic.
+ * In both a masked key or value of the same sequence may take part with weight 0, so an infinity or
+ * NaN there can reach rows that do not see it; other sequences' rows never do.             */
 gdn_status gdn_cpr_window_attn_bwd(const gdn_cpr_attn *attn, int32_t num_seqs, int32_t total_q,
                                    int32_t total_k, const int32_t *cu_q, const int32_t *cu_k,
                                    const void *q, const void *k, const void *v, const void *out,
