@@ -13,11 +13,12 @@
 // other needs), per key block dk and dv.  There a cluster of CTAs shares out the group's heads and
 // adds its sums in ascending order through its shared memory (one CTA per key block, head after
 // head, took 77 us in the first case below, whose 39 blocks of 2 key heads leave half of the SMs
-// without one).
+// without one; 8 x 2048 tokens took 3.67 ms in all instead of 3.01).
 // R is 4, or 2 where 64-row tiles would leave SMs without work: a row's arithmetic is the same in
 // both (the column blocks do not move), so its bits do not depend on the choice.
-// Forward and gradient, fp32, d = 64: 7 sequences of 54 to 271 tokens, 4 / 2 heads, 115 us with R = 2, 160
-// with 4; 4 of 512, 8 / 2 heads, 415 against 495; 8 of 2048, window 512, 3.99 ms against 3.67 with R = 4.
+// Forward and gradient, fp32, d = 64: 7 sequences of 54 to 271 tokens, 4 / 2 heads, 80 us with R = 2, 113
+// with 4; 4 of 512, 8 / 2 heads, 327 against 315 (near the rule's edge); 8 of 2048, window 512, 3.48 ms
+// against 3.01 with R = 4.
 // The short cases are bound by the latency of a tile's chain of products, barriers and exchanges,
 // the long ones by shared memory's reads beside the fp32 units.
 #include "attn_window.cuh"
