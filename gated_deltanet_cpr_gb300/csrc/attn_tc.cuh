@@ -67,6 +67,17 @@ __device__ __forceinline__ bool elect_one() {
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity)) != 0;
 }
+// After a wait gave up, before memory is given back: the copies announced on a barrier, in whichever
+// phase they are, and (whole warp) the MMAs that this warp has issued; each with a limit of its own.
+__device__ __forceinline__ void settle(uint64_t* bar) {
+  mbar_wait(bar, 0, 1u << 10);
+  mbar_wait(bar, 1, 1u << 10);
+}
+__device__ __forceinline__ void settle_mma(uint64_t* unused) {
+  __syncwarp();
+  if (elect_one()) mma_commit(unused);
+  mbar_wait(unused, 0, 1u << 12);
+}
 __device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
 
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {

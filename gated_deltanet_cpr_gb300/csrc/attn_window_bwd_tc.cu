@@ -107,7 +107,7 @@ struct Tmem {
 
 struct Bars {
   uint64_t item_full[2], item_empty[2], x_full, x_empty, u_full[4], u_empty[4], w_full[4], w_empty[4], s_full[2], s_free,
-      p_full[2], p_free[2], acc_full, acc_empty, vec_full, vec_free, aux[2];
+      p_full[2], p_free[2], acc_full, acc_empty, vec_full, vec_free, aux[2], drain[2];
   uint32_t tmem;
   Item item[2];
 };
@@ -159,6 +159,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&B.item_full[i], 1);
       mbar_init(&B.item_empty[i], 11);  // all warps but the one that hands them out
       mbar_init(&B.aux[i], 1);
+      mbar_init(&B.drain[i], 1);
       mbar_init(&B.s_full[i], 1);
       mbar_init(&B.p_full[i], WARPS);
       mbar_init(&B.p_free[i], 1);
@@ -535,11 +536,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (!ok) set_error(a.hdr, GDN_DEVERR_TIMEOUT);
   if (__syncthreads_or(!ok)) {
-    // something gave up: copies that were issued land before the memory is given back
+    // something gave up: copies and MMAs that were issued end before the memory is given back
     if (warp == kLoadWarp && lane == 0) {
-      for (int i = 0; i < L::NU; ++i) mbar_wait(&B.u_full[i], 0, 1u << 12);
-      for (int i = 0; i < L::NW; ++i) mbar_wait(&B.w_full[i], 0, 1u << 12);
+      for (int i = 0; i < L::NU; ++i) settle(&B.u_full[i]);
+      settle(&B.x_full);
     }
+    if (warp == kLoadWarp2 && lane == 0)
+      for (int i = 0; i < L::NW; ++i) settle(&B.w_full[i]);
+    if (warp == kScoreWarp || warp == kAccWarp) settle_mma(&B.drain[warp == kAccWarp]);
   }
   __syncthreads();
   if (warp == kScoreWarp) tmem_dealloc(tm, 512);

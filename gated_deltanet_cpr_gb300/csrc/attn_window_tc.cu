@@ -95,7 +95,7 @@ struct FwdSmem {
 
 struct FwdBars {
   uint64_t item_full[2], item_empty[2], q_full, q_empty, kv_full[8], kv_empty[8], s_full[2], s_free, p_full[2], pv_done[2],
-      o_empty[2], aux;
+      o_empty[2], aux, drain[2];
   uint32_t tmem;
   Item item[2];
 };
@@ -129,6 +129,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&B.q_full, 1);
     mbar_init(&B.q_empty, 1);
     mbar_init(&B.aux, 1);
+    mbar_init(&B.drain[0], 1);
+    mbar_init(&B.drain[1], 1);
     fence_mbar_init();
   }
   __syncthreads();
@@ -412,9 +414,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (!ok) set_error(a.hdr, GDN_DEVERR_TIMEOUT);
   if (__syncthreads_or(!ok)) {
-    // something gave up: copies that were issued land before the memory is given back
-    if (warp == kLoadWarp && lane == 0)
-      for (int i = 0; i < L::STAGES; ++i) mbar_wait(&B.kv_full[i], 0, 1u << 12);
+    // something gave up: copies and MMAs that were issued end before the memory is given back
+    if (warp == kLoadWarp && lane == 0) {
+      for (int i = 0; i < L::STAGES; ++i) settle(&B.kv_full[i]);
+      settle(&B.q_full);
+    }
+    if (warp == kScoreWarp || warp == kAccWarp) settle_mma(&B.drain[warp == kAccWarp]);
   }
   __syncthreads();
   if (warp == kScoreWarp) tmem_dealloc(tm, 512);
