@@ -7,6 +7,7 @@ raises api.GdnError.  Shapes, masks and errors: include/gdn_cpr.h.
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
@@ -64,7 +65,8 @@ def rope_tables(rows, rot, base=10000.0, scale=1.0, device="cuda"):
 
 
 # The calls below run once or more per layer of a decode step, so the wrappers keep their own cost
-# low: one check per tensor, the raw stream handle, one allocation where several results go together.
+# low: one check per tensor that the caller gives, the raw stream handle, one allocation where several results
+# go together; descriptions of shapes and their workspace sizes are kept by their values.
 _raw_stream = torch._C._cuda_getCurrentRawStream
 
 
@@ -87,11 +89,13 @@ def _opt(x, shape, dtype, name):
 
 def _rows(x, heads, d, name):
     """(pointer, token stride) of [T, heads, d] whose heads are dense; tokens may be strided."""
-    if x.dim() != 3 or x.shape[1] != heads or x.shape[2] != d or not x.is_cuda:
+    shape = x.shape
+    if len(shape) != 3 or shape[1] != heads or shape[2] != d or not x.is_cuda:
         raise ValueError(f"{name} is {tuple(x.shape)} on {x.device}, expected [T, {heads}, {d}] on the GPU")
-    if x.numel() and (x.stride(2) != 1 or x.stride(1) != d):
+    tokens, head, entry = x.stride()
+    if (entry != 1 or head != d) and x.numel():
         raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return x.data_ptr(), (x.stride(0) if x.shape[0] > 1 else heads * d)
+    return x.data_ptr(), (tokens if shape[0] > 1 else heads * d)
 
 
 def _bytes(fn, *args):
@@ -102,6 +106,12 @@ def _bytes(fn, *args):
 
 def _workspace(x, nbytes):
     return torch.empty(nbytes, dtype=torch.uint8, device=x.device)
+
+
+@functools.lru_cache(maxsize=1024)
+def _norm_rope_desc(T, hq, hk, d, rot, rows, norm, layout, eps, in_dtype, out_dtype, grad_dtype, qs, ks, vs):
+    return NormRopeStruct(T, hq, hk, d, rot, rows, NORMS[norm], LAYOUTS[layout], eps, _dt(in_dtype), _dt(out_dtype),
+                          _dt(grad_dtype), qs, ks, vs)
 
 
 def _norm_rope_struct(q, k, v, norm, eps, cos, sin, positions, layout, out_dtype, grad_dtype):
@@ -120,9 +130,8 @@ def _norm_rope_struct(q, k, v, norm, eps, cos, sin, positions, layout, out_dtype
     vp, vs = (None, hk * d) if v is None else _rows(v, hk, d, "v")
     if v is not None and v.shape[0] != T:
         raise ValueError("q, k and v have the same tokens and dtype")
-    st = NormRopeStruct(T, hq, hk, d, rot, rows, NORMS[norm], LAYOUTS[layout], eps, _dt(q.dtype), _dt(out_dtype),
-                        _dt(grad_dtype), qs, ks, vs)
-    return st, qp, kp, vp, cp, sp, pp
+    return _norm_rope_desc(T, hq, hk, d, rot, rows, norm, layout, eps, q.dtype, out_dtype, grad_dtype, qs, ks, vs), \
+        qp, kp, vp, cp, sp, pp
 
 
 def qk_norm_rope(q, k, v=None, *, norm="rms", q_weight=None, k_weight=None, eps=1e-6, cos=None, sin=None,
@@ -133,22 +142,28 @@ def qk_norm_rope(q, k, v=None, *, norm="rms", q_weight=None, k_weight=None, eps=
     at slot_map [T] as well.  Returns (q_out, k_out); want_q / want_k leave one out."""
     od = out_dtype or (cache.k.dtype if cache is not None else q.dtype)
     st, qp, kp, vp, cp, sp, pp = _norm_rope_struct(q, k, v, norm, eps, cos, sin, positions, layout, od, od)
-    T, d = st.tokens, st.d
-    if q_out is None and want_q:
-        q_out = torch.empty((T, st.h_q, d), dtype=od, device=q.device)
-    if k_out is None and want_k:
-        k_out = torch.empty((T, st.h_k, d), dtype=od, device=q.device)
+    T, hq, hk, d = st.tokens, st.h_q, st.h_k, st.d
+    if q_out is not None:
+        qo = _want(q_out, (T, hq, d), od, "q_out")
+    else:
+        q_out = torch.empty((T, hq, d), dtype=od, device=q.device) if want_q else None
+        qo = q_out.data_ptr() if want_q else None
+    if k_out is not None:
+        ko = _want(k_out, (T, hk, d), od, "k_out")
+    else:
+        k_out = torch.empty((T, hk, d), dtype=od, device=q.device) if want_k else None
+        ko = k_out.data_ptr() if want_k else None
     kc = vc = slots = None
     pages = page = 0
     if cache is not None:
-        if cache.h_kv != st.h_k or cache.d != d or cache.k.dtype != od or v is None:
+        if cache.h_kv != hk or cache.d != d or cache.k.dtype != od or v is None:
             raise ValueError("the cache holds heads, size and dtype of k_out, and needs v")
         (kc, vc), pages, page = cache.pointers(), cache.pages, cache.page_size
         slots = _want(slot_map, (T,), torch.int32, "slot_map")
     _check("gdn_cpr_qk_norm_rope", api.load().gdn_cpr_qk_norm_rope(
         ctypes.byref(st), qp, kp, vp, _opt(q_weight, (d,), torch.float32, "q_weight"),
-        _opt(k_weight, (d,), torch.float32, "k_weight"), cp, sp, pp, _opt(q_out, (T, st.h_q, d), od, "q_out"),
-        _opt(k_out, (T, st.h_k, d), od, "k_out"), kc, vc, pages, page, slots, _raw_stream(q.device.index)))
+        _opt(k_weight, (d,), torch.float32, "k_weight"), cp, sp, pp, qo, ko, kc, vc, pages, page,
+        slots, _raw_stream(q.device.index)))
     return q_out, k_out
 
 
@@ -188,7 +203,10 @@ def page_map(lens, new_lens, free_pages, block_table, page_size, total_tokens):
     # one allocation: the header, then the results, positions and slots on 16-byte boundaries
     pad = -T % 4
     buf = torch.empty(HEADER_BYTES // 4 + 2 * (T + pad) + 2 * N + 2, dtype=i32, device=lens.device)
-    ws, pos, _, slots, _, seq, cu, used = buf.split_with_sizes([HEADER_BYTES // 4, T, pad, T, pad, N, N + 1, 1])
+    if pad:
+        ws, pos, _, slots, _, seq, cu, used = buf.split_with_sizes([HEADER_BYTES // 4, T, pad, T, pad, N, N + 1, 1])
+    else:
+        ws, pos, slots, seq, cu, used = buf.split_with_sizes([HEADER_BYTES // 4, T, T, N, N + 1, 1])
     at = buf.data_ptr()
     a_pos = at + HEADER_BYTES
     a_slots = a_pos + 4 * (T + pad)
@@ -203,8 +221,14 @@ def page_map(lens, new_lens, free_pages, block_table, page_size, total_tokens):
     return dict(seq_lens=seq, cu_seqlens=cu, positions=pos, slot_map=slots, pages_used=used, ws=ws)
 
 
+@functools.lru_cache(maxsize=1024)
 def _attn_struct(hq, hkv, d, window, sinks, scale, dtype):
     return AttnStruct(hq, hkv, d, window, sinks, scale or 0.0, _dt(dtype))
+
+
+@functools.lru_cache(maxsize=4096)
+def _attn_bytes(fn, hq, hkv, d, window, sinks, scale, dtype, *args):
+    return _bytes(fn, ctypes.byref(_attn_struct(hq, hkv, d, window, sinks, scale, dtype)), *args)
 
 
 def paged_decode(q, cache: PagedCache, block_table, seq_lens, *, window=0, sinks=0, scale=None, max_len=None, out=None,
@@ -212,26 +236,32 @@ def paged_decode(q, cache: PagedCache, block_table, seq_lens, *, window=0, sinks
     """gdn_cpr_paged_decode: attention of one token per request, q [N, Hq, d], over the cache's
     first seq_lens[n] tokens.  max_len bounds seq_lens (default: what block_table can hold).
     Returns out [N, Hq, d], or (out, lse) with want_lse."""
-    N, hq, d = q.shape
-    if cache.d != d or cache.k.dtype is not q.dtype:
+    shape, dtype, device = q.shape, q.dtype, q.device
+    N, hq, d = shape
+    if cache.d != d or cache.k.dtype is not dtype:
         raise ValueError("q and the cache have the same d and dtype")
-    if block_table.dim() != 2 or block_table.shape[0] != N:
+    table = block_table.shape
+    if len(table) != 2 or table[0] != N:
         raise ValueError("block_table is [N, max_blocks]")
+    blocks = table[1]
     if max_len is None:
-        max_len = block_table.shape[1] * cache.page_size
-    st = _attn_struct(hq, cache.h_kv, d, window, sinks, scale, q.dtype)
-    qp = _want(q, q.shape, q.dtype, "q")
+        max_len = blocks * cache.page_size
+    desc = (hq, cache.h_kv, d, window, sinks, scale, dtype)
+    qp = _want(q, shape, dtype, "q")
     if out is None:
         out = torch.empty_like(q)
-    lse = torch.empty((N, hq), dtype=torch.float32, device=q.device) if want_lse else None
+        op = out.data_ptr()
+    else:
+        op = _want(out, shape, dtype, "out")
+    lse = torch.empty((N, hq), dtype=torch.float32, device=device) if want_lse else None
     if ws is None:
-        ws = _workspace(q, _bytes("gdn_cpr_paged_decode_workspace_size", ctypes.byref(st), N, max_len))
+        ws = _workspace(q, _attn_bytes("gdn_cpr_paged_decode_workspace_size", *desc, N, max_len))
     kp, vp = cache.pointers()
     _check("gdn_cpr_paged_decode", api.load().gdn_cpr_paged_decode(
-        ctypes.byref(st), N, max_len, qp, kp, vp, cache.pages, cache.page_size,
-        _want(block_table, block_table.shape, torch.int32, "block_table"), block_table.shape[1],
-        _want(seq_lens, (N,), torch.int32, "seq_lens"), _want(out, q.shape, q.dtype, "out"),
-        None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.numel(), _raw_stream(q.device.index)))
+        ctypes.byref(_attn_struct(*desc)), N, max_len, qp, kp, vp, cache.pages, cache.page_size,
+        _want(block_table, table, torch.int32, "block_table"), blocks,
+        _want(seq_lens, (N,), torch.int32, "seq_lens"), op,
+        None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.numel(), _raw_stream(device.index)))
     return (out, lse) if want_lse else out
 
 
@@ -240,12 +270,14 @@ def _window_setup(q, k, v, cu_q, cu_k, window, sinks, scale, backward, ws):
     Tk, hkv, _ = k.shape
     N = cu_q.numel() - 1
     cu_k = cu_q if cu_k is None else cu_k
-    st = _attn_struct(hq, hkv, d, window, sinks, scale, q.dtype)
-    args = (ctypes.byref(st), N, Tq, Tk, _want(cu_q, (N + 1,), torch.int32, "cu_seqlens"),
-            _want(cu_k, (N + 1,), torch.int32, "cu_seqlens_k"), _want(q, q.shape, q.dtype, "q"),
-            _want(k, (Tk, hkv, d), q.dtype, "k"), _want(v, (Tk, hkv, d), q.dtype, "v"))
+    dtype, shape = q.dtype, (Tk, hkv, d)
+    desc = (hq, hkv, d, window, sinks, scale, dtype)
+    offsets = _want(cu_q, (N + 1,), torch.int32, "cu_seqlens")
+    args = (ctypes.byref(_attn_struct(*desc)), N, Tq, Tk, offsets,
+            offsets if cu_k is cu_q else _want(cu_k, (N + 1,), torch.int32, "cu_seqlens_k"),
+            _want(q, q.shape, dtype, "q"), _want(k, shape, dtype, "k"), _want(v, shape, dtype, "v"))
     if ws is None:
-        ws = _workspace(q, _bytes("gdn_cpr_window_attn_workspace_size", args[0], Tq, int(backward)))
+        ws = _workspace(q, _attn_bytes("gdn_cpr_window_attn_workspace_size", *desc, Tq, int(backward)))
     return args, ws
 
 
