@@ -59,6 +59,13 @@ def test_grouped_heads(attn, hq, hk, dtype):
     check(attn, [70, 200], hq=hq, hk=hk, d=128, dtype=dtype, window=50, sinks=2)
 
 
+@pytest.mark.parametrize("dtype,d", [(BF, 128), (BF, 32), (F32, 128), (F32, 32)])
+@pytest.mark.parametrize("hq", [9, 12, 17])
+def test_more_than_eight_heads_of_a_key_head(attn, dtype, d, hq):
+    """In 32 bits the gradient shares them out over at most eight CTAs, some of which then have none."""
+    check(attn, [90, 0, 150], hq=hq, hk=1, d=d, dtype=dtype, window=60, sinks=3)
+
+
 @pytest.mark.parametrize("dtype,d", [(BF, 128), (BF, 64), (BF, 32), (F32, 64)])
 @pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (5, 2), (64, 0), (100, 4), (128, 130), (129, 300), (0, 7),
                                           (300, 1), (1000, 3), (2 ** 31 - 1, 2 ** 31 - 1)])
