@@ -106,6 +106,19 @@ def test_batch_and_pages_do_not_change_bits(attn, gdn):
         assert a.shape == b.shape and torch.isfinite(b).all()
 
 
+@pytest.mark.parametrize("dtype,d", [(BF, 64), (BF, 128), (F32, 64), (BF, 32)])
+def test_many_requests_beside_a_long_one(attn, gdn, dtype, d):
+    """More runs than warps, most of them empty, and requests of one to many runs; the same bits whatever
+    max_len says, and alone."""
+    lens = [(37 * i) % 211 for i in range(250)] + [3000, 700, 9000, 1]
+    out = check(attn, gdn, lens, 8, 4, d, 16, dtype, seed=3)
+    q, _, _, cache, table, n = make(attn, lens, 8, 4, d, 16, dtype, seed=3)
+    assert torch.equal(out, attn.paged_decode(q.cuda(), cache, table, n, max_len=100000))
+    for i in (5, 249, 250, 251, 252):
+        one = attn.paged_decode(q[i:i + 1].cuda(), cache, table[i:i + 1].contiguous(), n[i:i + 1], max_len=lens[i])
+        assert torch.equal(one, out[i:i + 1]), i
+
+
 def test_bad_lengths_and_pages_are_reported(attn, gdn):
     for lens in ([50, 60, 70], [400, 300, 900]):
         q, ks, vs, cache, table, n = make(attn, lens, 4, 2, 64, 16, BF)
