@@ -161,6 +161,7 @@ __device__ __forceinline__ HeadRun head_run(const NormRope& a, int c) {
   return r;
 }
 
+// Eight blocks an SM (64 registers): with six the prefill case took 92 us, with nine, which spill, 100.
 template <int D, typename TI, typename TO, int U>
 __global__ void __launch_bounds__(kNormThreads, U > 1 ? 8 : 1) k_norm_rope(const NormRope a, const int runs) {
   constexpr int LPR = RowLanes<D>::LPR, GPW = RowLanes<D>::GPW;
