@@ -78,7 +78,7 @@ __host__ __device__ inline int target_shift(int n, int hkv) {
   return x < 128 * kRunsPerRequest ? 6 : x < 256 * kRunsPerRequest ? 7 : x < 512 * kRunsPerRequest ? 8 : 9;
 }
 __host__ __device__ inline int target_runs(int n, int hkv) {
-  const int s = target_shift(n, hkv), r = (n + (1 << s >> 1)) >> s;
+  const int s = target_shift(n, hkv), r = (int)(((unsigned)n + (1u << s >> 1)) >> s);  // n + 256 may pass 2^31
   return r < 1 ? 1 : r;
 }
 struct Split {

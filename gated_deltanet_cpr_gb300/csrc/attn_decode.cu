@@ -55,10 +55,13 @@ __device__ __forceinline__ void cp_async16_or_zero(uint32_t smem, const void* gm
 }
 
 // One run: request i, key head and part of its query heads, which run, and its keys [u, end); bad:
-// a key's page is outside the cache.
+// a key's page is outside the cache.  Keys are numbered without a sign: a request may end a tile
+// short of 2^31, and the walk steps past its end.
 struct Run {
-  int i, y, run, runs, u, end, head, skip, bad;
-  __device__ __forceinline__ int key(int x) const { return x < head ? x : x + skip; }
+  int i, y, run, runs;
+  uint32_t u, end;
+  int head, skip, bad;
+  __device__ __forceinline__ int key(uint32_t x) const { return (int)x < head ? (int)x : (int)x + skip; }
 };
 
 // Where a run's (m, l, a) or output goes: rows of its heads.
@@ -423,8 +426,8 @@ struct Walk {
         mine.run = next_run;
         mine.runs = s.runs;
         have = next_run < s.runs;
-        mine.u = next_run * s.keys;
-        mine.end = min(rq.n, mine.u + s.keys);
+        mine.u = (uint32_t)next_run * (uint32_t)s.keys;
+        mine.end = min((uint32_t)rq.n, mine.u + (uint32_t)s.keys);
         mine.head = rq.head;
         mine.skip = rq.skip;
         if (s.runs == 0 && next_run == 0) write_empty(a, mine, parts, rq.bad);
@@ -561,7 +564,7 @@ __global__ void __launch_bounds__(32 * DecodeSmem<E>::WARPS, 1) k_decode(const P
       put = put + 1 == E::RING ? 0 : put + 1;
       asm volatile("cp.async.wait_group %0;" ::"n"(E::RING - 1) : "memory");
       __syncwarp();
-      eng.tile(a, sh + get * L::STAGE, r.end - r.u, lane);
+      eng.tile(a, sh + get * L::STAGE, (int)(r.end - r.u), lane);
       get = get + 1 == E::RING ? 0 : get + 1;
       __syncwarp();
     }

@@ -477,11 +477,13 @@ typedef struct {
 /* Attention of one new token per request over the paged cache: q [N, H_q, d] is the token at
  * position seq_lens[n] - 1, whose key and value are already in the cache.  seq_lens[n] = 0
  * gives zeros.  The visible keys are split over their count and joined in a fixed order.
- *   seq_lens [N] int32; max_len >= every seq_lens (sizes the grid; a longer or negative one
- *   sets GDN_DEVERR_POS and gives NaN for that request); a page index outside [0, num_pages)
- *   sets GDN_DEVERR_PAGES, NaN likewise
+ *   seq_lens [N] int32; max_len >= every seq_lens (sizes the grid and, without a window, the
+ *   workspace: about H_q max_len / 512 records of d + 2 floats a request; a longer or negative
+ *   length sets GDN_DEVERR_POS and gives NaN for that request); a page index outside
+ *   [0, num_pages) sets GDN_DEVERR_PAGES, NaN likewise
  *   out [N, H_q, d];  lse NULL or [N, H_q] fp32: the log-sum-exp of the scaled scores
- *   num_pages * H_kv * page_size < 2^32 - 1
+ *   num_pages * H_kv * page_size < 2^32 - 1; N <= 65535; fewer than 2^30 runs at max_len over
+ *   the batch (N H_kv ceil(H_q / H_kv / 16) max(1, max_len / 512), or by the visible keys)
  *   ws: gdn_cpr_paged_decode_workspace_size bytes; its error word is set by every call      */
 gdn_status gdn_cpr_paged_decode(const gdn_cpr_attn *attn, int32_t num_seqs, int32_t max_len,
                                 const void *q, const void *k_pages, const void *v_pages,

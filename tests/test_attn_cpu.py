@@ -96,6 +96,32 @@ def test_decode_workspace_grows_with_the_splits(lib):
     assert size(10 ** 6, window=100, sinks=4) == size(104)
 
 
+def split_runs(n, hkv):
+    """Runs of a request that sees n keys, by the rule of csrc/attn.h in unbounded integers."""
+    x = n * hkv
+    shift = 6 if x < 128 * 32 else 7 if x < 256 * 32 else 8 if x < 512 * 32 else 9
+    r = max(1, (n + (1 << shift >> 1)) >> shift)
+    keys = (-(-n // r) + 31) // 32 * 32
+    return -(-n // keys) if n else 0
+
+
+@pytest.mark.parametrize("hkv", [1, 2, 3, 8, 40])
+def test_decode_workspace_holds_every_run(lib, hkv):
+    """Up to the largest length that 32 bits hold; the join reads a record for each run."""
+    d, N = 64, 2
+    top = 2 ** 31 - 1
+    lengths = sorted({*range(1, 700), *range(700, 40000, 97), *(32 * x // hkv + e for x in (128, 256, 512) for e in (-2, -1, 0, 1, 2)),
+                      10 ** 6, 10 ** 8, *(top - e for e in (300, 257, 256, 255, 254, 129, 128, 64, 32, 31, 1, 0))})
+    before = 0
+    for m in lengths:
+        n, st = ctypes.c_size_t(0), attn_struct(h_q=hkv, h_kv=hkv, d=d)
+        assert lib.gdn_cpr_paged_decode_workspace_size(ctypes.byref(st), N, m, ctypes.byref(n)) == 0
+        runs = split_runs(m, hkv)
+        assert runs <= 1 or n.value >= 256 + N * hkv * runs * (d + 2) * 4, m
+        assert n.value >= before, m
+        before = n.value
+
+
 def test_window_attn_refusals(lib):
     def fwd(N=2, Tq=10, Tk=10, ws=FAKE, n=1 << 30, cq=FAKE, q=FAKE, k=FAKE, out=FAKE, lse=FAKE, **kw):
         st = attn_struct(**kw)
