@@ -49,6 +49,7 @@ bool ok_stride(int64_t stride, int heads, const gdn_cpr_norm_rope* c) {
 
 gdn_status check_tables(const gdn_cpr_norm_rope* c, const float* cos, const float* sin, const int32_t* pos) {
   if (c->rot == 0 || c->tokens == 0) return GDN_OK;
+  if (c->table_rows < 1) return GDN_ERR_INVALID_ARG;  // a token outside the tables still reads their row 0
   return ok_ptr(cos, 16) && ok_ptr(sin, 16) && ok_ptr(pos, 4) ? GDN_OK : GDN_ERR_INVALID_ARG;
 }
 

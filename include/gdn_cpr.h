@@ -395,7 +395,7 @@ typedef struct {
     int32_t h_q, h_k;    /* heads of q and of k (and v); T (h_q + 2 h_k) < 2^31 */
     int32_t d;
     int32_t rot;         /* rotated entries at the front of every head: 0 or a multiple of 8, <= d */
-    int32_t table_rows;  /* rows of cos and sin */
+    int32_t table_rows;  /* rows of cos and sin; at least 1 where tokens are rotated */
     gdn_norm norm;
     gdn_rope_layout layout;
     float eps;

@@ -50,6 +50,15 @@ def test_norm_rope_refusals(lib):
     assert bwd(dwk=None) == 1 and bwd(rot=12) == 2 and bwd(k_stride=32) == 1
 
 
+def test_norm_rope_refuses_empty_tables(lib):
+    """Tokens outside the tables read their first row, so there has to be one."""
+    for rows, tokens, rot, code in [(0, 4, 16, 1), (0, 0, 16, 0), (-1, 4, 16, 1)]:
+        st = norm_struct(table_rows=rows, tokens=tokens, rot=rot)
+        assert lib.gdn_cpr_qk_norm_rope(ctypes.byref(st), *[FAKE] * 10, None, None, 0, 16, None, None) == code
+    st = norm_struct(table_rows=0)
+    assert lib.gdn_cpr_qk_norm_rope_bwd(ctypes.byref(st), *[FAKE] * 13, FAKE, 1 << 30, None) == 1
+
+
 def test_page_map_refusals(lib):
     def call(N=2, T=4, page=16, blocks=4, free=3, ws=FAKE, n=256, **kw):
         p = {m: kw.pop(m, FAKE) for m in ("lens", "new", "fp", "table", "seq", "cu", "pos", "slots", "used")}
