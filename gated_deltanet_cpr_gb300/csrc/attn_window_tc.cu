@@ -15,9 +15,10 @@
 // tokens, window 2048: 329 us at 58% tensor activity).
 // The probabilities are rounded to bf16 for their product (the row sums are of the unrounded fp32
 // values); S, O, m, l stay in 32 bits.  The maximum that P is scaled by is only moved, and O
-// rescaled, when a row's true maximum passes it by more than 2^8: P then stays below 2^8, where
-// bf16 and fp32 are as exact as below 1, and the rescaling (a TMEM round trip) is rare.  Blocks
-// that no row of a tile sees are skipped tile by tile.
+// rescaled, when a true maximum of the warp's rows passes it by more than 2^8: P then stays below 2^8,
+// where bf16 and fp32 are as exact as below 1, and the rescaling (a TMEM round trip) is rare.  Only the
+// sequence's own rows count there, so that its bits do not depend on what follows it.  Blocks that no
+// row of a tile sees are skipped tile by tile.
 //
 // Warps: 0-3 softmax of tile 0, 4-7 of tile 1, 8 issues the scores' products, 9 loads (TMA), 10
 // issues P V, 11 only completes the warpgroup whose registers the softmax warps take over.  The loader
@@ -331,7 +332,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int c = 4; c < BN; c += 4) mx = max3(mx, s[c], s[c + 1]), my = max3(my, s[c + 2], s[c + 3]);
         mx = fmaxf(mx, my);
-        const bool move = __fmul_rn(__fsub_rn(mx, m), sc) > 8.f;  // true for the first finite maximum
+        // true for the first finite maximum; rows past the sequence's end, which hold another's queries, do
+        // not decide by which maximum the warp's other rows are scaled
+        const bool move = row < tile.rows && __fmul_rn(__fsub_rn(mx, m), sc) > 8.f;
         if (started) {  // P V of the last block is done: P's place is free, and O at rest
           ok = mbar_wait(&B.pv_done[t], (npv - 1) & 1);
           if (!ok) break;

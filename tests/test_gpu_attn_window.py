@@ -117,6 +117,25 @@ def test_other_sequences_do_not_matter(attn, dtype, d):
             assert torch.equal(alone[n], dirty[n][a:b]), (n, junk)
 
 
+@pytest.mark.parametrize("dtype,d", [(BF, 128), (BF, 64), (BF, 32), (F32, 64)])
+@pytest.mark.parametrize("n,window,sinks,scale", [(200, 73, 0, None), (333, 90, 3, 0.5), (333, 0, 0, None), (530, 0, 0, 0.4),
+                                                  (141, 0, 0, 5.0), (700, 256, 1, 5.0)])
+def test_later_sequences_do_not_move_a_row_s_maximum(attn, dtype, d, n, window, sinks, scale):
+    """Sequences of several key blocks that end inside a tile and inside a warp's rows: the same bits alone
+    and before rows of any size, whose scores move their running maximum at every block."""
+    kw = dict(window=window, sinks=sinks, scale=scale)
+    x = make([n, 150], [n, 150], 4, 2, d, dtype, seed=n)
+    one = {m: x[m][:n] for m in ("q", "k", "v", "do")} | dict(cq=cu([n]), ck=cu([n]))
+    alone = run(attn, one, **kw)
+    for size in (1.0, 1e3, -1e3, float("nan"), float("inf")):
+        y = {m: t.clone() for m, t in x.items()}
+        for m in ("q", "k", "v", "do"):
+            y[m][n:] *= size
+        got = run(attn, y, **kw)
+        for m in alone:
+            assert torch.equal(alone[m], got[m][:n]), (m, size)
+
+
 @pytest.mark.parametrize("dtype,d", [(BF, 128), (BF, 64), (BF, 32), (F32, 128), (F32, 32)])
 def test_batch_size_does_not_change_bits(attn, dtype, d):
     """A sequence alone and among many (which may choose other tiles and schedules)."""
