@@ -540,9 +540,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kLoadWarp && lane == 0) {
       for (int i = 0; i < L::NU; ++i) settle(&B.u_full[i]);
       settle(&B.x_full);
+      settle(&B.aux[0]);
     }
-    if (warp == kLoadWarp2 && lane == 0)
+    if (warp == kLoadWarp2 && lane == 0) {
       for (int i = 0; i < L::NW; ++i) settle(&B.w_full[i]);
+      settle(&B.aux[1]);
+    }
     if (warp == kScoreWarp || warp == kAccWarp) settle_mma(&B.drain[warp == kAccWarp]);
   }
   __syncthreads();

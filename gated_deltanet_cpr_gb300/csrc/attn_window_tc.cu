@@ -421,6 +421,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kLoadWarp && lane == 0) {
       for (int i = 0; i < L::STAGES; ++i) settle(&B.kv_full[i]);
       settle(&B.q_full);
+      settle(&B.aux);
     }
     if (warp == kScoreWarp || warp == kAccWarp) settle_mma(&B.drain[warp == kAccWarp]);
   }
