@@ -422,8 +422,8 @@ def noalloc_device_error(device=None) -> int:
 
 
 def test_wait_timeout(calls: int) -> None:
-    """gdn_cpr_test_wait_timeout (test hook): the next `calls` tensor-core prefills from
-    this thread make one boundary-chain CTA's bounded wait run out."""
+    """gdn_cpr_test_wait_timeout (test hook): the next `calls` tensor-core prefills or window
+    attention calls from this thread make one CTA's bounded wait run out."""
     load().gdn_cpr_test_wait_timeout(int(calls))
 
 

@@ -135,6 +135,8 @@ gdn_status window_args(const gdn_cpr_attn* attn, int32_t N, int32_t Tq, int32_t 
   return GDN_OK;
 }
 
+bool window_on_tensor_cores(const gdn_cpr_attn* a) { return a->dtype == GDN_BF16 && a->d != 32; }
+
 size_t window_bytes(const gdn_cpr_attn* a, int32_t Tq, bool backward) {
   return align_up(GDN_CPR_ATTN_HEADER_BYTES + (backward ? 2 * (size_t)Tq * a->h_q * sizeof(float) : 0));
 }
@@ -353,6 +355,7 @@ gdn_status gdn_cpr_window_attn(const gdn_cpr_attn* attn, int32_t num_seqs, int32
   w.out = out;
   w.lse = lse;
   w.hdr = static_cast<WsHeader*>(ws);
+  w.fault_wait = take_wait_fault(window_on_tensor_cores(attn));
   Stages stg(stream, kWindowStages);
   if (!launch_window_attn(w, attn->dtype == GDN_BF16, stream)) return GDN_ERR_CUDA;
   stg.mark(1);
@@ -380,6 +383,7 @@ gdn_status gdn_cpr_window_attn_bwd(const gdn_cpr_attn* attn, int32_t num_seqs, i
   w.dv = dv;
   w.delta = reinterpret_cast<float*>(at(ws, GDN_CPR_ATTN_HEADER_BYTES));
   w.hdr = static_cast<WsHeader*>(ws);
+  w.fault_wait = take_wait_fault(window_on_tensor_cores(attn));
   Stages stg(stream, kWindowBwdStages);
   if (!launch_window_dq(w, attn->dtype == GDN_BF16, stream)) return GDN_ERR_CUDA;
   stg.mark(1);

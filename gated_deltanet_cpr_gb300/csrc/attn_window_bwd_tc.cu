@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   __syncthreads();
   const uint32_t tm = B.tmem;
-  bool ok = true;
+  bool ok = !fault_wait(a) || warp == kLoadWarp;
 
   if (warp >= 8) {
     regs_less<kOtherRegs>();
@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int c0 = DKV ? (c.from + blk) * BC : c.col0(i), head = DKV ? it.h * group + gh : it.h / group;
           if (DKV && ++blk == c.nb) blk = 0, ++gh;
           const int left = len - c0;  // rows of this sequence in the tile
-          ok = mbar_wait(&empty[at], (round & 1) ^ 1);
+          ok = mbar_wait(&empty[at], (round & 1) ^ 1 ^ fault_wait(a), wait_limit(a));
           if (!ok) break;
           unsigned char* dst = tiles + at * L::COLS;
           uint64_t* bar = left < BC ? aux : &full[at];

@@ -137,7 +137,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   const uint32_t tm = B.tmem;
   const uint32_t tS = tm, tP[2] = {tm + 128, tm + 192}, tO[2] = {tm + 256, tm + 256 + D};
-  bool ok = true;
+  bool ok = !fault_wait(a) || warp == kLoadWarp;
 
   if (warp >= 8) {
     regs_less<kOtherRegs>();
@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; i < p.count() && ok; ++i) {
         const int j0 = p.block(i) * BN;
         for (int kv = 0; kv < 2; ++kv) {
-          ok = mbar_wait(&B.kv_empty[stage], (round & 1) ^ 1);
+          ok = mbar_wait(&B.kv_empty[stage], (round & 1) ^ 1 ^ fault_wait(a), wait_limit(a));
           if (!ok) break;
           unsigned char* dst = sm + L::KV + stage * L::TILE;
           const bool tail = kv == 1 && j0 + BN > it.q.Lk;

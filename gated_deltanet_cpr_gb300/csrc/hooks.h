@@ -1,4 +1,4 @@
-// hooks.h -- the profiling hook and the NVTX ranges of the C-ABI entry points.
+// hooks.h -- the profiling hook, the wait-timeout test hook and the NVTX ranges of the C-ABI entry points.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -10,6 +10,15 @@ namespace gdn {
 
 // set by gdn_cpr_set_profile for the calling thread
 extern thread_local gdn_cpr_profile* t_profile;
+// set by gdn_cpr_test_wait_timeout for the calling thread: calls left whose first CTA gives up a wait
+// that nothing completes
+extern thread_local int32_t t_wait_fault;
+// one such call, where it has a wait to give up
+inline int take_wait_fault(bool has_one) {
+  if (!has_one || t_wait_fault <= 0) return 0;
+  --t_wait_fault;
+  return 1;
+}
 
 // NVTX range over one entry point (host-side markers for profilers such as Nsight; no
 // effect without a tool attached).

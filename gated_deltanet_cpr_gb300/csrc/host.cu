@@ -15,6 +15,7 @@
 
 namespace gdn {
 thread_local gdn_cpr_profile* t_profile = nullptr;
+thread_local int32_t t_wait_fault = 0;
 }
 
 namespace {
@@ -133,10 +134,6 @@ gdn_status check_cache(const gdn_cpr_cache* c) {
     return GDN_ERR_INVALID_ARG;
   return GDN_OK;
 }
-
-// gdn_cpr_test_wait_timeout: calls left that make the tensor-core chain's first CTA give up
-// a wait that nothing completes
-thread_local int32_t t_wait_fault = 0;
 
 // Continued prefill: the virtual prefill's regions, then the virtual cu_seqlens, tail
 // lengths, base positions, the gathered q, k, v, g, beta and the virtual output.
@@ -267,10 +264,7 @@ gdn_status run_forward(const gdn_cpr_shape* shape, const void* q, const void* k,
     cw.cache_slots = cache->slots;
     cw.slot_of_seq = slot_of_seq;
   }
-  if (t_wait_fault > 0 && boundary_on_tensor_cores(d)) {
-    cw.fault_wait = 1;
-    --t_wait_fault;
-  }
+  cw.fault_wait = take_wait_fault(boundary_on_tensor_cores(d));
   launch_chain(d, k, W, U, gamma, cw, hdr, st);
   stg.mark(1);
 

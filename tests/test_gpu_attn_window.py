@@ -204,3 +204,28 @@ def test_nothing_to_do(attn, gdn):
         assert (got["dk"] == 0).all() and (got["dv"] == 0).all()
         got = run(attn, make([5, 0], [0, 0], 2, 1, d, dtype))
         assert (got["out"] == 0).all() and (got["dq"] == 0).all() and (got["lse"] == -float("inf")).all()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_a_wait_that_runs_out_is_reported(attn, gdn, d):
+    """The test hook makes the loader of the first CTA wait for a phase that nothing completes, its row tiles'
+    copies under way, and give up: the memory is given back, the error word says so, and the next calls run as
+    usual."""
+    x = make([500, 260], [500, 260], 4, 2, d, BF)
+    ref = run(attn, x, window=100, sinks=2)
+    c = {n: t.cuda() for n, t in x.items()}
+    ws = gdn.alloc_workspace(1 << 20, "cuda")
+    kw = dict(cu_seqlens_k=c["ck"], window=100, sinks=2, ws=ws)
+    calls = (lambda: attn.window_attn(c["q"], c["k"], c["v"], c["cq"], **kw),
+             lambda: attn.window_attn_bwd(c["q"], c["k"], c["v"], ref["out"], ref["lse"], c["do"], c["cq"], **kw))
+    for call in calls:
+        gdn.test_wait_timeout(1)
+        try:
+            call()
+            assert gdn.device_error(ws) == 4  # GDN_DEVERR_TIMEOUT
+        finally:
+            gdn.test_wait_timeout(0)
+        call()
+        assert gdn.device_error(ws) == 0
+    got = run(attn, x, window=100, sinks=2)
+    assert all(torch.equal(got[n], ref[n]) for n in ref)
