@@ -97,6 +97,17 @@ int decode_splits(const gdn_cpr_attn* a, int32_t max_len) {
   return paged_decode_max_splits(visible_keys(max_len, a->window, a->sinks), a->h_kv);
 }
 
+// An empty call sets its error word too.  It queues nothing else, so it also passes where there is no
+// device, and memory that the device does not know is left alone.
+gdn_status empty_call(void* ws, cudaStream_t st) {
+  cudaPointerAttributes p{};
+  if (cudaPointerGetAttributes(&p, ws) != cudaSuccess || p.type == cudaMemoryTypeUnregistered) {
+    cudaGetLastError();
+    return GDN_OK;
+  }
+  return cudaMemsetAsync(ws, 0, sizeof(WsHeader), st) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
 gdn_status finish() { return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA; }
 
 // Rows of a packed batch of window_attn: position + window stays inside 32 bits.
@@ -304,7 +315,7 @@ gdn_status gdn_cpr_paged_decode(const gdn_cpr_attn* attn, int32_t num_seqs, int3
   const int64_t parts = (attn->h_q / attn->h_kv + 15) / 16;
   if ((double)num_seqs * attn->h_kv * parts * splits >= (double)(1 << 30)) return GDN_ERR_UNSUPPORTED;
   if (!ok_ws(ws, ws_bytes, decode_bytes(attn, num_seqs, splits))) return GDN_ERR_WORKSPACE;
-  if (num_seqs == 0) return GDN_OK;
+  if (num_seqs == 0) return empty_call(ws, stream);
   PagedDecode a{};
   a.N = num_seqs;
   a.hq = attn->h_q;
@@ -351,7 +362,7 @@ gdn_status gdn_cpr_window_attn(const gdn_cpr_attn* attn, int32_t num_seqs, int32
   if (rc != GDN_OK) return rc;
   if (total_q > 0 && (!ok_ptr(out, 16) || !ok_ptr(lse, 4))) return GDN_ERR_INVALID_ARG;
   if (!ok_ws(ws, ws_bytes, window_bytes(attn, total_q, false))) return GDN_ERR_WORKSPACE;
-  if (num_seqs == 0) return GDN_OK;
+  if (num_seqs == 0) return empty_call(ws, stream);
   w.out = out;
   w.lse = lse;
   w.hdr = static_cast<WsHeader*>(ws);
@@ -374,7 +385,7 @@ gdn_status gdn_cpr_window_attn_bwd(const gdn_cpr_attn* attn, int32_t num_seqs, i
     return GDN_ERR_INVALID_ARG;
   if (total_k > 0 && (!ok_ptr(dk, 16) || !ok_ptr(dv, 16))) return GDN_ERR_INVALID_ARG;
   if (!ok_ws(ws, ws_bytes, window_bytes(attn, total_q, true))) return GDN_ERR_WORKSPACE;
-  if (num_seqs == 0) return GDN_OK;
+  if (num_seqs == 0) return empty_call(ws, stream);
   w.out = const_cast<void*>(out);
   w.lse = const_cast<float*>(lse);
   w.dout = dout;

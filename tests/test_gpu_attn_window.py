@@ -206,6 +206,40 @@ def test_nothing_to_do(attn, gdn):
         assert (got["out"] == 0).all() and (got["dq"] == 0).all() and (got["lse"] == -float("inf")).all()
 
 
+def test_empty_calls_set_the_error_word(attn, gdn):
+    """A workspace that held an error, or anything at all, says after a call of no sequences that nothing was wrong."""
+    for dtype, d in ((BF, 128), (BF, 32), (F32, 64)):
+        x = {n: t.cuda() for n, t in make([100, 30], [100, 30], 2, 1, d, dtype).items()}
+        e = {n: t.cuda() for n, t in make([], [], 2, 1, d, dtype).items()}
+        q1 = torch.zeros((1, 2, d), dtype=dtype, device="cuda")
+        cache = attn.PagedCache(2, 16, 1, d, dtype)
+        table, none = torch.zeros((1, 2), dtype=torch.int32, device="cuda"), torch.zeros(0, dtype=torch.int32, device="cuda")
+        bad = torch.tensor([0, 140, 130], dtype=torch.int32, device="cuda")
+        ws = gdn.alloc_workspace(1 << 20, "cuda")
+        empty = (lambda: attn.window_attn(e["q"], e["k"], e["v"], e["cq"], ws=ws),
+                 lambda: attn.window_attn_bwd(e["q"], e["k"], e["v"], e["q"], e["q"][..., 0].float(), e["q"], e["cq"], ws=ws),
+                 lambda: attn.paged_decode(q1[:0], cache, table[:0], none, ws=ws))
+        for call in empty:
+            attn.window_attn(x["q"], x["k"], x["v"], bad, ws=ws)
+            assert gdn.device_error(ws) == 1
+            call()
+            assert gdn.device_error(ws) == 0
+            ws.fill_(0x55)
+            call()
+            assert gdn.device_error(ws) == 0
+    # and inside a graph
+    ws.fill_(0x55)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        for call in empty:
+            call()
+    for _ in range(2):
+        ws.fill_(0x55)
+        g.replay()
+        assert gdn.device_error(ws) == 0
+
+
 @pytest.mark.parametrize("d", [64, 128])
 def test_a_wait_that_runs_out_is_reported(attn, gdn, d):
     """The test hook makes the loader of the first CTA wait for a phase that nothing completes, its row tiles'
