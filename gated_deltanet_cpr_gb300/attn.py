@@ -87,6 +87,12 @@ def _opt(x, shape, dtype, name):
     return None if x is None else _want(x, shape, dtype, name)
 
 
+def _clip(x):
+    """A window, a count of first tokens or a bound on lengths, in 32 bits: lengths have no more, so anything
+    past them means the same; negative ones stay so, for the library to refuse."""
+    return max(-1, min(int(x), 2 ** 31 - 1))
+
+
 def _rows(x, heads, d, name):
     """(pointer, token stride) of [T, heads, d] whose heads are dense; tokens may be strided."""
     shape = x.shape
@@ -199,6 +205,8 @@ def page_map(lens, new_lens, free_pages, block_table, page_size, total_tokens):
     cu_seqlens, positions, slot_map, pages_used, and ws, whose error word says what was wrong
     (api.device_error)."""
     N, T = lens.numel(), int(total_tokens)
+    if not 0 <= T < 2 ** 31:
+        raise ValueError(f"total_tokens is {T}: not a count that fits 32 bits")
     i32 = torch.int32
     # one allocation: the header, then the results, positions and slots on 16-byte boundaries
     pad = -T % 4
@@ -214,7 +222,7 @@ def page_map(lens, new_lens, free_pages, block_table, page_size, total_tokens):
     if block_table.dim() != 2 or block_table.shape[0] != N:
         raise ValueError("block_table is [N, max_blocks]")
     _check("gdn_cpr_page_map", api.load().gdn_cpr_page_map(
-        N, T, page_size, block_table.shape[1], free_pages.numel(), _want(lens, (N,), i32, "lens"),
+        N, T, _clip(page_size), block_table.shape[1], free_pages.numel(), _want(lens, (N,), i32, "lens"),
         _want(new_lens, (N,), i32, "new_lens"), _want(free_pages, free_pages.shape, i32, "free_pages"),
         _want(block_table, block_table.shape, i32, "block_table"), a_seq, a_seq + 4 * N, a_pos, a_slots,
         a_seq + 8 * N + 4, at, HEADER_BYTES, _raw_stream(lens.device.index)))
@@ -223,7 +231,7 @@ def page_map(lens, new_lens, free_pages, block_table, page_size, total_tokens):
 
 @functools.lru_cache(maxsize=1024)
 def _attn_struct(hq, hkv, d, window, sinks, scale, dtype):
-    return AttnStruct(hq, hkv, d, window, sinks, scale or 0.0, _dt(dtype))
+    return AttnStruct(hq, hkv, d, _clip(window), _clip(sinks), scale or 0.0, _dt(dtype))
 
 
 @functools.lru_cache(maxsize=4096)
@@ -246,6 +254,7 @@ def paged_decode(q, cache: PagedCache, block_table, seq_lens, *, window=0, sinks
     blocks = table[1]
     if max_len is None:
         max_len = blocks * cache.page_size
+    max_len = _clip(max_len)
     desc = (hq, cache.h_kv, d, window, sinks, scale, dtype)
     qp = _want(q, shape, dtype, "q")
     if out is None:

@@ -161,6 +161,19 @@ def test_binding_refuses_tensors_that_do_not_fit():
             call()
 
 
+def test_binding_keeps_sizes_past_32_bits():
+    """They used to wrap: a window of 2^32 + 5 became one of 5."""
+    top = 2 ** 31 - 1
+    for given, meant in [(0, 0), (5, 5), (top, top), (top + 1, top), (2 ** 32, top), (2 ** 32 + 5, top), (-1, -1),
+                         (-2 ** 31 - 3, -1)]:
+        st = attn._attn_struct(4, 2, 64, given, given, None, torch.bfloat16)
+        assert st.window == st.sinks == meant
+    z = torch.zeros(2, dtype=torch.int32)
+    for total in (2 ** 31, 2 ** 32 + 4, -1):
+        with pytest.raises(ValueError, match="total_tokens"):
+            attn.page_map(z, z, z, z[:, None], 16, total)
+
+
 def test_rope_tables():
     c, s = attn.rope_tables(10, 8, base=100.0, scale=2.0, device="cpu")
     ang = 7 / 2.0 * 100.0 ** (-torch.arange(0, 8, 2).double() / 8)

@@ -119,6 +119,15 @@ def test_many_requests_beside_a_long_one(attn, gdn, dtype, d):
         assert torch.equal(one, out[i:i + 1]), i
 
 
+def test_sizes_past_32_bits(attn):
+    """A bound, a window or a count of first tokens past 2^31 is none."""
+    q, _, _, cache, table, n = make(attn, [500, 20], 4, 2, 64, 16, BF)
+    near = attn.paged_decode(q.cuda(), cache, table, n, window=64)
+    for most in (2 ** 31, 2 ** 32 + 10):
+        assert torch.equal(near, attn.paged_decode(q.cuda(), cache, table, n, window=64, max_len=most))
+        assert torch.equal(attn.paged_decode(q.cuda(), cache, table, n), attn.paged_decode(q.cuda(), cache, table, n, window=most))
+
+
 def test_bad_lengths_and_pages_are_reported(attn, gdn):
     for lens in ([50, 60, 70], [400, 300, 900]):
         q, ks, vs, cache, table, n = make(attn, lens, 4, 2, 64, 16, BF)
