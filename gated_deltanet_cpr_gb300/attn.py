@@ -99,7 +99,7 @@ def _rows(x, heads, d, name):
     if len(shape) != 3 or shape[1] != heads or shape[2] != d or not x.is_cuda:
         raise ValueError(f"{name} is {tuple(x.shape)} on {x.device}, expected [T, {heads}, {d}] on the GPU")
     tokens, head, entry = x.stride()
-    if (entry != 1 or head != d) and x.numel():
+    if (entry != 1 or (head != d and heads > 1)) and x.numel():
         raise ValueError(f"{name}: the heads of a token must be contiguous")
     return x.data_ptr(), (tokens if shape[0] > 1 else heads * d)
 

@@ -90,6 +90,15 @@ def test_strided_projection_and_other_stream(attn):
         attn.qk_norm_rope(q[:, ::2], k, norm="l2")
 
 
+def test_one_head_of_any_stride(attn):
+    """The stride of an axis of one head says nothing: a tensor that is dense all the same is taken."""
+    k = torch.randn(1, 9, 64, device="cuda").to(BF).transpose(0, 1)
+    q = torch.randn(9, 2, 64, device="cuda").to(BF)
+    assert k.is_contiguous() and k.stride(1) != 64
+    got, ref = attn.qk_norm_rope(q, k, norm="l2"), attn.qk_norm_rope(q, k.clone(memory_format=torch.contiguous_format).view(9, 1, 64), norm="l2")
+    assert torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1])
+
+
 def test_cache_write_and_skipped_slots(attn):
     T, hq, hk, d, page = 37, 4, 2, 128, 16
     x, _ = inputs(T, hq, hk, d, 32, BF, 3, True)
