@@ -119,6 +119,33 @@ def test_many_requests_beside_a_long_one(attn, gdn, dtype, d):
         assert torch.equal(one, out[i:i + 1]), i
 
 
+@pytest.mark.parametrize("dtype,d", [(BF, 64), (BF, 128), (F32, 128), (BF, 32)])
+def test_pages_do_not_change_bits(attn, dtype, d):
+    """The same keys and values on pages of every size, in any order, between rows of any kind."""
+    lens, hk = [700, 1, 2500, 64, 129], 2
+    g = torch.Generator().manual_seed(7)
+    q, ks, vs = (torch.randn((n, h, d), generator=g).to(dtype) for n, h in
+                 ((len(lens), 8), (sum(lens), hk), (sum(lens), hk)))
+    n, first = torch.tensor(lens, dtype=torch.int32).cuda(), None
+    for page in (16, 32, 64, 128, 256):
+        for seed, junk in ((0, 0.0), (1, float("nan")), (2, 3e38)):
+            blocks = [-(-x // page) for x in lens]
+            ids = torch.randperm(sum(blocks) + 5, generator=g.manual_seed(seed)).tolist()
+            kp, vp = (torch.full((len(ids), hk, page, d), junk, dtype=dtype) for _ in range(2))
+            table, at = torch.full((len(lens), max(blocks)), -1, dtype=torch.int32), 0
+            for i, x in enumerate(lens):
+                for b in range(blocks[i]):
+                    p, m = ids.pop(), min(page, x - b * page)
+                    table[i, b] = p
+                    kp[p, :, :m] = ks[at:at + m].transpose(0, 1)
+                    vp[p, :, :m] = vs[at:at + m].transpose(0, 1)
+                    at += m
+            cache = attn.PagedCache.wrap(kp.cuda(), vp.cuda())
+            got = [attn.paged_decode(q.cuda(), cache, table.cuda(), n, window=w, sinks=s) for w, s in ((0, 0), (300, 5))]
+            first = first or got
+            assert all(torch.equal(a, b) for a, b in zip(got, first)), (page, junk)
+
+
 def test_sizes_past_32_bits(attn):
     """A bound, a window or a count of first tokens past 2^31 is none."""
     q, _, _, cache, table, n = make(attn, [500, 20], 4, 2, 64, 16, BF)
