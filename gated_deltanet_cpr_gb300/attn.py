@@ -207,6 +207,8 @@ def page_map(lens, new_lens, free_pages, block_table, page_size, total_tokens):
     N, T = lens.numel(), int(total_tokens)
     if not 0 <= T < 2 ** 31:
         raise ValueError(f"total_tokens is {T}: not a count that fits 32 bits")
+    if page_size >= 2 ** 31:
+        page_size = -1
     i32 = torch.int32
     # one allocation: the header, then the results, positions and slots on 16-byte boundaries
     pad = -T % 4
@@ -222,7 +224,7 @@ def page_map(lens, new_lens, free_pages, block_table, page_size, total_tokens):
     if block_table.dim() != 2 or block_table.shape[0] != N:
         raise ValueError("block_table is [N, max_blocks]")
     _check("gdn_cpr_page_map", api.load().gdn_cpr_page_map(
-        N, T, _clip(page_size), block_table.shape[1], free_pages.numel(), _want(lens, (N,), i32, "lens"),
+        N, T, page_size, block_table.shape[1], free_pages.numel(), _want(lens, (N,), i32, "lens"),
         _want(new_lens, (N,), i32, "new_lens"), _want(free_pages, free_pages.shape, i32, "free_pages"),
         _want(block_table, block_table.shape, i32, "block_table"), a_seq, a_seq + 4 * N, a_pos, a_slots,
         a_seq + 8 * N + 4, at, HEADER_BYTES, _raw_stream(lens.device.index)))
@@ -254,7 +256,8 @@ def paged_decode(q, cache: PagedCache, block_table, seq_lens, *, window=0, sinks
     blocks = table[1]
     if max_len is None:
         max_len = blocks * cache.page_size
-    max_len = _clip(max_len)
+    if not 0 <= max_len < 2 ** 31:
+        max_len = _clip(max_len)
     desc = (hq, cache.h_kv, d, window, sinks, scale, dtype)
     qp = _want(q, shape, dtype, "q")
     if out is None:
