@@ -423,7 +423,7 @@ def noalloc_device_error(device=None) -> int:
 
 def test_wait_timeout(calls: int) -> None:
     """gdn_cpr_test_wait_timeout (test hook): the next `calls` tensor-core prefills or window
-    attention calls from this thread make one CTA's bounded wait run out."""
+    attention calls from this thread make bounded waits run out."""
     load().gdn_cpr_test_wait_timeout(int(calls))
 
 

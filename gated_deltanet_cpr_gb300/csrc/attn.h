@@ -108,8 +108,8 @@ struct WindowAttn {
   float* delta;  // 2 Tq hq floats that dq leaves for dk, dv: do . o [Tq, hq] (fp32 SIMT), or
                  // lse log2 e [hq, Tq] (infinite for a row that sees nothing) and do . o [hq, Tq]
   WsHeader* hdr;
-  int fault_wait;  // test hook of the tensor-core kernels, 0 or 1: the first CTA's loader waits for a phase that
-                   // nothing completes, with the row tiles' copies under way
+  int fault_wait;  // test hook of the tensor-core kernels: they start a copy, wait for a phase that nothing
+                   // completes, and give up
 };
 // false: nothing was queued
 bool launch_window_attn(const WindowAttn& a, bool bf16, cudaStream_t st);

@@ -94,6 +94,17 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, i
       : "memory");
 }
 
+// Test hook, all threads of a CTA: the warp with `load` starts the copy of the map's first box, of
+// `bytes`, on `full`, and all wait for a phase of `unused` that nothing completes.  False: they gave up.
+__device__ __forceinline__ bool wait_for_nothing(const CUtensorMap* map, void* box, uint32_t bytes, uint64_t* full,
+                                                 uint64_t* unused, bool load) {
+  if (load && elect_one()) {
+    mbar_expect_tx(full, bytes);
+    tma_load_3d(box, map, 0, 0, 0, full);
+  }
+  return mbar_wait(unused, 0, 1u << 10);
+}
+
 // Warp: 128 consecutive fp32 columns of this thread's TMEM lane in one load, waited for
 __device__ __forceinline__ void tmem_ld128(uint32_t taddr, float* v) {
   uint32_t r[128];

@@ -68,13 +68,6 @@ __device__ __forceinline__ void check_tables(const WindowAttn& a) {
   if (threadIdx.x == 0) a.hdr->err = any ? GDN_DEVERR_CU_SEQLENS : 0;
 }
 
-// Test hook (0 or 1): turns the parity of a wait of the first CTA's loader, so that nothing completes it,
-// and its limit down; the CTA's other warps have given up from the start.
-__device__ __forceinline__ uint32_t fault_wait(const WindowAttn& a) {
-  return blockIdx.x == 0 ? (uint32_t)a.fault_wait : 0u;
-}
-__device__ __forceinline__ uint32_t wait_limit(const WindowAttn& a) { return a.fault_wait ? 1u << 10 : 1u << 22; }
-
 __device__ __forceinline__ bool visible(int p, int j, int window, int sinks) {
   return j <= p && (window <= 0 || p - j < window || j < sinks);
 }

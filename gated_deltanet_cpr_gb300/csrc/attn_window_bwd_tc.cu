@@ -139,7 +139,8 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
-template <int D, bool DKV>
+// FAULT: the test hook's form, which gives up at once.
+template <int D, bool DKV, bool FAULT>
 __global__ void __launch_bounds__(kThreads, 1)
     k_window_bwd_tc(const WindowAttn a, const int64_t blocks, const int64_t work, int* next_item, float* vec,
                     const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap my,
@@ -183,9 +184,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   __syncthreads();
   const uint32_t tm = B.tmem;
-  bool ok = !fault_wait(a) || warp == kLoadWarp;
+  bool ok = true;
 
-  if (warp >= 8) {
+  if constexpr (FAULT) {
+    ok = wait_for_nothing(&mx, sm + L::X, BR * 128, &B.x_full, &B.drain[0],
+                          warp == kLoadWarp && (DKV ? a.Tk : a.Tq) > 0);
+  } else if (warp >= 8) {
     regs_less<kOtherRegs>();
     if (warp == kLoadWarp || warp == kLoadWarp2) {
       // --------------------------------------------------------------- loaders ----
@@ -246,7 +250,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int c0 = DKV ? (c.from + blk) * BC : c.col0(i), head = DKV ? it.h * group + gh : it.h / group;
           if (DKV && ++blk == c.nb) blk = 0, ++gh;
           const int left = len - c0;  // rows of this sequence in the tile
-          ok = mbar_wait(&empty[at], (round & 1) ^ 1 ^ fault_wait(a), wait_limit(a));
+          ok = mbar_wait(&empty[at], (round & 1) ^ 1);
           if (!ok) break;
           unsigned char* dst = tiles + at * L::COLS;
           uint64_t* bar = left < BC ? aux : &full[at];
@@ -552,7 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kScoreWarp) tmem_dealloc(tm, 512);
 }
 
-template <int D, bool DKV>
+template <int D, bool DKV, bool FAULT>
 bool bwd_tc(const WindowAttn& a, cudaStream_t st) {
   CUtensorMap mx, my, mu, mw;
   constexpr int BC = kCols<DKV>;
@@ -569,10 +573,16 @@ bool bwd_tc(const WindowAttn& a, cudaStream_t st) {
   const int64_t blocks = item_count(DKV ? a.Tk : a.Tq, BR, a.N);
   const int64_t work = DKV ? (blocks + a.N) * a.hkv : blocks * a.hq;
   static std::atomic<uint64_t> ready{0};
-  ensure_smem(k_window_bwd_tc<D, DKV>, (Smem<D, DKV>::BYTES), ready);
-  k_window_bwd_tc<D, DKV><<<(unsigned)(work < kSms ? work : kSms), kThreads, (Smem<D, DKV>::BYTES), st>>>(
+  ensure_smem(k_window_bwd_tc<D, DKV, FAULT>, (Smem<D, DKV>::BYTES), ready);
+  k_window_bwd_tc<D, DKV, FAULT><<<(unsigned)(work < kSms ? work : kSms), kThreads, (Smem<D, DKV>::BYTES), st>>>(
       a, blocks, work, a.hdr->pad + (DKV ? 1 : 0), a.delta, mx, my, mu, mw);
   return true;
+}
+
+template <bool DKV>
+bool by_size(const WindowAttn& a, cudaStream_t st) {
+  if (a.fault_wait) return a.d == 128 ? bwd_tc<128, DKV, true>(a, st) : bwd_tc<64, DKV, true>(a, st);
+  return a.d == 128 ? bwd_tc<128, DKV, false>(a, st) : bwd_tc<64, DKV, false>(a, st);
 }
 
 }  // namespace
@@ -580,10 +590,10 @@ bool bwd_tc(const WindowAttn& a, cudaStream_t st) {
 bool launch_window_dq_tc(const WindowAttn& a, cudaStream_t st) {
   // the error word and the two item counters
   if (cudaMemsetAsync(a.hdr, 0, sizeof(WsHeader), st) != cudaSuccess) return false;
-  return a.d == 128 ? bwd_tc<128, false>(a, st) : bwd_tc<64, false>(a, st);
+  return by_size<false>(a, st);
 }
 bool launch_window_dkv_tc(const WindowAttn& a, cudaStream_t st) {
-  return a.d == 128 ? bwd_tc<128, true>(a, st) : bwd_tc<64, true>(a, st);
+  return by_size<true>(a, st);
 }
 
 }  // namespace gdn

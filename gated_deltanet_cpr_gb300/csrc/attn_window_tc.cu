@@ -305,7 +305,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int cnt = tile.head + tile.to - tile.from, r0 = it.row0 + BM * t, p0 = r0 + it.q.Lk - it.q.Lq;
       const int p1 = p0 + tile.rows - 1, pos = p0 + row;
       const int lo = a.window > 0 ? pos - a.window + 1 : 0;
-      float m = -INFINITY;  // the maximum that P and O are scaled by
+      // The maximum that P and O are scaled by.  Rows past the sequence's end, which hold another's queries,
+      // start above all: they never decide by which maximum the warp's other rows are scaled.
+      float m = row < tile.rows ? -INFINITY : INFINITY;
       float2 l2 = make_float2(0.f, 0.f);
       bool started = false;
       for (int i = 0; i < cnt; ++i) {
@@ -332,9 +334,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int c = 4; c < BN; c += 4) mx = max3(mx, s[c], s[c + 1]), my = max3(my, s[c + 2], s[c + 3]);
         mx = fmaxf(mx, my);
-        // true for the first finite maximum; rows past the sequence's end, which hold another's queries, do
-        // not decide by which maximum the warp's other rows are scaled
-        const bool move = row < tile.rows && __fmul_rn(__fsub_rn(mx, m), sc) > 8.f;
+        const bool move = __fmul_rn(__fsub_rn(mx, m), sc) > 8.f;  // true for a live row's first finite maximum
         if (started) {  // P V of the last block is done: P's place is free, and O at rest
           ok = mbar_wait(&B.pv_done[t], (npv - 1) & 1);
           if (!ok) break;

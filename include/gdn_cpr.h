@@ -355,8 +355,7 @@ gdn_status gdn_cpr_noalloc_device_error(gdn_stream_t stream, int32_t *code);
  * memory and exits, so gdn_cpr_get_device_error reports the timeout and the context stays
  * usable.  The outputs of such a call are not valid.  calls <= 0 switches it off.
  * gdn_cpr_window_attn and gdn_cpr_window_attn_bwd calls on tensor cores (bf16, d = 64 or 128) count too:
- * there the loading warp of one CTA (of each gradient kernel) waits so, and gives up, with its first
- * copies under way.                                                                     */
+ * there every CTA (of both gradient kernels) waits so, and gives up, with a copy under way. */
 void gdn_cpr_test_wait_timeout(int32_t calls);
 
 /* Synchronises `stream`, then reads the device error word of `ws` (the workspace of the

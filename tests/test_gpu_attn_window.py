@@ -242,9 +242,8 @@ def test_empty_calls_set_the_error_word(attn, gdn):
 
 @pytest.mark.parametrize("d", [64, 128])
 def test_a_wait_that_runs_out_is_reported(attn, gdn, d):
-    """The test hook makes the loader of the first CTA wait for a phase that nothing completes, its row tiles'
-    copies under way, and give up: the memory is given back, the error word says so, and the next calls run as
-    usual."""
+    """The test hook makes the kernels start a copy, wait for a phase that nothing completes, and give up: their
+    memory is given back, the error word says so, and the next calls run as usual."""
     x = make([500, 260], [500, 260], 4, 2, d, BF)
     ref = run(attn, x, window=100, sinks=2)
     c = {n: t.cuda() for n, t in x.items()}
