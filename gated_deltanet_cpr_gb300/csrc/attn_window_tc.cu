@@ -102,7 +102,8 @@ struct FwdBars {
 };
 static_assert(sizeof(FwdBars) <= 1024, "fits its place");
 
-template <int D>
+// FAULT: the test hook's form, which gives up at once.
+template <int D, bool FAULT>
 __global__ void __launch_bounds__(kThreads, 1)
     k_window_fwd_tc(const WindowAttn a, const int64_t items, int* next_item, const __grid_constant__ CUtensorMap mq,
                     const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
@@ -137,9 +138,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   const uint32_t tm = B.tmem;
   const uint32_t tS = tm, tP[2] = {tm + 128, tm + 192}, tO[2] = {tm + 256, tm + 256 + D};
-  bool ok = !fault_wait(a) || warp == kLoadWarp;
+  bool ok = true;
 
-  if (warp >= 8) {
+  if constexpr (FAULT) {
+    ok = wait_for_nothing(&mq, sm + L::Q, BM * 128, &B.q_full, &B.drain[0], warp == kLoadWarp && a.Tq > 0);
+  } else if (warp >= 8) {
     regs_less<kOtherRegs>();
     if (warp == kLoadWarp) {
     // ------------------------------------------------------------------ loader ----
@@ -183,7 +186,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; i < p.count() && ok; ++i) {
         const int j0 = p.block(i) * BN;
         for (int kv = 0; kv < 2; ++kv) {
-          ok = mbar_wait(&B.kv_empty[stage], (round & 1) ^ 1 ^ fault_wait(a), wait_limit(a));
+          ok = mbar_wait(&B.kv_empty[stage], (round & 1) ^ 1);
           if (!ok) break;
           unsigned char* dst = sm + L::KV + stage * L::TILE;
           const bool tail = kv == 1 && j0 + BN > it.q.Lk;
@@ -429,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kScoreWarp) tmem_dealloc(tm, 512);
 }
 
-template <int D>
+template <int D, bool FAULT>
 bool fwd_tc(const WindowAttn& a, cudaStream_t st) {
   CUtensorMap mq, mk, mv;
   if (!make_rows_map(&mq, a.q, a.Tq, a.hq, D, BM, a.hdr) || !make_rows_map(&mk, a.k, a.Tk, a.hkv, D, BN, a.hdr) ||
@@ -437,14 +440,15 @@ bool fwd_tc(const WindowAttn& a, cudaStream_t st) {
     return false;
   const int64_t items = item_count(a.Tq, 2 * BM, a.N), work = items * a.hq;
   static std::atomic<uint64_t> ready{0};
-  ensure_smem(k_window_fwd_tc<D>, FwdSmem<D>::BYTES, ready);
+  ensure_smem(k_window_fwd_tc<D, FAULT>, FwdSmem<D>::BYTES, ready);
   // more items than CTAs: they take the next one from a counter, as sequences' blocks differ in work
   int* next_item = nullptr;
   if (work > kSms) {
     if (cudaMemsetAsync(a.hdr, 0, sizeof(WsHeader), st) != cudaSuccess) return false;
     next_item = a.hdr->pad;
   }
-  k_window_fwd_tc<D><<<(unsigned)(work < kSms ? work : kSms), kThreads, FwdSmem<D>::BYTES, st>>>(a, items, next_item, mq, mk, mv);
+  k_window_fwd_tc<D, FAULT><<<(unsigned)(work < kSms ? work : kSms), kThreads, FwdSmem<D>::BYTES, st>>>(
+      a, items, next_item, mq, mk, mv);
   return true;
 }
 
@@ -474,7 +478,8 @@ bool make_rows_map(CUtensorMap* map, const void* base, int T, int H, int d, int 
 }
 
 bool launch_window_fwd_tc(const WindowAttn& a, cudaStream_t st) {
-  return a.d == 128 ? fwd_tc<128>(a, st) : fwd_tc<64>(a, st);
+  if (a.fault_wait) return a.d == 128 ? fwd_tc<128, true>(a, st) : fwd_tc<64, true>(a, st);
+  return a.d == 128 ? fwd_tc<128, false>(a, st) : fwd_tc<64, false>(a, st);
 }
 
 }  // namespace gdn
