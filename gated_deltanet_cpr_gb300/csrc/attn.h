@@ -105,6 +105,7 @@ struct WindowAttn {
   // backward
   const void* dout;
   void *dq, *dk, *dv;
+  int few;       // rows at positions [0, few) have their delta from k_window_delta; 0 in fp32
   float* delta;  // 2 Tq hq floats that dq leaves for dk, dv: do . o [Tq, hq] (fp32 SIMT), or
                  // lse log2 e [hq, Tq] (infinite for a row that sees nothing) and do . o [hq, Tq]
   WsHeader* hdr;
@@ -117,7 +118,18 @@ bool launch_window_attn(const WindowAttn& a, bool bf16, cudaStream_t st);
 bool launch_window_fwd_tc(const WindowAttn& a, cudaStream_t st);
 bool launch_window_dq_tc(const WindowAttn& a, cudaStream_t st);
 bool launch_window_dkv_tc(const WindowAttn& a, cudaStream_t st);
-// the gradient: dq (and delta), then dk and dv, which read delta
+// bf16: delta of the rows that see 1 to kFewKeys keys, from do . v and the probabilities.  From the output, which is
+// rounded to bf16, it is off by u |do . o|, and with few keys do . v_j - delta is not much larger: on unit-size
+// inputs 39% of the rows that see 2 keys got a dq more than 5e-3 off (some by its own size), 4% with 8 keys,
+// 1% with 16, 0.2% with 32; a delta in 32 bits leaves 0.04% at most.
+constexpr int kFewKeys = 16;
+// These are the rows at positions [0, few): a row sees min(position + 1, window + sinks) keys.
+inline int few_positions(int window, int sinks) {
+  return window > 0 && (int64_t)window + sinks <= kFewKeys ? INT32_MAX : kFewKeys;
+}
+__device__ __forceinline__ bool few_keys(int pos, int few) { return (unsigned)pos < (unsigned)few; }
+void launch_window_delta(const WindowAttn& a, cudaStream_t st);
+// the gradient: dq (and delta, of few-key rows by a kernel before it), then dk and dv, which read delta
 bool launch_window_dq(const WindowAttn& a, bool bf16, cudaStream_t st);
 bool launch_window_dkv(const WindowAttn& a, bool bf16, cudaStream_t st);
 

@@ -222,18 +222,6 @@ struct SimtEngine {
 // 32 keys: scores [16 heads x 32 keys], the running maximum and sum, then P V with P as the sum of
 // two bf16 (so that its rounding does not show in the output).  Rows are swizzled so that the 8
 // rows of a matrix load lie in 8 bank groups: piece c of row r at c ^ (r & 7).
-__device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   const __nv_bfloat162 x = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&x);
@@ -287,9 +275,9 @@ struct MmaEngine {
 #pragma unroll
       for (int n = 0; n < NT; n += 2) {
         uint32_t b[4];
-        ldsm_x4(st + place(kr + 8 * n, 2 * k + kc), b);
-        mma16816(x[n], q[k], b[0], b[1]);
-        mma16816(x[n + 1], q[k], b[2], b[3]);
+        tc::ldsm_x4(st + place(kr + 8 * n, 2 * k + kc), b);
+        tc::mma16816(x[n], q[k], b[0], b[1]);
+        tc::mma16816(x[n + 1], q[k], b[2], b[3]);
       }
     if (keys < KEYS) {
 #pragma unroll
@@ -340,10 +328,10 @@ struct MmaEngine {
       for (int j = 0; j < D / 16; ++j) {
         uint32_t b[4];
         tc::ldsm_x4_trans(st + KEYS * ROWB + place(vr + 8 * n, 2 * j + vc), b);
-        mma16816(o[2 * j], hi, b[0], b[1]);
-        mma16816(o[2 * j + 1], hi, b[2], b[3]);
-        mma16816(o[2 * j], lo, b[0], b[1]);
-        mma16816(o[2 * j + 1], lo, b[2], b[3]);
+        tc::mma16816(o[2 * j], hi, b[0], b[1]);
+        tc::mma16816(o[2 * j + 1], hi, b[2], b[3]);
+        tc::mma16816(o[2 * j], lo, b[0], b[1]);
+        tc::mma16816(o[2 * j + 1], lo, b[2], b[3]);
       }
     }
   }

@@ -396,9 +396,11 @@ gdn_status gdn_cpr_window_attn_bwd(const gdn_cpr_attn* attn, int32_t num_seqs, i
   w.hdr = static_cast<WsHeader*>(ws);
   w.fault_wait = take_wait_fault(window_on_tensor_cores(attn));
   Stages stg(stream, kWindowBwdStages);
-  if (!launch_window_dq(w, attn->dtype == GDN_BF16, stream)) return GDN_ERR_CUDA;
-  stg.mark(1);
-  if (!launch_window_dkv(w, attn->dtype == GDN_BF16, stream)) return GDN_ERR_CUDA;
+  const bool bf16 = attn->dtype == GDN_BF16;
+  w.few = bf16 ? few_positions(w.window, w.sinks) : 0;
+  if (!launch_window_dq(w, bf16, stream)) return GDN_ERR_CUDA;
+  stg.mark(bf16 ? 2 : 1);
+  if (!launch_window_dkv(w, bf16, stream)) return GDN_ERR_CUDA;
   stg.mark(1);
   return finish();
 }

@@ -10,7 +10,7 @@
 // the probabilities lie doubled and transposed in shared memory, so that one 16-byte read gives
 // the multipliers of two rows.  One pass over the keys with a running maximum and sum per row.
 // The gradient is two kernels, each deterministic: per query block dq (and do . o, which the
-// other needs), per key block dk and dv.  There a cluster of CTAs shares out the group's heads and
+// other needs), per key block dk and dv; before them, for bf16, k_window_delta.  There a cluster of CTAs shares out the group's heads and
 // adds its sums in ascending order through its shared memory (one CTA per key block, head after
 // head, took 77 us in the first case below, whose 39 blocks of 2 key heads leave half of the SMs
 // without one; 8 x 2048 tokens took 3.67 ms in all instead of 3.01).
@@ -22,6 +22,7 @@
 // The short cases are bound by the latency of a tile's chain of products, barriers and exchanges,
 // the long ones by shared memory's reads beside the fp32 units.
 #include "attn_window.cuh"
+#include "tc.cuh"
 
 namespace gdn {
 
@@ -315,7 +316,8 @@ __global__ void __launch_bounds__(kThreads) k_window_dq(const WindowAttn a) {
     if (row0 + row < q.Lq) {
       const int64_t at = (int64_t)(q.q0 + row0 + row) * a.hq + h;
       lse2[r] = __fmul_rn(a.lse[at], kLog2e);
-      if (tx == 0) a.delta[at] = delta[r];
+      if (sizeof(T) == 2 && few_keys(pos[r], a.few)) delta[r] = a.delta[at];
+      else if (tx == 0) a.delta[at] = delta[r];
     }
   }
   NextTile<D, T> kn, vn;
@@ -346,6 +348,124 @@ __global__ void __launch_bounds__(kThreads) k_window_dq(const WindowAttn a) {
 #pragma unroll
   for (int r = 0; r < R; ++r) f[r] = a.scale;
   dq.template store<T>(a.dq, q.q0, row0, q.Lq, a.hq, h, ty, tx, f);
+}
+
+// delta of the rows that see at most kFewKeys keys: delta = sum_j p_j (do . v_j) over the visible keys.  A CTA takes 16
+// rows of a key head, whose keys (at most 31: 16 + window - 1 + first ones) lie in shared memory; a warp forms S = Q K^T
+// and T = dO V^T of a query head on warp-level MMAs and sums over each row.  With a window and first tokens of at most
+// kFewKeys together every row is such a row (16 to an item); else those at a sequence's first positions (an item per
+// sequence).  dq's products start beside it.  The gradient with delta from the output everywhere, and so: packed training
+// case (32387 tokens of 16 / 4 heads, window 2048) 1179 and 1175 us; 4 sequences of 512, 8 / 2 heads, 55.2 and 56.1; 64 of
+// 20 to 40 tokens 41.6 and 45.2 (a chain of loads); 32768 tokens, window 12 and 4 first ones, 502 and 522 (lanes that form a
+// row's products one after the other from shared memory instead took 1020).
+template <int D>
+__global__ void __launch_bounds__(256) k_window_delta(const WindowAttn a, const bool by_head) {
+  asm volatile("griddepcontrol.launch_dependents;");  // dq's other warps may start
+  const bool every_row = a.few > kFewKeys;
+  constexpr int ROWS = 16, KEYS = 32, P = 2 * D + 16, KS = D / 16;  // P: bytes of a row; 8 of them in 8 bank groups
+  __shared__ __align__(16) unsigned char ks[KEYS * P], vs[KEYS * P];
+  using T = __nv_bfloat16;
+  int row0;
+  Seq q;
+  if (every_row) {
+    q = find_seq(a, blockIdx.x, ROWS, false, row0);
+  } else {
+    q.s = blockIdx.x;
+    q.ok = valid_range(a.cu_q, q.s, a.Tq) && valid_range(a.cu_k, q.s, a.Tk);
+    q.q0 = a.cu_q[q.s], q.Lq = a.cu_q[q.s + 1] - q.q0;
+    q.k0 = a.cu_k[q.s], q.Lk = a.cu_k[q.s + 1] - q.k0;
+    row0 = max(0, q.Lq - q.Lk);  // at position 0, or past it where keys lie before the queries
+  }
+  if (!q.ok || row0 >= q.Lq) return;
+  const int p0 = row0 + q.Lk - q.Lq, p1 = min(row0 + ROWS, q.Lq) - 1 + q.Lk - q.Lq;  // positions of the rows
+  if (p1 < 0 || !few_keys(max(p0, 0), a.few)) return;
+  // place i holds key i (first ones) or lo + i - first
+  const int first = every_row ? min(a.sinks, p1 + 1) : 0, lo = every_row ? max(first, p0 - a.window + 1) : 0;
+  const int keys = min(every_row ? KEYS : kFewKeys, first + max(0, p1 + 1 - lo));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5, group = a.hq / a.hkv;
+  // this lane's rows: lane / 4 and 8 more
+  const int ra = min(row0 + (lane >> 2), q.Lq - 1), rb = min(row0 + (lane >> 2) + 8, q.Lq - 1);
+  uint32_t qa[KS][4], ga[KS][4];
+  auto load = [&](int g) {
+    const int64_t h = blockIdx.y * group + g;
+    const int64_t xa = ((int64_t)(q.q0 + ra) * a.hq + h) * D + 2 * (lane & 3), xb = ((int64_t)(q.q0 + rb) * a.hq + h) * D + 2 * (lane & 3);
+    const T *qp = static_cast<const T*>(a.q), *gp = static_cast<const T*>(a.dout);
+#pragma unroll
+    for (int k = 0; k < KS; ++k)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int64_t at = (e & 1 ? xb : xa) + 16 * k + 8 * (e >> 1);
+        qa[k][e] = *reinterpret_cast<const uint32_t*>(qp + at);
+        ga[k][e] = *reinterpret_cast<const uint32_t*>(gp + at);
+      }
+  };
+  if (warp < group) load(warp);
+  for (int e = threadIdx.x; e < keys * (D / 8); e += blockDim.x) {
+    const int i = e / (D / 8), c = e % (D / 8), j = i < first ? i : lo + i - first;
+    const int64_t at = ((int64_t)(q.k0 + j) * a.hkv + blockIdx.y) * D + 8 * c;
+    *reinterpret_cast<uint4*>(ks + i * P + 16 * c) = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.k) + at);
+    *reinterpret_cast<uint4*>(vs + i * P + 16 * c) = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.v) + at);
+  }
+  __syncthreads();
+  const uint32_t at = tc::smem_u32(ks) + ((lane & 7) + ((lane >> 4) << 3)) * P + ((lane >> 3) & 1) * 16;
+  const uint32_t to_v = tc::smem_u32(vs) - tc::smem_u32(ks);
+  const float sc = __fmul_rn(a.scale, kLog2e);
+  for (int g = warp; g < group; g += warps) {
+    if (g != warp) load(g);
+    float s[4][4], t[4][4];
+#pragma unroll
+    for (int n = 0; n < 4; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[n][e] = t[n][e] = 0.f;
+#pragma unroll
+    for (int n = 0; n < 4; n += 2) {
+      if (8 * n >= keys) break;
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        uint32_t b[4];
+        tc::ldsm_x4(at + 8 * n * P + 32 * k, b);
+        tc::mma16816(s[n], qa[k], b[0], b[1]);
+        tc::mma16816(s[n + 1], qa[k], b[2], b[3]);
+        tc::ldsm_x4(at + to_v + 8 * n * P + 32 * k, b);
+        tc::mma16816(t[n], ga[k], b[0], b[1]);
+        tc::mma16816(t[n + 1], ga[k], b[2], b[3]);
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int row = row0 + (lane >> 2) + 8 * r, pos = row + q.Lk - q.Lq;
+      float m = -INFINITY, l = 0.f, x = 0.f;
+#pragma unroll
+      for (int n = 0; n < 4; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int i = 8 * n + 2 * (lane & 3) + e, j = i < first ? i : lo + i - first;
+          float& y = s[n][2 * r + e];
+          y = i < keys && visible(pos, j, a.window, a.sinks) ? __fmul_rn(y, sc) : -INFINITY;
+          m = fmaxf(m, y);
+        }
+      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+#pragma unroll
+      for (int n = 0; n < 4; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float y = s[n][2 * r + e];
+          const float p = y == -INFINITY ? 0.f : exp2_approx(__fsub_rn(y, m));
+          l = __fadd_rn(l, p);
+          x = y == -INFINITY ? x : __fmaf_rn(p, t[n][2 * r + e], x);
+        }
+#pragma unroll
+      for (int o = 1; o < 4; o <<= 1) {
+        l = __fadd_rn(l, __shfl_xor_sync(0xffffffffu, l, o));
+        x = __fadd_rn(x, __shfl_xor_sync(0xffffffffu, x, o));
+      }
+      if ((lane & 3) == 0 && row < q.Lq && few_keys(pos, a.few)) {
+        const int64_t h = blockIdx.y * group + g;
+        a.delta[by_head ? (a.hq + h) * a.Tq + q.q0 + row : (int64_t)(q.q0 + row) * a.hq + h] = __fdiv_rn(x, l);
+      }
+    }
+  }
 }
 
 // CTAs of a key block: a power of two, from the group alone, so that it fixes the order of the sums
@@ -527,8 +647,20 @@ bool launch_window_attn(const WindowAttn& a, bool bf16, cudaStream_t st) {
   GDN_BY_TYPE(fwd_t)
   return true;
 }
+template <int D>
+void delta_t(const WindowAttn& a, bool by_head, cudaStream_t st) {
+  const int group = a.hq / a.hkv, threads = 32 * (group < 4 ? 4 : group < 8 ? group : 8);  // four to bring the keys in
+  const dim3 grid((unsigned)(a.few > kFewKeys ? item_count(a.Tq, 16, a.N) : a.N), a.hkv);
+  k_window_delta<D><<<grid, threads, 0, st>>>(a, by_head);
+}
+void launch_window_delta(const WindowAttn& a, cudaStream_t st) {
+  if (a.d == 32) delta_t<32>(a, false, st);
+  else if (a.d == 64) delta_t<64>(a, true, st);
+  else delta_t<128>(a, true, st);
+}
 bool launch_window_dq(const WindowAttn& a, bool bf16, cudaStream_t st) {
   if (bf16 && a.d != 32) return launch_window_dq_tc(a, st);
+  if (bf16) launch_window_delta(a, st);
   GDN_BY_TYPE(dq_t)
   return true;
 }

@@ -12,7 +12,8 @@
 // accumulating products read them while the groups are at the next block.  In dq the groups share
 // a block's columns, in dk, dv they take alternate blocks.
 // P and dS are rounded to bf16 for their products, as their other operands are; everything else
-// stays in 32 bits.
+// stays in 32 bits.  delta = do . o takes the forward's output, which is rounded to bf16, but for rows that see
+// few keys, where dP - delta would show it (k_window_delta).
 // What bounds them: a 128 x 128 block needs 512 clocks of the tensor core per product at d = 128, and
 // shared memory, at 128 bytes a clock, 512 for S and T each, 256 for an accumulating product and
 // 512 to take in U and W: 1792 against 1536 in dq.  At 128 x 64 (dk, dv, whose accumulators leave
@@ -187,6 +188,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   bool ok = true;
 
   if constexpr (FAULT) {
+    if (!DKV) asm volatile("griddepcontrol.wait;" ::: "memory");
     ok = wait_for_nothing(&mx, sm + L::X, BR * 128, &B.x_full, &B.drain[0],
                           warp == kLoadWarp && (DKV ? a.Tk : a.Tq) > 0);
   } else if (warp >= 8) {
@@ -363,6 +365,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float sc = __fmul_rn(a.scale, kLog2e);
     const float2 sc2 = make_float2(sc, sc);
     uint32_t n = 0, an = 0, gb = 0;  // gb: blocks so far
+    if (!DKV && wg) asm volatile("griddepcontrol.wait;" ::: "memory");  // the rows' delta that group 1 reads
     Ring<L::NU> ru;
     while (ok) {
       const uint32_t slot = n & 1;
@@ -378,29 +381,33 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int at = it.row0 + row + (DKV ? 0 : c.off);  // key, or the query's position
       float2 nl2, nd2;                                   // dq: -lse log2 e and -delta of the row
       if (!DKV) {
-        // Group 1 forms delta = do . o of its rows and hands it and lse to group 0.
+        // Group 1 forms delta = do . o of its rows, or takes it from k_window_delta, and hands it and lse to group 0.
         float dl = 0.f, ls = INFINITY;
         float* sh = reinterpret_cast<float*>(sm + L::VEC);
         if (wg) {
           if (live) {
             const int64_t r = (int64_t)(it.q.q0 + it.row0 + row) * a.hq + it.h;
-            const __nv_bfloat16* o = static_cast<const __nv_bfloat16*>(a.out) + r * D;
-            const __nv_bfloat16* g = static_cast<const __nv_bfloat16*>(a.dout) + r * D;
-            float x0 = 0.f, x1 = 0.f;
-#pragma unroll 8
-            for (int e = 0; e < D; e += 8) {
-              float x[8], y[8];
-              load8(o + e, x);
-              load8(g + e, y);
-#pragma unroll
-              for (int k = 0; k < 8; k += 2) x0 = __fmaf_rn(x[k], y[k], x0), x1 = __fmaf_rn(x[k + 1], y[k + 1], x1);
-            }
-            dl = __fadd_rn(x0, x1);
-            const float l = a.lse[r];
-            if (l != -INFINITY) ls = __fmul_rn(l, kLog2e);  // a row that sees nothing: P = exp2(-inf) = 0
             float* v = vec + (int64_t)it.h * a.Tq + it.q.q0 + it.row0 + row;
+            const float l = a.lse[r];
+            if (few_keys(at, a.few)) {
+              dl = v[(int64_t)a.hq * a.Tq];
+            } else {
+              const __nv_bfloat16* o = static_cast<const __nv_bfloat16*>(a.out) + r * D;
+              const __nv_bfloat16* g = static_cast<const __nv_bfloat16*>(a.dout) + r * D;
+              float x0 = 0.f, x1 = 0.f;
+#pragma unroll 8
+              for (int e = 0; e < D; e += 8) {
+                float x[8], y[8];
+                load8(o + e, x);
+                load8(g + e, y);
+#pragma unroll
+                for (int k = 0; k < 8; k += 2) x0 = __fmaf_rn(x[k], y[k], x0), x1 = __fmaf_rn(x[k + 1], y[k + 1], x1);
+              }
+              dl = __fadd_rn(x0, x1);
+              v[(int64_t)a.hq * a.Tq] = dl;
+            }
+            if (l != -INFINITY) ls = __fmul_rn(l, kLog2e);  // a row that sees nothing: P = exp2(-inf) = 0
             v[0] = ls;
-            v[(int64_t)a.hq * a.Tq] = dl;
           }
           ok = mbar_wait(&B.vec_free, (n & 1));  // group 0 has the last item's (n counts from 1 here)
           if (!ok) break;
@@ -574,8 +581,18 @@ bool bwd_tc(const WindowAttn& a, cudaStream_t st) {
   const int64_t work = DKV ? (blocks + a.N) * a.hkv : blocks * a.hq;
   static std::atomic<uint64_t> ready{0};
   ensure_smem(k_window_bwd_tc<D, DKV, FAULT>, (Smem<D, DKV>::BYTES), ready);
-  k_window_bwd_tc<D, DKV, FAULT><<<(unsigned)(work < kSms ? work : kSms), kThreads, (Smem<D, DKV>::BYTES), st>>>(
-      a, blocks, work, a.hdr->pad + (DKV ? 1 : 0), a.delta, mx, my, mu, mw);
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t c{};
+  c.gridDim = dim3((unsigned)(work < kSms ? work : kSms));
+  c.blockDim = dim3(kThreads);
+  c.dynamicSmemBytes = Smem<D, DKV>::BYTES;
+  c.stream = st;
+  c.attrs = &attr;
+  c.numAttrs = DKV ? 0 : 1;  // dq starts beside k_window_delta, for whose results its group 1 waits
+  cudaLaunchKernelEx(&c, k_window_bwd_tc<D, DKV, FAULT>, a, blocks, work, a.hdr->pad + (DKV ? 1 : 0), a.delta, mx, my, mu,
+                     mw);
   return true;
 }
 
@@ -590,6 +607,7 @@ bool by_size(const WindowAttn& a, cudaStream_t st) {
 bool launch_window_dq_tc(const WindowAttn& a, cudaStream_t st) {
   // the error word and the two item counters
   if (cudaMemsetAsync(a.hdr, 0, sizeof(WsHeader), st) != cudaSuccess) return false;
+  launch_window_delta(a, st);
   return by_size<false>(a, st);
 }
 bool launch_window_dkv_tc(const WindowAttn& a, cudaStream_t st) {
