@@ -2,7 +2,10 @@
 rotation of queries and keys, the paged cache's bookkeeping, decode attention over it, and
 sliding-window attention with its gradient.  A thin binding like api.py: tensors supply memory
 and the current stream, every step runs in the kernels of libgdn_cpr.so, and a refused call
-raises api.GdnError.  Shapes, masks and errors: include/gdn_cpr.h.
+raises api.GdnError.  What only the device can see (a length past max_len, a page outside the cache,
+a cu_seqlens table that does not fit) is in the error word of the workspace: pass `ws`
+(api.alloc_workspace) and read api.device_error(ws); a call that makes its own workspace does not
+keep it.  Shapes, masks and errors: include/gdn_cpr.h.
 """
 from __future__ import annotations
 

@@ -10,10 +10,10 @@
 // the probabilities lie doubled and transposed in shared memory, so that one 16-byte read gives
 // the multipliers of two rows.  One pass over the keys with a running maximum and sum per row.
 // The gradient is two kernels, each deterministic: per query block dq (and do . o, which the
-// other needs), per key block dk and dv; before them, for bf16, k_window_delta.  There a cluster of CTAs shares out the group's heads and
-// adds its sums in ascending order through its shared memory (one CTA per key block, head after
-// head, took 77 us in the first case below, whose 39 blocks of 2 key heads leave half of the SMs
-// without one; 8 x 2048 tokens took 3.67 ms in all instead of 3.01).
+// other needs), per key block dk and dv, where a cluster of CTAs shares out the group's heads and
+// adds its sums in ascending order through its shared memory; before them, for bf16, k_window_delta.
+// (One CTA per key block, head after head, took 77 us in the first case below, whose 39 blocks of 2 key
+// heads leave half of the SMs without one; 8 x 2048 tokens took 3.67 ms in all instead of 3.01.)
 // R is 4, or 2 where 64-row tiles would leave SMs without work: a row's arithmetic is the same in
 // both (the column blocks do not move), so its bits do not depend on the choice.
 // Forward and gradient, fp32, d = 64: 7 sequences of 54 to 271 tokens, 4 / 2 heads, 80 us with R = 2, 113

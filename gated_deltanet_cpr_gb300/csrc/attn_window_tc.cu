@@ -9,10 +9,11 @@
 // warps wait for the tensor core only where it is behind.  (With P written over S, the next S
 // had to wait for P V: 921 us against 830 for 32768 tokens, window 4096, 16 / 4 heads, d = 128.  Two
 // issuing warps instead of one then gave 707, items from a counter 690.)
-// What bounds it: the tensor core (S and O += P V are 512 clocks each per 128 x 128 at d = 128), fed at 79 to 85%
-// of a large bf16 library product's rate (1.47 to 1.57 PFLOP/s of visible scores' work in that case); where
-// a window is short or sequences are, an item's start and end count (packed sequences of 1446 to 7386
-// tokens, window 2048: 329 us at 58% tensor activity).
+// What bounds it: the tensor core (S and O += P V are 512 clocks each per 128 x 128 at d = 128).  That case takes
+// 661 us in bursts of 30 calls (SM clock 2070 MHz; 1.56 PFLOP/s of visible scores' work, 84% of a large bf16
+// library product's rate) and 690 to 720 over seconds, at the power limit (1930 MHz; 1.43 to 1.49, 77 to 81%).
+// Where a window is short or sequences are, an item's start and end count (packed sequences of 1446 to 7386
+// tokens, window 2048: 334 us at 57% tensor activity).
 // The probabilities are rounded to bf16 for their product (the row sums are of the unrounded fp32
 // values); S, O, m, l stay in 32 bits.  The maximum that P is scaled by is only moved, and O
 // rescaled, when a true maximum of the warp's rows passes it by more than 2^8: P then stays below 2^8,
