@@ -1,6 +1,6 @@
 """Attention-layer operators for hybrid models, beside the recurrence in api.py: norms and
-rotation of queries and keys, the paged cache's bookkeeping, decode attention over it, and
-sliding-window attention with its gradient.  A thin binding like api.py: tensors supply memory
+rotation of queries and keys, the paged cache's bookkeeping, decode attention over it, a cache in 8
+bits with its reading and writing, and sliding-window attention with its gradient.  A thin binding like api.py: tensors supply memory
 and the current stream, every step runs in the kernels of libgdn_cpr.so, and a refused call
 raises api.GdnError.  What only the device can see (a length past max_len, a page outside the cache,
 a cu_seqlens table that does not fit) is in the error word of the workspace: pass `ws`
@@ -19,6 +19,7 @@ from .api import GdnError, _dt
 
 NORMS = {"none": 0, "rms": 1, "l2": 2}
 LAYOUTS = {"half": 0, "interleaved": 1}
+CODES = {"int8": torch.int8, "e4m3": torch.float8_e4m3fn}
 HEADER_BYTES = 256
 
 
@@ -32,6 +33,12 @@ class NormRopeStruct(ctypes.Structure):
 class AttnStruct(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("h_q", "h_kv", "d", "window", "sinks")] + [
         ("scale", ctypes.c_float), ("dtype", ctypes.c_int)]
+
+
+class QuantCacheStruct(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("num_pages", "page_size", "block", "slots", "h_kv", "d")] + [
+        ("code", ctypes.c_int), ("dtype", ctypes.c_int)] + [
+        (n, ctypes.c_void_p) for n in ("k_pages", "v_pages", "k_scale", "v_scale", "k_tail", "v_tail")]
 
 
 class PagedCache:
@@ -59,6 +66,47 @@ class PagedCache:
         return _want(k, v.shape, v.dtype, "k pages"), _want(v, k.shape, k.dtype, "v pages")
 
 
+class QuantCache:
+    """Key-value cache in 8 bits: k, v [pages, H_kv, page_size, d] codes (int8 or float8_e4m3fn), k_scale, v_scale
+    [pages, H_kv, page_size / block] fp32, one scale for `block` tokens of a head, and k_tail, v_tail [slots, H_kv,
+    block, d] in dtype, where a request's last tokens wait, as they came, until they fill a block.  A request keeps
+    its slot while it lives, as in api.Cache; the tensors stay those that the cache was made with."""
+
+    def __init__(self, pages, page_size, h_kv, d, slots, *, code="int8", block=16, dtype=torch.bfloat16, device="cuda"):
+        if block <= 0 or page_size % block:
+            raise ValueError("pages hold whole blocks")
+        kw = dict(device=device)
+        self._set(*(torch.zeros((pages, h_kv, page_size, d), dtype=CODES[code], **kw) for _ in range(2)),
+                  *(torch.zeros((pages, h_kv, page_size // block), dtype=torch.float32, **kw) for _ in range(2)),
+                  *(torch.zeros((slots, h_kv, block, d), dtype=dtype, **kw) for _ in range(2)))
+
+    @classmethod
+    def wrap(cls, k, v, k_scale, v_scale, k_tail, v_tail):
+        """A cache over existing tensors."""
+        c = cls.__new__(cls)
+        c._set(k, v, k_scale, v_scale, k_tail, v_tail)
+        return c
+
+    def _set(self, k, v, k_scale, v_scale, k_tail, v_tail):
+        if k.dim() != 4 or k_tail.dim() != 4:
+            raise ValueError("pages are [pages, H_kv, page_size, d], tails [slots, H_kv, block, d]")
+        self.pages, self.h_kv, self.page_size, self.d = k.shape
+        self.slots, _, self.block, _ = k_tail.shape
+        code = 0 if k.dtype == torch.int8 else 1
+        if k.dtype not in CODES.values() or self.block <= 0 or self.page_size % self.block:
+            raise ValueError("pages hold int8 or float8_e4m3fn codes of whole blocks")
+        scales, tails = (self.pages, self.h_kv, self.page_size // self.block), (self.slots, self.h_kv, self.block, self.d)
+        self.k, self.v, self.k_scale, self.v_scale, self.k_tail, self.v_tail = k, v, k_scale, v_scale, k_tail, v_tail
+        self.dtype, self.device = k_tail.dtype, k.device
+        at = self.device
+        self.struct = QuantCacheStruct(
+            self.pages, self.page_size, self.block, self.slots, self.h_kv, self.d, code, _dt(self.dtype),
+            _want_on(k, k.shape, k.dtype, "k pages", at), _want_on(v, k.shape, k.dtype, "v pages", at),
+            _want_on(k_scale, scales, torch.float32, "k_scale", at), _want_on(v_scale, scales, torch.float32, "v_scale", at),
+            _want_on(k_tail, tails, self.dtype, "k_tail", at), _want_on(v_tail, tails, self.dtype, "v_tail", at))
+        self._ref = ctypes.byref(self.struct)
+
+
 def rope_tables(rows, rot, base=10000.0, scale=1.0, device="cuda"):
     """cos and sin [rows, rot / 2] fp32 of the angles (p / scale) base^(-2 i / rot), formed in 64
     bits.  scale > 1 compresses positions for contexts longer than the model was trained on."""
@@ -71,6 +119,7 @@ def rope_tables(rows, rot, base=10000.0, scale=1.0, device="cuda"):
 # low: one check per tensor that the caller gives, the raw stream handle, one allocation where several results
 # go together; descriptions of shapes and their workspace sizes are kept by their values.
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 
 
 def _check(fn, rc):
@@ -84,6 +133,13 @@ def _want(x, shape, dtype, name):
         raise ValueError(f"{name} is {x.dtype} {tuple(x.shape)} on {x.device}"
                          f"{'' if x.is_contiguous() else ', not contiguous'}; expected {dtype} {tuple(shape)} on the GPU")
     return x.data_ptr()
+
+
+def _want_on(x, shape, dtype, name, device):
+    """_want, of a tensor on that device."""
+    if x.device != device:
+        raise ValueError(f"{name} is on {x.device}, the cache on {device}")
+    return _want(x, shape, dtype, name)
 
 
 def _opt(x, shape, dtype, name):
@@ -278,6 +334,70 @@ def paged_decode(q, cache: PagedCache, block_table, seq_lens, *, window=0, sinks
         _want(seq_lens, (N,), torch.int32, "seq_lens"), op,
         None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.numel(), _raw_stream(device.index)))
     return (out, lse) if want_lse else out
+
+
+def _quant_requests(cache, block_table, seq_lens, slots):
+    """(N, pointers of the block table, its width, of lengths and of slots) of a call over an 8-bit cache."""
+    device = cache.device
+    if device.index != _current_device():
+        raise ValueError(f"the cache is on {device}, which is not the current device")
+    N, table = seq_lens.numel(), block_table.shape
+    if len(table) != 2 or table[0] != N:
+        raise ValueError("block_table is [N, max_blocks]")
+    i32 = torch.int32
+    if slots is None and N > cache.slots:
+        raise ValueError(f"{N} requests, and the cache has {cache.slots} tails")
+    return (N, _want_on(block_table, table, i32, "block_table", device), table[1],
+            _want_on(seq_lens, (N,), i32, "seq_lens", device),
+            None if slots is None else _want_on(slots, (N,), i32, "slots", device))
+
+
+def _header(ws, device):
+    return torch.empty(HEADER_BYTES, dtype=torch.uint8, device=device) if ws is None else ws
+
+
+def quant_append(k, v, cache: QuantCache, block_table, seq_lens, cu_seqlens, *, slots=None, ws=None):
+    """gdn_cpr_quant_append: new keys and values k, v [T, Hkv, d] (tokens may be strided) into the 8-bit cache.
+    Request n appends rows cu_seqlens[n] .. and has seq_lens[n] tokens afterwards (page_map gives both) and the tail
+    slots[n] (default: n).  Blocks that become whole are rounded to 8 bits in their pages, other rows wait in the
+    tail."""
+    T, hkv, device = k.shape[0], cache.h_kv, cache.device
+    if k.dtype is not cache.dtype or v.dtype is not cache.dtype or v.shape[0] != T:
+        raise ValueError("k and v have the same tokens and the cache's dtype")
+    if k.device != device or v.device != device:
+        raise ValueError("k, v and the cache are on one device")
+    N, table, width, lens, slot = _quant_requests(cache, block_table, seq_lens, slots)
+    kp, ks = _rows(k, hkv, cache.d, "k")
+    vp, vs = _rows(v, hkv, cache.d, "v")
+    ws = _header(ws, device)
+    _check("gdn_cpr_quant_append", api.load().gdn_cpr_quant_append(
+        cache._ref, N, T, kp, vp, ks, vs, _want_on(cu_seqlens, (N + 1,), torch.int32, "cu_seqlens", device), lens, table,
+        width, slot, ws.data_ptr(), ws.numel(), _raw_stream(device.index)))
+
+
+def quant_read(cache: QuantCache, block_table, seq_lens, cu_seqlens, total_tokens, *, slots=None, out_dtype=None,
+               k_out=None, v_out=None, ws=None):
+    """gdn_cpr_quant_read: the last cu_seqlens[n + 1] - cu_seqlens[n] cached positions of every request as packed rows
+    (k, v) [total_tokens, Hkv, d] in out_dtype (default: the cache's dtype), as window_attn takes them with
+    cu_seqlens_k."""
+    T, device = int(total_tokens), cache.device
+    if not 0 <= T < 2 ** 31:
+        raise ValueError(f"total_tokens is {T}: not a count that fits 32 bits")
+    od = out_dtype or (k_out.dtype if k_out is not None else cache.dtype)
+    N, table, width, lens, slot = _quant_requests(cache, block_table, seq_lens, slots)
+    shape = (T, cache.h_kv, cache.d)
+    if k_out is None and v_out is None:
+        k_out, v_out = torch.empty((2, *shape), dtype=od, device=device).unbind()
+        kp, vp = k_out.data_ptr(), v_out.data_ptr()
+    else:
+        k_out = torch.empty(shape, dtype=od, device=device) if k_out is None else k_out
+        v_out = torch.empty(shape, dtype=od, device=device) if v_out is None else v_out
+        kp, vp = _want_on(k_out, shape, od, "k_out", device), _want_on(v_out, shape, od, "v_out", device)
+    ws = _header(ws, device)
+    _check("gdn_cpr_quant_read", api.load().gdn_cpr_quant_read(
+        cache._ref, N, T, _want_on(cu_seqlens, (N + 1,), torch.int32, "cu_seqlens", device), lens, table, width, slot,
+        _dt(od), kp, vp, ws.data_ptr(), ws.numel(), _raw_stream(device.index)))
+    return k_out, v_out
 
 
 def _window_setup(q, k, v, cu_q, cu_k, window, sinks, scale, backward, ws):

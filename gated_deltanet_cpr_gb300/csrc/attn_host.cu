@@ -1,11 +1,12 @@
 // attn_host.cu -- the C ABI of the attention-layer operators (include/gdn_cpr.h): argument
 // checks and workspace sizes; the kernels are in attn_tokens.cu, attn_decode.cu,
-// attn_window.cu and attn_window_tc.cu.
+// attn_window.cu, attn_window_tc.cu and, of the 8-bit cache, attn_quant_rows.cu.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
 
 #include "attn.h"
+#include "attn_quant.h"
 #include "hooks.h"
 
 namespace {
@@ -117,6 +118,8 @@ const char* const kNormStages[] = {"norm and rotation", nullptr};
 const char* const kMapStages[] = {"page map", nullptr};
 const char* const kPagedStages[] = {"paged decode attention", nullptr};
 const char* const kWindowStages[] = {"window attention", nullptr};
+const char* const kQuantAppendStages[] = {"8-bit cache append", nullptr};
+const char* const kQuantReadStages[] = {"8-bit cache read", nullptr};
 const char* const kWindowBwdStages[] = {"window attention dq", "window attention dk, dv", nullptr};
 
 gdn_status window_args(const gdn_cpr_attn* attn, int32_t N, int32_t Tq, int32_t Tk, const int32_t* cu_q,
@@ -147,6 +150,69 @@ gdn_status window_args(const gdn_cpr_attn* attn, int32_t N, int32_t Tq, int32_t 
 }
 
 bool window_on_tensor_cores(const gdn_cpr_attn* a) { return a->dtype == GDN_BF16 && a->d != 32; }
+
+// An 8-bit cache's description and, where a call reaches it, its memory.
+gdn_status check_quant(const gdn_cpr_quant_cache* c, bool used) {
+  if (!c) return GDN_ERR_INVALID_ARG;
+  if (c->num_pages < 0 || c->page_size <= 0 || c->block <= 0 || c->slots < 0 || c->h_kv <= 0) return GDN_ERR_INVALID_ARG;
+  const int shift = page_shift_of(c->page_size);
+  if (shift < 0 || !ok_d(c->d) || c->h_kv > 65535 || !ok_dtype(c->dtype)) return GDN_ERR_UNSUPPORTED;
+  if (c->code != GDN_INT8 && c->code != GDN_E4M3) return GDN_ERR_UNSUPPORTED;
+  if ((c->block != 16 && c->block != 32 && c->block != 64 && c->block != 128) || c->block > c->page_size)
+    return GDN_ERR_UNSUPPORTED;
+  // the kernels number rows (page, head, offset) and (slot, head, row) in 32 bits
+  if ((((int64_t)c->num_pages * c->h_kv) << shift) >= (int64_t)UINT32_MAX) return GDN_ERR_UNSUPPORTED;
+  if ((int64_t)c->slots * c->h_kv * c->block >= (int64_t)UINT32_MAX) return GDN_ERR_UNSUPPORTED;
+  if (!used) return GDN_OK;
+  if (c->num_pages > 0 && (!ok_ptr(c->k_pages, 16) || !ok_ptr(c->v_pages, 16) || !ok_ptr(c->k_scale, 4) || !ok_ptr(c->v_scale, 4)))
+    return GDN_ERR_INVALID_ARG;
+  if (c->slots > 0 && (!ok_ptr(c->k_tail, 16) || !ok_ptr(c->v_tail, 16))) return GDN_ERR_INVALID_ARG;
+  return GDN_OK;
+}
+
+QuantCache quant_view(const gdn_cpr_quant_cache* c) {
+  QuantCache q{};
+  q.k_pages = static_cast<uint8_t*>(c->k_pages);
+  q.v_pages = static_cast<uint8_t*>(c->v_pages);
+  q.k_scale = c->k_scale;
+  q.v_scale = c->v_scale;
+  q.k_tail = c->k_tail;
+  q.v_tail = c->v_tail;
+  q.num_pages = c->num_pages;
+  q.page_shift = page_shift_of(c->page_size);
+  q.block_shift = c->block == 16 ? 4 : c->block == 32 ? 5 : c->block == 64 ? 6 : 7;
+  q.slots = c->slots;
+  q.hkv = c->h_kv;
+  q.e4m3 = c->code == GDN_E4M3;
+  return q;
+}
+
+// What append and read have in common.
+gdn_status quant_rows_args(const gdn_cpr_quant_cache* c, int32_t N, int32_t T, const int32_t* cu, const int32_t* seq_lens,
+                           const int32_t* block_table, int32_t max_blocks, const int32_t* slot, void* ws, size_t ws_bytes,
+                           bool by_block, QuantRows* a) {
+  if (N < 0 || T < 0 || max_blocks < 0 || (N == 0 && T > 0)) return GDN_ERR_INVALID_ARG;
+  const gdn_status rc = check_quant(c, N > 0);
+  if (rc != GDN_OK) return rc;
+  if (N > 65535) return GDN_ERR_UNSUPPORTED;
+  const QuantCache q = quant_view(c);
+  // a warp or more for each piece (a block to append, a granule to read) of each head of k and v, in 31 bits
+  if ((double)quant_pieces(N, T, by_block ? q.block_shift : kGranuleShift) * 2 * c->h_kv >= 2147483648.0) return GDN_ERR_UNSUPPORTED;
+  if (N > 0 && (!ok_ptr(cu, 4) || !ok_ptr(seq_lens, 4) || !aligned(slot, 4))) return GDN_ERR_INVALID_ARG;
+  if (N > 0 && max_blocks > 0 && !ok_ptr(block_table, 4)) return GDN_ERR_INVALID_ARG;
+  if (!ok_ws(ws, ws_bytes, GDN_CPR_ATTN_HEADER_BYTES)) return GDN_ERR_WORKSPACE;
+  *a = QuantRows{};
+  a->c = q;
+  a->N = N;
+  a->T = T;
+  a->max_blocks = max_blocks;
+  a->cu = cu;
+  a->seq_lens = seq_lens;
+  a->block_table = block_table;
+  a->slot = slot;
+  a->hdr = static_cast<WsHeader*>(ws);
+  return GDN_OK;
+}
 
 size_t window_bytes(const gdn_cpr_attn* a, int32_t Tq, bool backward) {
   return align_up(GDN_CPR_ATTN_HEADER_BYTES + (backward ? 2 * (size_t)Tq * a->h_q * sizeof(float) : 0));
@@ -402,6 +468,47 @@ gdn_status gdn_cpr_window_attn_bwd(const gdn_cpr_attn* attn, int32_t num_seqs, i
   stg.mark(bf16 ? 2 : 1);
   if (!launch_window_dkv(w, bf16, stream)) return GDN_ERR_CUDA;
   stg.mark(1);
+  return finish();
+}
+
+gdn_status gdn_cpr_quant_append(const gdn_cpr_quant_cache* cache, int32_t num_seqs, int32_t total_tokens, const void* k,
+                                const void* v, int64_t k_stride, int64_t v_stride, const int32_t* cu_seqlens,
+                                const int32_t* seq_lens, const int32_t* block_table, int32_t max_blocks,
+                                const int32_t* slot, void* ws, size_t ws_bytes, gdn_stream_t stream) {
+  NvtxRange nvtx("gdn_cpr_quant_append");
+  QuantRows a;
+  const gdn_status rc = quant_rows_args(cache, num_seqs, total_tokens, cu_seqlens, seq_lens, block_table, max_blocks, slot,
+                                        ws, ws_bytes, true, &a);
+  if (rc != GDN_OK) return rc;
+  const int64_t row = (int64_t)cache->h_kv * cache->d, step = cache->dtype == GDN_BF16 ? 8 : 4;
+  if (k_stride < row || v_stride < row || k_stride % step || v_stride % step) return GDN_ERR_INVALID_ARG;
+  if (total_tokens > 0 && (!ok_ptr(k, 16) || !ok_ptr(v, 16))) return GDN_ERR_INVALID_ARG;
+  if (num_seqs == 0) return empty_call(ws, stream);
+  a.k_in = k;
+  a.v_in = v;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  Stages stg(stream, kQuantAppendStages);
+  stg.mark(launch_quant_append(a, cache->d, cache->dtype == GDN_BF16, stream));
+  return finish();
+}
+
+gdn_status gdn_cpr_quant_read(const gdn_cpr_quant_cache* cache, int32_t num_seqs, int32_t total_tokens,
+                              const int32_t* cu_seqlens, const int32_t* seq_lens, const int32_t* block_table,
+                              int32_t max_blocks, const int32_t* slot, gdn_dtype out_dtype, void* k, void* v, void* ws,
+                              size_t ws_bytes, gdn_stream_t stream) {
+  NvtxRange nvtx("gdn_cpr_quant_read");
+  QuantRows a;
+  const gdn_status rc = quant_rows_args(cache, num_seqs, total_tokens, cu_seqlens, seq_lens, block_table, max_blocks, slot,
+                                        ws, ws_bytes, false, &a);
+  if (rc != GDN_OK) return rc;
+  if (!ok_dtype(out_dtype)) return GDN_ERR_UNSUPPORTED;
+  if (total_tokens > 0 && (!ok_ptr(k, 16) || !ok_ptr(v, 16))) return GDN_ERR_INVALID_ARG;
+  if (num_seqs == 0) return empty_call(ws, stream);
+  a.k_out = k;
+  a.v_out = v;
+  Stages stg(stream, kQuantReadStages);
+  stg.mark(launch_quant_read(a, cache->d, cache->dtype == GDN_BF16, out_dtype == GDN_BF16, stream));
   return finish();
 }
 

@@ -1,0 +1,451 @@
+// attn_quant_rows.cu -- the 8-bit cache's rows: rounding new keys and values to codes and scales as they are
+// written, and reading cached ones back into packed rows.
+//
+// Both kernels move every byte once and are bound by DRAM on long inputs, by launch and a chain of dependent
+// loads (offsets, lengths, page, rows) on short ones.  The position-aligned pieces of the requests are numbered so that a
+// warp finds its request with one search of the offsets, 32 of them at a time.
+#include "attn_quant.h"
+
+namespace gdn {
+
+namespace {
+
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+
+// The last n < N with cu[n] / piece + 2 n <= w: the request that piece w belongs to.  All lanes take part.
+__device__ __forceinline__ int request_of(const int32_t* cu, int N, int shift, uint32_t w, int lane) {
+  int lo = 0, n = N;
+  while (n > 1) {
+    const int step = (n + 31) >> 5, i = lo + lane * step;
+    const bool at = lane * step < n && (cu[i] >> shift) + 2 * i <= (int64_t)w;
+    const uint32_t m = __ballot_sync(0xffffffffu, at) | 1u;
+    const int k = (31 - __clz(m)) * step;
+    lo += k;
+    n = min(step, n - k);
+  }
+  return lo;
+}
+
+// A piece of a request: positions [first, first + (1 << shift)), of which [from, to) have rows, row r being at
+// position r - cu0 + from0.
+struct Piece {
+  int n, j;             // request, number of the piece in it
+  uint32_t first;       // position
+  uint32_t begin, len;  // the request's positions [begin, len) have rows
+  int cu0;
+  bool on;
+};
+__device__ __forceinline__ Piece piece_of(const QuantRows& a, int shift, uint32_t w, int lane) {
+  Piece p;
+  p.n = request_of(a.cu, a.N, shift, w, lane);
+  const int c0 = a.cu[p.n], c1 = a.cu[p.n + 1], len = a.seq_lens[p.n];
+  const int rows = c1 - c0;
+  p.cu0 = c0;
+  p.on = c0 >= 0 && c1 > c0 && c1 <= a.T;
+  const bool fits = len >= rows;
+  p.len = (uint32_t)len;
+  p.begin = (uint32_t)(len - rows);
+  p.j = (int)((int64_t)w - ((c0 >> shift) + 2 * (int64_t)p.n));
+  if (!fits) {  // numbered as if its rows began at position 0
+    p.begin = 0;
+    p.len = (uint32_t)rows;
+  }
+  p.first = ((p.begin >> shift) + (uint32_t)p.j) << shift;
+  p.on = p.on && p.j >= 0 && p.first < p.len;
+  if (!fits) p.len = 0;  // no position is valid
+  return p;
+}
+
+__device__ __forceinline__ void report(WsHeader* h, int code) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the word has been cleared
+  set_error(h, code);
+}
+
+// What is wrong with offsets, lengths and slots; one block.  APPEND: a slot is needed whatever the length.
+template <bool APPEND>
+__device__ void check_requests(const QuantRows& a) {
+  int bad = 0;
+  for (int n = threadIdx.x; n < a.N; n += kThreads) {
+    const int c0 = a.cu[n], c1 = a.cu[n + 1];
+    const int first = n == 0 ? 0 : c0, last = n == a.N - 1 ? a.T : c1;
+    if (c0 != first || c1 != last || c0 < 0 || c1 < c0 || c1 > a.T) {
+      bad |= 1;
+      continue;
+    }
+    if (c1 == c0) continue;
+    const int len = a.seq_lens[n], slot = a.slot ? a.slot[n] : n;
+    if (len < c1 - c0) bad |= 2;
+    else if ((slot < 0 || slot >= a.c.slots) && (APPEND || (len & ((1 << a.c.block_shift) - 1)))) bad |= 4;
+  }
+  bad = (__syncthreads_or(bad & 1) ? 1 : 0) | (__syncthreads_or(bad & 2) ? 2 : 0) | (__syncthreads_or(bad & 4) ? 4 : 0);
+  if (threadIdx.x == 0 && bad)
+    report(a.hdr, bad & 1 ? GDN_DEVERR_CU_SEQLENS : bad & 2 ? GDN_DEVERR_POS : GDN_DEVERR_SLOT);
+}
+
+// ------------------------------------------------------------------------- rounding ----
+// Codes of an int8 block: the quotient 127 x / m is rounded as it is in exact arithmetic.  t = x fl(127 / m) is
+// within 2^-16 of it, so only a t that close to a half needs more: there the sign of 254 x - (2 k + 1) m decides, which
+// the two products and what their rounding lost give exactly.
+struct Rounder {
+  float inv, m, scale;  // scale: what the block stores
+  float down;           // keeps the products of the exact comparison finite
+  bool e4m3;
+  __device__ __forceinline__ Rounder(uint32_t amax_bits, bool e4m3_) : e4m3(e4m3_) {
+    m = __uint_as_float(amax_bits);
+    inv = 0.f;
+    down = 1.f;
+    if (amax_bits >= 0x7f800000u) {
+      scale = __builtin_nanf("");
+      m = 0.f;
+    } else if (m < 0x1p-100f) {
+      scale = 0.f;
+      m = 0.f;
+    } else if (e4m3) {
+      // 448 = 1.75 2^8: the exponent of m less 8, one more where its significand is above 1.75
+      const int e = (int)(amax_bits >> 23) - 8 + ((amax_bits & 0x7fffffu) > 0x600000u ? 1 : 0);
+      scale = __uint_as_float((uint32_t)e << 23);
+      inv = __uint_as_float((uint32_t)(254 - e) << 23);
+    } else {
+      scale = __fdiv_rn(m, 127.f);
+      inv = __fdiv_rn(127.f, m);
+      if (m > 0x1p100f) down = 0x1p-20f;
+    }
+  }
+  static constexpr float kMagic = 12582912.f;  // 1.5 2^23: the sum's last bits are a whole number, ties to even
+  // t next to a half: the whole number on the right side of it, as x 127 / m has it
+  __device__ __noinline__ static float settle(float x, float m, float down, float r, float dist) {
+    const float s = dist < 0.f ? -1.f : 1.f, odd = 2.f * r + s;  // the half is odd / 2
+    x *= down;
+    m *= down;
+    const float q = 254.f * x, f = __fmaf_rn(254.f, x, -q), p = odd * m, e = __fmaf_rn(odd, m, -p);
+    const float diff = __fadd_rn(__fsub_rn(q, p), __fsub_rn(f, e)) * s;  // > 0: past the half
+    if (diff > 0.f) return r + s;
+    if (diff < 0.f) return r;
+    return ((int)r & 1) ? r + s : r;
+  }
+  // codes of 4 values
+  __device__ __forceinline__ uint32_t four(const float (&x)[4]) const {
+    if (m == 0.f) return 0u;
+    if (e4m3) {
+      uint16_t lo, hi;
+      asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(__fmul_rn(x[1], inv)), "f"(__fmul_rn(x[0], inv)));
+      asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(__fmul_rn(x[3], inv)), "f"(__fmul_rn(x[2], inv)));
+      return (uint32_t)lo | ((uint32_t)hi << 16);
+    }
+    float y[4];
+    bool near = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float t = __fmul_rn(x[i], inv);
+      y[i] = __fadd_rn(t, kMagic);
+      near |= fabsf(__fsub_rn(t, __fsub_rn(y[i], kMagic))) > 0.5f - 0x1p-14f;
+    }
+    if (near) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float t = __fmul_rn(x[i], inv), r = __fsub_rn(y[i], kMagic), dist = __fsub_rn(t, r);
+        if (fabsf(dist) > 0.5f - 0x1p-14f) y[i] = __fadd_rn(settle(x[i], m, down, r, dist), kMagic);
+      }
+    }
+    const uint32_t a = __byte_perm(__float_as_uint(y[0]), __float_as_uint(y[1]), 0x0040);
+    const uint32_t b = __byte_perm(__float_as_uint(y[2]), __float_as_uint(y[3]), 0x0040);
+    return __byte_perm(a, b, 0x5410);
+  }
+};
+
+// a lane's 16 bytes of a row
+template <typename T>
+struct Vec;
+template <>
+struct Vec<__nv_bfloat16> {
+  static constexpr int N = 8;
+  __device__ __forceinline__ static uint32_t amax(const uint4& u, uint32_t m) {  // of pairs
+    m = __vmaxu2(m, u.x & 0x7fff7fffu);
+    m = __vmaxu2(m, u.y & 0x7fff7fffu);
+    m = __vmaxu2(m, u.z & 0x7fff7fffu);
+    return __vmaxu2(m, u.w & 0x7fff7fffu);
+  }
+  __device__ __forceinline__ static uint32_t bits(uint32_t m) { return max(m << 16, m & 0xffff0000u); }
+  __device__ __forceinline__ static void store(const Rounder& r, const uint4& u, uint8_t* to) {
+    uint2 o;
+    o.x = r.four({__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
+                  __uint_as_float(u.y & 0xffff0000u)});
+    o.y = r.four({__uint_as_float(u.z << 16), __uint_as_float(u.z & 0xffff0000u), __uint_as_float(u.w << 16),
+                  __uint_as_float(u.w & 0xffff0000u)});
+    *reinterpret_cast<uint2*>(to) = o;
+  }
+};
+template <>
+struct Vec<float> {
+  static constexpr int N = 4;
+  __device__ __forceinline__ static uint32_t amax(const uint4& u, uint32_t m) {
+    return max(max(max(m, u.x & 0x7fffffffu), max(u.y & 0x7fffffffu, u.z & 0x7fffffffu)), u.w & 0x7fffffffu);
+  }
+  __device__ __forceinline__ static uint32_t bits(uint32_t m) { return m; }
+  __device__ __forceinline__ static void store(const Rounder& r, const uint4& u, uint8_t* to) {
+    *reinterpret_cast<uint32_t*>(to) =
+        r.four({__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z), __uint_as_float(u.w)});
+  }
+};
+
+// --------------------------------------------------------------------------- append ----
+// A unit is one block of one head of k or v; a warp takes 16 of its rows, block / 16 warps a unit, whose largest values
+// meet in shared memory.  The request's first block also takes care of its tail: a first block that is completed has the tail's
+// rows in registers before the rows of a later, unfinished one replace them.
+template <int D, typename T>
+__global__ void __launch_bounds__(kThreads) k_quant_append(const QuantRows a) {
+  constexpr int VEC = Vec<T>::N, LPR = D / VEC, RPP = 32 / LPR, PASSES = kGranule / RPP;
+  __shared__ uint32_t most[kWarps];
+  if (blockIdx.x == 0) {
+    check_requests<true>(a);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    return;
+  }
+  const QuantCache& c = a.c;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, B = 1 << c.block_shift;
+  const int each = B / kGranule, part = warp % each;  // warps of a unit, this one's rows of it
+  const uint32_t units = ((uint32_t)(a.T >> c.block_shift) + 2u * (uint32_t)a.N) * 2u * (uint32_t)c.hkv;
+  const uint32_t unit = (blockIdx.x - 1) * (uint32_t)(kWarps / each) + (uint32_t)(warp / each);
+  const uint32_t w = unit / (2u * (uint32_t)c.hkv), rest = unit - w * 2u * (uint32_t)c.hkv;
+  const int h = (int)(rest >> 1);
+  const bool is_v = rest & 1;
+  Piece p{};
+  if (unit < units) p = piece_of(a, c.block_shift, w, lane);
+  int slot = 0, page = -1;
+  if (p.on) {
+    slot = a.slot ? a.slot[p.n] : p.n;
+    p.on = p.len != 0 && slot >= 0 && slot < c.slots;  // if not, reported by block 0
+  }
+  const bool whole = p.on && p.first + (uint32_t)B <= p.len;
+  if (whole) {
+    const uint32_t b = p.first >> c.page_shift;
+    page = b < (uint32_t)a.max_blocks ? a.block_table[(int64_t)p.n * a.max_blocks + b] : -1;
+  }
+  const T* src = static_cast<const T*>(is_v ? a.v_in : a.k_in);
+  const int64_t stride = is_v ? a.v_stride : a.k_stride;
+  T* tail = static_cast<T*>(is_v ? c.v_tail : c.k_tail) + ((int64_t)slot * c.hkv + h) * B * D;
+  const int r0 = part * kGranule + lane / LPR, col = lane % LPR * VEC;
+  // row of the new token at a position
+  auto fresh = [&](uint32_t pos) { return src + (int64_t)(p.cu0 + (int)(pos - p.begin)) * stride + h * D + col; };
+  uint4 x[PASSES];
+#pragma unroll
+  for (int i = 0; i < PASSES; ++i) {
+    const int r = r0 + i * RPP;
+    const uint32_t pos = p.first + (uint32_t)r;
+    x[i] = make_uint4(0, 0, 0, 0);
+    if (!p.on || pos >= p.len) continue;
+    if (pos >= p.begin) x[i] = *reinterpret_cast<const uint4*>(fresh(pos));
+    else if (whole) x[i] = *reinterpret_cast<const uint4*>(tail + r * D + col);
+  }
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < PASSES; ++i) m = Vec<T>::amax(x[i], m);
+  m = __reduce_max_sync(0xffffffffu, Vec<T>::bits(m));
+  if (each > 1) {
+    if (lane == 0) most[warp] = m;
+    __syncthreads();  // the tail's rows are in registers, too
+    for (int i = 0; i < each; ++i) m = max(m, most[warp - part + i]);
+  } else {
+    __syncwarp();
+  }
+  if (whole) {
+    if (page < 0 || page >= c.num_pages) {
+      if (lane == 0) report(a.hdr, GDN_DEVERR_PAGES);
+    } else {
+      const Rounder round(m, c.e4m3);
+      const int64_t row = ((int64_t)page * c.hkv + h) << c.page_shift;
+      const uint32_t off = p.first & ((1u << c.page_shift) - 1u);
+      uint8_t* to = (is_v ? c.v_pages : c.k_pages) + (row + off) * D;
+#pragma unroll
+      for (int i = 0; i < PASSES; ++i) Vec<T>::store(round, x[i], to + (r0 + i * RPP) * D + col);
+      if (part == 0 && lane == 0) (is_v ? c.v_scale : c.k_scale)[(row + off) >> c.block_shift] = round.scale;
+    }
+  }
+  if (p.on && p.j == 0) {
+    if (!whole) {
+#pragma unroll
+      for (int i = 0; i < PASSES; ++i) {
+        const uint32_t pos = p.first + (uint32_t)(r0 + i * RPP);
+        if (pos >= p.begin && pos < p.len) *reinterpret_cast<uint4*>(tail + (r0 + i * RPP) * D + col) = x[i];
+      }
+    } else if (p.len & (uint32_t)(B - 1)) {
+      const uint32_t last = p.len & ~(uint32_t)(B - 1);  // the unfinished block begins here, after this one
+#pragma unroll
+      for (int i = 0; i < PASSES; ++i) {
+        const uint32_t pos = last + (uint32_t)(r0 + i * RPP);
+        if (pos < p.len) x[i] = *reinterpret_cast<const uint4*>(fresh(pos));
+      }
+#pragma unroll
+      for (int i = 0; i < PASSES; ++i)
+        if (last + (uint32_t)(r0 + i * RPP) < p.len) *reinterpret_cast<uint4*>(tail + (r0 + i * RPP) * D + col) = x[i];
+    }
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // so that the word is cleared before the next kernel begins
+}
+
+// ----------------------------------------------------------------------------- read ----
+__device__ __forceinline__ void widen(uint32_t four, bool e4m3, float scale, float (&y)[4]) {
+  if (e4m3) {
+    uint32_t lo, hi;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(lo) : "h"((uint16_t)(four & 0xffffu)));
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(hi) : "h"((uint16_t)(four >> 16)));
+    const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&lo));
+    const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+    y[0] = a.x, y[1] = a.y, y[2] = b.x, y[3] = b.y;
+  } else {
+    // 2^23 + (c + 128), less 2^23 + 128
+    const uint32_t u = four ^ 0x80808080u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[i] = __fsub_rn(__uint_as_float(__byte_perm(u, 0x4b000000u, 0x7440 + i)), 8388736.f);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) y[i] = __fmul_rn(y[i], scale);
+}
+
+// One granule of one head of k or v a warp: 16 rows, contiguous in the page.
+template <int D, typename T, typename TO>
+__global__ void __launch_bounds__(kThreads) k_quant_read(const QuantRows a) {
+  constexpr int LPR = D / 8, RPP = 32 / LPR, PASSES = kGranule / RPP;
+  if (blockIdx.x == 0) {
+    check_requests<false>(a);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    return;
+  }
+  const QuantCache& c = a.c;
+  const int lane = threadIdx.x & 31;
+  const uint32_t units = ((uint32_t)(a.T / kGranule) + 2u * (uint32_t)a.N) * 2u * (uint32_t)c.hkv;
+  const uint32_t unit = (blockIdx.x - 1) * (uint32_t)kWarps + (threadIdx.x >> 5);
+  if (unit < units) {
+    const uint32_t w = unit / (2u * (uint32_t)c.hkv), rest = unit - w * 2u * (uint32_t)c.hkv;
+    const int h = (int)(rest >> 1);
+    const bool is_v = rest & 1;
+    const Piece p = piece_of(a, kGranuleShift, w, lane);
+    if (p.on) {
+      const int B = 1 << c.block_shift, r0 = lane / LPR, col = lane % LPR * 8;
+      const bool valid = p.len != 0;
+      const int rows = a.cu[p.n + 1] - p.cu0;
+      const uint32_t end = valid ? p.len : (uint32_t)rows, waits = p.len & ~(uint32_t)(B - 1);
+      TO* out = static_cast<TO*>(is_v ? a.v_out : a.k_out) + ((int64_t)p.cu0 * c.hkv + h) * D + col;
+      auto put = [&](uint32_t pos, const float (&y)[8]) {
+        TO* to = out + (int64_t)(pos - p.begin) * c.hkv * D;
+        if constexpr (sizeof(TO) == 2) {
+          uint4 u;
+          uint32_t v[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const __nv_bfloat162 b = __floats2bfloat162_rn(y[2 * e], y[2 * e + 1]);
+            v[e] = *reinterpret_cast<const uint32_t*>(&b);
+          }
+          u = make_uint4(v[0], v[1], v[2], v[3]);
+          *reinterpret_cast<uint4*>(to) = u;
+        } else {
+          store4(reinterpret_cast<float*>(to), make_float4(y[0], y[1], y[2], y[3]));
+          store4(reinterpret_cast<float*>(to) + 4, make_float4(y[4], y[5], y[6], y[7]));
+        }
+      };
+      bool lost = !valid;
+      if (valid && p.first < waits) {
+        const uint32_t b = p.first >> c.page_shift;
+        const int page = b < (uint32_t)a.max_blocks ? a.block_table[(int64_t)p.n * a.max_blocks + b] : -1;
+        if (page < 0 || page >= c.num_pages) {
+          lost = true;
+          if (lane == 0) report(a.hdr, GDN_DEVERR_PAGES);
+        } else {
+          const int64_t row = (((int64_t)page * c.hkv + h) << c.page_shift) + (p.first & ((1u << c.page_shift) - 1u));
+          const uint8_t* from = (is_v ? c.v_pages : c.k_pages) + (row + r0) * D + col;
+          uint2 x[PASSES];
+#pragma unroll
+          for (int i = 0; i < PASSES; ++i) x[i] = *reinterpret_cast<const uint2*>(from + i * RPP * D);
+          const float scale = (is_v ? c.v_scale : c.k_scale)[row >> c.block_shift];
+#pragma unroll
+          for (int i = 0; i < PASSES; ++i) {
+            const uint32_t pos = p.first + (uint32_t)(r0 + i * RPP);
+            float lo[4], hi[4];
+            widen(x[i].x, c.e4m3, scale, lo);
+            widen(x[i].y, c.e4m3, scale, hi);
+            if (pos >= p.begin && pos < end) put(pos, {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]});
+          }
+        }
+      } else if (valid) {
+        const int slot = a.slot ? a.slot[p.n] : p.n;
+        lost = slot < 0 || slot >= c.slots;  // reported by block 0
+        const T* tail = static_cast<const T*>(is_v ? c.v_tail : c.k_tail) + ((int64_t)slot * c.hkv + h) * B * D + col;
+#pragma unroll
+        for (int i = 0; i < PASSES; ++i) {
+          const uint32_t pos = p.first + (uint32_t)(r0 + i * RPP);
+          if (lost || pos < p.begin || pos >= end) continue;
+          float y[8];
+          load8(tail + (int64_t)(pos - waits) * D, y);
+          put(pos, y);
+        }
+      }
+      if (lost) {
+        const float x = __builtin_nanf("");
+        for (int i = 0; i < PASSES; ++i) {
+          const uint32_t pos = p.first + (uint32_t)(r0 + i * RPP);
+          if (pos >= p.begin && pos < end) put(pos, {x, x, x, x, x, x, x, x});
+        }
+      }
+    }
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// The error word of a call; the rows' kernel starts beside this and waits for it where it has something to report.
+__global__ void k_quant_clear(WsHeader* hdr) {
+  asm volatile("griddepcontrol.launch_dependents;");
+  hdr->err = 0;
+}
+
+template <typename K>
+int launch(K* kernel, const QuantRows& a, int64_t ctas, cudaStream_t st) {
+  k_quant_clear<<<1, 1, 0, st>>>(a.hdr);
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t c{};
+  c.stream = st;
+  c.attrs = &attr;
+  c.numAttrs = 1;
+  c.gridDim = dim3((unsigned)(1 + ctas));
+  c.blockDim = dim3(kThreads);
+  cudaLaunchKernelEx(&c, kernel, a);
+  return 2;
+}
+
+template <int D, typename T>
+int append_t(const QuantRows& a, cudaStream_t st) {
+  const int per = kWarps / ((1 << a.c.block_shift) / kGranule);  // units of a CTA
+  const int64_t units = quant_pieces(a.N, a.T, a.c.block_shift) * 2 * a.c.hkv;
+  return launch(k_quant_append<D, T>, a, (units + per - 1) / per, st);
+}
+
+template <int D, typename T, typename TO>
+int read_t(const QuantRows& a, cudaStream_t st) {
+  const int64_t units = quant_pieces(a.N, a.T, kGranuleShift) * 2 * a.c.hkv;
+  return launch(k_quant_read<D, T, TO>, a, (units + kWarps - 1) / kWarps, st);
+}
+
+template <int D>
+int read_d(const QuantRows& a, bool bf16, bool out_bf16, cudaStream_t st) {
+  using H = __nv_bfloat16;
+  if (bf16) return out_bf16 ? read_t<D, H, H>(a, st) : read_t<D, H, float>(a, st);
+  return out_bf16 ? read_t<D, float, H>(a, st) : read_t<D, float, float>(a, st);
+}
+
+}  // namespace
+
+int launch_quant_append(const QuantRows& a, int d, bool bf16, cudaStream_t st) {
+  using H = __nv_bfloat16;
+  if (d == 32) return bf16 ? append_t<32, H>(a, st) : append_t<32, float>(a, st);
+  if (d == 64) return bf16 ? append_t<64, H>(a, st) : append_t<64, float>(a, st);
+  return bf16 ? append_t<128, H>(a, st) : append_t<128, float>(a, st);
+}
+
+int launch_quant_read(const QuantRows& a, int d, bool bf16, bool out_bf16, cudaStream_t st) {
+  if (d == 32) return read_d<32>(a, bf16, out_bf16, st);
+  if (d == 64) return read_d<64>(a, bf16, out_bf16, st);
+  return read_d<128>(a, bf16, out_bf16, st);
+}
+
+}  // namespace gdn

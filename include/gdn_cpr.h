@@ -521,6 +521,75 @@ gdn_status gdn_cpr_window_attn_bwd(const gdn_cpr_attn *attn, int32_t num_seqs, i
 gdn_status gdn_cpr_window_attn_workspace_size(const gdn_cpr_attn *attn, int32_t total_q,
                                               int32_t backward, size_t *bytes);
 
+/* =====================================================================================
+ * 8-bit cache
+ *
+ * The paged cache with keys and values in 8 bits: half the memory of bf16 pages, and half the
+ * bytes of a decode step.  A block is `block` consecutive tokens of one key head, x [block, d]; it
+ * is held as 8-bit codes c and one fp32 scale s and stands for c s:
+ *   GDN_INT8  s = max|x| / 127, c = 127 x / max|x| to the nearest whole number, ties to even
+ *   GDN_E4M3  s = the least power of two 2^e with max|x| <= 448 2^e, c = x / s to the nearest e4m3
+ *             value, ties to even
+ * A block whose max|x| lies below 2^-100 is held as zeros with s = 0; one that holds an infinity or
+ * a NaN as zeros with s = NaN, so that all of it reads as NaN.
+ *
+ * Only whole blocks are held in 8 bits.  The rows of a request's unfinished block wait, as they
+ * came, in its tail: of seq_len tokens the first seq_len / block * block are in the pages, the
+ * others in rows 0 .. of tail[slot].  So every block is rounded once, from the values that were
+ * appended, and what the cache holds does not depend on how the tokens were split over calls.
+ *
+ * Layouts:  k_pages, v_pages [num_pages, h_kv, page_size, d] 8 bits;  k_scale, v_scale [num_pages,
+ * h_kv, page_size / block] fp32;  k_tail, v_tail [slots, h_kv, block, d] in dtype.  Request n has
+ * the tail slot[n] (NULL: n); slots of one call are distinct.  block_table, seq_lens and the
+ * conventions of the attention-layer operators above apply.
+ * Claims: theirs, and block in {16, 32, 64, 128}, block <= page_size; num_pages * h_kv * page_size
+ * and slots * h_kv * block below 2^32 - 1; h_kv <= 65535, N <= 65535.
+ * ===================================================================================== */
+typedef enum { GDN_INT8 = 0, GDN_E4M3 = 1 } gdn_code;
+
+typedef struct {
+    int32_t num_pages, page_size, block, slots, h_kv, d;
+    gdn_code code;
+    gdn_dtype dtype; /* of the tails, of what is appended, and of q and out in decode */
+    void *k_pages, *v_pages;
+    float *k_scale, *v_scale;
+    void *k_tail, *v_tail;
+} gdn_cpr_quant_cache;
+
+/* New keys and values into the cache.  Request n appends the tokens cu_seqlens[n] .. of k and v; its
+ * length afterwards is seq_lens[n] (what gdn_cpr_page_map gives).  Every block that they complete is
+ * written to the page of the block table that covers it; the rows of an unfinished block go to the tail.
+ *   k, v        [total_tokens, h_kv, d] in dtype; k_stride, v_stride elements from one token to the
+ *               next (multiples of 16 bytes)
+ *   cu_seqlens  [N + 1] int32, seq_lens [N] int32, block_table [N, max_blocks] int32
+ *   Skipped, and reported by the error word: a request whose offsets are not 0 <= cu_seqlens[n] <=
+ *   cu_seqlens[n + 1] <= total_tokens, or all offsets if cu_seqlens does not run from 0 to
+ *   total_tokens (GDN_DEVERR_CU_SEQLENS; where its own offsets fit, a request may have been written);
+ *   a request whose length is negative or less than what it appends (GDN_DEVERR_POS); one whose
+ *   slot lies outside [0, slots) (GDN_DEVERR_SLOT); a block whose page lies outside the cache or the
+ *   block table (GDN_DEVERR_PAGES).  A request that appends nothing is left alone.
+ *   ws: GDN_CPR_ATTN_HEADER_BYTES, 256-byte aligned (the error word, set by every call)        */
+gdn_status gdn_cpr_quant_append(const gdn_cpr_quant_cache *cache, int32_t num_seqs,
+                                int32_t total_tokens, const void *k, const void *v,
+                                int64_t k_stride, int64_t v_stride, const int32_t *cu_seqlens,
+                                const int32_t *seq_lens, const int32_t *block_table,
+                                int32_t max_blocks, const int32_t *slot, void *ws, size_t ws_bytes,
+                                gdn_stream_t stream);
+
+/* Cached keys and values back into packed rows, as gdn_cpr_window_attn takes them for a prefill that
+ * continues requests: of request n its last cu_seqlens[n + 1] - cu_seqlens[n] positions.
+ *   k, v        [total_tokens, h_kv, d] in out_dtype
+ *   Rows of a request whose length is negative or less than the rows asked for (GDN_DEVERR_POS), rows
+ *   in a tail whose slot lies outside [0, slots) (GDN_DEVERR_SLOT) and rows on a page outside the cache
+ *   or the block table (GDN_DEVERR_PAGES) are NaN.  Offsets that do not fit (GDN_DEVERR_CU_SEQLENS): as
+ *   above, and the outputs are not valid.
+ *   ws: GDN_CPR_ATTN_HEADER_BYTES, 256-byte aligned (the error word, set by every call)        */
+gdn_status gdn_cpr_quant_read(const gdn_cpr_quant_cache *cache, int32_t num_seqs,
+                              int32_t total_tokens, const int32_t *cu_seqlens,
+                              const int32_t *seq_lens, const int32_t *block_table,
+                              int32_t max_blocks, const int32_t *slot, gdn_dtype out_dtype, void *k,
+                              void *v, void *ws, size_t ws_bytes, gdn_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
