@@ -36,7 +36,8 @@ EXPORTS = ("gdn_cpr_version", "gdn_cpr_status_string", "gdn_cpr_workspace_size",
            "gdn_cpr_qk_norm_rope", "gdn_cpr_qk_norm_rope_bwd", "gdn_cpr_qk_norm_rope_workspace_size",
            "gdn_cpr_page_map", "gdn_cpr_paged_decode", "gdn_cpr_paged_decode_workspace_size",
            "gdn_cpr_window_attn", "gdn_cpr_window_attn_bwd", "gdn_cpr_window_attn_workspace_size",
-           "gdn_cpr_quant_append", "gdn_cpr_quant_read")
+           "gdn_cpr_quant_append", "gdn_cpr_quant_read", "gdn_cpr_quant_decode",
+           "gdn_cpr_quant_decode_workspace_size")
 NOALLOC_SCRATCH_BYTES = 64 * 1024 * 1024
 
 
@@ -117,13 +118,16 @@ def load():
             L = ctypes.c_int64
             lib.gdn_cpr_quant_append.argtypes = [P, N, N, P, P, L, L, P, P, P, N, P, P, S, P]
             lib.gdn_cpr_quant_read.argtypes = [P, N, N, P, P, P, N, P, I, P, P, P, S, P]
+            lib.gdn_cpr_quant_decode.argtypes = [P, P, N, N, P, P, N, P, P, P, P, P, S, P]
+            lib.gdn_cpr_quant_decode_workspace_size.argtypes = [P, N, N, ctypes.POINTER(S)]
             for fn in ("gdn_cpr_workspace_size", "gdn_cpr_prefill", "gdn_cpr_decode_step",
                        "gdn_cpr_fwd", "gdn_cpr_bwd", "gdn_cpr_get_device_error",
                        "gdn_cpr_qk_norm_rope", "gdn_cpr_qk_norm_rope_bwd",
                        "gdn_cpr_qk_norm_rope_workspace_size", "gdn_cpr_page_map", "gdn_cpr_paged_decode",
                        "gdn_cpr_paged_decode_workspace_size", "gdn_cpr_window_attn",
                        "gdn_cpr_window_attn_bwd", "gdn_cpr_window_attn_workspace_size",
-                       "gdn_cpr_quant_append", "gdn_cpr_quant_read"):
+                       "gdn_cpr_quant_append", "gdn_cpr_quant_read", "gdn_cpr_quant_decode",
+                       "gdn_cpr_quant_decode_workspace_size"):
                 getattr(lib, fn).restype = I
             _lib = lib
     return _lib

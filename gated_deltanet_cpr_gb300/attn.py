@@ -400,6 +400,36 @@ def quant_read(cache: QuantCache, block_table, seq_lens, cu_seqlens, total_token
     return k_out, v_out
 
 
+def quant_decode(q, cache: QuantCache, block_table, seq_lens, *, slots=None, window=0, sinks=0, scale=None, max_len=None,
+                 out=None, want_lse=False, ws=None):
+    """gdn_cpr_quant_decode: paged_decode over the 8-bit cache, attention of one token per request, q [N, Hq, d] in the
+    cache's dtype.  max_len bounds seq_lens (default: what block_table can hold).  Returns out [N, Hq, d], or (out, lse)
+    with want_lse."""
+    shape, dtype, device = q.shape, q.dtype, cache.device
+    N, hq, d = shape
+    qp = _want_on(q, (N, hq, cache.d), cache.dtype, "q", device)
+    n, table, width, lens, slot = _quant_requests(cache, block_table, seq_lens, slots)
+    if n != N:
+        raise ValueError("q has a row and seq_lens a length for every request")
+    if max_len is None:
+        max_len = width * cache.page_size
+    if not 0 <= max_len < 2 ** 31:
+        max_len = _clip(max_len)
+    desc = (hq, cache.h_kv, d, window, sinks, scale, dtype)
+    if out is None:
+        out = torch.empty_like(q)
+        op = out.data_ptr()
+    else:
+        op = _want_on(out, shape, dtype, "out", device)
+    lse = torch.empty((N, hq), dtype=torch.float32, device=device) if want_lse else None
+    if ws is None:
+        ws = _workspace(q, _attn_bytes("gdn_cpr_quant_decode_workspace_size", *desc, N, max_len))
+    _check("gdn_cpr_quant_decode", api.load().gdn_cpr_quant_decode(
+        ctypes.byref(_attn_struct(*desc)), cache._ref, N, max_len, qp, table, width, lens, slot, op,
+        None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.numel(), _raw_stream(device.index)))
+    return (out, lse) if want_lse else out
+
+
 def _window_setup(q, k, v, cu_q, cu_k, window, sinks, scale, backward, ws):
     Tq, hq, d = q.shape
     Tk, hkv, _ = k.shape

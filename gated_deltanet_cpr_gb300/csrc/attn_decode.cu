@@ -17,22 +17,11 @@
 // which waits for its first keys and joins its warps at the end, reached 72% (runs of 256 keys) to
 // 94% (1024 keys) of it.  Few requests are bound by the latency of one run, the launch and the join:
 // 4 of about 700 tokens take 9.0 us.
-#include "attn.h"
-#include "tc.cuh"
+#include "attn_decode.cuh"
 
 namespace gdn {
 
 namespace {
-
-constexpr int kHeadsPerRun = 16;
-constexpr int kSms = 152;
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-
-__device__ __forceinline__ float exp2_approx(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 
 // What a warp needs to know of a request.
 struct Request {
@@ -48,11 +37,13 @@ struct Request {
     head = skip > 0 ? a.sinks : 0;
   }
   __device__ __forceinline__ int key(int u) const { return u < head ? u : u + skip; }
+  __device__ __forceinline__ int runs(const PagedDecode& a) const { return split_of(n, a.hkv).runs; }
 };
-
-__device__ __forceinline__ void cp_async16_or_zero(uint32_t smem, const void* gmem, bool load) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem), "l"(gmem), "r"(load ? 16 : 0) : "memory");
-}
+// What is read of a request before its turn.
+struct Ahead {
+  int len;
+  __device__ __forceinline__ void load(const PagedDecode& a, int i) { len = a.seq_lens[i]; }
+};
 
 // One run: request i, key head and part of its query heads, which run, and its keys [u, end); bad:
 // a key's page is outside the cache.  Keys are numbered without a sign: a request may end a tile
@@ -62,34 +53,46 @@ struct Run {
   uint32_t u, end;
   int head, skip, bad;
   __device__ __forceinline__ int key(uint32_t x) const { return (int)x < head ? (int)x : (int)x + skip; }
+  __device__ __forceinline__ void set(const PagedDecode& a, const Request& rq, const Ahead&) {
+    const Split s = split_of(rq.n, a.hkv);
+    runs = s.runs;
+    u = (uint32_t)run * (uint32_t)s.keys;
+    end = min((uint32_t)rq.n, u + (uint32_t)s.keys);
+    head = rq.head;
+    skip = rq.skip;
+  }
+  __device__ __forceinline__ void from(const Run& o, int lane) {
+    i = __shfl_sync(0xffffffffu, o.i, lane);
+    y = __shfl_sync(0xffffffffu, o.y, lane);
+    run = __shfl_sync(0xffffffffu, o.run, lane);
+    runs = __shfl_sync(0xffffffffu, o.runs, lane);
+    u = __shfl_sync(0xffffffffu, o.u, lane);
+    end = __shfl_sync(0xffffffffu, o.end, lane);
+    head = __shfl_sync(0xffffffffu, o.head, lane);
+    skip = __shfl_sync(0xffffffffu, o.skip, lane);
+  }
 };
 
-// Where a run's (m, l, a) or output goes: rows of its heads.
-struct Sink {
-  float* acc;   // record of head 0's run, or NULL: the run is the whole request
-  float2* ml;
-  int64_t acc_step, ml_step;  // from one head to the next
-  void* out;                  // row of head 0
-  float* lse;
-  int heads;
-  __device__ __forceinline__ Sink(const PagedDecode& a, const Run& r, int h0, int heads_, int elem) : heads(heads_) {
-    const int64_t row = (int64_t)r.i * a.hq + h0;
-    out = static_cast<char*>(a.out) + row * a.d * elem;
-    lse = a.lse ? a.lse + row : nullptr;
-    acc = nullptr;
-    ml = nullptr;
-    acc_step = ml_step = 0;
-    if (r.runs > 1) {
-      const int64_t rec = row * a.max_splits + r.run;
-      acc = a.partial + rec * a.d;
-      ml = reinterpret_cast<float2*>(a.partial + (int64_t)a.N * a.hq * a.max_splits * a.d) + rec;
-      acc_step = (int64_t)a.max_splits * a.d;
-      ml_step = a.max_splits;
+// What the engines below have in common: the call, and its requests' pages.
+struct Paged {
+  using Kind = Paged;
+  using Args = PagedDecode;
+  using Request = gdn::Request;
+  using Ahead = gdn::Ahead;
+  using Run = gdn::Run;
+  // a page of the request's visible keys is outside the cache
+  __device__ __forceinline__ static int check(const PagedDecode& a, const gdn::Request& rq, int i, int tid, int threads) {
+    bool lost = false;
+    if (rq.n) {
+      const int first = rq.key(rq.head) >> a.page_shift, last = (rq.len - 1) >> a.page_shift;
+      const int head_pages = rq.head ? ((rq.head - 1) >> a.page_shift) + 1 : 0;
+      for (int b = tid; b < head_pages + last - first + 1; b += threads) {
+        const int p = b < head_pages ? b : first + b - head_pages;
+        const int page = p < a.max_blocks ? a.block_table[(int64_t)i * a.max_blocks + p] : -1;
+        lost |= page < 0 || page >= a.num_pages;
+      }
     }
-  }
-  __device__ __forceinline__ void stats(int h, float m, float l) const {
-    if (ml) ml[h * ml_step] = make_float2(m, l);
-    else if (lse) lse[h] = __fmul_rn(__fadd_rn(m, log2f(l)), kLn2);
+    return lost ? GDN_DEVERR_PAGES : 0;
   }
 };
 
@@ -99,10 +102,10 @@ struct Sink {
 // values, which one halving exchange turns into one whole score per lane (LPR - 1 shuffles
 // instead of log2(LPR) per score), where its exponential is formed.  NC chunks of H heads.
 template <int D, typename T, int H, int NC>
-struct SimtEngine {
+struct SimtEngine : Paged {
   using Elem = T;
   static constexpr int DIM = D, KEYS = 32 / H, ROWB = D * sizeof(T), EXTRA = NC * H * D * 4;
-  static constexpr int RING = KEYS * ROWB > 4096 ? 2 : 3;
+  static constexpr int STAGE = 2 * KEYS * ROWB, RING = KEYS * ROWB > 4096 ? 2 : 3;
   static constexpr int LPR = D / 4, KPW = 32 / LPR, KT = KEYS / KPW;
   static constexpr bool MANY_REGS = NC == 4;  // more than 168 a thread
   static_assert(KT * H == LPR, "one score per lane");
@@ -232,9 +235,9 @@ __device__ __forceinline__ uint32_t pack2_rest(float lo, float hi, uint32_t pack
 }
 
 template <int D>
-struct MmaEngine {
+struct MmaEngine : Paged {
   using Elem = __nv_bfloat16;
-  static constexpr int DIM = D, KEYS = 32, ROWB = D * 2, RING = 2, EXTRA = 0, KS = D / 16, NT = KEYS / 8;
+  static constexpr int DIM = D, KEYS = 32, ROWB = D * 2, STAGE = 2 * KEYS * ROWB, RING = 2, EXTRA = 0, KS = D / 16, NT = KEYS / 8;
   static constexpr bool MANY_REGS = false;
   uint32_t q[KS][4];
   float m[2], l[2], o[D / 8][4];
@@ -358,98 +361,14 @@ struct MmaEngine {
   }
 };
 
-// ---------------------------------------------------------------------------- walk ----
-// One CTA per SM with as many warps as its shared memory has rings for (7, or as many on each
-// scheduler: 13 warps instead of 12 at d = 64 cost 200 requests 249 us against 225).  First slots are
-// dealt out across the SMs before a second warp of any gets one, so that a few runs spread over
-// all of them: with several smaller CTAs an SM, some SMs got three busy ones and some none (7 requests
-// of 4 to 22 thousand tokens, d = 64: 28.1 us against 23.9; 4 of about 700: 10.2 against 9.0).
-template <typename E>
-struct DecodeSmem {
-  static constexpr int STAGE = 2 * E::KEYS * E::ROWB, RING = E::RING * STAGE, EXTRA = RING, QUEUE = EXTRA + E::EXTRA;
-  static constexpr int WARP = (QUEUE + 4 * (int)sizeof(Run) + 127) / 128 * 128, MOST = 227 * 1024 / WARP;
-  static constexpr int WARPS = MOST < 8 ? MOST : MOST < 12 || E::MANY_REGS ? 8 : 12, HALF = 116 * 1024;
-  static constexpr int BYTES = WARPS * WARP > HALF ? WARPS * WARP : HALF;  // more than half: one CTA per SM
-};
-
 // The fetching side of a warp: which tile comes next, and where its keys lie.
 template <typename E>
-struct Walk {
-  // (run, request, part) slots are numbered with the run slowest and dealt out in chunks of `chunk`
-  // <= 32 consecutive ones, one per lane: the first by the warp's number, further ones from a
-  // counter, as runs differ in length and many slots of short requests are empty.
-  uint32_t total, chunk;
-  int32_t* counter;
-  uint32_t base;                 // the chunk after the present one, looked up a run ahead of its use:
-  int next_i, next_y, next_run;  // this lane's slot of it (next_run < 0: none)
-  int next_len;                  // and its request's length
-  uint32_t left;                 // slots of the present chunk that hold a run and are still to come
-  Run mine;                      // this lane's run of it
-  Run r;                         // the run being fetched
-  bool live;                     // there is one
-  int page;                      // lane < KEYS: page of key r.u + lane, on its way during the tile before
-
-  __device__ __forceinline__ void look_ahead(const PagedDecode& a, int parts, int lane) {
-    const uint32_t w = base + (uint32_t)lane, ny = (uint32_t)(a.hkv * parts), rows = (uint32_t)a.N * ny;
-    next_run = -1;
-    if (w >= total || lane >= (int)chunk) return;
-    next_run = (int)(w / rows);
-    const uint32_t v = w - (uint32_t)next_run * rows;
-    next_i = (int)(v / ny);
-    next_y = (int)(v - (uint32_t)next_i * ny);
-    next_len = a.seq_lens[next_i];
-  }
-
-  // The next run of this warp.  Requests without keys have their rows written here.
-  __device__ void seek(const PagedDecode& a, int parts, int lane) {
-    live = false;
-    while (!left) {
-      if (base >= total) return;
-      bool have = false;
-      if (next_run >= 0) {
-        const Request rq(a, next_len);
-        const Split s = split_of(rq.n, a.hkv);
-        mine.i = next_i;
-        mine.y = next_y;
-        mine.run = next_run;
-        mine.runs = s.runs;
-        have = next_run < s.runs;
-        mine.u = (uint32_t)next_run * (uint32_t)s.keys;
-        mine.end = min((uint32_t)rq.n, mine.u + (uint32_t)s.keys);
-        mine.head = rq.head;
-        mine.skip = rq.skip;
-        if (s.runs == 0 && next_run == 0) write_empty(a, mine, parts, rq.bad);
-      }
-      left = __ballot_sync(0xffffffffu, have);
-      int n = 0;
-      if (!counter) base = total;
-      else if (lane == 0) n = atomicAdd(counter, 1);
-      if (counter) base = (gridDim.x * DecodeSmem<E>::WARPS + (uint32_t)__shfl_sync(0xffffffffu, n, 0)) * chunk;
-      look_ahead(a, parts, lane);
-    }
-    const int src = __ffs(left) - 1;
-    left &= left - 1;
-    r.i = __shfl_sync(0xffffffffu, mine.i, src);
-    r.y = __shfl_sync(0xffffffffu, mine.y, src);
-    r.run = __shfl_sync(0xffffffffu, mine.run, src);
-    r.runs = __shfl_sync(0xffffffffu, mine.runs, src);
-    r.u = __shfl_sync(0xffffffffu, mine.u, src);
-    r.end = __shfl_sync(0xffffffffu, mine.end, src);
-    r.head = __shfl_sync(0xffffffffu, mine.head, src);
-    r.skip = __shfl_sync(0xffffffffu, mine.skip, src);
-    live = true;
-  }
-
-  // zeros for a request without keys, NaN for a length that is not valid; one lane
-  __device__ static void write_empty(const PagedDecode& a, const Run& c, int parts, bool bad) {
-    const int group = a.hq / a.hkv, g0 = (c.y % parts) * kHeadsPerRun, heads = min(kHeadsPerRun, group - g0);
-    const int64_t row = (int64_t)c.i * a.hq + (c.y / parts) * group + g0;
-    const float x = bad ? __builtin_nanf("") : 0.f;
-    for (int e = 0; e < heads * E::DIM; e += 4)
-      store4(static_cast<typename E::Elem*>(a.out) + row * E::DIM + e, make_float4(x, x, x, x));
-    if (a.lse)
-      for (int h = 0; h < heads; ++h) a.lse[row + h] = bad ? x : -INFINITY;
-  }
+struct Walk : Dealer<E> {
+  using Dealer<E>::r;
+  using Dealer<E>::live;
+  using Dealer<E>::seek;
+  using Dealer<E>::push;
+  int page;  // lane < KEYS: page of key r.u + lane, on its way during the tile before
 
   __device__ __forceinline__ bool has_key(int lane) const { return lane < E::KEYS && r.u + lane < r.end; }
 
@@ -500,15 +419,6 @@ struct Walk {
       if (live) push(a, parts, queue, tail, lane);
     }
     look_up(a, lane);
-  }
-  // a run that is fetched from here on: at most the computed one, two fetched tiles' and the next are open
-  __device__ __forceinline__ void push(const PagedDecode& a, int parts, Run* queue, int& tail, int lane) {
-    r.bad = 0;
-    if (lane == 0) queue[tail & 3] = r;
-    const int group = a.hq / a.hkv, g0 = (r.y % parts) * kHeadsPerRun, heads = min(kHeadsPerRun, group - g0);
-    const char* q = static_cast<const char*>(a.q) + ((int64_t)r.i * a.hq + (r.y / parts) * group + g0) * E::ROWB;
-    for (int e = lane * 128; e < heads * E::ROWB; e += 32 * 128) tc::prefetch_l2(q + e);
-    ++tail;
   }
 };
 
@@ -563,153 +473,16 @@ __global__ void __launch_bounds__(32 * DecodeSmem<E>::WARPS, 1) k_decode(const P
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-// ---------------------------------------------------------------------------- join ----
-// D / 4 lanes per (request, head) add the runs' records in ascending order, 16 at a time so that their
-// loads are in flight together; more than 16 runs are shared out to the groups of lanes of a
-// block that has the head to itself (SPLIT), whose sums are added in order.  How a request's runs are added
-// depends on their number alone.  A request's CTAs also check its length and the pages of its
-// visible keys for the error word.
-constexpr int kJoinAtOnce = 16;
-template <int D, typename T, bool SPLIT>
-__global__ void __launch_bounds__(SPLIT ? 256 : 128) k_decode_join(const PagedDecode a) {
-  constexpr int THREADS = SPLIT ? 256 : 128, LANES = D / 4, GROUPS = THREADS / LANES, B = kJoinAtOnce;
-  __shared__ float4 so[SPLIT ? GROUPS : 1][LANES];
-  __shared__ float2 sml[SPLIT ? GROUPS : 1];
-  // what does not come from the runs' kernel is read while that still runs
-  const int g = threadIdx.x / LANES, lane = threadIdx.x % LANES, c = 4 * lane;
-  const int i = blockIdx.y, h = SPLIT ? blockIdx.x : blockIdx.x * GROUPS + g;
-  const Request rq(a, a.seq_lens[i]);
-  const int runs = split_of(rq.n, a.hkv).runs;
-  const bool shared = SPLIT && runs > B;
-  const int per = shared ? (runs + GROUPS - 1) / GROUPS : runs;
-  const int begin = shared ? min(runs, g * per) : 0, end = shared ? min(runs, begin + per) : runs;
-  bool lost = false;  // a page of the request's visible keys is outside the cache
-  if (rq.n) {
-    const int first = rq.key(rq.head) >> a.page_shift, last = (rq.len - 1) >> a.page_shift;
-    const int head_pages = rq.head ? ((rq.head - 1) >> a.page_shift) + 1 : 0;
-    for (int b = blockIdx.x * THREADS + threadIdx.x; b < head_pages + last - first + 1; b += gridDim.x * THREADS) {
-      const int p = b < head_pages ? b : first + b - head_pages;
-      const int page = p < a.max_blocks ? a.block_table[(int64_t)i * a.max_blocks + p] : -1;
-      lost |= page < 0 || page >= a.num_pages;
-    }
-  }
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the runs' kernel has finished
-  if (rq.bad && threadIdx.x == 0) set_error(a.hdr, GDN_DEVERR_POS);
-  if (lost) set_error(a.hdr, GDN_DEVERR_PAGES);
-  if (runs > 1 && h < a.hq && (shared || !SPLIT || g == 0)) {
-    const int64_t row = (int64_t)i * a.hq + h;
-    const float* rec = a.partial + row * a.max_splits * D + c;
-    const float2* mls =
-        reinterpret_cast<const float2*>(a.partial + (int64_t)a.N * a.hq * a.max_splits * D) + row * a.max_splits;
-    float m = -INFINITY, l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    auto add = [&](const float2 (&ml)[B], const float4 (&x)[B]) {
-      float mx = m;
-#pragma unroll
-      for (int r = 0; r < B; ++r) mx = fmaxf(mx, ml[r].x);
-      const float base = mx == -INFINITY ? 0.f : mx, f0 = exp2_approx(__fsub_rn(m, base));
-      m = mx;
-      l = __fmul_rn(l, f0);
-      o = make_float4(__fmul_rn(o.x, f0), __fmul_rn(o.y, f0), __fmul_rn(o.z, f0), __fmul_rn(o.w, f0));
-#pragma unroll
-      for (int r = 0; r < B; ++r) {
-        const float f = exp2_approx(__fsub_rn(ml[r].x, base));
-        l = __fmaf_rn(f, ml[r].y, l);
-        o = make_float4(__fmaf_rn(f, x[r].x, o.x), __fmaf_rn(f, x[r].y, o.y), __fmaf_rn(f, x[r].z, o.z),
-                        __fmaf_rn(f, x[r].w, o.w));
-      }
-    };
-    float2 ml[B];
-    float4 x[B];
-    for (int r0 = begin; r0 < end; r0 += B) {
-#pragma unroll
-      for (int r = 0; r < B; ++r) {
-        ml[r] = make_float2(-INFINITY, 0.f);
-        x[r] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (r0 + r < end) {
-          ml[r] = mls[r0 + r];
-          x[r] = *reinterpret_cast<const float4*>(rec + (int64_t)(r0 + r) * D);
-        }
-      }
-      add(ml, x);
-    }
-    if (shared) {
-      so[g][lane] = o;
-      if (lane == 0) sml[g] = make_float2(m, l);
-      __syncthreads();  // every thread of the block is here: `shared` is the request's
-      m = -INFINITY, l = 0.f, o = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int g0 = 0; g0 < GROUPS; g0 += B) {
-#pragma unroll
-        for (int r = 0; r < B; ++r) {
-          ml[r] = g0 + r < GROUPS ? sml[g0 + r] : make_float2(-INFINITY, 0.f);
-          x[r] = g0 + r < GROUPS ? so[g0 + r][lane] : make_float4(0.f, 0.f, 0.f, 0.f);
-        }
-        add(ml, x);
-      }
-    }
-    if (g == 0 || !SPLIT) {
-      store4(static_cast<T*>(a.out) + row * D + c,
-             make_float4(__fdiv_rn(o.x, l), __fdiv_rn(o.y, l), __fdiv_rn(o.z, l), __fdiv_rn(o.w, l)));
-      if (a.lse && c == 0) a.lse[row] = __fmul_rn(__fadd_rn(m, log2f(l)), kLn2);
-    }
-  }
-}
-
-// The counter of a call whose warps take more than one chunk; the runs' kernel starts beside this.
-__global__ void k_decode_clear(int32_t* counter) {
-  asm volatile("griddepcontrol.launch_dependents;");
-  *counter = 0;
-}
-
-template <typename E>
-int launch_decode(const PagedDecode& a, cudaStream_t st) {
-  constexpr int D = E::DIM, BYTES = DecodeSmem<E>::BYTES;
-  static std::atomic<uint64_t> ready{0};
-  ensure_smem(k_decode<E>, BYTES, ready);
-  const int group = a.hq / a.hkv, parts = (group + kHeadsPerRun - 1) / kHeadsPerRun;
-  const int64_t total = (int64_t)a.N * a.hkv * parts * a.max_splits, ctas = total < kSms ? total : kSms;
-  const int64_t warps = ctas * DecodeSmem<E>::WARPS;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t c{};
-  c.stream = st;
-  c.attrs = &attr;
-  c.numAttrs = 0;
-  int32_t* counter = nullptr;
-  if (total > warps) {
-    counter = a.hdr->pad;
-    k_decode_clear<<<1, 1, 0, st>>>(counter);
-    c.numAttrs = 1;
-  }
-  // about eight chunks a warp, of single slots unless there are many
-  const int64_t chunk = total / (8 * warps);
-  c.gridDim = dim3((unsigned)ctas);
-  c.blockDim = dim3(32 * DecodeSmem<E>::WARPS);
-  c.dynamicSmemBytes = BYTES;
-  cudaLaunchKernelEx(&c, k_decode<E>, a, parts, (uint32_t)(chunk < 1 ? 1 : chunk > 32 ? 32 : chunk), counter);
-  const bool split = a.max_splits > kJoinAtOnce;
-  c.gridDim = dim3(split ? a.hq : (a.hq + 512 / D - 1) / (512 / D), a.N);
-  c.blockDim = dim3(split ? 256 : 128);
-  c.dynamicSmemBytes = 0;
-  c.numAttrs = 1;
-  if (split)
-    cudaLaunchKernelEx(&c, k_decode_join<D, typename E::Elem, true>, a);
-  else
-    cudaLaunchKernelEx(&c, k_decode_join<D, typename E::Elem, false>, a);
-  return counter ? 3 : 2;
-}
-
 template <int D, typename T>
 int decode_t(const PagedDecode& a, cudaStream_t st) {
   const int group = a.hq / a.hkv;
   if constexpr (D >= 64 && sizeof(T) == 2) {
-    return launch_decode<MmaEngine<D>>(a, st);
+    return launch_decode<MmaEngine<D>>(k_decode<MmaEngine<D>>, a, st);
   } else {
-    if (group <= 2) return launch_decode<SimtEngine<D, T, 2, 1>>(a, st);
-    if (group <= 4) return launch_decode<SimtEngine<D, T, 4, 1>>(a, st);
-    if (group <= 8) return launch_decode<SimtEngine<D, T, 4, 2>>(a, st);
-    return launch_decode<SimtEngine<D, T, 4, 4>>(a, st);
+    if (group <= 2) return launch_decode<SimtEngine<D, T, 2, 1>>(k_decode<SimtEngine<D, T, 2, 1>>, a, st);
+    if (group <= 4) return launch_decode<SimtEngine<D, T, 4, 1>>(k_decode<SimtEngine<D, T, 4, 1>>, a, st);
+    if (group <= 8) return launch_decode<SimtEngine<D, T, 4, 2>>(k_decode<SimtEngine<D, T, 4, 2>>, a, st);
+    return launch_decode<SimtEngine<D, T, 4, 4>>(k_decode<SimtEngine<D, T, 4, 4>>, a, st);
   }
 }
 

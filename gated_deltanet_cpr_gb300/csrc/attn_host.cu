@@ -1,6 +1,7 @@
 // attn_host.cu -- the C ABI of the attention-layer operators (include/gdn_cpr.h): argument
 // checks and workspace sizes; the kernels are in attn_tokens.cu, attn_decode.cu,
-// attn_window.cu, attn_window_tc.cu and, of the 8-bit cache, attn_quant_rows.cu.
+// attn_window.cu, attn_window_tc.cu and, of the 8-bit cache, attn_quant_rows.cu and
+// attn_quant_decode.cu.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -119,6 +120,7 @@ const char* const kMapStages[] = {"page map", nullptr};
 const char* const kPagedStages[] = {"paged decode attention", nullptr};
 const char* const kWindowStages[] = {"window attention", nullptr};
 const char* const kQuantAppendStages[] = {"8-bit cache append", nullptr};
+const char* const kQuantDecodeStages[] = {"8-bit cache decode attention", nullptr};
 const char* const kQuantReadStages[] = {"8-bit cache read", nullptr};
 const char* const kWindowBwdStages[] = {"window attention dq", "window attention dk, dv", nullptr};
 
@@ -212,6 +214,11 @@ gdn_status quant_rows_args(const gdn_cpr_quant_cache* c, int32_t N, int32_t T, c
   a->slot = slot;
   a->hdr = static_cast<WsHeader*>(ws);
   return GDN_OK;
+}
+
+int quant_splits(const gdn_cpr_attn* a, int32_t max_len) {
+  const int64_t keys = quant_granules(max_len, a->window, a->sinks) << kGranuleShift;
+  return paged_decode_max_splits(keys < INT32_MAX ? (int)keys : INT32_MAX, a->h_kv);
 }
 
 size_t window_bytes(const gdn_cpr_attn* a, int32_t Tq, bool backward) {
@@ -509,6 +516,63 @@ gdn_status gdn_cpr_quant_read(const gdn_cpr_quant_cache* cache, int32_t num_seqs
   a.v_out = v;
   Stages stg(stream, kQuantReadStages);
   stg.mark(launch_quant_read(a, cache->d, cache->dtype == GDN_BF16, out_dtype == GDN_BF16, stream));
+  return finish();
+}
+
+gdn_status gdn_cpr_quant_decode_workspace_size(const gdn_cpr_attn* attn, int32_t num_seqs, int32_t max_len,
+                                               size_t* bytes) {
+  if (!bytes) return GDN_ERR_INVALID_ARG;
+  const gdn_status rc = check_attn(attn);
+  if (rc != GDN_OK) return rc;
+  if (num_seqs < 0 || max_len < 0) return GDN_ERR_INVALID_ARG;
+  *bytes = decode_bytes(attn, num_seqs, quant_splits(attn, max_len));
+  return GDN_OK;
+}
+
+gdn_status gdn_cpr_quant_decode(const gdn_cpr_attn* attn, const gdn_cpr_quant_cache* cache, int32_t num_seqs,
+                                int32_t max_len, const void* q, const int32_t* block_table, int32_t max_blocks,
+                                const int32_t* seq_lens, const int32_t* slot, void* out, float* lse, void* ws,
+                                size_t ws_bytes, gdn_stream_t stream) {
+  NvtxRange nvtx("gdn_cpr_quant_decode");
+  gdn_status rc = check_attn(attn);
+  if (rc != GDN_OK) return rc;
+  if (num_seqs < 0 || max_len < 0 || max_blocks < 0) return GDN_ERR_INVALID_ARG;
+  rc = check_quant(cache, num_seqs > 0);
+  if (rc != GDN_OK) return rc;
+  if (cache->h_kv != attn->h_kv || cache->d != attn->d || cache->dtype != attn->dtype) return GDN_ERR_INVALID_ARG;
+  if (num_seqs > 65535) return GDN_ERR_UNSUPPORTED;
+  if (num_seqs > 0 && (!ok_ptr(q, 16) || !ok_ptr(out, 16) || !ok_ptr(seq_lens, 4) || !aligned(slot, 4) || !aligned(lse, 4)))
+    return GDN_ERR_INVALID_ARG;
+  if (num_seqs > 0 && max_blocks > 0 && !ok_ptr(block_table, 4)) return GDN_ERR_INVALID_ARG;
+  const int splits = quant_splits(attn, max_len);
+  // runs are numbered in 32 bits (at most 16 query heads of a key head to one)
+  const int64_t parts = (attn->h_q / attn->h_kv + 15) / 16;
+  if ((double)num_seqs * attn->h_kv * parts * splits >= (double)(1 << 30)) return GDN_ERR_UNSUPPORTED;
+  if (!ok_ws(ws, ws_bytes, decode_bytes(attn, num_seqs, splits))) return GDN_ERR_WORKSPACE;
+  if (num_seqs == 0) return empty_call(ws, stream);
+  QuantDecode a{};
+  a.N = num_seqs;
+  a.hq = attn->h_q;
+  a.hkv = attn->h_kv;
+  a.d = attn->d;
+  a.window = attn->window;
+  a.sinks = attn->sinks;
+  a.max_len = max_len;
+  a.scale = scale_of(attn);
+  a.q = q;
+  a.page_shift = page_shift_of(cache->page_size);
+  a.max_blocks = max_blocks;
+  a.block_table = block_table;
+  a.seq_lens = seq_lens;
+  a.out = out;
+  a.lse = lse;
+  a.partial = reinterpret_cast<float*>(at(ws, GDN_CPR_ATTN_HEADER_BYTES));
+  a.max_splits = splits;
+  a.hdr = static_cast<WsHeader*>(ws);
+  a.c = quant_view(cache);
+  a.slot = slot;
+  Stages stg(stream, kQuantDecodeStages);
+  stg.mark(launch_quant_decode(a, attn->dtype == GDN_BF16, stream));
   return finish();
 }
 

@@ -33,6 +33,20 @@ struct QuantRows {
 // leaves every request enough numbers without a sum over the others.
 inline int64_t quant_pieces(int N, int T, int shift) { return (int64_t)(T >> shift) + 2 * (int64_t)N; }
 
+// Decode attention: a request's visible keys are counted in granules that hold any.
+struct QuantDecode : PagedDecode {
+  QuantCache c;
+  const int32_t* slot;
+};
+// At most that many granules of a request of `len` keys hold visible ones.
+inline int64_t quant_granules(int64_t len, int window, int sinks) {
+  const int64_t all = (len + kGranule - 1) / kGranule;
+  if (window <= 0 || len <= window) return all;
+  const int64_t some = ((int64_t)sinks + kGranule - 1) / kGranule + ((int64_t)window + 2 * kGranule - 2) / kGranule;
+  return some < all ? some : all;
+}
+int launch_quant_decode(const QuantDecode& a, bool bf16, cudaStream_t st);
+
 int launch_quant_append(const QuantRows& a, int d, bool bf16, cudaStream_t st);
 int launch_quant_read(const QuantRows& a, int d, bool bf16, bool out_bf16, cudaStream_t st);
 

@@ -590,6 +590,22 @@ gdn_status gdn_cpr_quant_read(const gdn_cpr_quant_cache *cache, int32_t num_seqs
                               int32_t max_blocks, const int32_t *slot, gdn_dtype out_dtype, void *k,
                               void *v, void *ws, size_t ws_bytes, gdn_stream_t stream);
 
+/* gdn_cpr_paged_decode over the 8-bit cache: q [N, H_q, d] is the token at position seq_lens[n] - 1,
+ * whose key and value have been appended.  Keys and values are what the cache holds them as; windows,
+ * first tokens, scale, lse and errors as there.  attn and cache agree in h_kv, d and dtype.
+ *   slot        NULL or [N] int32: the requests' tails; one outside [0, slots) sets GDN_DEVERR_SLOT and
+ *               gives NaN for a request whose tail holds tokens
+ *   A key or value that is not finite gives NaN in its request's rows if it is visible, and wherever it
+ *   lies in a block that holds a visible key; masked keys of a block may take part with weight 0.
+ *   ws: gdn_cpr_quant_decode_workspace_size bytes; its error word is set by every call        */
+gdn_status gdn_cpr_quant_decode(const gdn_cpr_attn *attn, const gdn_cpr_quant_cache *cache,
+                                int32_t num_seqs, int32_t max_len, const void *q,
+                                const int32_t *block_table, int32_t max_blocks,
+                                const int32_t *seq_lens, const int32_t *slot, void *out, float *lse,
+                                void *ws, size_t ws_bytes, gdn_stream_t stream);
+gdn_status gdn_cpr_quant_decode_workspace_size(const gdn_cpr_attn *attn, int32_t num_seqs,
+                                               int32_t max_len, size_t *bytes);
+
 #ifdef __cplusplus
 }
 #endif

@@ -107,3 +107,62 @@ def test_plain_rounding_by_hand():
         x[0, 2, 3] = v
         c, s = R.quantise(x, "int8")
         assert c.eq(0).all() and (s.isnan().all() if want != want else s.eq(0).all())
+
+
+BAD_ATTN = [(dict(h_q=3), 2), (dict(h_q=0), 1), (dict(window=-1), 1), (dict(sinks=-2), 1), (dict(scale=-1.0), 1),
+            (dict(scale=float("inf")), 1), (dict(a_h_kv=4), 1), (dict(a_d=128), 1), (dict(a_dtype=0), 1), (dict(a_d=80), 2)]
+
+
+def test_decode_refusals(lib):
+    def call(**kw):
+        at = {n: kw.pop(n) for n in ("h_q", "window", "sinks", "scale", "a_h_kv", "a_d", "a_dtype", "max_len", "q") if n in kw}
+        p, c = split(kw)
+        g = lambda n, x=FAKE: p.get(n, x)  # noqa: E731
+        st = attn.AttnStruct(at.get("h_q", 4), at.get("a_h_kv", 2), at.get("a_d", 64), at.get("window", 0), at.get("sinks", 0),
+                             at.get("scale", 0.0), at.get("a_dtype", 1))
+        return lib.gdn_cpr_quant_decode(ctypes.byref(st), ctypes.byref(c), g("N", 2), at.get("max_len", 300), at.get("q", FAKE),
+                                        g("table"), g("blocks", 4), g("lens"), g("slot"), g("out"), None, g("ws"), g("n", 1 << 30), None)
+
+    # a head count or size that is refused by itself is refused before it is compared with attn's
+    for kw, code in BAD_CACHE + BAD_ATTN + [
+            (dict(N=-1), 1), (dict(N=65536), 2), (dict(max_len=-1), 1), (dict(blocks=-1), 1), (dict(q=None), 1), (dict(out=FAKE + 8), 1),
+            (dict(lens=None), 1), (dict(table=None), 1), (dict(slot=FAKE + 2), 1), (dict(n=256), 4), (dict(ws=FAKE + 128), 4),
+            (dict(N=0, q=None, k_pages=None), 0)]:
+        assert call(**kw) == code, kw
+
+
+def split_runs(n, hkv):
+    """Runs of a request that sees n keys, by the rule of csrc/attn.h in unbounded integers."""
+    x = n * hkv
+    shift = 6 if x < 128 * 32 else 7 if x < 256 * 32 else 8 if x < 512 * 32 else 9
+    r = max(1, (n + (1 << shift >> 1)) >> shift)
+    keys = (-(-n // r) + 31) // 32 * 32
+    return -(-n // keys) if n else 0
+
+
+def granules(L, window, sinks):
+    """Granules of 16 keys that hold visible ones."""
+    if not window or L <= window:
+        return -(-L // 16)
+    first = (L - window) // 16
+    return min(-(-min(sinks, L) // 16), first) + (L - 1) // 16 - first + 1
+
+
+@pytest.mark.parametrize("hkv", [1, 3, 8, 40])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (100, 4), (2033, 17), (1, 0), (5000, 3000)])
+def test_decode_workspace_holds_every_run(lib, hkv, window, sinks):
+    """Of every length up to its bound, the join reads a record for each run."""
+    d, N, top = 64, 2, 2 ** 31 - 1
+
+    def size(m):
+        n, st = ctypes.c_size_t(0), attn.AttnStruct(hkv, hkv, d, window, sinks, 0.0, 1)
+        assert lib.gdn_cpr_quant_decode_workspace_size(ctypes.byref(st), N, m, ctypes.byref(n)) == 0
+        return n.value
+
+    most, before = 0, 0
+    for L in sorted({*range(0, 6000), *range(6000, 40000, 97), 10 ** 6, 10 ** 8, top - 300, top - 16, top - 1, top}):
+        most = max(most, split_runs(min(16 * granules(L, window, sinks), top), hkv))
+        n = size(L)
+        assert most <= 1 or n >= 256 + N * hkv * most * (d + 2) * 4, L
+        assert n >= before
+        before = n
