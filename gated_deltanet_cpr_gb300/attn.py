@@ -5,7 +5,7 @@ and the current stream, every step runs in the kernels of libgdn_cpr.so, and a r
 raises api.GdnError.  What only the device can see (a length past max_len, a page outside the cache,
 a cu_seqlens table that does not fit) is in the error word of the workspace: pass `ws`
 (api.alloc_workspace) and read api.device_error(ws); a call that makes its own workspace does not
-keep it.  Shapes, masks and errors: include/gdn_cpr.h.
+keep it, and one that needs none reports nothing without it.  Shapes, masks and errors: include/gdn_cpr.h.
 """
 from __future__ import annotations
 
@@ -20,6 +20,7 @@ from .api import GdnError, _dt
 NORMS = {"none": 0, "rms": 1, "l2": 2}
 LAYOUTS = {"half": 0, "interleaved": 1}
 CODES = {"int8": torch.int8, "e4m3": torch.float8_e4m3fn}
+_CODE_OF = {torch.int8: 0, torch.float8_e4m3fn: 1}
 HEADER_BYTES = 256
 
 
@@ -88,22 +89,22 @@ class QuantCache:
         return c
 
     def _set(self, k, v, k_scale, v_scale, k_tail, v_tail):
-        if k.dim() != 4 or k_tail.dim() != 4:
+        pages, tails, code = k.shape, k_tail.shape, _CODE_OF.get(k.dtype)
+        if len(pages) != 4 or len(tails) != 4:
             raise ValueError("pages are [pages, H_kv, page_size, d], tails [slots, H_kv, block, d]")
-        self.pages, self.h_kv, self.page_size, self.d = k.shape
-        self.slots, _, self.block, _ = k_tail.shape
-        code = 0 if k.dtype == torch.int8 else 1
-        if k.dtype not in CODES.values() or self.block <= 0 or self.page_size % self.block:
-            raise ValueError("pages hold int8 or float8_e4m3fn codes of whole blocks")
-        scales, tails = (self.pages, self.h_kv, self.page_size // self.block), (self.slots, self.h_kv, self.block, self.d)
+        self.pages, self.h_kv, self.page_size, self.d = pages
+        self.slots, hkv, block, d = tails
+        if code is None or block <= 0 or self.page_size % block or hkv != self.h_kv or d != self.d:
+            raise ValueError("pages hold int8 or float8_e4m3fn codes of whole blocks of the tails' heads and size")
+        self.block = block
         self.k, self.v, self.k_scale, self.v_scale, self.k_tail, self.v_tail = k, v, k_scale, v_scale, k_tail, v_tail
-        self.dtype, self.device = k_tail.dtype, k.device
-        at = self.device
+        self.dtype, self.device = dtype, at = k_tail.dtype, k.device
+        scales, f32 = (self.pages, hkv, self.page_size // block), torch.float32
         self.struct = QuantCacheStruct(
-            self.pages, self.page_size, self.block, self.slots, self.h_kv, self.d, code, _dt(self.dtype),
-            _want_on(k, k.shape, k.dtype, "k pages", at), _want_on(v, k.shape, k.dtype, "v pages", at),
-            _want_on(k_scale, scales, torch.float32, "k_scale", at), _want_on(v_scale, scales, torch.float32, "v_scale", at),
-            _want_on(k_tail, tails, self.dtype, "k_tail", at), _want_on(v_tail, tails, self.dtype, "v_tail", at))
+            self.pages, self.page_size, block, self.slots, hkv, d, code, _dt(dtype),
+            _want(k, pages, k.dtype, "k pages"), _want_on(v, pages, k.dtype, "v pages", at),
+            _want_on(k_scale, scales, f32, "k_scale", at), _want_on(v_scale, scales, f32, "v_scale", at),
+            _want_on(k_tail, tails, dtype, "k_tail", at), _want_on(v_tail, tails, dtype, "v_tail", at))
         self._ref = ctypes.byref(self.struct)
 
 
@@ -352,10 +353,6 @@ def _quant_requests(cache, block_table, seq_lens, slots):
             None if slots is None else _want_on(slots, (N,), i32, "slots", device))
 
 
-def _header(ws, device):
-    return torch.empty(HEADER_BYTES, dtype=torch.uint8, device=device) if ws is None else ws
-
-
 def quant_append(k, v, cache: QuantCache, block_table, seq_lens, cu_seqlens, *, slots=None, ws=None):
     """gdn_cpr_quant_append: new keys and values k, v [T, Hkv, d] (tokens may be strided) into the 8-bit cache.
     Request n appends rows cu_seqlens[n] .. and has seq_lens[n] tokens afterwards (page_map gives both) and the tail
@@ -369,10 +366,10 @@ def quant_append(k, v, cache: QuantCache, block_table, seq_lens, cu_seqlens, *, 
     N, table, width, lens, slot = _quant_requests(cache, block_table, seq_lens, slots)
     kp, ks = _rows(k, hkv, cache.d, "k")
     vp, vs = _rows(v, hkv, cache.d, "v")
-    ws = _header(ws, device)
+    wp, nbytes = (None, 0) if ws is None else (ws.data_ptr(), ws.numel())
     _check("gdn_cpr_quant_append", api.load().gdn_cpr_quant_append(
         cache._ref, N, T, kp, vp, ks, vs, _want_on(cu_seqlens, (N + 1,), torch.int32, "cu_seqlens", device), lens, table,
-        width, slot, ws.data_ptr(), ws.numel(), _raw_stream(device.index)))
+        width, slot, wp, nbytes, _raw_stream(device.index)))
 
 
 def quant_read(cache: QuantCache, block_table, seq_lens, cu_seqlens, total_tokens, *, slots=None, out_dtype=None,
@@ -386,17 +383,21 @@ def quant_read(cache: QuantCache, block_table, seq_lens, cu_seqlens, total_token
     od = out_dtype or (k_out.dtype if k_out is not None else cache.dtype)
     N, table, width, lens, slot = _quant_requests(cache, block_table, seq_lens, slots)
     shape = (T, cache.h_kv, cache.d)
-    if k_out is None and v_out is None:
-        k_out, v_out = torch.empty((2, *shape), dtype=od, device=device).unbind()
-        kp, vp = k_out.data_ptr(), v_out.data_ptr()
+    # two allocations cost less than one and its views
+    if k_out is None:
+        k_out = torch.empty(shape, dtype=od, device=device)
+        kp = k_out.data_ptr()
     else:
-        k_out = torch.empty(shape, dtype=od, device=device) if k_out is None else k_out
-        v_out = torch.empty(shape, dtype=od, device=device) if v_out is None else v_out
-        kp, vp = _want_on(k_out, shape, od, "k_out", device), _want_on(v_out, shape, od, "v_out", device)
-    ws = _header(ws, device)
+        kp = _want_on(k_out, shape, od, "k_out", device)
+    if v_out is None:
+        v_out = torch.empty(shape, dtype=od, device=device)
+        vp = v_out.data_ptr()
+    else:
+        vp = _want_on(v_out, shape, od, "v_out", device)
+    wp, nbytes = (None, 0) if ws is None else (ws.data_ptr(), ws.numel())
     _check("gdn_cpr_quant_read", api.load().gdn_cpr_quant_read(
         cache._ref, N, T, _want_on(cu_seqlens, (N + 1,), torch.int32, "cu_seqlens", device), lens, table, width, slot,
-        _dt(od), kp, vp, ws.data_ptr(), ws.numel(), _raw_stream(device.index)))
+        _dt(od), kp, vp, wp, nbytes, _raw_stream(device.index)))
     return k_out, v_out
 
 

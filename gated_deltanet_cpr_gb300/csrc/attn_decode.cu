@@ -61,7 +61,7 @@ struct Run {
     head = rq.head;
     skip = rq.skip;
   }
-  __device__ __forceinline__ void from(const Run& o, int lane) {
+  __device__ __forceinline__ void from(const PagedDecode&, const Run& o, int lane) {
     i = __shfl_sync(0xffffffffu, o.i, lane);
     y = __shfl_sync(0xffffffffu, o.y, lane);
     run = __shfl_sync(0xffffffffu, o.run, lane);
@@ -80,6 +80,7 @@ struct Paged {
   using Request = gdn::Request;
   using Ahead = gdn::Ahead;
   using Run = gdn::Run;
+  using Seed = gdn::Run;
   // a page of the request's visible keys is outside the cache
   __device__ __forceinline__ static int check(const PagedDecode& a, const gdn::Request& rq, int i, int tid, int threads) {
     bool lost = false;
@@ -107,7 +108,7 @@ struct SimtEngine : Paged {
   static constexpr int DIM = D, KEYS = 32 / H, ROWB = D * sizeof(T), EXTRA = NC * H * D * 4;
   static constexpr int STAGE = 2 * KEYS * ROWB, RING = KEYS * ROWB > 4096 ? 2 : 3;
   static constexpr int LPR = D / 4, KPW = 32 / LPR, KT = KEYS / KPW;
-  static constexpr bool MANY_REGS = NC == 4;  // more than 168 a thread
+  static constexpr int MOST_WARPS = NC == 4 ? 8 : 12;  // 168 registers a thread for 12
   static_assert(KT * H == LPR, "one score per lane");
   const float* qs;  // [NC * H][D], scaled
   float m[NC], l[NC];
@@ -238,7 +239,7 @@ template <int D>
 struct MmaEngine : Paged {
   using Elem = __nv_bfloat16;
   static constexpr int DIM = D, KEYS = 32, ROWB = D * 2, STAGE = 2 * KEYS * ROWB, RING = 2, EXTRA = 0, KS = D / 16, NT = KEYS / 8;
-  static constexpr bool MANY_REGS = false;
+  static constexpr int MOST_WARPS = 12;
   uint32_t q[KS][4];
   float m[2], l[2], o[D / 8][4];
 

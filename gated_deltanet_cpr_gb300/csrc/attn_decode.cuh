@@ -64,13 +64,15 @@ template <typename E>
 struct DecodeSmem {
   static constexpr int STAGE = E::STAGE, RING = E::RING * STAGE, EXTRA = RING, QUEUE = EXTRA + E::EXTRA;
   static constexpr int WARP = (QUEUE + 4 * (int)sizeof(typename E::Run) + 127) / 128 * 128, MOST = 227 * 1024 / WARP;
-  static constexpr int WARPS = MOST < 8 ? MOST : MOST < 12 || E::MANY_REGS ? 8 : 12, HALF = 116 * 1024;
+  static constexpr int FEW = MOST < E::MOST_WARPS ? MOST : E::MOST_WARPS;
+  static constexpr int WARPS = FEW < 8 ? FEW : FEW / 4 * 4, HALF = 116 * 1024;
   static constexpr int BYTES = WARPS * WARP > HALF ? WARPS * WARP : HALF;  // more than half: one CTA per SM
 };
 
 // Which run a warp takes next.  An engine E has a type Request, made from the call and a length (n: its
-// visible units, bad, runs(a)), a type Run (i, y, run, runs, units [u, end), set(a, request, ahead) and
-// from(other, lane)) and a type Ahead, what is read of a request before its turn (len and perhaps more).
+// visible units, bad, runs(a)), a type Seed, a lane's run (i, y, run, runs, set(a, request, ahead)), a type Run (i, y,
+// run, runs, units [u, end), from(a, seed, lane)) and a type Ahead, what is read of a request before its turn (len and
+// perhaps more).
 template <typename E>
 struct Dealer {
   using Args = typename E::Args;
@@ -84,7 +86,7 @@ struct Dealer {
   int next_i, next_y, next_run;  // this lane's slot of it (next_run < 0: none)
   typename E::Ahead next;        // and of its request
   uint32_t left;                 // slots of the present chunk that hold a run and are still to come
-  Run mine;                      // this lane's run of it
+  typename E::Seed mine;         // this lane's run of it
   Run r;                         // the run being fetched
   bool live;                     // there is one
 
@@ -99,36 +101,46 @@ struct Dealer {
     next.load(a, next_i);
   }
 
-  // The next run of this warp.  Requests without keys have their rows written here.
+  // lane 0: the number of a further chunk, on its way
+  __device__ __forceinline__ int ask(int lane) const { return counter && lane == 0 ? atomicAdd(counter, 1) : 0; }
+  __device__ __forceinline__ void answer(const Args& a, int parts, int lane, int n) {
+    if (!counter) base = total;
+    else base = (gridDim.x * DecodeSmem<E>::WARPS + (uint32_t)__shfl_sync(0xffffffffu, n, 0)) * chunk;
+    look_ahead(a, parts, lane);
+  }
+  // The runs of the chunk looked up.  Requests without keys have their rows written here.
+  __device__ __forceinline__ void take(const Args& a, int parts) {
+    bool have = false;
+    if (next_run >= 0) {
+      const typename E::Request rq(a, next.len);
+      mine.i = next_i;
+      mine.y = next_y;
+      mine.run = next_run;
+      mine.set(a, rq, next);
+      have = next_run < mine.runs;
+      if (mine.runs == 0 && next_run == 0) write_empty(a, mine, parts, rq.bad);
+    }
+    left = __ballot_sync(0xffffffffu, have);
+  }
+  // The next run of this warp.
   __device__ void seek(const Args& a, int parts, int lane) {
     live = false;
     while (!left) {
       if (base >= total) return;
-      bool have = false;
-      if (next_run >= 0) {
-        const typename E::Request rq(a, next.len);
-        mine.i = next_i;
-        mine.y = next_y;
-        mine.run = next_run;
-        mine.set(a, rq, next);
-        have = next_run < mine.runs;
-        if (mine.runs == 0 && next_run == 0) write_empty(a, mine, parts, rq.bad);
-      }
-      left = __ballot_sync(0xffffffffu, have);
-      int n = 0;
-      if (!counter) base = total;
-      else if (lane == 0) n = atomicAdd(counter, 1);
-      if (counter) base = (gridDim.x * DecodeSmem<E>::WARPS + (uint32_t)__shfl_sync(0xffffffffu, n, 0)) * chunk;
-      look_ahead(a, parts, lane);
+      take(a, parts);
+      answer(a, parts, lane, ask(lane));
     }
+    begin(a);
+  }
+  __device__ __forceinline__ void begin(const Args& a) {
     const int src = __ffs(left) - 1;
     left &= left - 1;
-    r.from(mine, src);
+    r.from(a, mine, src);
     live = true;
   }
 
   // zeros for a request without keys, NaN for a length that is not valid; one lane
-  __device__ static void write_empty(const Args& a, const Run& c, int parts, bool bad) {
+  __device__ static void write_empty(const Args& a, const typename E::Seed& c, int parts, bool bad) {
     const int group = a.hq / a.hkv, g0 = (c.y % parts) * kHeadsPerRun, heads = min(kHeadsPerRun, group - g0);
     const int64_t row = (int64_t)c.i * a.hq + (c.y / parts) * group + g0;
     const float x = bad ? __builtin_nanf("") : 0.f;

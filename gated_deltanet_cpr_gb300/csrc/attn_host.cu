@@ -202,7 +202,7 @@ gdn_status quant_rows_args(const gdn_cpr_quant_cache* c, int32_t N, int32_t T, c
   if ((double)quant_pieces(N, T, by_block ? q.block_shift : kGranuleShift) * 2 * c->h_kv >= 2147483648.0) return GDN_ERR_UNSUPPORTED;
   if (N > 0 && (!ok_ptr(cu, 4) || !ok_ptr(seq_lens, 4) || !aligned(slot, 4))) return GDN_ERR_INVALID_ARG;
   if (N > 0 && max_blocks > 0 && !ok_ptr(block_table, 4)) return GDN_ERR_INVALID_ARG;
-  if (!ok_ws(ws, ws_bytes, GDN_CPR_ATTN_HEADER_BYTES)) return GDN_ERR_WORKSPACE;
+  if (ws && !ok_ws(ws, ws_bytes, GDN_CPR_ATTN_HEADER_BYTES)) return GDN_ERR_WORKSPACE;
   *a = QuantRows{};
   a->c = q;
   a->N = N;
@@ -217,8 +217,7 @@ gdn_status quant_rows_args(const gdn_cpr_quant_cache* c, int32_t N, int32_t T, c
 }
 
 int quant_splits(const gdn_cpr_attn* a, int32_t max_len) {
-  const int64_t keys = quant_granules(max_len, a->window, a->sinks) << kGranuleShift;
-  return paged_decode_max_splits(keys < INT32_MAX ? (int)keys : INT32_MAX, a->h_kv);
+  return quant_max_splits(quant_granules(max_len, a->window, a->sinks), a->h_kv);
 }
 
 size_t window_bytes(const gdn_cpr_attn* a, int32_t Tq, bool backward) {
@@ -490,7 +489,7 @@ gdn_status gdn_cpr_quant_append(const gdn_cpr_quant_cache* cache, int32_t num_se
   const int64_t row = (int64_t)cache->h_kv * cache->d, step = cache->dtype == GDN_BF16 ? 8 : 4;
   if (k_stride < row || v_stride < row || k_stride % step || v_stride % step) return GDN_ERR_INVALID_ARG;
   if (total_tokens > 0 && (!ok_ptr(k, 16) || !ok_ptr(v, 16))) return GDN_ERR_INVALID_ARG;
-  if (num_seqs == 0) return empty_call(ws, stream);
+  if (num_seqs == 0) return ws ? empty_call(ws, stream) : GDN_OK;
   a.k_in = k;
   a.v_in = v;
   a.k_stride = k_stride;
@@ -511,7 +510,7 @@ gdn_status gdn_cpr_quant_read(const gdn_cpr_quant_cache* cache, int32_t num_seqs
   if (rc != GDN_OK) return rc;
   if (!ok_dtype(out_dtype)) return GDN_ERR_UNSUPPORTED;
   if (total_tokens > 0 && (!ok_ptr(k, 16) || !ok_ptr(v, 16))) return GDN_ERR_INVALID_ARG;
-  if (num_seqs == 0) return empty_call(ws, stream);
+  if (num_seqs == 0) return ws ? empty_call(ws, stream) : GDN_OK;
   a.k_out = k;
   a.v_out = v;
   Stages stg(stream, kQuantReadStages);

@@ -24,7 +24,8 @@ struct QuantRows {
   QuantCache c;
   int N, T, max_blocks;
   const int32_t *cu, *seq_lens, *block_table, *slot;
-  WsHeader* hdr;
+  WsHeader* hdr;            // or NULL: what is wrong is not reported
+  bool by_token;            // pieces are numbered by the first of their rows, not as below
   const void *k_in, *v_in;  // append
   int64_t k_stride, v_stride;
   void *k_out, *v_out;  // read
@@ -32,6 +33,8 @@ struct QuantRows {
 // Pieces of `1 << shift` positions that hold rows: numbered with a request's first at cu[n] / piece + 2 n, which
 // leaves every request enough numbers without a sum over the others.
 inline int64_t quant_pieces(int N, int T, int shift) { return (int64_t)(T >> shift) + 2 * (int64_t)N; }
+// With few rows a request it is fewer to number every row, and to leave out those that do not begin a piece.
+inline bool quant_by_token(int N, int T, int shift) { return T < quant_pieces(N, T, shift); }
 
 // Decode attention: a request's visible keys are counted in granules that hold any.
 struct QuantDecode : PagedDecode {
@@ -45,6 +48,28 @@ inline int64_t quant_granules(int64_t len, int window, int sinks) {
   const int64_t some = ((int64_t)sinks + kGranule - 1) / kGranule + ((int64_t)window + 2 * kGranule - 2) / kGranule;
   return some < all ? some : all;
 }
+// Granules of a run (Split::keys) and runs of a request, from the request's granules and the number of key heads alone, so
+// that a request's result does not depend on the batch: about kQuantRuns runs over a request's heads, of 4 to 32
+// granules, evened out.
+constexpr int kQuantRuns = 32, kQuantMinShift = 2, kQuantMaxShift = 5;
+__host__ __device__ inline int quant_shift(int n, int hkv) {
+  const int64_t x = (int64_t)n * hkv;
+  int s = kQuantMinShift;
+  while (s < kQuantMaxShift && x >= (int64_t)kQuantRuns << (s + 1)) ++s;
+  return s;
+}
+__host__ __device__ inline int quant_target(int n, int hkv) {
+  const int s = quant_shift(n, hkv), r = (n + (1 << s >> 1)) >> s;
+  return r < 1 ? 1 : r;
+}
+__host__ __device__ inline Split quant_split(int n, int hkv) {
+  const int r = quant_target(n, hkv);
+  Split s;
+  s.keys = (n + r - 1) / r;
+  s.runs = n == 0 ? 0 : (n + s.keys - 1) / s.keys;
+  return s;
+}
+int quant_max_splits(int64_t granules, int hkv);
 int launch_quant_decode(const QuantDecode& a, bool bf16, cudaStream_t st);
 
 int launch_quant_append(const QuantRows& a, int d, bool bf16, cudaStream_t st);

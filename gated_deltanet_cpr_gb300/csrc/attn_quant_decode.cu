@@ -41,11 +41,7 @@ struct QuantRequest {
     }
   }
   __device__ __forceinline__ int granule(int u) const { return u < head ? u : u + skip; }
-  __device__ __forceinline__ Split split(const QuantDecode& a) const {
-    const uint32_t keys = (uint32_t)n << kGranuleShift;
-    return split_of(keys > 0x7fffffffu ? 0x7fffffff : (int)keys, a.hkv);
-  }
-  __device__ __forceinline__ int runs(const QuantDecode& a) const { return split(a).runs; }
+  __device__ __forceinline__ int runs(const QuantDecode& a) const { return quant_split(n, a.hkv).runs; }
 };
 
 struct QuantAhead {
@@ -56,36 +52,38 @@ struct QuantAhead {
   }
 };
 
-// Granules [u, end) of request i, those from `tail` on in its tail; bad: a page or the slot is outside the cache.
-struct QuantRun {
-  int i, y, run, runs;
-  uint32_t u, end, tail;
-  int head, skip, len, slot, bad;
-  __device__ __forceinline__ int granule(uint32_t x) const { return (int)x < head ? (int)x : (int)x + skip; }
+// A lane's run, from which all lanes form a QuantRun when its turn comes: few values, as registers are short.
+struct QuantSeed {
+  int i, y, run, runs, len, slot;
   __device__ __forceinline__ void set(const QuantDecode& a, const QuantRequest& rq, const QuantAhead& ahead) {
-    const Split s = rq.split(a);
-    runs = s.runs;
-    u = (uint32_t)run * (uint32_t)(s.keys >> kGranuleShift);
-    end = min((uint32_t)rq.n, u + (uint32_t)(s.keys >> kGranuleShift));
-    head = rq.head;
-    skip = rq.skip;
+    runs = rq.runs(a);
     len = rq.len;
     slot = ahead.slot;
-    const int g = (rq.len >> a.c.block_shift) << (a.c.block_shift - kGranuleShift);  // first granule of the tail
-    tail = (uint32_t)(g <= head ? g : max(head, g - skip));
   }
-  __device__ __forceinline__ void from(const QuantRun& o, int lane) {
+};
+// Granules [u, end) of request i, those from `tail` on in its tail; only granules edge - 1 and edge of the others can hold
+// keys that are not visible; bad: a page or the slot is outside the cache.
+struct QuantRun {
+  int i, y, run, runs;
+  uint32_t u, end, tail, edge;
+  int head, skip, len, slot, bad;
+  __device__ __forceinline__ int granule(uint32_t x) const { return (int)x < head ? (int)x : (int)x + skip; }
+  __device__ __forceinline__ void from(const QuantDecode& a, const QuantSeed& o, int lane) {
     i = __shfl_sync(0xffffffffu, o.i, lane);
     y = __shfl_sync(0xffffffffu, o.y, lane);
     run = __shfl_sync(0xffffffffu, o.run, lane);
-    runs = __shfl_sync(0xffffffffu, o.runs, lane);
-    u = __shfl_sync(0xffffffffu, o.u, lane);
-    end = __shfl_sync(0xffffffffu, o.end, lane);
-    tail = __shfl_sync(0xffffffffu, o.tail, lane);
-    head = __shfl_sync(0xffffffffu, o.head, lane);
-    skip = __shfl_sync(0xffffffffu, o.skip, lane);
     len = __shfl_sync(0xffffffffu, o.len, lane);
     slot = __shfl_sync(0xffffffffu, o.slot, lane);
+    const QuantRequest rq(a, len);
+    const Split s = quant_split(rq.n, a.hkv);
+    runs = s.runs;
+    u = (uint32_t)run * (uint32_t)s.keys;
+    end = min((uint32_t)rq.n, u + (uint32_t)s.keys);
+    head = rq.head;
+    skip = rq.skip;
+    edge = a.window > 0 && len > a.window ? (uint32_t)head : 1u << 30;
+    const int g = (len >> a.c.block_shift) << (a.c.block_shift - kGranuleShift);  // first granule of the tail
+    tail = (uint32_t)(g <= head ? g : max(head, g - skip));
   }
 };
 
@@ -94,6 +92,7 @@ struct Quant {
   using Args = QuantDecode;
   using Request = QuantRequest;
   using Ahead = QuantAhead;
+  using Seed = QuantSeed;
   using Run = QuantRun;
   // a page of the request's visible whole blocks, or its tail's slot, is outside the cache
   __device__ __forceinline__ static int check(const QuantDecode& a, const QuantRequest& rq, int i, int tid, int threads) {
@@ -120,16 +119,42 @@ struct Quant {
 };
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// the same with nothing to add to
+__device__ __forceinline__ void mma_f16_from0(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
 // an 8 x 8 matrix of pairs, transposed over the warp
 __device__ __forceinline__ uint32_t transposed(uint32_t x) {
   uint32_t y;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
+}
+// four 8 x 8 matrices at addr + OFF
+template <bool TRANS, int OFF>
+__device__ __forceinline__ void load_matrices(uint32_t addr, uint32_t (&r)[4]) {
+  if constexpr (TRANS)
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4 + %5];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr), "n"(OFF)
+                 : "memory");
+  else
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4 + %5];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr), "n"(OFF)
+                 : "memory");
+}
+// 16 bytes at gmem + G to smem + S
+template <int S, int G>
+__device__ __forceinline__ void copy16(uint32_t smem, const void* gmem) {
+  asm volatile("cp.async.cg.shared.global [%0 + %2], [%1 + %3], 16;" ::"r"(smem), "l"(gmem), "n"(S), "n"(G) : "memory");
 }
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   const __half2 x = __floats2half2_rn(lo, hi);
@@ -139,6 +164,14 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
 __device__ __forceinline__ uint32_t pack_f16_rest(float lo, float hi, uint32_t packed) {
   const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&packed));
   return pack_f16(__fsub_rn(lo, p.x), __fsub_rn(hi, p.y));
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 x = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&x);
+}
+__device__ __forceinline__ uint32_t f16_to_bf16(uint32_t x) {
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&x));
+  return pack_bf16(f.x, f.y);
 }
 // 2^e
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
@@ -169,32 +202,40 @@ __device__ __forceinline__ void widen16(uint32_t four, uint32_t& first, uint32_t
 }
 
 // ------------------------------------------------------------------------- engine ----
-// A tile is up to T granules of the pages, or one of the tail.  NH column tiles of 8 heads.  Lane (g, t) = (lane / 4,
-// lane % 4) holds of scores^T keys g, g + 8 of a granule for heads 2 t, 2 t + 1, of out^T columns 16 j + 2 g, + 1 for them.
-// The MMAs' inner order is free as long as both operands agree: k-steps of 16 take columns 16 s + 4 t .. + 3 of lane t, so
-// that a lane's four codes of a row are one register of a matrix load.
+// A tile is up to T granules of the pages, or up to TAIL_ROWS rows of a granule of the tail.  NH column tiles of 8 heads.
+// Lane (g, t) = (lane / 4, lane % 4) holds of scores^T keys g, g + 8 of a granule for heads 2 t, 2 t + 1, of out^T columns
+// 16 j + 2 g, + 1 for them.  The MMAs' inner order is free as long as both operands agree: k-steps of 16 take columns 16 s +
+// 4 t .. + 3 of lane t, so that a lane's four codes of a row are one register of a matrix load.  Granules are gone
+// through in pairs, whose chains of loads, conversions and products overlap.
 template <int D, typename T_, int NH, bool E4M3>
 struct QuantEngine : Quant {
   using Elem = T_;
   static constexpr int DIM = D, ROWB = D, TAILB = D * (int)sizeof(Elem);  // bytes of a row
   static constexpr bool SPLIT = sizeof(Elem) == 4;                        // two f16 for q, P and the tail's rows
-  static constexpr int T = D == 128 && !SPLIT ? 2 : 4;
-  static constexpr int ROWS = T * kGranule, SIDE = ROWS * ROWB;  // keys of a tile and the bytes of them, or of their values
-  static constexpr int META = 2 * SIDE, STAGE = META + 128, RING = 2, EXTRA = 0;
-  static constexpr bool MANY_REGS = SPLIT && NH == 2;
-  static_assert(kGranule * TAILB <= SIDE, "a granule of the tail fits a tile");
-  // of a tile: granules, whether it is of the tail, first keys, scales
+  static constexpr int T = 256 / D;
+  static constexpr int SIDE = T * kGranule * ROWB;  // bytes of a tile's keys, or of its values
+  static constexpr int TAIL_ROWS = SIDE / TAILB < kGranule ? SIDE / TAILB : kGranule;
+  static constexpr int STAGE = 2 * SIDE + 128, EXTRA = 0;
+  // of a tile, behind its rows
   struct Meta {
-    int count, tail;
-    int key[T];
-    float ks[T], vs[T];
+    float ks[T], vs[T];  // scales of its granules
+    alignas(16) int key; // first key of its first granule, or of its rows in the tail
+    int what;            // granules in the pages, 0: rows of the tail; + kLast, + kEdge
+    int skip;            // granules whose number is skip_from or more lie `skip` keys further on
+    int skip_from;
   };
-  static_assert(sizeof(Meta) <= 128, "");
+  static_assert(sizeof(Meta) <= 128 && (2 * SIDE) % 128 == 0 && STAGE % 128 == 0, "key is stored with the three behind it, 16 bytes");
+  static constexpr int kLast = 64, kEdge = 128;  // the run's last tile; some keys may not be visible
+  // 12 warps with a tile on its way take 256 requests of about 2112 tokens in 200 us, 8 with two in 206, 16 with a granule a
+  // tile (128 registers) in 216; 16 heads and fp32 need more registers than 168 a thread
+  static constexpr bool MANY_REGS = SPLIT || NH == 2;
+  static constexpr int MOST_WARPS = MANY_REGS ? 8 : 12, RING = MANY_REGS ? 3 : 2;
+  static_assert(RING <= 3, "the queue holds four runs: the computed one, those of RING - 1 tiles ahead and the next");
   static constexpr int KS = D / 16, P = 1 + SPLIT;  // steps, parts of a split value
 
   uint32_t q[P][KS][NH][2];
   float qs[NH][2];  // scale of the scores
-  float m[NH][2], l[NH][2], o[D / 16][NH][4];
+  float m[NH][2], base[NH][2], l[NH][2], o[KS][NH][4];  // base: what is taken off a score, m - 14 or 0
 
   // place of 16-byte piece c of row r: 8 rows of a matrix load lie in 8 bank groups
   __device__ __forceinline__ static uint32_t place(int r, int c) {
@@ -242,46 +283,52 @@ struct QuantEngine : Quant {
       for (int b = 0; b < 2; ++b) {
         qs[h][b] = __shfl_sync(0xffffffffu, f, 4 * (2 * t + b));
         m[h][b] = -INFINITY;
-        l[h][b] = 0.f;
+        base[h][b] = l[h][b] = 0.f;
       }
     }
 #pragma unroll
-    for (int j = 0; j < D / 16; ++j)
+    for (int j = 0; j < KS; ++j)
 #pragma unroll
       for (int h = 0; h < NH; ++h)
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[j][h][e] = 0.f;
   }
 
-  // Scores of G granules (of which `count` are there) to probabilities p 2^14, with the running maximum and sum.
-  // x: products; on return the probabilities.
+  // Products x of G granules with their keys, the first `rows` from key[i] on, to probabilities p 2^14, with the running
+  // maximum and sum.
   template <int G>
-  __device__ __forceinline__ void softmax(const QuantDecode& a, const Meta& meta, int count, int len, float (&x)[G][NH][4], int lane) {
-    float mx[NH][2];
-#pragma unroll
-    for (int h = 0; h < NH; ++h) mx[h][0] = mx[h][1] = -INFINITY;
-    const int lo = a.window > 0 ? len - a.window : 0;
+  __device__ __forceinline__ void softmax(const QuantDecode& a, const float (&ks)[G], bool full, const int (&key)[G],
+                                          int rows, int len, float (&x)[G][NH][4], int lane) {
 #pragma unroll
     for (int i = 0; i < G; ++i) {
-      const int key = meta.key[i];
-      const float ks = meta.ks[i];
-      // all keys of the granule visible, as in all but a few
-      const bool full = i < count && key + (kGranule - 1) < len && (key >= lo || key + kGranule <= a.sinks);
 #pragma unroll
-      for (int h = 0; h < NH; ++h)
+      for (int h = 0; h < NH; ++h) {
+        const float f[2] = {__fmul_rn(ks[i], qs[h][0]), __fmul_rn(ks[i], qs[h][1])};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          x[i][h][e] = __fmul_rn(x[i][h][e], __fmul_rn(ks, qs[h][e & 1]));
-          if (!full) {
-            const int k = key + (lane >> 2) + 8 * (e >> 1);
-            if (i >= count || k >= len || (k < lo && k >= a.sinks)) x[i][h][e] = -INFINITY;
-          }
-          mx[h][e & 1] = fmaxf(mx[h][e & 1], x[i][h][e]);
+        for (int e = 0; e < 4; ++e) x[i][h][e] = __fmul_rn(x[i][h][e], f[e & 1]);
+      }
+      if (!full) {  // some may not be visible
+        const int lo = a.window > 0 ? len - a.window : 0;
+#pragma unroll
+        for (int e = 0; e < 4; e += 2) {
+          const int r = (lane >> 2) + 4 * e, k = key[i] + r;
+          if (r < rows && k < len && (k >= lo || k < a.sinks)) continue;
+#pragma unroll
+          for (int h = 0; h < NH; ++h) x[i][h][e] = x[i][h][e + 1] = -INFINITY;
         }
+      }
     }
+    float mx[NH][2];
     bool more = false;
 #pragma unroll
-    for (int h = 0; h < NH; ++h) more |= mx[h][0] > m[h][0] || mx[h][1] > m[h][1];
+    for (int h = 0; h < NH; ++h)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        mx[h][e] = fmaxf(x[0][h][e], x[0][h][e + 2]);
+#pragma unroll
+        for (int i = 1; i < G; ++i) mx[h][e] = fmaxf(mx[h][e], fmaxf(x[i][h][e], x[i][h][e + 2]));
+        more |= mx[h][e] > m[h][e];
+      }
     if (__any_sync(0xffffffffu, more)) {
 #pragma unroll
       for (int h = 0; h < NH; ++h) {
@@ -294,10 +341,11 @@ struct QuantEngine : Quant {
           y = fmaxf(y, m[h][e]);
           f[e] = m[h][e] == -INFINITY ? 0.f : exp2_approx(__fsub_rn(m[h][e], y));
           m[h][e] = y;
+          base[h][e] = y == -INFINITY ? 0.f : __fsub_rn(y, (float)kShiftP);
           l[h][e] = __fmul_rn(l[h][e], f[e]);
         }
 #pragma unroll
-        for (int j = 0; j < D / 16; ++j)
+        for (int j = 0; j < KS; ++j)
 #pragma unroll
           for (int e = 0; e < 4; ++e) o[j][h][e] = __fmul_rn(o[j][h][e], f[e & 1]);
       }
@@ -306,14 +354,12 @@ struct QuantEngine : Quant {
     for (int h = 0; h < NH; ++h)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const float base = m[h][e] == -INFINITY ? 0.f : __fsub_rn(m[h][e], (float)kShiftP);
 #pragma unroll
-        for (int i = 0; i < G; ++i)
-#pragma unroll
-          for (int b = e; b < 4; b += 2) {
-            x[i][h][b] = exp2_approx(__fsub_rn(x[i][h][b], base));
-            l[h][e] = __fadd_rn(l[h][e], x[i][h][b]);
-          }
+        for (int i = 0; i < G; ++i) {
+          x[i][h][e] = exp2_approx(__fsub_rn(x[i][h][e], base[h][e]));
+          x[i][h][e + 2] = exp2_approx(__fsub_rn(x[i][h][e + 2], base[h][e]));
+          l[h][e] = __fadd_rn(l[h][e], __fadd_rn(x[i][h][e], x[i][h][e + 2]));
+        }
       }
   }
   // P^T of a granule as the MMA's right operand: keys 2 t, 2 t + 1 (+ 8) of head g
@@ -322,8 +368,8 @@ struct QuantEngine : Quant {
     b[0][0] = transposed(lo);
     b[0][1] = transposed(hi);
     if constexpr (SPLIT) {
-      b[1][0] = transposed(pack_f16_rest(p[0], p[1], lo));
-      b[1][1] = transposed(pack_f16_rest(p[2], p[3], hi));
+      b[P - 1][0] = transposed(pack_f16_rest(p[0], p[1], lo));
+      b[P - 1][1] = transposed(pack_f16_rest(p[2], p[3], hi));
     }
   }
   __device__ __forceinline__ void add(int j, int h, const float (&c)[4], float scale) {
@@ -331,160 +377,212 @@ struct QuantEngine : Quant {
     for (int e = 0; e < 4; ++e) o[j][h][e] = __fmaf_rn(c[e], scale, o[j][h][e]);
   }
 
-  __device__ __forceinline__ void tile(const QuantDecode& a, const unsigned char* stage, int len, int lane) {
-    const Meta& meta = *reinterpret_cast<const Meta*>(stage + META);
-    const int count = meta.count;
-    const uint32_t st = tc::smem_u32(stage);
-    // matrix-load addresses: keys 0 .. 7 and 8 .. 15 of a granule, piece 0 and 1 of a pair
-    const int kr = (lane & 7) + (lane & 8), kc = lane >> 4;
-    float x[T][NH][4];
+  // Granules i .. i + G - 1 of the tile, in the pages.
+  template <int G>
+  __device__ __forceinline__ void granules(const QuantDecode& a, const unsigned char* stage, int i, bool full, int len, int lane) {
+    const Meta& meta = *reinterpret_cast<const Meta*>(stage + 2 * SIDE);
+    // this lane's row for matrix loads (keys 0 .. 7 and 8 .. 15) and, s steps on, its piece (0 and 1 of a pair): the
+    // swizzle turns bits, and a stage begins at a multiple of 128 bytes
+    const uint32_t at = tc::smem_u32(stage) + i * (kGranule * ROWB) + place((lane & 7) + (lane & 8), lane >> 4);
+    uint32_t r[G][KS / 2][4];
+    float x[G][NH][4], y[G][NH][4];  // of even and odd steps
+    load_all<G, false, 0>(at, r);
 #pragma unroll
-    for (int i = 0; i < T; ++i) {
+    for (int s = 0; s < KS; ++s)
+#pragma unroll
+      for (int b = 0; b < G; ++b) {
+        uint32_t k[4];
+        widen16<E4M3, false>(r[b][s / 2][2 * (s & 1)], k[0], k[2]);
+        widen16<E4M3, false>(r[b][s / 2][2 * (s & 1) + 1], k[1], k[3]);
+#pragma unroll
+        for (int h = 0; h < NH; ++h) {
+          float(&c)[4] = s & 1 ? y[b][h] : x[b][h];
+          if (s < 2) mma_f16_from0(c, k, q[0][s][h][0], q[0][s][h][1]);
+          else mma_f16(c, k, q[0][s][h][0], q[0][s][h][1]);
+          if constexpr (SPLIT) mma_f16(c, k, q[P - 1][s][h][0], q[P - 1][s][h][1]);
+        }
+      }
+    load_all<G, true, SIDE>(at, r);
+    float ks[G], vs[G];
+    int key[G];
+#pragma unroll
+    for (int b = 0; b < G; ++b) {
 #pragma unroll
       for (int h = 0; h < NH; ++h)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[i][h][e] = 0.f;
-      if (i >= count) continue;
+        for (int e = 0; e < 4; ++e) x[b][h][e] = __fadd_rn(x[b][h][e], y[b][h][e]);
+      ks[b] = meta.ks[i + b];
+      vs[b] = meta.vs[i + b];
+      key[b] = meta.key + ((i + b) << kGranuleShift) + (i + b >= meta.skip_from ? meta.skip : 0);
+    }
+    softmax<G>(a, ks, full, key, kGranule, len, x, lane);
+    uint32_t p[G][NH][P][2];
 #pragma unroll
-      for (int s = 0; s < KS; s += 2) {
-        uint32_t r[4];
-        tc::ldsm_x4(st + place(kGranule * i + kr, s + kc), r);
+    for (int b = 0; b < G; ++b)
 #pragma unroll
-        for (int w = 0; w < 2; ++w) {
-          uint32_t k[4];
-          widen16<E4M3, false>(r[2 * w], k[0], k[2]);
-          widen16<E4M3, false>(r[2 * w + 1], k[1], k[3]);
+      for (int h = 0; h < NH; ++h) operand(x[b][h], p[b][h]);
 #pragma unroll
-          for (int h = 0; h < NH; ++h)
+    for (int j = 0; j < KS; ++j)
 #pragma unroll
-            for (int p = 0; p < P; ++p) mma_f16(x[i][h], k, q[p][s + w][h][0], q[p][s + w][h][1]);
+      for (int b = 0; b < G; ++b) {
+        uint32_t v[4];
+        widen16<E4M3, true>(r[b][j / 2][2 * (j & 1)], v[0], v[1]);
+        widen16<E4M3, true>(r[b][j / 2][2 * (j & 1) + 1], v[2], v[3]);
+#pragma unroll
+        for (int h = 0; h < NH; ++h) {
+          float c[4];
+          mma_f16_from0(c, v, p[b][h][0][0], p[b][h][0][1]);
+          if constexpr (SPLIT) mma_f16(c, v, p[b][h][P - 1][0], p[b][h][P - 1][1]);
+          add(j, h, c, vs[b]);
         }
       }
+  }
+  template <int G, bool TRANS, int OFF>
+  __device__ __forceinline__ static void load_all(uint32_t at, uint32_t (&r)[G][KS / 2][4]) {
+#pragma unroll
+    for (int s = 0; s < KS / 2; ++s) {
+      load_matrices<TRANS, OFF>(at ^ (uint32_t)(s << 5), r[0][s]);
+      if constexpr (G == 2) load_matrices<TRANS, OFF + kGranule * ROWB>(at ^ (uint32_t)(s << 5), r[1][s]);
     }
-    softmax<T>(a, meta, count, len, x, lane);
+  }
+
+  // Keys key .. key + TAIL_ROWS - 1 of the tail.  bf16 rows are operands as they are, with q in bf16 (its f16 form has
+  // no more bits) and P as the sum of two bf16.
+  __device__ __forceinline__ void tail_bf16(const QuantDecode& a, const unsigned char* stage, int key, int len, int lane) {
+    const int g = lane >> 2, t = lane & 3;
+    float xs[1][NH][4];
+    float(&x)[NH][4] = xs[0];
 #pragma unroll
-    for (int i = 0; i < T; ++i) {
-      if (i >= count) continue;
-      uint32_t b[NH][P][2];
+    for (int s = 0; s < KS; ++s) {
+      uint32_t k[4] = {0, 0, 0, 0};
 #pragma unroll
-      for (int h = 0; h < NH; ++h) operand(x[i][h], b[h]);
-      const float vs = meta.vs[i];
+      for (int r = 0; r < TAIL_ROWS / 8; ++r) {
+        const int at = (16 * s + 4 * t) * 2;
+        const uint2 u = *reinterpret_cast<const uint2*>(stage + place_tail(g + 8 * r, at >> 4) + (at & 15));
+        k[r] = u.x;
+        k[r + 2] = u.y;
+      }
 #pragma unroll
-      for (int j = 0; j < KS; j += 2) {
-        uint32_t r[4];
-        tc::ldsm_x4_trans(st + SIDE + place(kGranule * i + kr, j + kc), r);
+      for (int h = 0; h < NH; ++h) {
+        const uint32_t b0 = f16_to_bf16(q[0][s][h][0]), b1 = f16_to_bf16(q[0][s][h][1]);
+        if (s == 0) x[h][0] = x[h][1] = x[h][2] = x[h][3] = 0.f;
+        tc::mma16816(x[h], k, b0, b1);
+      }
+    }
+    // a key that is not finite gives NaN, not a weight of 0
 #pragma unroll
-        for (int w = 0; w < 2; ++w) {
-          uint32_t v[4];
-          widen16<E4M3, true>(r[2 * w], v[0], v[1]);
-          widen16<E4M3, true>(r[2 * w + 1], v[2], v[3]);
+    for (int h = 0; h < NH; ++h)
 #pragma unroll
-          for (int h = 0; h < NH; ++h) {
-            float c[4] = {0.f, 0.f, 0.f, 0.f};
+      for (int e = 0; e < 4; ++e) x[h][e] = __fmaf_rn(x[h][e], 0.f, x[h][e]);
+    softmax<1>(a, {1.f}, false, {key}, TAIL_ROWS, len, xs, lane);
+    uint32_t b[NH][2][2];
 #pragma unroll
-            for (int p = 0; p < P; ++p) mma_f16(c, v, b[h][p][0], b[h][p][1]);
-            add(j + w, h, c, vs);
-          }
-        }
+    for (int h = 0; h < NH; ++h)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const uint32_t hi = pack_bf16(x[h][2 * r], x[h][2 * r + 1]);
+        b[h][0][r] = transposed(hi);
+        b[h][1][r] = transposed(pack_bf16(__fsub_rn(x[h][2 * r], __uint_as_float(hi << 16)),
+                                          __fsub_rn(x[h][2 * r + 1], __uint_as_float(hi & 0xffff0000u))));
+      }
+#pragma unroll
+    for (int j = 0; j < KS; ++j) {
+      uint32_t v[4] = {0, 0, 0, 0};
+      const int at = (16 * j + 2 * g) * 2;
+#pragma unroll
+      for (int r = 0; r < TAIL_ROWS / 8; ++r) {  // keys 2 t, 2 t + 1 and those + 8
+        const unsigned char* src = stage + SIDE + (at & 15);
+        const uint32_t k0 = *reinterpret_cast<const uint32_t*>(src + place_tail(8 * r + 2 * t, at >> 4));
+        const uint32_t k1 = *reinterpret_cast<const uint32_t*>(src + place_tail(8 * r + 2 * t + 1, at >> 4));
+        v[2 * r] = __byte_perm(k0, k1, 0x5410);
+        v[2 * r + 1] = __byte_perm(k0, k1, 0x7632);
+      }
+#pragma unroll
+      for (int h = 0; h < NH; ++h) {
+        tc::mma16816(o[j][h], v, b[h][0][0], b[h][0][1]);
+        tc::mma16816(o[j][h], v, b[h][1][0], b[h][1][1]);
       }
     }
   }
 
-  // Largest magnitude of a granule of the tail: NaN where one of them is not finite.
+  // Largest magnitude of a tail tile's keys or values: NaN where one of them is not finite.
   __device__ __forceinline__ static float tail_max(const unsigned char* side, int lane) {
     uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < kGranule * TAILB / 512; ++i) {
+    for (int i = 0; i < TAIL_ROWS * TAILB / 512; ++i) {
       const uint4 u = *reinterpret_cast<const uint4*>(side + 512 * i + 16 * lane);
-      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        m = max(m, SPLIT ? w[e] & 0x7fffffffu : max((w[e] << 16) & 0x7fffffffu, w[e] & 0x7fff0000u));
+      m = max(max(max(m, u.x & 0x7fffffffu), max(u.y & 0x7fffffffu, u.z & 0x7fffffffu)), u.w & 0x7fffffffu);
     }
     m = __reduce_max_sync(0xffffffffu, m);
     return m >= 0x7f800000u ? __builtin_nanf("") : __uint_as_float(m);
   }
+  // 0 where the tile is not finite: its scale says so
+  __device__ __forceinline__ static float scaled(float x, float down) { return down == 0.f ? 0.f : __fmul_rn(x, down); }
 
-  // The same over one granule of the tail, whose keys and values are scaled by powers of two to f16.
-  __device__ __forceinline__ void tail(const QuantDecode& a, unsigned char* stage, int len, int lane) {
-    Meta& meta = *reinterpret_cast<Meta*>(stage + META);
+  // The same of fp32 rows, which are scaled by powers of two to sums of two f16.
+  __device__ __forceinline__ void tail_f32(const QuantDecode& a, const unsigned char* stage, int key, int len, int lane) {
     const int g = lane >> 2, t = lane & 3;
     const float km = tail_max(stage, lane), vm = tail_max(stage + SIDE, lane);
     const int ke = f16_exponent(km), ve = f16_exponent(vm);
     const float kd = km == km ? pow2(-ke) : 0.f, vd = vm == vm ? pow2(-ve) : 0.f;
-    if (lane == 0) {
-      meta.ks[0] = km == km ? pow2(ke) : km;
-      meta.vs[0] = vm == vm ? pow2(ve) : vm;
-    }
-    __syncwarp();
-    float x[1][NH][4];
-#pragma unroll
-    for (int h = 0; h < NH; ++h)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) x[0][h][e] = 0.f;
+    const float vs = vm == vm ? pow2(ve) : vm;
+    float xs[1][NH][4];
+    float(&x)[NH][4] = xs[0];
 #pragma unroll
     for (int s = 0; s < KS; ++s) {
-      uint32_t k[P][4];
+      uint32_t k[2][4];
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        constexpr int BYTES = 4 * (int)sizeof(Elem);
-        const int at = (16 * s + 4 * t) * (int)sizeof(Elem);
-        const float4 v =
-            load4(reinterpret_cast<const Elem*>(stage + place_tail(g + 8 * r, at >> 4) + (BYTES < 16 ? at & 15 : 0)));
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (g + 8 * r < TAIL_ROWS) v = *reinterpret_cast<const float4*>(stage + place_tail(g + 8 * r, 4 * s + t));
         const float y[4] = {scaled(v.x, kd), scaled(v.y, kd), scaled(v.z, kd), scaled(v.w, kd)};
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
           k[0][r + 2 * b] = pack_f16(y[2 * b], y[2 * b + 1]);
-          if constexpr (SPLIT) k[P - 1][r + 2 * b] = pack_f16_rest(y[2 * b], y[2 * b + 1], k[0][r + 2 * b]);
+          k[1][r + 2 * b] = pack_f16_rest(y[2 * b], y[2 * b + 1], k[0][r + 2 * b]);
         }
       }
 #pragma unroll
       for (int h = 0; h < NH; ++h) {
-        mma_f16(x[0][h], k[0], q[0][s][h][0], q[0][s][h][1]);
-        if constexpr (SPLIT) {
-          mma_f16(x[0][h], k[0], q[P - 1][s][h][0], q[P - 1][s][h][1]);
-          mma_f16(x[0][h], k[P - 1], q[0][s][h][0], q[0][s][h][1]);
-        }
+        if (s == 0) mma_f16_from0(x[h], k[0], q[0][s][h][0], q[0][s][h][1]);
+        else mma_f16(x[h], k[0], q[0][s][h][0], q[0][s][h][1]);
+        mma_f16(x[h], k[0], q[P - 1][s][h][0], q[P - 1][s][h][1]);
+        mma_f16(x[h], k[1], q[0][s][h][0], q[0][s][h][1]);
       }
     }
-    softmax<1>(a, meta, 1, len, x, lane);
-    const float vs = meta.vs[0];
+    softmax<1>(a, {km == km ? pow2(ke) : km}, false, {key}, TAIL_ROWS, len, xs, lane);
     uint32_t b[NH][P][2];
 #pragma unroll
-    for (int h = 0; h < NH; ++h) operand(x[0][h], b[h]);
+    for (int h = 0; h < NH; ++h) operand(x[h], b[h]);
 #pragma unroll
     for (int j = 0; j < KS; ++j) {
-      uint32_t v[P][4];
-      const int at = (16 * j + 2 * g) * (int)sizeof(Elem);
+      uint32_t v[2][4];
+      const int at = (16 * j + 2 * g) * 4;
 #pragma unroll
       for (int r = 0; r < 2; ++r) {  // keys 2 t, 2 t + 1 and those + 8
-        float y[2][2];
+        float2 y[2];
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
-          const Elem* src = reinterpret_cast<const Elem*>(stage + SIDE + place_tail(8 * r + 2 * t + w, at >> 4) + (at & 15));
-          y[w][0] = scaled(to_f32(src[0]), vd);
-          y[w][1] = scaled(to_f32(src[1]), vd);
+          const int row = 8 * r + 2 * t + w;
+          y[w] = make_float2(0.f, 0.f);
+          if (row < TAIL_ROWS) y[w] = *reinterpret_cast<const float2*>(stage + SIDE + place_tail(row, at >> 4) + (at & 15));
+          y[w] = make_float2(scaled(y[w].x, vd), scaled(y[w].y, vd));
         }
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          v[0][2 * r + c] = pack_f16(y[0][c], y[1][c]);
-          if constexpr (SPLIT) v[P - 1][2 * r + c] = pack_f16_rest(y[0][c], y[1][c], v[0][2 * r + c]);
-        }
+        v[0][2 * r] = pack_f16(y[0].x, y[1].x);
+        v[0][2 * r + 1] = pack_f16(y[0].y, y[1].y);
+        v[1][2 * r] = pack_f16_rest(y[0].x, y[1].x, v[0][2 * r]);
+        v[1][2 * r + 1] = pack_f16_rest(y[0].y, y[1].y, v[0][2 * r + 1]);
       }
 #pragma unroll
       for (int h = 0; h < NH; ++h) {
-        float c[4] = {0.f, 0.f, 0.f, 0.f};
-        mma_f16(c, v[0], b[h][0][0], b[h][0][1]);
-        if constexpr (SPLIT) {
-          mma_f16(c, v[0], b[h][P - 1][0], b[h][P - 1][1]);
-          mma_f16(c, v[P - 1], b[h][0][0], b[h][0][1]);
-        }
+        float c[4];
+        mma_f16_from0(c, v[0], b[h][0][0], b[h][0][1]);
+        mma_f16(c, v[0], b[h][P - 1][0], b[h][P - 1][1]);
+        mma_f16(c, v[1], b[h][0][0], b[h][0][1]);
         add(j, h, c, vs);
       }
     }
   }
-  // 0 where the granule is not finite: its scale says so
-  __device__ __forceinline__ static float scaled(float x, float down) { return down == 0.f ? 0.f : __fmul_rn(x, down); }
 
   __device__ __forceinline__ void finish(const Sink& k, bool bad, int lane) {
     const int g = lane >> 2, t = lane & 3;
@@ -499,17 +597,18 @@ struct QuantEngine : Quant {
         const int head = 8 * h + 2 * t + e;
         if (head >= k.heads) continue;
         if (g == 0) k.stats(head, __fsub_rn(m[h][e], (float)kShiftP), s);
+        if (k.acc) {
+          float* to = k.acc + head * k.acc_step + 2 * g;
 #pragma unroll
-        for (int j = 0; j < D / 16; ++j) {
-          const int c = 16 * j + 2 * g;
-          const float y0 = o[j][h][e], y1 = o[j][h][2 + e];
-          if (k.acc) {
-            *reinterpret_cast<float2*>(k.acc + head * k.acc_step + c) = make_float2(y0, y1);
-          } else if constexpr (SPLIT) {
-            *reinterpret_cast<float2*>(static_cast<float*>(k.out) + head * D + c) = make_float2(__fdiv_rn(y0, s), __fdiv_rn(y1, s));
-          } else {
-            *reinterpret_cast<__nv_bfloat162*>(static_cast<Elem*>(k.out) + head * D + c) =
-                __floats2bfloat162_rn(__fdiv_rn(y0, s), __fdiv_rn(y1, s));
+          for (int j = 0; j < KS; ++j) *reinterpret_cast<float2*>(to + 16 * j) = make_float2(o[j][h][e], o[j][h][2 + e]);
+        } else {
+          Elem* to = static_cast<Elem*>(k.out) + head * D + 2 * g;
+          const float f = __fdiv_rn(1.f, s);
+#pragma unroll
+          for (int j = 0; j < KS; ++j) {
+            const float y0 = __fmul_rn(o[j][h][e], f), y1 = __fmul_rn(o[j][h][2 + e], f);
+            if constexpr (SPLIT) *reinterpret_cast<float2*>(to + 16 * j) = make_float2(y0, y1);
+            else *reinterpret_cast<uint32_t*>(to + 16 * j) = pack_bf16(y0, y1);
           }
         }
       }
@@ -517,70 +616,111 @@ struct QuantEngine : Quant {
 };
 
 // --------------------------------------------------------------------------- walk ----
-// The fetching side of a warp: which tile comes next, and where its rows lie.
+// The fetching side of a warp: which tile comes next, and where its rows lie.  It leaves what the computing side needs to
+// know beside the rows, so that only one of them walks.
 template <typename E>
 struct QuantWalk : Dealer<E> {
   using Dealer<E>::r;
   using Dealer<E>::live;
-  using Dealer<E>::seek;
   using Dealer<E>::push;
-  int page;  // lane < T: page of granule r.u + lane, on its way during the tile before
-
-  __device__ __forceinline__ bool in_pages(int lane) const { return lane < E::T && r.u + lane < min(r.end, r.tail); }
+  // A further chunk is asked for when the present run comes to its end, so that a warp on a long one does not
+  // keep it from others, in two steps a tile apart (a number from the counter, then its requests' lengths).
+  enum { kNone, kAsked, kKnown } more;
+  int number;
+  uint32_t first;  // pages are looked up for 32 granules at once, one a lane: those from this one on
+  int page;        // this lane's
+  int sub;         // rows of the tail's granule that earlier tiles took
 
   __device__ __forceinline__ void look_up(const QuantDecode& a, int lane) {
-    page = -1;
-    if (!live || !in_pages(lane)) return;
+    first = r.u;
+    page = 0;
+    if (r.u + lane >= min(r.end, r.tail)) return;
     const int b = (int)(((uint32_t)r.granule(r.u + lane) << kGranuleShift) >> a.page_shift);
-    if (b < a.max_blocks) page = a.block_table[(int64_t)r.i * a.max_blocks + b];
+    page = b < a.max_blocks ? a.block_table[(int64_t)r.i * a.max_blocks + b] : -1;
+  }
+  __device__ __forceinline__ void prepare(const QuantDecode& a, int parts, int lane) {
+    if (more == kNone) {
+      number = this->ask(lane);
+      more = kAsked;
+    } else if (more == kAsked) {
+      this->answer(a, parts, lane, number);
+      more = kKnown;
+    }
+  }
+  // the first run, or the one after r
+  __device__ __forceinline__ void next_run(const QuantDecode& a, int parts, int lane, QuantRun* queue, int& tail) {
+    live = false;
+    while (!this->left) {
+      while (more != kKnown) prepare(a, parts, lane);
+      if (this->base >= this->total) return;
+      this->take(a, parts);
+      more = kNone;
+    }
+    this->begin(a);
+    push(a, parts, queue, tail, lane);
+    look_up(a, lane);
+    sub = 0;
   }
 
-  // The current tile into `stage`, then on to the next one (its pages are looked up meanwhile).
+  // The current tile into `stage`, then on to the next one.
   __device__ __forceinline__ void fetch(const QuantDecode& a, int parts, unsigned char* stage, int lane, QuantRun* queue, int& tail) {
     if (live) {
+      if (!this->left && r.end - r.u <= 3 * E::T) prepare(a, parts, lane);
       const uint32_t st = tc::smem_u32(stage);
-      typename E::Meta& meta = *reinterpret_cast<typename E::Meta*>(stage + E::META);
-      const int h = r.y / parts;
-      const bool waits = r.u >= r.tail;
-      const int count = waits ? 1 : (int)min((uint32_t)E::T, min(r.end, r.tail) - r.u);
-      const int key = r.granule(r.u + min(lane, count - 1)) << kGranuleShift;  // of this lane's granule
-      if (lane < E::T) meta.key[lane] = key;
-      if (lane == 0) meta.count = count, meta.tail = waits;
-      bool lost = false;
-      if (!waits) {
-        uint32_t row = ~0u;  // of this lane's granule in the pages: none, or its page is outside the cache
-        lost = lane < count && (page < 0 || page >= a.c.num_pages);
-        if (lane < count && !lost)
-          row = (uint32_t)((((int64_t)page * a.hkv + h) << a.page_shift) + (key & ((1 << a.page_shift) - 1)));
-        if (lane < count) {
-          if (lost) {
-            meta.ks[lane] = meta.vs[lane] = 0.f;
-          } else {
-            tc::cp_async4(&meta.ks[lane], a.c.k_scale + (row >> a.c.block_shift));
-            tc::cp_async4(&meta.vs[lane], a.c.v_scale + (row >> a.c.block_shift));
-          }
-        }
-        constexpr int PIECES = kGranule * E::ROWB / 16;  // of a granule
+      const int h = parts == 1 ? r.y : r.y / parts;
+      int key = r.granule(r.u) << kGranuleShift, what, skip_from = E::T;
+      if (r.u < r.tail) {
+        const uint32_t stop = min(r.end, r.tail);
+        const int n = (int)min((uint32_t)E::T, stop - r.u);
+        if (r.u - first + n > 32) look_up(a, lane);
+        const bool lost = (uint32_t)page >= (uint32_t)a.c.num_pages && first + lane < stop;
+        if (!__any_sync(0xffffffffu, lost)) {
+          constexpr int PIECES = E::ROWB / 16;
+          // where this lane's first piece of a granule goes; its next ones are 512 bytes on, in the same piece of rows 4
+          // (d = 128: the swizzle's upper bit turns) or more further on
+          const uint32_t dst = st + E::place(lane / PIECES, lane % PIECES);
+          const uint32_t mask = (1u << a.page_shift) - 1u;
+          uint32_t rows = 0;  // lane i: row of granule i in the pages
 #pragma unroll
-        for (int i = 0; i < E::T; ++i) {
-          if (i >= count) break;
-          const uint32_t at = __shfl_sync(0xffffffffu, row, i);
-          const bool load = at != ~0u;
-          const int64_t off = load ? (int64_t)at * E::ROWB : 0;
-#pragma unroll
-          for (int p = lane; p < PIECES; p += 32) {
-            const uint32_t dst = st + E::place(kGranule * i + p / (E::ROWB / 16), p % (E::ROWB / 16));
-            cp_async16_or_zero(dst, a.c.k_pages + off + 16 * p, load);
-            cp_async16_or_zero(dst + E::SIDE, a.c.v_pages + off + 16 * p, load);
+          for (int i = 0; i < E::T; ++i) {
+            if (i >= n) break;
+            const uint32_t at = (uint32_t)__shfl_sync(0xffffffffu, page, r.u - first + i) * (uint32_t)a.hkv + (uint32_t)h;
+            const uint32_t row = (at << a.page_shift) + (((uint32_t)r.granule(r.u + i) << kGranuleShift) & mask);
+            rows = lane % E::T == i ? row : rows;
+            const int64_t off = (int64_t)row * E::ROWB + 16 * lane;
+            const uint8_t *kp = a.c.k_pages + off, *vp = a.c.v_pages + off;
+            const uint32_t to = dst + i * (kGranule * E::ROWB);
+            copy16<0, 0>(to, kp);
+            copy16<E::SIDE, 0>(to, vp);
+            if constexpr (E::ROWB >= 64) {
+              const uint32_t odd = E::ROWB == 128 ? to ^ 64u : to;
+              copy16<512, 512>(odd, kp);
+              copy16<E::SIDE + 512, 512>(odd, vp);
+              if constexpr (E::ROWB == 128) {
+                copy16<1024, 1024>(to, kp);
+                copy16<E::SIDE + 1024, 1024>(to, vp);
+                copy16<1536, 1536>(odd, kp);
+                copy16<E::SIDE + 1536, 1536>(odd, vp);
+              }
+            }
           }
+          // scales: lanes 0 .. T - 1 those of keys, T .. 2 T - 1 of values
+          if (lane < 2 * E::T && lane % E::T < n)
+            copy4(st + 2 * E::SIDE + 4 * lane, (lane < E::T ? a.c.k_scale : a.c.v_scale) + (rows >> a.c.block_shift));
+        } else if (lane == 0) {
+          queue[(tail - 1) & 3].bad = 1;  // the tile holds what it held: the run's results are NaN
         }
+        what = n + (r.u + (uint32_t)n - r.edge <= (uint32_t)n ? E::kEdge : 0);  // it holds granule edge - 1 or edge
+        if (r.u < (uint32_t)r.head) skip_from = min(E::T, r.head - (int)r.u);
+        r.u += n;
       } else {
         // only rows that are visible: what else the tail holds is nobody's
-        lost = r.slot < 0 || r.slot >= a.c.slots;
+        const bool lost = r.slot < 0 || r.slot >= a.c.slots;
         const int B = 1 << a.c.block_shift, lo = a.window > 0 ? r.len - a.window : 0;
+        key += sub;
         const int64_t off = lost ? 0 : (((int64_t)r.slot * a.hkv + h) * B + (key & (B - 1))) * E::TAILB;
-        constexpr int PIECES = kGranule * E::TAILB / 16, PER = E::TAILB / 16;
-#pragma unroll
+        constexpr int PIECES = E::TAIL_ROWS * E::TAILB / 16, PER = E::TAILB / 16;
+#pragma unroll 4
         for (int p = lane; p < PIECES; p += 32) {
           const int k = key + p / PER;
           const bool load = !lost && k < r.len && (k >= lo || k < a.sinks);
@@ -589,16 +729,22 @@ struct QuantWalk : Dealer<E> {
           cp_async16_or_zero(dst, static_cast<const char*>(a.c.k_tail) + from, load);
           cp_async16_or_zero(dst + E::SIDE, static_cast<const char*>(a.c.v_tail) + from, load);
         }
+        if (lost && lane == 0) queue[(tail - 1) & 3].bad = 1;
+        what = 0;
+        sub += E::TAIL_ROWS;
+        if (sub == kGranule || key + E::TAIL_ROWS >= r.len) sub = 0, ++r.u;
       }
-      if (__any_sync(0xffffffffu, lost) && lane == 0) queue[(tail - 1) & 3].bad = 1;
-      r.u += count;
-      if (r.u >= r.end) {
-        seek(a, parts, lane);
-        if (live) push(a, parts, queue, tail, lane);
+      if (lane == 0) {
+        typename E::Meta& meta = *reinterpret_cast<typename E::Meta*>(stage + 2 * E::SIDE);
+        *reinterpret_cast<int4*>(&meta.key) =
+            make_int4(key, what + (r.u >= r.end ? E::kLast : 0), r.skip << kGranuleShift, skip_from);
       }
-      look_up(a, lane);
+      if (r.u >= r.end) next_run(a, parts, lane, queue, tail);
     }
     tc::cp_async_commit();
+  }
+  __device__ __forceinline__ static void copy4(uint32_t smem, const void* gmem) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem), "l"(gmem) : "memory");
   }
 };
 
@@ -617,13 +763,12 @@ __global__ void __launch_bounds__(32 * DecodeSmem<E>::WARPS, 1) k_quant_decode(c
   f.counter = counter;
   f.base = ((threadIdx.x >> 5) * gridDim.x + blockIdx.x) * chunk;
   f.left = 0;
+  f.more = QuantWalk<E>::kKnown;
   int head = 0, tail = 0, put = 0, get = 0;
   f.look_ahead(a, parts, lane);
   if (counter) asm volatile("griddepcontrol.wait;" ::: "memory");  // it has been cleared
-  f.seek(a, parts, lane);
-  if (f.live) f.push(a, parts, queue, tail, lane);
-  f.look_up(a, lane);
-#pragma unroll
+  f.next_run(a, parts, lane, queue, tail);
+#pragma unroll 1
   for (int s = 0; s < E::RING - 1; ++s) {
     f.fetch(a, parts, sh + put * L::STAGE, lane, queue, tail);
     put = put + 1 == E::RING ? 0 : put + 1;
@@ -631,26 +776,38 @@ __global__ void __launch_bounds__(32 * DecodeSmem<E>::WARPS, 1) k_quant_decode(c
   E eng;
   while (head != tail) {
     __syncwarp();
-    QuantRun r = queue[head & 3];
-    const int g0 = (r.y % parts) * kHeadsPerRun, heads = min(kHeadsPerRun, group - g0);
-    const int h0 = (r.y / parts) * group + g0;
-    eng.start(a, (int64_t)r.i * a.hq + h0, heads, lane);
-    while (r.u < r.end) {
+    const QuantRun& r = queue[head & 3];
+    const int len = r.len;
+    {
+      const int g0 = (r.y % parts) * kHeadsPerRun;
+      eng.start(a, (int64_t)r.i * a.hq + (r.y / parts) * group + g0, min(kHeadsPerRun, group - g0), lane);
+    }
+    int what;
+    do {
       // the next tile on its way first, into the place that every lane has read
       f.fetch(a, parts, sh + put * L::STAGE, lane, queue, tail);
       put = put + 1 == E::RING ? 0 : put + 1;
       asm volatile("cp.async.wait_group %0;" ::"n"(E::RING - 1) : "memory");
       __syncwarp();
-      unsigned char* stage = sh + get * L::STAGE;
-      const typename E::Meta& meta = *reinterpret_cast<const typename E::Meta*>(stage + E::META);
-      r.u += meta.count;
-      if (meta.tail) eng.tail(a, stage, r.len, lane);
-      else eng.tile(a, stage, r.len, lane);
+      const unsigned char* stage = sh + get * L::STAGE;
+      const typename E::Meta& meta = *reinterpret_cast<const typename E::Meta*>(stage + 2 * E::SIDE);
+      what = meta.what;
+      const int n = what & (E::kLast - 1);
+      if (n) {
+        const bool full = !(what & E::kEdge);
+        int i = 0;
+#pragma unroll 1
+        for (; i + 2 <= n; i += 2) eng.template granules<2>(a, stage, i, full, len, lane);
+        if (i < n) eng.template granules<1>(a, stage, i, full, len, lane);
+      } else {
+        if constexpr (E::SPLIT) eng.tail_f32(a, stage, meta.key, len, lane);
+        else eng.tail_bf16(a, stage, meta.key, len, lane);
+      }
       get = get + 1 == E::RING ? 0 : get + 1;
       __syncwarp();
-    }
-    __syncwarp();
-    eng.finish(Sink(a, r, h0, heads, sizeof(typename E::Elem)), queue[head & 3].bad != 0, lane);
+    } while (!(what & E::kLast));
+    const int g0 = (r.y % parts) * kHeadsPerRun, heads = min(kHeadsPerRun, group - g0);
+    eng.finish(Sink(a, r, (r.y / parts) * group + g0, heads, sizeof(typename E::Elem)), r.bad != 0, lane);
     ++head;
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
@@ -676,6 +833,18 @@ int decode(const QuantDecode& a, cudaStream_t st) {
 }
 
 }  // namespace
+
+// A bound on the runs of any request of that many granules or fewer: quant_target grows with them between the counts
+// where quant_shift changes, and a request has at most quant_target runs.
+int quant_max_splits(int64_t granules, int hkv) {
+  int best = 1;
+  for (int s = kQuantMinShift; s <= kQuantMaxShift; ++s) {
+    const int64_t last = s < kQuantMaxShift ? (((int64_t)kQuantRuns << (s + 1)) - 1) / hkv : granules;
+    const int n = (int)(last < granules ? last : granules);
+    if (n > 0 && quant_target(n, hkv) > best) best = quant_target(n, hkv);
+  }
+  return best;
+}
 
 int launch_quant_decode(const QuantDecode& a, bool bf16, cudaStream_t st) {
   return bf16 ? decode<__nv_bfloat16>(a, st) : decode<float>(a, st);

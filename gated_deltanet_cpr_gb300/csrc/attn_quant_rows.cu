@@ -12,12 +12,12 @@ namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 
-// The last n < N with cu[n] / piece + 2 n <= w: the request that piece w belongs to.  All lanes take part.
-__device__ __forceinline__ int request_of(const int32_t* cu, int N, int shift, uint32_t w, int lane) {
+// The last n < N with (cu[n] >> shift) + gap n <= w: the request that piece w belongs to.  All lanes take part.
+__device__ __forceinline__ int request_of(const int32_t* cu, int N, int shift, int gap, uint32_t w, int lane) {
   int lo = 0, n = N;
   while (n > 1) {
     const int step = (n + 31) >> 5, i = lo + lane * step;
-    const bool at = lane * step < n && (cu[i] >> shift) + 2 * i <= (int64_t)w;
+    const bool at = lane * step < n && (cu[i] >> shift) + (int64_t)gap * i <= (int64_t)w;
     const uint32_t m = __ballot_sync(0xffffffffu, at) | 1u;
     const int k = (31 - __clz(m)) * step;
     lo += k;
@@ -26,37 +26,52 @@ __device__ __forceinline__ int request_of(const int32_t* cu, int N, int shift, u
   return lo;
 }
 
-// A piece of a request: positions [first, first + (1 << shift)), of which [from, to) have rows, row r being at
-// position r - cu0 + from0.
+// A piece of a request: `1 << shift` positions from `first` on.
 struct Piece {
   int n, j;             // request, number of the piece in it
   uint32_t first;       // position
-  uint32_t begin, len;  // the request's positions [begin, len) have rows
-  int cu0;
+  uint32_t begin, len;  // the request's positions [begin, len) have rows; len 0: its length is not valid
+  int cu0;              // row of position `begin`
   bool on;
 };
 __device__ __forceinline__ Piece piece_of(const QuantRows& a, int shift, uint32_t w, int lane) {
   Piece p;
-  p.n = request_of(a.cu, a.N, shift, w, lane);
-  const int c0 = a.cu[p.n], c1 = a.cu[p.n + 1], len = a.seq_lens[p.n];
-  const int rows = c1 - c0;
-  p.cu0 = c0;
-  p.on = c0 >= 0 && c1 > c0 && c1 <= a.T;
-  const bool fits = len >= rows;
-  p.len = (uint32_t)len;
-  p.begin = (uint32_t)(len - rows);
-  p.j = (int)((int64_t)w - ((c0 >> shift) + 2 * (int64_t)p.n));
-  if (!fits) {  // numbered as if its rows began at position 0
-    p.begin = 0;
-    p.len = (uint32_t)rows;
+  const int s = a.by_token ? 0 : shift, gap = a.by_token ? 0 : 2;
+  int c0 = -1, c1 = -1;
+  p.n = 0;
+  if (a.by_token && a.T == a.N) {  // a row each, as in a decode step: no search, if that is so
+    p.n = (int)w;
+    c0 = a.cu[p.n];
+    c1 = a.cu[p.n + 1];
   }
-  p.first = ((p.begin >> shift) + (uint32_t)p.j) << shift;
-  p.on = p.on && p.j >= 0 && p.first < p.len;
-  if (!fits) p.len = 0;  // no position is valid
+  if (c0 != (int)w || c1 != (int)w + 1) {
+    p.n = request_of(a.cu, a.N, s, gap, w, lane);
+    c0 = a.cu[p.n];
+    c1 = a.cu[p.n + 1];
+  }
+  const int len = a.seq_lens[p.n], rows = c1 - c0;
+  const bool fits = len >= rows;
+  p.cu0 = c0;
+  p.begin = fits ? (uint32_t)(len - rows) : 0u;  // if not, numbered as if its rows began at position 0
+  const uint32_t end = fits ? (uint32_t)len : (uint32_t)rows;
+  p.on = c0 >= 0 && c1 > c0 && c1 <= a.T;
+  const int64_t at = (int64_t)w - ((c0 >> s) + (int64_t)gap * p.n);  // row or piece of the request
+  const uint32_t mask = (1u << shift) - 1u;
+  if (a.by_token) {
+    const uint32_t pos = p.begin + (uint32_t)at;
+    p.on = p.on && at >= 0 && at < rows && (at == 0 || (pos & mask) == 0u);
+    p.first = pos & ~mask;
+  } else {
+    p.first = ((p.begin >> shift) + (uint32_t)at) << shift;
+    p.on = p.on && at >= 0 && p.first < end;
+  }
+  p.j = (int)((p.first >> shift) - (p.begin >> shift));
+  p.len = fits ? end : 0u;
   return p;
 }
 
 __device__ __forceinline__ void report(WsHeader* h, int code) {
+  if (!h) return;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the word has been cleared
   set_error(h, code);
 }
@@ -83,8 +98,8 @@ __device__ void check_requests(const QuantRows& a) {
 }
 
 // ------------------------------------------------------------------------- rounding ----
-// Codes of an int8 block: the quotient 127 x / m is rounded as it is in exact arithmetic.  t = x fl(127 / m) is
-// within 2^-16 of it, so only a t that close to a half needs more: there the sign of 254 x - (2 k + 1) m decides, which
+// Codes of an int8 block: the quotient 127 x / m is rounded as it is in exact arithmetic.  x fl(127 / m) is
+// within 2^-17 of it, so only one that close to a half needs more (2 or 3 of 2048 normal values in bf16): there the sign of 254 x - (2 k + 1) m decides, which
 // the two products and what their rounding lost give exactly.
 struct Rounder {
   float inv, m, scale;  // scale: what the block stores
@@ -112,44 +127,49 @@ struct Rounder {
     }
   }
   static constexpr float kMagic = 12582912.f;  // 1.5 2^23: the sum's last bits are a whole number, ties to even
-  // t next to a half: the whole number on the right side of it, as x 127 / m has it
-  __device__ __noinline__ static float settle(float x, float m, float down, float r, float dist) {
-    const float s = dist < 0.f ? -1.f : 1.f, odd = 2.f * r + s;  // the half is odd / 2
-    x *= down;
-    m *= down;
-    const float q = 254.f * x, f = __fmaf_rn(254.f, x, -q), p = odd * m, e = __fmaf_rn(odd, m, -p);
-    const float diff = __fadd_rn(__fsub_rn(q, p), __fsub_rn(f, e)) * s;  // > 0: past the half
-    if (diff > 0.f) return r + s;
-    if (diff < 0.f) return r;
-    return ((int)r & 1) ? r + s : r;
+  static constexpr float kNear = 0.5f - 0x1p-14f;
+  // y = x inv + kMagic rounded to a whole number r, and d what that took off: if x inv lies next to a half, the whole number on
+  // the right side of it, as x 127 / m has it.
+  __device__ __forceinline__ static float settle(float x, float y, float d, float m, float down) {
+    const float r = __fsub_rn(y, kMagic), s = d < 0.f ? -1.f : 1.f, odd = __fmaf_rn(2.f, r, s);  // the half is odd / 2
+    const float a = __fmul_rn(x, down), b = __fmul_rn(m, down);
+    const float q = __fmul_rn(254.f, a), f = __fmaf_rn(254.f, a, -q), p = __fmul_rn(odd, b), e = __fmaf_rn(odd, b, -p);
+    const float diff = __fmul_rn(__fadd_rn(__fsub_rn(q, p), __fsub_rn(f, e)), s);  // > 0: past the half
+    return fabsf(d) > kNear && (diff > 0.f || (diff == 0.f && ((int)r & 1))) ? __fadd_rn(y, s) : y;
   }
-  // codes of 4 values
-  __device__ __forceinline__ uint32_t four(const float (&x)[4]) const {
+  // codes of 4 values, pairs (x0, x1) and (x2, x3)
+  __device__ __forceinline__ uint32_t four(const float2 (&x)[2]) const {
     if (m == 0.f) return 0u;
     if (e4m3) {
       uint16_t lo, hi;
-      asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(__fmul_rn(x[1], inv)), "f"(__fmul_rn(x[0], inv)));
-      asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(__fmul_rn(x[3], inv)), "f"(__fmul_rn(x[2], inv)));
+      const float2 i2 = make_float2(inv, inv), a = mul2(x[0], i2), b = mul2(x[1], i2);
+      asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(a.y), "f"(a.x));
+      asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(b.y), "f"(b.x));
       return (uint32_t)lo | ((uint32_t)hi << 16);
     }
-    float y[4];
-    bool near = false;
+    const float2 i2 = make_float2(inv, inv), up = make_float2(kMagic, kMagic), one = make_float2(1.f, 1.f);
+    float2 y[2], d[2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float t = __fmul_rn(x[i], inv);
-      y[i] = __fadd_rn(t, kMagic);
-      near |= fabsf(__fsub_rn(t, __fsub_rn(y[i], kMagic))) > 0.5f - 0x1p-14f;
+    for (int i = 0; i < 2; ++i) {
+      y[i] = fma2(x[i], i2, up);
+      const float2 r = fma2(y[i], one, make_float2(-kMagic, -kMagic));
+      d[i] = fma2(x[i], i2, make_float2(-r.x, -r.y));  // what the rounding took off
     }
-    if (near) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float t = __fmul_rn(x[i], inv), r = __fsub_rn(y[i], kMagic), dist = __fsub_rn(t, r);
-        if (fabsf(dist) > 0.5f - 0x1p-14f) y[i] = __fadd_rn(settle(x[i], m, down, r, dist), kMagic);
-      }
-    }
-    const uint32_t a = __byte_perm(__float_as_uint(y[0]), __float_as_uint(y[1]), 0x0040);
-    const uint32_t b = __byte_perm(__float_as_uint(y[2]), __float_as_uint(y[3]), 0x0040);
+    if (fmaxf(fmaxf(fabsf(d[0].x), fabsf(d[0].y)), fmaxf(fabsf(d[1].x), fabsf(d[1].y))) > kNear)
+      return settled(make_float4(x[0].x, x[0].y, x[1].x, x[1].y), make_float4(d[0].x, d[0].y, d[1].x, d[1].y),
+                     make_float4(y[0].x, y[0].y, y[1].x, y[1].y), m, down);
+    return bytes(y[0].x, y[0].y, y[1].x, y[1].y);
+  }
+  // the last bytes of four sums with kMagic
+  __device__ __forceinline__ static uint32_t bytes(float y0, float y1, float y2, float y3) {
+    const uint32_t a = __byte_perm(__float_as_uint(y0), __float_as_uint(y1), 0x0040);
+    const uint32_t b = __byte_perm(__float_as_uint(y2), __float_as_uint(y3), 0x0040);
     return __byte_perm(a, b, 0x5410);
+  }
+  // a call of its own: in place it would fill the instruction cache
+  __device__ __noinline__ static uint32_t settled(float4 x, float4 d, float4 y, float m, float down) {
+    return bytes(settle(x.x, y.x, d.x, m, down), settle(x.y, y.y, d.y, m, down), settle(x.z, y.z, d.z, m, down),
+                 settle(x.w, y.w, d.w, m, down));
   }
 };
 
@@ -166,12 +186,13 @@ struct Vec<__nv_bfloat16> {
     return __vmaxu2(m, u.w & 0x7fff7fffu);
   }
   __device__ __forceinline__ static uint32_t bits(uint32_t m) { return max(m << 16, m & 0xffff0000u); }
+  __device__ __forceinline__ static float2 pair(uint32_t u) {
+    return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+  }
   __device__ __forceinline__ static void store(const Rounder& r, const uint4& u, uint8_t* to) {
     uint2 o;
-    o.x = r.four({__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
-                  __uint_as_float(u.y & 0xffff0000u)});
-    o.y = r.four({__uint_as_float(u.z << 16), __uint_as_float(u.z & 0xffff0000u), __uint_as_float(u.w << 16),
-                  __uint_as_float(u.w & 0xffff0000u)});
+    o.x = r.four({pair(u.x), pair(u.y)});
+    o.y = r.four({pair(u.z), pair(u.w)});
     *reinterpret_cast<uint2*>(to) = o;
   }
 };
@@ -184,7 +205,7 @@ struct Vec<float> {
   __device__ __forceinline__ static uint32_t bits(uint32_t m) { return m; }
   __device__ __forceinline__ static void store(const Rounder& r, const uint4& u, uint8_t* to) {
     *reinterpret_cast<uint32_t*>(to) =
-        r.four({__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z), __uint_as_float(u.w)});
+        r.four({make_float2(__uint_as_float(u.x), __uint_as_float(u.y)), make_float2(__uint_as_float(u.z), __uint_as_float(u.w))});
   }
 };
 
@@ -197,20 +218,20 @@ __global__ void __launch_bounds__(kThreads) k_quant_append(const QuantRows a) {
   constexpr int VEC = Vec<T>::N, LPR = D / VEC, RPP = 32 / LPR, PASSES = kGranule / RPP;
   __shared__ uint32_t most[kWarps];
   if (blockIdx.x == 0) {
-    check_requests<true>(a);
+    if (a.hdr) check_requests<true>(a);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     return;
   }
   const QuantCache& c = a.c;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, B = 1 << c.block_shift;
   const int each = B / kGranule, part = warp % each;  // warps of a unit, this one's rows of it
-  const uint32_t units = ((uint32_t)(a.T >> c.block_shift) + 2u * (uint32_t)a.N) * 2u * (uint32_t)c.hkv;
-  const uint32_t unit = (blockIdx.x - 1) * (uint32_t)(kWarps / each) + (uint32_t)(warp / each);
-  const uint32_t w = unit / (2u * (uint32_t)c.hkv), rest = unit - w * 2u * (uint32_t)c.hkv;
+  const uint32_t pieces = a.by_token ? (uint32_t)a.T : (uint32_t)(a.T >> c.block_shift) + 2u * (uint32_t)a.N;
+  const uint32_t all = 2u * (uint32_t)c.hkv, unit = (blockIdx.x - 1) * (uint32_t)(kWarps / each) + (uint32_t)(warp / each);
+  const uint32_t w = unit / all, rest = unit - w * all;
   const int h = (int)(rest >> 1);
   const bool is_v = rest & 1;
   Piece p{};
-  if (unit < units) p = piece_of(a, c.block_shift, w, lane);
+  if (w < pieces) p = piece_of(a, c.block_shift, w, lane);
   int slot = 0, page = -1;
   if (p.on) {
     slot = a.slot ? a.slot[p.n] : p.n;
@@ -221,63 +242,59 @@ __global__ void __launch_bounds__(kThreads) k_quant_append(const QuantRows a) {
     const uint32_t b = p.first >> c.page_shift;
     page = b < (uint32_t)a.max_blocks ? a.block_table[(int64_t)p.n * a.max_blocks + b] : -1;
   }
-  const T* src = static_cast<const T*>(is_v ? a.v_in : a.k_in);
-  const int64_t stride = is_v ? a.v_stride : a.k_stride;
-  T* tail = static_cast<T*>(is_v ? c.v_tail : c.k_tail) + ((int64_t)slot * c.hkv + h) * B * D;
   const int r0 = part * kGranule + lane / LPR, col = lane % LPR * VEC;
-  // row of the new token at a position
-  auto fresh = [&](uint32_t pos) { return src + (int64_t)(p.cu0 + (int)(pos - p.begin)) * stride + h * D + col; };
+  const int64_t stride = is_v ? a.v_stride : a.k_stride;
+  const T* src = static_cast<const T*>(is_v ? a.v_in : a.k_in) + h * D + col;
+  T* tail = static_cast<T*>(is_v ? c.v_tail : c.k_tail) + (((int64_t)slot * c.hkv + h) * B + r0) * D + col;
+  // rows [0, PASSES) of this lane of the block at `first`: new tokens' rows from src, earlier ones' from the tail
   uint4 x[PASSES];
+  auto load = [&](uint32_t first, bool from_tail) {
+    const T* s = src + (int64_t)(p.cu0 + (int)(first + (uint32_t)r0 - p.begin)) * stride;  // of a row that may not be there
 #pragma unroll
-  for (int i = 0; i < PASSES; ++i) {
-    const int r = r0 + i * RPP;
-    const uint32_t pos = p.first + (uint32_t)r;
-    x[i] = make_uint4(0, 0, 0, 0);
-    if (!p.on || pos >= p.len) continue;
-    if (pos >= p.begin) x[i] = *reinterpret_cast<const uint4*>(fresh(pos));
-    else if (whole) x[i] = *reinterpret_cast<const uint4*>(tail + r * D + col);
-  }
+    for (int i = 0; i < PASSES; ++i) {
+      const uint32_t pos = first + (uint32_t)(r0 + i * RPP);
+      x[i] = make_uint4(0, 0, 0, 0);
+      if (pos < p.len && pos >= p.begin) x[i] = *reinterpret_cast<const uint4*>(s + i * RPP * stride);
+      else if (pos < p.begin && from_tail) x[i] = *reinterpret_cast<const uint4*>(tail + i * RPP * D);
+    }
+  };
   uint32_t m = 0;
+  if (whole && p.first >= p.begin) {  // all of it new, as in a prefill
+    const T* s = src + (int64_t)(p.cu0 + (int)(p.first + (uint32_t)r0 - p.begin)) * stride;
 #pragma unroll
-  for (int i = 0; i < PASSES; ++i) m = Vec<T>::amax(x[i], m);
-  m = __reduce_max_sync(0xffffffffu, Vec<T>::bits(m));
+    for (int i = 0; i < PASSES; ++i) x[i] = *reinterpret_cast<const uint4*>(s + i * RPP * stride);
+  } else if (p.on) {
+    load(p.first, whole);
+  }
+  if (whole) {
+#pragma unroll
+    for (int i = 0; i < PASSES; ++i) m = Vec<T>::amax(x[i], m);
+    m = __reduce_max_sync(0xffffffffu, Vec<T>::bits(m));
+  }
   if (each > 1) {
     if (lane == 0) most[warp] = m;
     __syncthreads();  // the tail's rows are in registers, too
     for (int i = 0; i < each; ++i) m = max(m, most[warp - part + i]);
-  } else {
-    __syncwarp();
   }
   if (whole) {
     if (page < 0 || page >= c.num_pages) {
       if (lane == 0) report(a.hdr, GDN_DEVERR_PAGES);
     } else {
       const Rounder round(m, c.e4m3);
-      const int64_t row = ((int64_t)page * c.hkv + h) << c.page_shift;
-      const uint32_t off = p.first & ((1u << c.page_shift) - 1u);
-      uint8_t* to = (is_v ? c.v_pages : c.k_pages) + (row + off) * D;
+      const int64_t row = (((int64_t)page * c.hkv + h) << c.page_shift) + (p.first & ((1u << c.page_shift) - 1u));
+      uint8_t* to = (is_v ? c.v_pages : c.k_pages) + (row + r0) * D + col;
 #pragma unroll
-      for (int i = 0; i < PASSES; ++i) Vec<T>::store(round, x[i], to + (r0 + i * RPP) * D + col);
-      if (part == 0 && lane == 0) (is_v ? c.v_scale : c.k_scale)[(row + off) >> c.block_shift] = round.scale;
+      for (int i = 0; i < PASSES; ++i) Vec<T>::store(round, x[i], to + i * RPP * D);
+      if (part == 0 && lane == 0) (is_v ? c.v_scale : c.k_scale)[row >> c.block_shift] = round.scale;
     }
   }
-  if (p.on && p.j == 0) {
-    if (!whole) {
+  const uint32_t last = p.len & ~(uint32_t)(B - 1);  // where the request's unfinished block begins
+  if (p.on && p.j == 0 && last < p.len) {
+    if (whole) load(last, false);  // after the first one, whose rows the tail held
 #pragma unroll
-      for (int i = 0; i < PASSES; ++i) {
-        const uint32_t pos = p.first + (uint32_t)(r0 + i * RPP);
-        if (pos >= p.begin && pos < p.len) *reinterpret_cast<uint4*>(tail + (r0 + i * RPP) * D + col) = x[i];
-      }
-    } else if (p.len & (uint32_t)(B - 1)) {
-      const uint32_t last = p.len & ~(uint32_t)(B - 1);  // the unfinished block begins here, after this one
-#pragma unroll
-      for (int i = 0; i < PASSES; ++i) {
-        const uint32_t pos = last + (uint32_t)(r0 + i * RPP);
-        if (pos < p.len) x[i] = *reinterpret_cast<const uint4*>(fresh(pos));
-      }
-#pragma unroll
-      for (int i = 0; i < PASSES; ++i)
-        if (last + (uint32_t)(r0 + i * RPP) < p.len) *reinterpret_cast<uint4*>(tail + (r0 + i * RPP) * D + col) = x[i];
+    for (int i = 0; i < PASSES; ++i) {
+      const uint32_t pos = last + (uint32_t)(r0 + i * RPP);
+      if (pos < p.len && pos >= p.begin) *reinterpret_cast<uint4*>(tail + i * RPP * D) = x[i];
     }
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");  // so that the word is cleared before the next kernel begins
@@ -307,13 +324,13 @@ template <int D, typename T, typename TO>
 __global__ void __launch_bounds__(kThreads) k_quant_read(const QuantRows a) {
   constexpr int LPR = D / 8, RPP = 32 / LPR, PASSES = kGranule / RPP;
   if (blockIdx.x == 0) {
-    check_requests<false>(a);
+    if (a.hdr) check_requests<false>(a);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     return;
   }
   const QuantCache& c = a.c;
   const int lane = threadIdx.x & 31;
-  const uint32_t units = ((uint32_t)(a.T / kGranule) + 2u * (uint32_t)a.N) * 2u * (uint32_t)c.hkv;
+  const uint32_t units = (a.by_token ? (uint32_t)a.T : (uint32_t)(a.T / kGranule) + 2u * (uint32_t)a.N) * 2u * (uint32_t)c.hkv;
   const uint32_t unit = (blockIdx.x - 1) * (uint32_t)kWarps + (threadIdx.x >> 5);
   if (unit < units) {
     const uint32_t w = unit / (2u * (uint32_t)c.hkv), rest = unit - w * 2u * (uint32_t)c.hkv;
@@ -399,30 +416,32 @@ __global__ void k_quant_clear(WsHeader* hdr) {
 
 template <typename K>
 int launch(K* kernel, const QuantRows& a, int64_t ctas, cudaStream_t st) {
-  k_quant_clear<<<1, 1, 0, st>>>(a.hdr);
+  if (a.hdr) k_quant_clear<<<1, 1, 0, st>>>(a.hdr);
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t c{};
   c.stream = st;
   c.attrs = &attr;
-  c.numAttrs = 1;
+  c.numAttrs = a.hdr ? 1 : 0;
   c.gridDim = dim3((unsigned)(1 + ctas));
   c.blockDim = dim3(kThreads);
   cudaLaunchKernelEx(&c, kernel, a);
-  return 2;
+  return a.hdr ? 2 : 1;
 }
 
 template <int D, typename T>
-int append_t(const QuantRows& a, cudaStream_t st) {
+int append_t(QuantRows a, cudaStream_t st) {
   const int per = kWarps / ((1 << a.c.block_shift) / kGranule);  // units of a CTA
-  const int64_t units = quant_pieces(a.N, a.T, a.c.block_shift) * 2 * a.c.hkv;
+  a.by_token = quant_by_token(a.N, a.T, a.c.block_shift);
+  const int64_t units = (a.by_token ? a.T : quant_pieces(a.N, a.T, a.c.block_shift)) * 2 * a.c.hkv;
   return launch(k_quant_append<D, T>, a, (units + per - 1) / per, st);
 }
 
 template <int D, typename T, typename TO>
-int read_t(const QuantRows& a, cudaStream_t st) {
-  const int64_t units = quant_pieces(a.N, a.T, kGranuleShift) * 2 * a.c.hkv;
+int read_t(QuantRows a, cudaStream_t st) {
+  a.by_token = quant_by_token(a.N, a.T, kGranuleShift);
+  const int64_t units = (a.by_token ? a.T : quant_pieces(a.N, a.T, kGranuleShift)) * 2 * a.c.hkv;
   return launch(k_quant_read<D, T, TO>, a, (units + kWarps - 1) / kWarps, st);
 }
 

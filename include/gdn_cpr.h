@@ -568,7 +568,8 @@ typedef struct {
  *   a request whose length is negative or less than what it appends (GDN_DEVERR_POS); one whose
  *   slot lies outside [0, slots) (GDN_DEVERR_SLOT); a block whose page lies outside the cache or the
  *   block table (GDN_DEVERR_PAGES).  A request that appends nothing is left alone.
- *   ws: GDN_CPR_ATTN_HEADER_BYTES, 256-byte aligned (the error word, set by every call)        */
+ *   ws: GDN_CPR_ATTN_HEADER_BYTES, 256-byte aligned (the error word, set by every call), or NULL:
+ *   what is wrong is skipped as above and not reported, and the call is one kernel            */
 gdn_status gdn_cpr_quant_append(const gdn_cpr_quant_cache *cache, int32_t num_seqs,
                                 int32_t total_tokens, const void *k, const void *v,
                                 int64_t k_stride, int64_t v_stride, const int32_t *cu_seqlens,
@@ -583,7 +584,8 @@ gdn_status gdn_cpr_quant_append(const gdn_cpr_quant_cache *cache, int32_t num_se
  *   in a tail whose slot lies outside [0, slots) (GDN_DEVERR_SLOT) and rows on a page outside the cache
  *   or the block table (GDN_DEVERR_PAGES) are NaN.  Offsets that do not fit (GDN_DEVERR_CU_SEQLENS): as
  *   above, and the outputs are not valid.
- *   ws: GDN_CPR_ATTN_HEADER_BYTES, 256-byte aligned (the error word, set by every call)        */
+ *   ws: GDN_CPR_ATTN_HEADER_BYTES, 256-byte aligned (the error word, set by every call), or NULL:
+ *   what is wrong is skipped as above and not reported, and the call is one kernel            */
 gdn_status gdn_cpr_quant_read(const gdn_cpr_quant_cache *cache, int32_t num_seqs,
                               int32_t total_tokens, const int32_t *cu_seqlens,
                               const int32_t *seq_lens, const int32_t *block_table,
@@ -595,8 +597,9 @@ gdn_status gdn_cpr_quant_read(const gdn_cpr_quant_cache *cache, int32_t num_seqs
  * first tokens, scale, lse and errors as there.  attn and cache agree in h_kv, d and dtype.
  *   slot        NULL or [N] int32: the requests' tails; one outside [0, slots) sets GDN_DEVERR_SLOT and
  *               gives NaN for a request whose tail holds tokens
- *   A key or value that is not finite gives NaN in its request's rows if it is visible, and wherever it
- *   lies in a block that holds a visible key; masked keys of a block may take part with weight 0.
+ *   A visible key that is not finite gives NaN in its request's rows, a visible value at least in its
+ *   column's entries (infinities or NaN); in a block, where all of it reads as NaN, either gives NaN
+ *   if any key of the block is visible.  Masked keys of a block may take part with weight 0.
  *   ws: gdn_cpr_quant_decode_workspace_size bytes; its error word is set by every call        */
 gdn_status gdn_cpr_quant_decode(const gdn_cpr_attn *attn, const gdn_cpr_quant_cache *cache,
                                 int32_t num_seqs, int32_t max_len, const void *q,

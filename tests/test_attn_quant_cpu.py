@@ -31,8 +31,8 @@ BAD_CACHE = [(dict(num_pages=-1), 1), (dict(page_size=0), 1), (dict(page_size=24
              (dict(k_scale=FAKE + 2), 1), (dict(v_scale=None), 1), (dict(k_tail=None), 1), (dict(v_tail=FAKE + 4), 1)]
 BAD_ROWS = [(dict(N=-1), 1), (dict(T=-1), 1), (dict(blocks=-1), 1), (dict(N=0), 1), (dict(N=65536), 2), (dict(cu=None), 1),
             (dict(lens=None), 1), (dict(table=None), 1), (dict(slot=FAKE + 1), 1), (dict(k=None), 1), (dict(v=FAKE + 8), 1),
-            (dict(ws=None), 4), (dict(ws=FAKE + 64), 4), (dict(n=255), 4), (dict(h_kv=65535, T=1 << 30), 2),
-            (dict(N=0, T=0, cu=None, lens=None, k_pages=None, k_tail=None), 0)]
+            (dict(ws=FAKE + 64), 4), (dict(n=255), 4), (dict(h_kv=65535, T=1 << 30), 2),
+            (dict(N=0, T=0, cu=None, lens=None, k_pages=None, k_tail=None), 0), (dict(N=0, T=0, ws=None, n=0), 0)]
 
 
 def split(kw):
@@ -132,11 +132,11 @@ def test_decode_refusals(lib):
 
 
 def split_runs(n, hkv):
-    """Runs of a request that sees n keys, by the rule of csrc/attn.h in unbounded integers."""
-    x = n * hkv
-    shift = 6 if x < 128 * 32 else 7 if x < 256 * 32 else 8 if x < 512 * 32 else 9
-    r = max(1, (n + (1 << shift >> 1)) >> shift)
-    keys = (-(-n // r) + 31) // 32 * 32
+    """Runs of a request of n granules, by the rule of csrc/attn_quant.h in unbounded integers."""
+    s = 2
+    while s < 5 and n * hkv >= 32 << (s + 1):
+        s += 1
+    keys = -(-n // max(1, (n + (1 << s >> 1)) >> s))
     return -(-n // keys) if n else 0
 
 
@@ -161,7 +161,7 @@ def test_decode_workspace_holds_every_run(lib, hkv, window, sinks):
 
     most, before = 0, 0
     for L in sorted({*range(0, 6000), *range(6000, 40000, 97), 10 ** 6, 10 ** 8, top - 300, top - 16, top - 1, top}):
-        most = max(most, split_runs(min(16 * granules(L, window, sinks), top), hkv))
+        most = max(most, split_runs(granules(L, window, sinks), hkv))
         n = size(L)
         assert most <= 1 or n >= 256 + N * hkv * most * (d + 2) * 4, L
         assert n >= before
