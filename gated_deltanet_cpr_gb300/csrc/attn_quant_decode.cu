@@ -385,7 +385,9 @@ struct QuantEngine : Quant {
     // swizzle turns bits, and a stage begins at a multiple of 128 bytes
     const uint32_t at = tc::smem_u32(stage) + i * (kGranule * ROWB) + place((lane & 7) + (lane & 8), lane >> 4);
     uint32_t r[G][KS / 2][4];
-    float x[G][NH][4], y[G][NH][4];  // of even and odd steps
+    // sums of even and odd steps; of fp32 queries' upper and lower parts: the products' own sums are cut, not rounded, so only
+    // those of the lower part, 2^-11 of the other's size, run through all steps
+    float x[G][NH][4], y[G][NH][4];
     load_all<G, false, 0>(at, r);
 #pragma unroll
     for (int s = 0; s < KS; ++s)
@@ -396,10 +398,13 @@ struct QuantEngine : Quant {
         widen16<E4M3, false>(r[b][s / 2][2 * (s & 1) + 1], k[1], k[3]);
 #pragma unroll
         for (int h = 0; h < NH; ++h) {
-          float(&c)[4] = s & 1 ? y[b][h] : x[b][h];
-          if (s < 2) mma_f16_from0(c, k, q[0][s][h][0], q[0][s][h][1]);
-          else mma_f16(c, k, q[0][s][h][0], q[0][s][h][1]);
-          if constexpr (SPLIT) mma_f16(c, k, q[P - 1][s][h][0], q[P - 1][s][h][1]);
+          if constexpr (SPLIT) {
+            add_step(x[b][h], y[b][h], s, k, h);
+          } else {
+            float(&c)[4] = s & 1 ? y[b][h] : x[b][h];
+            if (s < 2) mma_f16_from0(c, k, q[0][s][h][0], q[0][s][h][1]);
+            else mma_f16(c, k, q[0][s][h][0], q[0][s][h][1]);
+          }
         }
       }
     load_all<G, true, SIDE>(at, r);
@@ -432,10 +437,24 @@ struct QuantEngine : Quant {
         for (int h = 0; h < NH; ++h) {
           float c[4];
           mma_f16_from0(c, v, p[b][h][0][0], p[b][h][0][1]);
-          if constexpr (SPLIT) mma_f16(c, v, p[b][h][P - 1][0], p[b][h][P - 1][1]);
+          if constexpr (SPLIT) {
+            float rest[4];
+            mma_f16_from0(rest, v, p[b][h][P - 1][0], p[b][h][P - 1][1]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) c[e] = __fadd_rn(c[e], rest[e]);
+          }
           add(j, h, c, vs[b]);
         }
       }
+  }
+  // fp32 queries: step s of keys k for head tile h, upper part to x, lower part to y
+  __device__ __forceinline__ void add_step(float (&x)[4], float (&y)[4], int s, const uint32_t (&k)[4], int h) const {
+    float c[4];
+    mma_f16_from0(c, k, q[0][s][h][0], q[0][s][h][1]);
+    if (s == 0) mma_f16_from0(y, k, q[P - 1][s][h][0], q[P - 1][s][h][1]);
+    else mma_f16(y, k, q[P - 1][s][h][0], q[P - 1][s][h][1]);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] = s == 0 ? c[e] : __fadd_rn(x[e], c[e]);
   }
   template <int G, bool TRANS, int OFF>
   __device__ __forceinline__ static void load_all(uint32_t at, uint32_t (&r)[G][KS / 2][4]) {
@@ -526,7 +545,7 @@ struct QuantEngine : Quant {
     const int ke = f16_exponent(km), ve = f16_exponent(vm);
     const float kd = km == km ? pow2(-ke) : 0.f, vd = vm == vm ? pow2(-ve) : 0.f;
     const float vs = vm == vm ? pow2(ve) : vm;
-    float xs[1][NH][4];
+    float xs[1][NH][4], ys[NH][4];
     float(&x)[NH][4] = xs[0];
 #pragma unroll
     for (int s = 0; s < KS; ++s) {
@@ -544,12 +563,14 @@ struct QuantEngine : Quant {
       }
 #pragma unroll
       for (int h = 0; h < NH; ++h) {
-        if (s == 0) mma_f16_from0(x[h], k[0], q[0][s][h][0], q[0][s][h][1]);
-        else mma_f16(x[h], k[0], q[0][s][h][0], q[0][s][h][1]);
-        mma_f16(x[h], k[0], q[P - 1][s][h][0], q[P - 1][s][h][1]);
-        mma_f16(x[h], k[1], q[0][s][h][0], q[0][s][h][1]);
+        add_step(x[h], ys[h], s, k[0], h);
+        mma_f16(ys[h], k[1], q[0][s][h][0], q[0][s][h][1]);
       }
     }
+#pragma unroll
+    for (int h = 0; h < NH; ++h)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[h][e] = __fadd_rn(x[h][e], ys[h][e]);
     softmax<1>(a, {km == km ? pow2(ke) : km}, false, {key}, TAIL_ROWS, len, xs, lane);
     uint32_t b[NH][P][2];
 #pragma unroll
@@ -575,10 +596,12 @@ struct QuantEngine : Quant {
       }
 #pragma unroll
       for (int h = 0; h < NH; ++h) {
-        float c[4];
+        float c[4], rest[4];
         mma_f16_from0(c, v[0], b[h][0][0], b[h][0][1]);
-        mma_f16(c, v[0], b[h][P - 1][0], b[h][P - 1][1]);
-        mma_f16(c, v[1], b[h][0][0], b[h][0][1]);
+        mma_f16_from0(rest, v[0], b[h][P - 1][0], b[h][P - 1][1]);
+        mma_f16(rest, v[1], b[h][0][0], b[h][0][1]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) c[e] = __fadd_rn(c[e], rest[e]);
         add(j, h, c, vs);
       }
     }
