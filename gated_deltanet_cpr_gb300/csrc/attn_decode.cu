@@ -39,11 +39,6 @@ struct Request {
   __device__ __forceinline__ int key(int u) const { return u < head ? u : u + skip; }
   __device__ __forceinline__ int runs(const PagedDecode& a) const { return split_of(n, a.hkv).runs; }
 };
-// What is read of a request before its turn.
-struct Ahead {
-  int len;
-  __device__ __forceinline__ void load(const PagedDecode& a, int i) { len = a.seq_lens[i]; }
-};
 
 // One run: request i, key head and part of its query heads, which run, and its keys [u, end); bad:
 // a key's page is outside the cache.  Keys are numbered without a sign: a request may end a tile
@@ -53,24 +48,6 @@ struct Run {
   uint32_t u, end;
   int head, skip, bad;
   __device__ __forceinline__ int key(uint32_t x) const { return (int)x < head ? (int)x : (int)x + skip; }
-  __device__ __forceinline__ void set(const PagedDecode& a, const Request& rq, const Ahead&) {
-    const Split s = split_of(rq.n, a.hkv);
-    runs = s.runs;
-    u = (uint32_t)run * (uint32_t)s.keys;
-    end = min((uint32_t)rq.n, u + (uint32_t)s.keys);
-    head = rq.head;
-    skip = rq.skip;
-  }
-  __device__ __forceinline__ void from(const PagedDecode&, const Run& o, int lane) {
-    i = __shfl_sync(0xffffffffu, o.i, lane);
-    y = __shfl_sync(0xffffffffu, o.y, lane);
-    run = __shfl_sync(0xffffffffu, o.run, lane);
-    runs = __shfl_sync(0xffffffffu, o.runs, lane);
-    u = __shfl_sync(0xffffffffu, o.u, lane);
-    end = __shfl_sync(0xffffffffu, o.end, lane);
-    head = __shfl_sync(0xffffffffu, o.head, lane);
-    skip = __shfl_sync(0xffffffffu, o.skip, lane);
-  }
 };
 
 // What the engines below have in common: the call, and its requests' pages.
@@ -78,9 +55,7 @@ struct Paged {
   using Kind = Paged;
   using Args = PagedDecode;
   using Request = gdn::Request;
-  using Ahead = gdn::Ahead;
   using Run = gdn::Run;
-  using Seed = gdn::Run;
   // a page of the request's visible keys is outside the cache
   __device__ __forceinline__ static int check(const PagedDecode& a, const gdn::Request& rq, int i, int tid, int threads) {
     bool lost = false;
@@ -364,12 +339,82 @@ struct MmaEngine : Paged {
 
 // The fetching side of a warp: which tile comes next, and where its keys lie.
 template <typename E>
-struct Walk : Dealer<E> {
-  using Dealer<E>::r;
-  using Dealer<E>::live;
-  using Dealer<E>::seek;
-  using Dealer<E>::push;
-  int page;  // lane < KEYS: page of key r.u + lane, on its way during the tile before
+struct Walk {
+  // (run, request, part) slots are numbered with the run slowest and dealt out in chunks of `chunk`
+  // <= 32 consecutive ones, one per lane: the first by the warp's number, further ones from a
+  // counter, as runs differ in length and many slots of short requests are empty.
+  uint32_t total, chunk;
+  int32_t* counter;
+  uint32_t base;                 // the chunk after the present one, looked up a run ahead of its use:
+  int next_i, next_y, next_run;  // this lane's slot of it (next_run < 0: none)
+  int next_len;                  // and its request's length
+  uint32_t left;                 // slots of the present chunk that hold a run and are still to come
+  Run mine;                      // this lane's run of it
+  Run r;                         // the run being fetched
+  bool live;                     // there is one
+  int page;                      // lane < KEYS: page of key r.u + lane, on its way during the tile before
+
+  __device__ __forceinline__ void look_ahead(const PagedDecode& a, int parts, int lane) {
+    const uint32_t w = base + (uint32_t)lane, ny = (uint32_t)(a.hkv * parts), rows = (uint32_t)a.N * ny;
+    next_run = -1;
+    if (w >= total || lane >= (int)chunk) return;
+    next_run = (int)(w / rows);
+    const uint32_t v = w - (uint32_t)next_run * rows;
+    next_i = (int)(v / ny);
+    next_y = (int)(v - (uint32_t)next_i * ny);
+    next_len = a.seq_lens[next_i];
+  }
+
+  // The next run of this warp.  Requests without keys have their rows written here.
+  __device__ void seek(const PagedDecode& a, int parts, int lane) {
+    live = false;
+    while (!left) {
+      if (base >= total) return;
+      bool have = false;
+      if (next_run >= 0) {
+        const Request rq(a, next_len);
+        const Split s = split_of(rq.n, a.hkv);
+        mine.i = next_i;
+        mine.y = next_y;
+        mine.run = next_run;
+        mine.runs = s.runs;
+        have = next_run < s.runs;
+        mine.u = (uint32_t)next_run * (uint32_t)s.keys;
+        mine.end = min((uint32_t)rq.n, mine.u + (uint32_t)s.keys);
+        mine.head = rq.head;
+        mine.skip = rq.skip;
+        if (s.runs == 0 && next_run == 0) write_empty(a, mine, parts, rq.bad);
+      }
+      left = __ballot_sync(0xffffffffu, have);
+      int n = 0;
+      if (!counter) base = total;
+      else if (lane == 0) n = atomicAdd(counter, 1);
+      if (counter) base = (gridDim.x * DecodeSmem<E>::WARPS + (uint32_t)__shfl_sync(0xffffffffu, n, 0)) * chunk;
+      look_ahead(a, parts, lane);
+    }
+    const int src = __ffs(left) - 1;
+    left &= left - 1;
+    r.i = __shfl_sync(0xffffffffu, mine.i, src);
+    r.y = __shfl_sync(0xffffffffu, mine.y, src);
+    r.run = __shfl_sync(0xffffffffu, mine.run, src);
+    r.runs = __shfl_sync(0xffffffffu, mine.runs, src);
+    r.u = __shfl_sync(0xffffffffu, mine.u, src);
+    r.end = __shfl_sync(0xffffffffu, mine.end, src);
+    r.head = __shfl_sync(0xffffffffu, mine.head, src);
+    r.skip = __shfl_sync(0xffffffffu, mine.skip, src);
+    live = true;
+  }
+
+  // zeros for a request without keys, NaN for a length that is not valid; one lane
+  __device__ static void write_empty(const PagedDecode& a, const Run& c, int parts, bool bad) {
+    const int group = a.hq / a.hkv, g0 = (c.y % parts) * kHeadsPerRun, heads = min(kHeadsPerRun, group - g0);
+    const int64_t row = (int64_t)c.i * a.hq + (c.y / parts) * group + g0;
+    const float x = bad ? __builtin_nanf("") : 0.f;
+    for (int e = 0; e < heads * E::DIM; e += 4)
+      store4(static_cast<typename E::Elem*>(a.out) + row * E::DIM + e, make_float4(x, x, x, x));
+    if (a.lse)
+      for (int h = 0; h < heads; ++h) a.lse[row + h] = bad ? x : -INFINITY;
+  }
 
   __device__ __forceinline__ bool has_key(int lane) const { return lane < E::KEYS && r.u + lane < r.end; }
 
@@ -420,6 +465,15 @@ struct Walk : Dealer<E> {
       if (live) push(a, parts, queue, tail, lane);
     }
     look_up(a, lane);
+  }
+  // a run that is fetched from here on: at most the computed one, two fetched tiles' and the next are open
+  __device__ __forceinline__ void push(const PagedDecode& a, int parts, Run* queue, int& tail, int lane) {
+    r.bad = 0;
+    if (lane == 0) queue[tail & 3] = r;
+    const int group = a.hq / a.hkv, g0 = (r.y % parts) * kHeadsPerRun, heads = min(kHeadsPerRun, group - g0);
+    const char* q = static_cast<const char*>(a.q) + ((int64_t)r.i * a.hq + (r.y / parts) * group + g0) * E::ROWB;
+    for (int e = lane * 128; e < heads * E::ROWB; e += 32 * 128) tc::prefetch_l2(q + e);
+    ++tail;
   }
 };
 

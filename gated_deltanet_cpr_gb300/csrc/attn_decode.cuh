@@ -1,6 +1,7 @@
-// attn_decode.cuh -- what decode attention over the paged cache and over the 8-bit one share: runs of a request's
-// visible keys are dealt out to warps that work alone, each leaves (m, l, a) or the output, and k_decode_join
-// adds a request's runs in ascending order.
+// attn_decode.cuh -- what decode attention over the paged cache and over the 8-bit one share: a warp takes a run of a
+// request's visible keys and leaves (m, l, a) or the output, and k_decode_join adds a request's runs in ascending
+// order.  An engine E has a Kind with the types Args (the call) and Request (of a length: its runs) and check(), what
+// is wrong with a request's pages, and a type Run.
 #pragma once
 
 #include "attn.h"
@@ -67,97 +68,6 @@ struct DecodeSmem {
   static constexpr int FEW = MOST < E::MOST_WARPS ? MOST : E::MOST_WARPS;
   static constexpr int WARPS = FEW < 8 ? FEW : FEW / 4 * 4, HALF = 116 * 1024;
   static constexpr int BYTES = WARPS * WARP > HALF ? WARPS * WARP : HALF;  // more than half: one CTA per SM
-};
-
-// Which run a warp takes next.  An engine E has a type Request, made from the call and a length (n: its
-// visible units, bad, runs(a)), a type Seed, a lane's run (i, y, run, runs, set(a, request, ahead)), a type Run (i, y,
-// run, runs, units [u, end), from(a, seed, lane)) and a type Ahead, what is read of a request before its turn (len and
-// perhaps more).
-template <typename E>
-struct Dealer {
-  using Args = typename E::Args;
-  using Run = typename E::Run;
-  // (run, request, part) slots are numbered with the run slowest and dealt out in chunks of `chunk`
-  // <= 32 consecutive ones, one per lane: the first by the warp's number, further ones from a
-  // counter, as runs differ in length and many slots of short requests are empty.
-  uint32_t total, chunk;
-  int32_t* counter;
-  uint32_t base;                 // the chunk after the present one, looked up a run ahead of its use:
-  int next_i, next_y, next_run;  // this lane's slot of it (next_run < 0: none)
-  typename E::Ahead next;        // and of its request
-  uint32_t left;                 // slots of the present chunk that hold a run and are still to come
-  typename E::Seed mine;         // this lane's run of it
-  Run r;                         // the run being fetched
-  bool live;                     // there is one
-
-  __device__ __forceinline__ void look_ahead(const Args& a, int parts, int lane) {
-    const uint32_t w = base + (uint32_t)lane, ny = (uint32_t)(a.hkv * parts), rows = (uint32_t)a.N * ny;
-    next_run = -1;
-    if (w >= total || lane >= (int)chunk) return;
-    next_run = (int)(w / rows);
-    const uint32_t v = w - (uint32_t)next_run * rows;
-    next_i = (int)(v / ny);
-    next_y = (int)(v - (uint32_t)next_i * ny);
-    next.load(a, next_i);
-  }
-
-  // lane 0: the number of a further chunk, on its way
-  __device__ __forceinline__ int ask(int lane) const { return counter && lane == 0 ? atomicAdd(counter, 1) : 0; }
-  __device__ __forceinline__ void answer(const Args& a, int parts, int lane, int n) {
-    if (!counter) base = total;
-    else base = (gridDim.x * DecodeSmem<E>::WARPS + (uint32_t)__shfl_sync(0xffffffffu, n, 0)) * chunk;
-    look_ahead(a, parts, lane);
-  }
-  // The runs of the chunk looked up.  Requests without keys have their rows written here.
-  __device__ __forceinline__ void take(const Args& a, int parts) {
-    bool have = false;
-    if (next_run >= 0) {
-      const typename E::Request rq(a, next.len);
-      mine.i = next_i;
-      mine.y = next_y;
-      mine.run = next_run;
-      mine.set(a, rq, next);
-      have = next_run < mine.runs;
-      if (mine.runs == 0 && next_run == 0) write_empty(a, mine, parts, rq.bad);
-    }
-    left = __ballot_sync(0xffffffffu, have);
-  }
-  // The next run of this warp.
-  __device__ void seek(const Args& a, int parts, int lane) {
-    live = false;
-    while (!left) {
-      if (base >= total) return;
-      take(a, parts);
-      answer(a, parts, lane, ask(lane));
-    }
-    begin(a);
-  }
-  __device__ __forceinline__ void begin(const Args& a) {
-    const int src = __ffs(left) - 1;
-    left &= left - 1;
-    r.from(a, mine, src);
-    live = true;
-  }
-
-  // zeros for a request without keys, NaN for a length that is not valid; one lane
-  __device__ static void write_empty(const Args& a, const typename E::Seed& c, int parts, bool bad) {
-    const int group = a.hq / a.hkv, g0 = (c.y % parts) * kHeadsPerRun, heads = min(kHeadsPerRun, group - g0);
-    const int64_t row = (int64_t)c.i * a.hq + (c.y / parts) * group + g0;
-    const float x = bad ? __builtin_nanf("") : 0.f;
-    for (int e = 0; e < heads * E::DIM; e += 4)
-      store4(static_cast<typename E::Elem*>(a.out) + row * E::DIM + e, make_float4(x, x, x, x));
-    if (a.lse)
-      for (int h = 0; h < heads; ++h) a.lse[row + h] = bad ? x : -INFINITY;
-  }
-  // a run that is fetched from here on: at most the computed one, two fetched tiles' and the next are open
-  __device__ __forceinline__ void push(const Args& a, int parts, Run* queue, int& tail, int lane) {
-    r.bad = 0;
-    if (lane == 0) queue[tail & 3] = r;
-    const int group = a.hq / a.hkv, g0 = (r.y % parts) * kHeadsPerRun, heads = min(kHeadsPerRun, group - g0);
-    const char* q = static_cast<const char*>(a.q) + ((int64_t)r.i * a.hq + (r.y / parts) * group + g0) * (E::DIM * (int)sizeof(typename E::Elem));
-    for (int e = lane * 128; e < heads * (E::DIM * (int)sizeof(typename E::Elem)); e += 32 * 128) tc::prefetch_l2(q + e);
-    ++tail;
-  }
 };
 
 // ---------------------------------------------------------------------------- join ----

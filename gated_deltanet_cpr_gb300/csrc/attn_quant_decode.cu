@@ -44,55 +44,15 @@ struct QuantRequest {
   __device__ __forceinline__ int runs(const QuantDecode& a) const { return quant_split(n, a.hkv).runs; }
 };
 
-struct QuantAhead {
-  int len, slot;
-  __device__ __forceinline__ void load(const QuantDecode& a, int i) {
-    len = a.seq_lens[i];
-    slot = a.slot ? a.slot[i] : i;
-  }
-};
-
-// A lane's run, from which all lanes form a QuantRun when its turn comes: few values, as registers are short.
-struct QuantSeed {
-  int i, y, run, runs, len, slot;
-  __device__ __forceinline__ void set(const QuantDecode& a, const QuantRequest& rq, const QuantAhead& ahead) {
-    runs = rq.runs(a);
-    len = rq.len;
-    slot = ahead.slot;
-  }
-};
-// Granules [u, end) of request i, those from `tail` on in its tail; only granules edge - 1 and edge of the others can hold
-// keys that are not visible; bad: a page or the slot is outside the cache.
+// A run as the computing side needs it; bad: a page or the slot is outside the cache.
 struct QuantRun {
-  int i, y, run, runs;
-  uint32_t u, end, tail, edge;
-  int head, skip, len, slot, bad;
-  __device__ __forceinline__ int granule(uint32_t x) const { return (int)x < head ? (int)x : (int)x + skip; }
-  __device__ __forceinline__ void from(const QuantDecode& a, const QuantSeed& o, int lane) {
-    i = __shfl_sync(0xffffffffu, o.i, lane);
-    y = __shfl_sync(0xffffffffu, o.y, lane);
-    run = __shfl_sync(0xffffffffu, o.run, lane);
-    len = __shfl_sync(0xffffffffu, o.len, lane);
-    slot = __shfl_sync(0xffffffffu, o.slot, lane);
-    const QuantRequest rq(a, len);
-    const Split s = quant_split(rq.n, a.hkv);
-    runs = s.runs;
-    u = (uint32_t)run * (uint32_t)s.keys;
-    end = min((uint32_t)rq.n, u + (uint32_t)s.keys);
-    head = rq.head;
-    skip = rq.skip;
-    edge = a.window > 0 && len > a.window ? (uint32_t)head : 1u << 30;
-    const int g = (len >> a.c.block_shift) << (a.c.block_shift - kGranuleShift);  // first granule of the tail
-    tail = (uint32_t)(g <= head ? g : max(head, g - skip));
-  }
+  int i, y, run, runs, len, slot, bad;
 };
 
 struct Quant {
   using Kind = Quant;
   using Args = QuantDecode;
   using Request = QuantRequest;
-  using Ahead = QuantAhead;
-  using Seed = QuantSeed;
   using Run = QuantRun;
   // a page of the request's visible whole blocks, or its tail's slot, is outside the cache
   __device__ __forceinline__ static int check(const QuantDecode& a, const QuantRequest& rq, int i, int tid, int threads) {
@@ -639,63 +599,128 @@ struct QuantEngine : Quant {
 };
 
 // --------------------------------------------------------------------------- walk ----
-// The fetching side of a warp: which tile comes next, and where its rows lie.  It leaves what the computing side needs to
-// know beside the rows, so that only one of them walks.
+// The fetching side of a warp: which run it takes, which tile comes next, and where its rows lie.  It leaves what the computing
+// side needs to know beside the rows, so that only one of them walks, and keeps few values, as registers are short: with 38
+// instead of 19 the kernel's 168 registers held 17% more instructions.
 template <typename E>
-struct QuantWalk : Dealer<E> {
-  using Dealer<E>::r;
-  using Dealer<E>::live;
-  using Dealer<E>::push;
-  // A further chunk is asked for when the present run comes to its end, so that a warp on a long one does not
-  // keep it from others, in two steps a tile apart (a number from the counter, then its requests' lengths).
+struct QuantWalk {
+  // (run, request, part) slots are numbered with the run slowest and dealt out in chunks of `chunk` <= 32 consecutive ones,
+  // one per lane: the first by the warp's number, further ones from a counter, as runs differ in length and many slots
+  // of short requests are empty.  A further chunk is asked for when the present run comes to its end, so that a warp on a
+  // long one does not keep it from others, in two steps a tile apart (a number from the counter, then its requests' lengths).
+  uint32_t total, chunk;
+  int32_t* counter;
   enum { kNone, kAsked, kKnown } more;
-  int number;
+  uint32_t slot_no;  // this lane's of the chunk (total or more: none), or lane 0's number from the counter
+  int len, slot;     // its request's length and tail
+  uint32_t left;     // lanes of the chunk whose runs are still to come
+  // the run being fetched: granules [u, end), those from `tail` on in its tail; only granules edge - 1 and edge of the others
+  // can hold keys that are not visible; granule number x lies `skip` further on from `head` on; of key head h
+  bool live;
+  uint32_t u, end, tail, edge;
+  int head, skip, h;
   uint32_t first;  // pages are looked up for 32 granules at once, one a lane: those from this one on
   int page;        // this lane's
   int sub;         // rows of the tail's granule that earlier tiles took
 
-  __device__ __forceinline__ void look_up(const QuantDecode& a, int lane) {
-    first = r.u;
-    page = 0;
-    if (r.u + lane >= min(r.end, r.tail)) return;
-    const int b = (int)(((uint32_t)r.granule(r.u + lane) << kGranuleShift) >> a.page_shift);
-    page = b < a.max_blocks ? a.block_table[(int64_t)r.i * a.max_blocks + b] : -1;
+  __device__ __forceinline__ int granule(uint32_t x) const { return (int)x < head ? (int)x : (int)x + skip; }
+
+  __device__ __forceinline__ void look_ahead(const QuantDecode& a, int parts, uint32_t base, int lane) {
+    slot_no = lane < (int)chunk ? base + (uint32_t)lane : total;
+    more = kKnown;
+    if (slot_no >= total) return;
+    const uint32_t ny = (uint32_t)(a.hkv * parts);
+    const int i = (int)(slot_no % ((uint32_t)a.N * ny) / ny);
+    len = a.seq_lens[i];
+    slot = a.slot ? a.slot[i] : i;
   }
   __device__ __forceinline__ void prepare(const QuantDecode& a, int parts, int lane) {
     if (more == kNone) {
-      number = this->ask(lane);
+      if (counter && lane == 0) slot_no = (uint32_t)atomicAdd(counter, 1);
       more = kAsked;
     } else if (more == kAsked) {
-      this->answer(a, parts, lane, number);
-      more = kKnown;
+      const uint32_t n = __shfl_sync(0xffffffffu, slot_no, 0);
+      look_ahead(a, parts, counter ? (gridDim.x * DecodeSmem<E>::WARPS + n) * chunk : total, lane);
     }
   }
-  // the first run, or the one after r
-  __device__ __forceinline__ void next_run(const QuantDecode& a, int parts, int lane, QuantRun* queue, int& tail) {
+  __device__ __forceinline__ void look_up(const QuantDecode& a, int lane, const QuantRun& r) {
+    first = u;
+    page = 0;
+    if (u + lane >= min(end, tail)) return;
+    const int b = (int)(((uint32_t)granule(u + lane) << kGranuleShift) >> a.page_shift);
+    page = b < a.max_blocks ? a.block_table[(int64_t)r.i * a.max_blocks + b] : -1;
+  }
+  // The first run, or the next one: to the queue, which holds at most the computed one, those of RING - 1 tiles ahead and
+  // this.  Requests without keys have their rows written here.
+  __device__ void next_run(const QuantDecode& a, int parts, int lane, QuantRun* queue, int& put) {
     live = false;
-    while (!this->left) {
+    const uint32_t ny = (uint32_t)(a.hkv * parts), rows = (uint32_t)a.N * ny;
+    while (!left) {
       while (more != kKnown) prepare(a, parts, lane);
-      if (this->base >= this->total) return;
-      this->take(a, parts);
+      if (__shfl_sync(0xffffffffu, slot_no, 0) >= total) return;
+      bool have = false;
+      if (slot_no < total) {
+        const QuantRequest rq(a, len);
+        const int run = (int)(slot_no / rows), runs = rq.runs(a);
+        have = run < runs;
+        if (runs == 0 && run == 0) write_empty(a, (int)(slot_no % rows / ny), (int)(slot_no % ny), parts, rq.bad);
+      }
+      left = __ballot_sync(0xffffffffu, have);
       more = kNone;
     }
-    this->begin(a);
-    push(a, parts, queue, tail, lane);
-    look_up(a, lane);
+    const int src = __ffs(left) - 1;
+    left &= left - 1;
+    const uint32_t w = __shfl_sync(0xffffffffu, slot_no, src);
+    QuantRun r;
+    r.run = (int)(w / rows);
+    r.i = (int)(w % rows / ny);
+    r.y = (int)(w % ny);
+    r.len = __shfl_sync(0xffffffffu, len, src);
+    r.slot = __shfl_sync(0xffffffffu, slot, src);
+    r.bad = 0;
+    const QuantRequest rq(a, r.len);
+    const Split s = quant_split(rq.n, a.hkv);
+    r.runs = s.runs;
+    live = true;
+    u = (uint32_t)r.run * (uint32_t)s.keys;
+    end = min((uint32_t)rq.n, u + (uint32_t)s.keys);
+    head = rq.head;
+    skip = rq.skip;
+    edge = a.window > 0 && r.len > a.window ? (uint32_t)head : 1u << 30;
+    const int g = (r.len >> a.c.block_shift) << (a.c.block_shift - kGranuleShift);  // first granule of the tail
+    tail = (uint32_t)(g <= head ? g : max(head, g - skip));
+    h = r.y / parts;
     sub = 0;
+    if (lane == 0) queue[put & 3] = r;
+    ++put;
+    look_up(a, lane, r);
+    const int group = a.hq / a.hkv, g0 = (r.y % parts) * kHeadsPerRun, heads = min(kHeadsPerRun, group - g0);
+    constexpr int ROW = E::DIM * (int)sizeof(typename E::Elem);
+    const char* q = static_cast<const char*>(a.q) + ((int64_t)r.i * a.hq + h * group + g0) * ROW;
+    for (int e = lane * 128; e < heads * ROW; e += 32 * 128) tc::prefetch_l2(q + e);
+    __syncwarp();
+  }
+  // zeros for a request without keys, NaN for a length that is not valid; one lane
+  __device__ static void write_empty(const QuantDecode& a, int i, int y, int parts, bool bad) {
+    const int group = a.hq / a.hkv, g0 = (y % parts) * kHeadsPerRun, heads = min(kHeadsPerRun, group - g0);
+    const int64_t row = (int64_t)i * a.hq + (y / parts) * group + g0;
+    const float x = bad ? __builtin_nanf("") : 0.f;
+    for (int e = 0; e < heads * E::DIM; e += 4)
+      store4(static_cast<typename E::Elem*>(a.out) + row * E::DIM + e, make_float4(x, x, x, x));
+    if (a.lse)
+      for (int k = 0; k < heads; ++k) a.lse[row + k] = bad ? x : -INFINITY;
   }
 
   // The current tile into `stage`, then on to the next one.
-  __device__ __forceinline__ void fetch(const QuantDecode& a, int parts, unsigned char* stage, int lane, QuantRun* queue, int& tail) {
+  __device__ __forceinline__ void fetch(const QuantDecode& a, int parts, unsigned char* stage, int lane, QuantRun* queue, int& put) {
     if (live) {
-      if (!this->left && r.end - r.u <= 3 * E::T) prepare(a, parts, lane);
+      if (!left && end - u <= 3 * E::T) prepare(a, parts, lane);
       const uint32_t st = tc::smem_u32(stage);
-      const int h = parts == 1 ? r.y : r.y / parts;
-      int key = r.granule(r.u) << kGranuleShift, what, skip_from = E::T;
-      if (r.u < r.tail) {
-        const uint32_t stop = min(r.end, r.tail);
-        const int n = (int)min((uint32_t)E::T, stop - r.u);
-        if (r.u - first + n > 32) look_up(a, lane);
+      int key = granule(u) << kGranuleShift, what, skip_from = E::T;
+      if (u < tail) {
+        const uint32_t stop = min(end, tail);
+        const int n = (int)min((uint32_t)E::T, stop - u);
+        if (u - first + n > 32) look_up(a, lane, queue[(put - 1) & 3]);
         const bool lost = (uint32_t)page >= (uint32_t)a.c.num_pages && first + lane < stop;
         if (!__any_sync(0xffffffffu, lost)) {
           constexpr int PIECES = E::ROWB / 16;
@@ -707,8 +732,8 @@ struct QuantWalk : Dealer<E> {
 #pragma unroll
           for (int i = 0; i < E::T; ++i) {
             if (i >= n) break;
-            const uint32_t at = (uint32_t)__shfl_sync(0xffffffffu, page, r.u - first + i) * (uint32_t)a.hkv + (uint32_t)h;
-            const uint32_t row = (at << a.page_shift) + (((uint32_t)r.granule(r.u + i) << kGranuleShift) & mask);
+            const uint32_t at = (uint32_t)__shfl_sync(0xffffffffu, page, u - first + i) * (uint32_t)a.hkv + (uint32_t)h;
+            const uint32_t row = (at << a.page_shift) + (((uint32_t)granule(u + i) << kGranuleShift) & mask);
             rows = lane % E::T == i ? row : rows;
             const int64_t off = (int64_t)row * E::ROWB + 16 * lane;
             const uint8_t *kp = a.c.k_pages + off, *vp = a.c.v_pages + off;
@@ -731,38 +756,39 @@ struct QuantWalk : Dealer<E> {
           if (lane < 2 * E::T && lane % E::T < n)
             copy4(st + 2 * E::SIDE + 4 * lane, (lane < E::T ? a.c.k_scale : a.c.v_scale) + (rows >> a.c.block_shift));
         } else if (lane == 0) {
-          queue[(tail - 1) & 3].bad = 1;  // the tile holds what it held: the run's results are NaN
+          queue[(put - 1) & 3].bad = 1;  // the tile holds what it held: the run's results are NaN
         }
-        what = n + (r.u + (uint32_t)n - r.edge <= (uint32_t)n ? E::kEdge : 0);  // it holds granule edge - 1 or edge
-        if (r.u < (uint32_t)r.head) skip_from = min(E::T, r.head - (int)r.u);
-        r.u += n;
+        what = n + (u + (uint32_t)n - edge <= (uint32_t)n ? E::kEdge : 0);  // it holds granule edge - 1 or edge
+        if (u < (uint32_t)head) skip_from = min(E::T, head - (int)u);
+        u += n;
       } else {
         // only rows that are visible: what else the tail holds is nobody's
+        const QuantRun& r = queue[(put - 1) & 3];
+        const int n = r.len, B = 1 << a.c.block_shift, lo = a.window > 0 ? n - a.window : 0;
         const bool lost = r.slot < 0 || r.slot >= a.c.slots;
-        const int B = 1 << a.c.block_shift, lo = a.window > 0 ? r.len - a.window : 0;
         key += sub;
         const int64_t off = lost ? 0 : (((int64_t)r.slot * a.hkv + h) * B + (key & (B - 1))) * E::TAILB;
         constexpr int PIECES = E::TAIL_ROWS * E::TAILB / 16, PER = E::TAILB / 16;
 #pragma unroll 4
         for (int p = lane; p < PIECES; p += 32) {
           const int k = key + p / PER;
-          const bool load = !lost && k < r.len && (k >= lo || k < a.sinks);
+          const bool load = !lost && k < n && (k >= lo || k < a.sinks);
           const uint32_t dst = st + E::place_tail(p / PER, p % PER);
           const int64_t from = load ? off + 16 * p : 0;
           cp_async16_or_zero(dst, static_cast<const char*>(a.c.k_tail) + from, load);
           cp_async16_or_zero(dst + E::SIDE, static_cast<const char*>(a.c.v_tail) + from, load);
         }
-        if (lost && lane == 0) queue[(tail - 1) & 3].bad = 1;
+        if (lost && lane == 0) queue[(put - 1) & 3].bad = 1;
         what = 0;
         sub += E::TAIL_ROWS;
-        if (sub == kGranule || key + E::TAIL_ROWS >= r.len) sub = 0, ++r.u;
+        if (sub == kGranule || key + E::TAIL_ROWS >= n) sub = 0, ++u;
       }
       if (lane == 0) {
         typename E::Meta& meta = *reinterpret_cast<typename E::Meta*>(stage + 2 * E::SIDE);
         *reinterpret_cast<int4*>(&meta.key) =
-            make_int4(key, what + (r.u >= r.end ? E::kLast : 0), r.skip << kGranuleShift, skip_from);
+            make_int4(key, what + (u >= end ? E::kLast : 0), skip << kGranuleShift, skip_from);
       }
-      if (r.u >= r.end) next_run(a, parts, lane, queue, tail);
+      if (u >= end) next_run(a, parts, lane, queue, put);
     }
     tc::cp_async_commit();
   }
@@ -784,11 +810,9 @@ __global__ void __launch_bounds__(32 * DecodeSmem<E>::WARPS, 1) k_quant_decode(c
   f.total = (uint32_t)(a.N * a.hkv * parts * a.max_splits);
   f.chunk = chunk;
   f.counter = counter;
-  f.base = ((threadIdx.x >> 5) * gridDim.x + blockIdx.x) * chunk;
   f.left = 0;
-  f.more = QuantWalk<E>::kKnown;
   int head = 0, tail = 0, put = 0, get = 0;
-  f.look_ahead(a, parts, lane);
+  f.look_ahead(a, parts, ((threadIdx.x >> 5) * gridDim.x + blockIdx.x) * chunk, lane);
   if (counter) asm volatile("griddepcontrol.wait;" ::: "memory");  // it has been cleared
   f.next_run(a, parts, lane, queue, tail);
 #pragma unroll 1
