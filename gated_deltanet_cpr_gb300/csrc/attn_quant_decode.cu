@@ -165,8 +165,7 @@ __device__ __forceinline__ void widen16(uint32_t four, uint32_t& first, uint32_t
 // A tile is up to T granules of the pages, or up to TAIL_ROWS rows of a granule of the tail.  NH column tiles of 8 heads.
 // Lane (g, t) = (lane / 4, lane % 4) holds of scores^T keys g, g + 8 of a granule for heads 2 t, 2 t + 1, of out^T columns
 // 16 j + 2 g, + 1 for them.  The MMAs' inner order is free as long as both operands agree: k-steps of 16 take columns 16 s +
-// 4 t .. + 3 of lane t, so that a lane's four codes of a row are one register of a matrix load.  Granules are gone
-// through in pairs, whose chains of loads, conversions and products overlap.
+// 4 t .. + 3 of lane t, so that a lane's four codes of a row are one register of a matrix load.
 template <int D, typename T_, int NH, bool E4M3>
 struct QuantEngine : Quant {
   using Elem = T_;
@@ -186,10 +185,12 @@ struct QuantEngine : Quant {
   };
   static_assert(sizeof(Meta) <= 128 && (2 * SIDE) % 128 == 0 && STAGE % 128 == 0, "key is stored with the three behind it, 16 bytes");
   static constexpr int kLast = 64, kEdge = 128;  // the run's last tile; some keys may not be visible
-  // 12 warps with a tile on its way take 256 requests of about 2112 tokens in 200 us, 8 with two in 206, 16 with a granule a
-  // tile (128 registers) in 216; 16 heads and fp32 need more registers than 168 a thread
-  static constexpr bool MANY_REGS = SPLIT || NH == 2;
-  static constexpr int MOST_WARPS = MANY_REGS ? 8 : 12, RING = MANY_REGS ? 3 : 2;
+  // Granules are gone through one by one: the instructions of two at a time (198 us for 256 requests of about 2112 tokens
+  // against 193, fp32 window case 32.7 against 27.3) overflow the nearest cache.  Two column tiles have more in flight
+  // by themselves and gain from pairs (48.7 against 49.8), but need more registers than 12 warps leave.  12 warps with a tile on its way take
+  // those 256 requests in 193 us, 8 with two 206, 16 with tiles of one granule 209.
+  static constexpr bool PAIRS = NH == 2 && !SPLIT;
+  static constexpr int MOST_WARPS = NH == 2 ? 8 : 12, RING = NH == 2 ? 3 : 2;
   static_assert(RING <= 3, "the queue holds four runs: the computed one, those of RING - 1 tiles ahead and the next");
   static constexpr int KS = D / 16, P = 1 + SPLIT;  // steps, parts of a split value
 
@@ -600,8 +601,8 @@ struct QuantEngine : Quant {
 
 // --------------------------------------------------------------------------- walk ----
 // The fetching side of a warp: which run it takes, which tile comes next, and where its rows lie.  It leaves what the computing
-// side needs to know beside the rows, so that only one of them walks, and keeps few values, as registers are short: with 38
-// instead of 19 the kernel's 168 registers held 17% more instructions.
+// side needs to know beside the rows, so that only one of them walks, and keeps few values, as registers are short (38 instead of 19:
+// 10% more instructions).
 template <typename E>
 struct QuantWalk {
   // (run, request, part) slots are numbered with the run slowest and dealt out in chunks of `chunk` <= 32 consecutive ones,
@@ -843,9 +844,14 @@ __global__ void __launch_bounds__(32 * DecodeSmem<E>::WARPS, 1) k_quant_decode(c
       if (n) {
         const bool full = !(what & E::kEdge);
         int i = 0;
+        if constexpr (E::PAIRS) {
 #pragma unroll 1
-        for (; i + 2 <= n; i += 2) eng.template granules<2>(a, stage, i, full, len, lane);
-        if (i < n) eng.template granules<1>(a, stage, i, full, len, lane);
+          for (; i + 2 <= n; i += 2) eng.template granules<2>(a, stage, i, full, len, lane);
+          if (i < n) eng.template granules<1>(a, stage, i, full, len, lane);
+        } else {
+#pragma unroll 1
+          for (; i < n; ++i) eng.template granules<1>(a, stage, i, full, len, lane);
+        }
       } else {
         if constexpr (E::SPLIT) eng.tail_f32(a, stage, meta.key, len, lane);
         else eng.tail_bf16(a, stage, meta.key, len, lane);
