@@ -101,9 +101,11 @@ __device__ void check_requests(const QuantRows& a) {
 }
 
 // ------------------------------------------------------------------------- rounding ----
-// Codes of an int8 block: the quotient 127 x / m is rounded as it is in exact arithmetic.  x fl(127 / m) is
-// within 2^-17 of it, so only one that close to a half needs more (2 or 3 of 2048 normal values in bf16): there the sign of 254 x - (2 k + 1) m decides, which
-// the two products and what their rounding lost give exactly.
+// Codes of an int8 block: the quotient 127 x / m is rounded as it is in exact arithmetic.  inv is 127 / m rounded up, so that x inv
+// is the quotient or up to 2^-23 of it more (in magnitude), and only one that rounds up from next to a half can be wrong.  There the sign
+// of 254 x - (2 k + 1) m decides, which the two products and what their rounding lost give exactly.  In bf16 a
+// quotient that is no half lies 2^-16 of itself or more away from one (254 x has 16 bits), so such an x inv is a half, which
+// belongs to the even side: mostly x = m / 2, 63.5, which 2 or 3 of 2048 normal values are, and 64 is right.
 struct Rounder {
   float inv, m, scale;  // scale: what the block stores
   float down;           // keeps the products of the exact comparison finite
@@ -125,7 +127,7 @@ struct Rounder {
       inv = __uint_as_float((uint32_t)(254 - e) << 23);
     } else {
       scale = __fdiv_rn(m, 127.f);
-      inv = __fdiv_rn(127.f, m);
+      inv = __fdiv_ru(127.f, m);
       if (m > 0x1p100f) down = 0x1p-20f;
     }
   }
@@ -141,6 +143,7 @@ struct Rounder {
     return fabsf(d) > kNear && (diff > 0.f || (diff == 0.f && ((int)r & 1))) ? __fadd_rn(y, s) : y;
   }
   // codes of 4 values, pairs (x0, x1) and (x2, x3)
+  template <bool BF16>
   __device__ __forceinline__ uint32_t four(const float2 (&x)[2]) const {
     if (m == 0.f) return 0u;
     if (e4m3) {
@@ -158,10 +161,16 @@ struct Rounder {
       const float2 r = fma2(y[i], one, make_float2(-kMagic, -kMagic));
       d[i] = fma2(x[i], i2, make_float2(-r.x, -r.y));  // what the rounding took off
     }
-    if (fmaxf(fmaxf(fabsf(d[0].x), fabsf(d[0].y)), fmaxf(fabsf(d[1].x), fabsf(d[1].y))) > kNear)
+    if (fmaxf(fmaxf(fabsf(d[0].x), fabsf(d[0].y)), fmaxf(fabsf(d[1].x), fabsf(d[1].y))) > kNear &&
+        (doubtful<BF16>(y[0].x, d[0].x) || doubtful<BF16>(y[0].y, d[0].y) || doubtful<BF16>(y[1].x, d[1].x) ||
+         doubtful<BF16>(y[1].y, d[1].y)))
       return settled(make_float4(x[0].x, x[0].y, x[1].x, x[1].y), make_float4(d[0].x, d[0].y, d[1].x, d[1].y),
                      make_float4(y[0].x, y[0].y, y[1].x, y[1].y), m, down);
     return bytes(y[0].x, y[0].y, y[1].x, y[1].y);
+  }
+  template <bool BF16>
+  __device__ __forceinline__ static bool doubtful(float y, float d) {
+    return fabsf(d) > kNear && (!BF16 || (__float_as_uint(y) & 1u));
   }
   // the last bytes of four sums with kMagic
   __device__ __forceinline__ static uint32_t bytes(float y0, float y1, float y2, float y3) {
@@ -194,8 +203,8 @@ struct Vec<__nv_bfloat16> {
   }
   __device__ __forceinline__ static void store(const Rounder& r, const uint4& u, uint8_t* to) {
     uint2 o;
-    o.x = r.four({pair(u.x), pair(u.y)});
-    o.y = r.four({pair(u.z), pair(u.w)});
+    o.x = r.four<true>({pair(u.x), pair(u.y)});
+    o.y = r.four<true>({pair(u.z), pair(u.w)});
     *reinterpret_cast<uint2*>(to) = o;
   }
 };
@@ -208,7 +217,7 @@ struct Vec<float> {
   __device__ __forceinline__ static uint32_t bits(uint32_t m) { return m; }
   __device__ __forceinline__ static void store(const Rounder& r, const uint4& u, uint8_t* to) {
     *reinterpret_cast<uint32_t*>(to) =
-        r.four({make_float2(__uint_as_float(u.x), __uint_as_float(u.y)), make_float2(__uint_as_float(u.z), __uint_as_float(u.w))});
+        r.four<false>({make_float2(__uint_as_float(u.x), __uint_as_float(u.y)), make_float2(__uint_as_float(u.z), __uint_as_float(u.w))});
   }
 };
 
