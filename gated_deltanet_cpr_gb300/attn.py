@@ -89,22 +89,23 @@ class QuantCache:
         return c
 
     def _set(self, k, v, k_scale, v_scale, k_tail, v_tail):
-        pages, tails, code = k.shape, k_tail.shape, _CODE_OF.get(k.dtype)
+        pages, tails, codes, dtype, at = k.shape, k_tail.shape, k.dtype, k_tail.dtype, k.device
         if len(pages) != 4 or len(tails) != 4:
             raise ValueError("pages are [pages, H_kv, page_size, d], tails [slots, H_kv, block, d]")
-        self.pages, self.h_kv, self.page_size, self.d = pages
-        self.slots, hkv, block, d = tails
-        if code is None or block <= 0 or self.page_size % block or hkv != self.h_kv or d != self.d:
+        n, hkv, page_size, d = pages
+        slots, tail_heads, block, tail_d = tails
+        code = _CODE_OF.get(codes)
+        if code is None or block <= 0 or page_size % block or tail_heads != hkv or tail_d != d:
             raise ValueError("pages hold int8 or float8_e4m3fn codes of whole blocks of the tails' heads and size")
-        self.block = block
+        self.pages, self.h_kv, self.page_size, self.d, self.slots, self.block = n, hkv, page_size, d, slots, block
         self.k, self.v, self.k_scale, self.v_scale, self.k_tail, self.v_tail = k, v, k_scale, v_scale, k_tail, v_tail
-        self.dtype, self.device = dtype, at = k_tail.dtype, k.device
-        scales, f32 = (self.pages, hkv, self.page_size // block), torch.float32
+        self.dtype, self.device = dtype, at
+        scales, f32 = (n, hkv, page_size // block), torch.float32
         self.struct = QuantCacheStruct(
-            self.pages, self.page_size, block, self.slots, hkv, d, code, _dt(dtype),
-            _want(k, pages, k.dtype, "k pages"), _want_on(v, pages, k.dtype, "v pages", at),
-            _want_on(k_scale, scales, f32, "k_scale", at), _want_on(v_scale, scales, f32, "v_scale", at),
-            _want_on(k_tail, tails, dtype, "k_tail", at), _want_on(v_tail, tails, dtype, "v_tail", at))
+            n, page_size, block, slots, hkv, d, code, _dt(dtype), _want(k, pages, codes, "k pages"),
+            _at(v, pages, codes, "v pages", at), _at(k_scale, scales, f32, "k_scale", at),
+            _at(v_scale, scales, f32, "v_scale", at), _at(k_tail, tails, dtype, "k_tail", at),
+            _at(v_tail, tails, dtype, "v_tail", at))
         self._ref = ctypes.byref(self.struct)
 
 
@@ -136,11 +137,13 @@ def _want(x, shape, dtype, name):
     return x.data_ptr()
 
 
-def _want_on(x, shape, dtype, name, device):
-    """_want, of a tensor on that device."""
+def _at(x, shape, dtype, name, device):
+    """Pointer of a contiguous tensor of that shape and dtype on an 8-bit cache's device."""
+    if x.dtype is dtype and x.device == device and x.shape == shape and x.is_contiguous():
+        return x.data_ptr()
     if x.device != device:
         raise ValueError(f"{name} is on {x.device}, the cache on {device}")
-    return _want(x, shape, dtype, name)
+    return _want(x, shape, dtype, name)  # says what is wrong
 
 
 def _opt(x, shape, dtype, name):
@@ -342,15 +345,22 @@ def _quant_requests(cache, block_table, seq_lens, slots):
     device = cache.device
     if device.index != _current_device():
         raise ValueError(f"the cache is on {device}, which is not the current device")
-    N, table = seq_lens.numel(), block_table.shape
-    if len(table) != 2 or table[0] != N:
-        raise ValueError("block_table is [N, max_blocks]")
-    i32 = torch.int32
-    if slots is None and N > cache.slots:
+    n, table, i32 = seq_lens.shape, block_table.shape, torch.int32
+    if len(n) != 1 or len(table) != 2 or table[0] != n[0]:
+        raise ValueError("seq_lens is [N], block_table [N, max_blocks]")
+    N, width = table
+    if slots is not None:
+        slots = _at(slots, n, i32, "slots", device)
+    elif N > cache.slots:
         raise ValueError(f"{N} requests, and the cache has {cache.slots} tails")
-    return (N, _want_on(block_table, table, i32, "block_table", device), table[1],
-            _want_on(seq_lens, (N,), i32, "seq_lens", device),
-            None if slots is None else _want_on(slots, (N,), i32, "slots", device))
+    return N, _at(block_table, table, i32, "block_table", device), width, _at(seq_lens, n, i32, "seq_lens", device), slots
+
+
+@functools.lru_cache(maxsize=4096)
+def _quant_desc(N, max_len, *desc):
+    """The description of a decode call's heads, by reference, and its workspace size."""
+    st = ctypes.byref(_attn_struct(*desc))
+    return st, _bytes("gdn_cpr_quant_decode_workspace_size", st, N, max_len)
 
 
 def quant_append(k, v, cache: QuantCache, block_table, seq_lens, cu_seqlens, *, slots=None, ws=None):
@@ -368,7 +378,7 @@ def quant_append(k, v, cache: QuantCache, block_table, seq_lens, cu_seqlens, *, 
     vp, vs = _rows(v, hkv, cache.d, "v")
     wp, nbytes = (None, 0) if ws is None else (ws.data_ptr(), ws.numel())
     _check("gdn_cpr_quant_append", api.load().gdn_cpr_quant_append(
-        cache._ref, N, T, kp, vp, ks, vs, _want_on(cu_seqlens, (N + 1,), torch.int32, "cu_seqlens", device), lens, table,
+        cache._ref, N, T, kp, vp, ks, vs, _at(cu_seqlens, (N + 1,), torch.int32, "cu_seqlens", device), lens, table,
         width, slot, wp, nbytes, _raw_stream(device.index)))
 
 
@@ -388,15 +398,15 @@ def quant_read(cache: QuantCache, block_table, seq_lens, cu_seqlens, total_token
         k_out = torch.empty(shape, dtype=od, device=device)
         kp = k_out.data_ptr()
     else:
-        kp = _want_on(k_out, shape, od, "k_out", device)
+        kp = _at(k_out, shape, od, "k_out", device)
     if v_out is None:
         v_out = torch.empty(shape, dtype=od, device=device)
         vp = v_out.data_ptr()
     else:
-        vp = _want_on(v_out, shape, od, "v_out", device)
+        vp = _at(v_out, shape, od, "v_out", device)
     wp, nbytes = (None, 0) if ws is None else (ws.data_ptr(), ws.numel())
     _check("gdn_cpr_quant_read", api.load().gdn_cpr_quant_read(
-        cache._ref, N, T, _want_on(cu_seqlens, (N + 1,), torch.int32, "cu_seqlens", device), lens, table, width, slot,
+        cache._ref, N, T, _at(cu_seqlens, (N + 1,), torch.int32, "cu_seqlens", device), lens, table, width, slot,
         _dt(od), kp, vp, wp, nbytes, _raw_stream(device.index)))
     return k_out, v_out
 
@@ -408,7 +418,7 @@ def quant_decode(q, cache: QuantCache, block_table, seq_lens, *, slots=None, win
     with want_lse."""
     shape, dtype, device = q.shape, q.dtype, cache.device
     N, hq, d = shape
-    qp = _want_on(q, (N, hq, cache.d), cache.dtype, "q", device)
+    qp = _at(q, (N, hq, cache.d), cache.dtype, "q", device)
     n, table, width, lens, slot = _quant_requests(cache, block_table, seq_lens, slots)
     if n != N:
         raise ValueError("q has a row and seq_lens a length for every request")
@@ -416,18 +426,20 @@ def quant_decode(q, cache: QuantCache, block_table, seq_lens, *, slots=None, win
         max_len = width * cache.page_size
     if not 0 <= max_len < 2 ** 31:
         max_len = _clip(max_len)
-    desc = (hq, cache.h_kv, d, window, sinks, scale, dtype)
+    desc, nbytes = _quant_desc(N, max_len, hq, cache.h_kv, d, window, sinks, scale, dtype)
     if out is None:
         out = torch.empty_like(q)
         op = out.data_ptr()
     else:
-        op = _want_on(out, shape, dtype, "out", device)
+        op = _at(out, shape, dtype, "out", device)
     lse = torch.empty((N, hq), dtype=torch.float32, device=device) if want_lse else None
     if ws is None:
-        ws = _workspace(q, _attn_bytes("gdn_cpr_quant_decode_workspace_size", *desc, N, max_len))
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    else:
+        nbytes = ws.numel()
     _check("gdn_cpr_quant_decode", api.load().gdn_cpr_quant_decode(
-        ctypes.byref(_attn_struct(*desc)), cache._ref, N, max_len, qp, table, width, lens, slot, op,
-        None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.numel(), _raw_stream(device.index)))
+        desc, cache._ref, N, max_len, qp, table, width, lens, slot, op, None if lse is None else lse.data_ptr(),
+        ws.data_ptr(), nbytes, _raw_stream(device.index)))
     return (out, lse) if want_lse else out
 
 
