@@ -2,10 +2,10 @@
 // written, and reading cached ones back into packed rows.
 //
 // Both kernels move every byte once.  Reading is bound by DRAM: 282 thousand rows of 4 heads, d = 128, 869 MB, in 133 us, 6.5 TB/s
-// (98% of a copy's rate).  Writing is bound by instructions, about 900 for the 2048 values of a block, half of them its rounding, and
-// by the chain of dependent loads that a warp makes for one unit (offsets, lengths, rows): 16384 tokens of 8 heads, 101 MB, in 31 us.
-// A warp that took several units after one search was slower (40 to 45 us: more registers, fewer warps).  Short calls are
-// launch and that chain: 256 single tokens 9.4 us, 23 chunks 5.7.  The position-aligned pieces of the requests are numbered so
+// (98% of a copy's rate).  Writing is bound by instructions, about 650 for the 2048 values of a block, and by the chain of dependent loads
+// that a warp makes for one unit (offsets, lengths, rows): 16384 tokens of 8 heads, 101 MB, in 20 us, 5.1 TB/s.
+// A warp that took several units after one search was slower (more registers, fewer warps).  Short calls are
+// launch and that chain: 256 single tokens 5.1 us, 23 chunks 5.1.  The position-aligned pieces of the requests are numbered so
 // that a warp finds its request with one search of the offsets, 32 of them at a time.
 #include "attn_quant.h"
 
@@ -102,15 +102,15 @@ __device__ void check_requests(const QuantRows& a) {
 
 // ------------------------------------------------------------------------- rounding ----
 // Codes of an int8 block: the quotient 127 x / m is rounded as it is in exact arithmetic.  inv is 127 / m rounded up, so that x inv
-// is the quotient or up to 2^-23 of it more (in magnitude), and only one that rounds up from next to a half can be wrong.  There the sign
-// of 254 x - (2 k + 1) m decides, which the two products and what their rounding lost give exactly.  In bf16 a
-// quotient that is no half lies 2^-16 of itself or more away from one (254 x has 16 bits), so such an x inv is a half, which
-// belongs to the even side: mostly x = m / 2, 63.5, which 2 or 3 of 2048 normal values are, and 64 is right.
+// is the quotient or up to 2^-23 of it more (in magnitude), and one fma rounds it to a whole number.  In bf16 that is right as it
+// stands, in three cases, with X and M the 8-bit significands of x and m.  A quotient that is no half lies 2^-16 of itself or more away from
+// one, 254 X 2^t and odd M 2^u being whole numbers of 16 bits.  One that is a half, 254 x = odd m, has a 127 in odd or in M: 63.5 goes
+// up to 64, which is even; M = 254 makes 127 / m a power of two, and a half goes to even by itself.  In fp32 one that rounds up from next to a
+// half can be wrong: there the sign of 254 x - (2 k + 1) m decides, which the two products and what their rounding lost give exactly.
 struct Rounder {
-  float inv, m, scale;  // scale: what the block stores
+  float inv, m, scale;  // scale: what the block stores; m == 0: its codes are zeros
   float down;           // keeps the products of the exact comparison finite
-  bool e4m3;
-  __device__ __forceinline__ Rounder(uint32_t amax_bits, bool e4m3_) : e4m3(e4m3_) {
+  __device__ __forceinline__ Rounder(uint32_t amax_bits, bool e4m3) {
     m = __uint_as_float(amax_bits);
     inv = 0.f;
     down = 1.f;
@@ -143,34 +143,31 @@ struct Rounder {
     return fabsf(d) > kNear && (diff > 0.f || (diff == 0.f && ((int)r & 1))) ? __fadd_rn(y, s) : y;
   }
   // codes of 4 values, pairs (x0, x1) and (x2, x3)
-  template <bool BF16>
+  template <bool E4M3, bool BF16>
   __device__ __forceinline__ uint32_t four(const float2 (&x)[2]) const {
-    if (m == 0.f) return 0u;
-    if (e4m3) {
+    const float2 i2 = make_float2(inv, inv);
+    if constexpr (E4M3) {
       uint16_t lo, hi;
-      const float2 i2 = make_float2(inv, inv), a = mul2(x[0], i2), b = mul2(x[1], i2);
+      const float2 a = mul2(x[0], i2), b = mul2(x[1], i2);
       asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(a.y), "f"(a.x));
       asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(b.y), "f"(b.x));
       return (uint32_t)lo | ((uint32_t)hi << 16);
-    }
-    const float2 i2 = make_float2(inv, inv), up = make_float2(kMagic, kMagic), one = make_float2(1.f, 1.f);
-    float2 y[2], d[2];
+    } else {
+      const float2 up = make_float2(kMagic, kMagic), one = make_float2(1.f, 1.f);
+      const float2 y[2] = {fma2(x[0], i2, up), fma2(x[1], i2, up)};
+      if constexpr (!BF16) {
+        float2 d[2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      y[i] = fma2(x[i], i2, up);
-      const float2 r = fma2(y[i], one, make_float2(-kMagic, -kMagic));
-      d[i] = fma2(x[i], i2, make_float2(-r.x, -r.y));  // what the rounding took off
+        for (int i = 0; i < 2; ++i) {
+          const float2 r = fma2(y[i], one, make_float2(-kMagic, -kMagic));
+          d[i] = fma2(x[i], i2, make_float2(-r.x, -r.y));  // what the rounding took off
+        }
+        if (fmaxf(fmaxf(fabsf(d[0].x), fabsf(d[0].y)), fmaxf(fabsf(d[1].x), fabsf(d[1].y))) > kNear)
+          return settled(make_float4(x[0].x, x[0].y, x[1].x, x[1].y), make_float4(d[0].x, d[0].y, d[1].x, d[1].y),
+                         make_float4(y[0].x, y[0].y, y[1].x, y[1].y), m, down);
+      }
+      return bytes(y[0].x, y[0].y, y[1].x, y[1].y);
     }
-    if (fmaxf(fmaxf(fabsf(d[0].x), fabsf(d[0].y)), fmaxf(fabsf(d[1].x), fabsf(d[1].y))) > kNear &&
-        (doubtful<BF16>(y[0].x, d[0].x) || doubtful<BF16>(y[0].y, d[0].y) || doubtful<BF16>(y[1].x, d[1].x) ||
-         doubtful<BF16>(y[1].y, d[1].y)))
-      return settled(make_float4(x[0].x, x[0].y, x[1].x, x[1].y), make_float4(d[0].x, d[0].y, d[1].x, d[1].y),
-                     make_float4(y[0].x, y[0].y, y[1].x, y[1].y), m, down);
-    return bytes(y[0].x, y[0].y, y[1].x, y[1].y);
-  }
-  template <bool BF16>
-  __device__ __forceinline__ static bool doubtful(float y, float d) {
-    return fabsf(d) > kNear && (!BF16 || (__float_as_uint(y) & 1u));
   }
   // the last bytes of four sums with kMagic
   __device__ __forceinline__ static uint32_t bytes(float y0, float y1, float y2, float y3) {
@@ -201,10 +198,11 @@ struct Vec<__nv_bfloat16> {
   __device__ __forceinline__ static float2 pair(uint32_t u) {
     return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
   }
+  template <bool E4M3>
   __device__ __forceinline__ static void store(const Rounder& r, const uint4& u, uint8_t* to) {
     uint2 o;
-    o.x = r.four<true>({pair(u.x), pair(u.y)});
-    o.y = r.four<true>({pair(u.z), pair(u.w)});
+    o.x = r.four<E4M3, true>({pair(u.x), pair(u.y)});
+    o.y = r.four<E4M3, true>({pair(u.z), pair(u.w)});
     *reinterpret_cast<uint2*>(to) = o;
   }
 };
@@ -215,9 +213,10 @@ struct Vec<float> {
     return max(max(max(m, u.x & 0x7fffffffu), max(u.y & 0x7fffffffu, u.z & 0x7fffffffu)), u.w & 0x7fffffffu);
   }
   __device__ __forceinline__ static uint32_t bits(uint32_t m) { return m; }
+  template <bool E4M3>
   __device__ __forceinline__ static void store(const Rounder& r, const uint4& u, uint8_t* to) {
     *reinterpret_cast<uint32_t*>(to) =
-        r.four<false>({make_float2(__uint_as_float(u.x), __uint_as_float(u.y)), make_float2(__uint_as_float(u.z), __uint_as_float(u.w))});
+        r.four<E4M3, false>({make_float2(__uint_as_float(u.x), __uint_as_float(u.y)), make_float2(__uint_as_float(u.z), __uint_as_float(u.w))});
   }
 };
 
@@ -296,7 +295,16 @@ __global__ void __launch_bounds__(kThreads) k_quant_append(const QuantRows a) {
       const int64_t row = (((int64_t)page * c.hkv + h) << c.page_shift) + (p.first & ((1u << c.page_shift) - 1u));
       uint8_t* to = (is_v ? c.v_pages : c.k_pages) + (row + r0) * D + col;
 #pragma unroll
-      for (int i = 0; i < PASSES; ++i) Vec<T>::store(round, x[i], to + i * RPP * D);
+      for (int i = 0; i < PASSES; ++i) {
+        if (round.m == 0.f) x[i] = make_uint4(0, 0, 0, 0);
+      }
+      if (c.e4m3) {
+#pragma unroll
+        for (int i = 0; i < PASSES; ++i) Vec<T>::template store<true>(round, x[i], to + i * RPP * D);
+      } else {
+#pragma unroll
+        for (int i = 0; i < PASSES; ++i) Vec<T>::template store<false>(round, x[i], to + i * RPP * D);
+      }
       if (part == 0 && lane == 0) (is_v ? c.v_scale : c.k_scale)[row >> c.block_shift] = round.scale;
     }
   }
