@@ -18,6 +18,17 @@ struct QuantCache {
   bool e4m3;
 };
 
+// n / d for n below 2^31 by a product (d >= 2): with 2^(l-1) < d <= 2^l, mul = floor(2^(31+l) / d) + 1 fits 32 bits, and
+// n mul / 2^(31+l) exceeds n / d by less than 1 / d.
+struct Divide {
+  uint32_t mul, shift;
+};
+inline Divide divide_by(uint32_t d) {
+  uint32_t l = 1;
+  while ((uint64_t)1 << l < d) ++l;
+  return {(uint32_t)(((uint64_t)1 << (31 + l)) / d + 1), l - 1};
+}
+
 // What append and read share: request n has rows cu[n] .. cu[n + 1] of the packed tensors, which are the last
 // ones of its seq_lens[n] positions.
 struct QuantRows {
@@ -25,6 +36,7 @@ struct QuantRows {
   int N, T, max_blocks;
   const int32_t *cu, *seq_lens, *block_table, *slot;
   WsHeader* hdr;            // or NULL: what is wrong is not reported
+  Divide heads;             // by 2 hkv, the units of a piece
   bool by_token;            // pieces are numbered by the first of their rows, not as below
   const void *k_in, *v_in;  // append
   int64_t k_stride, v_stride;

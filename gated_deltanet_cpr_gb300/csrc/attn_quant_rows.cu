@@ -2,10 +2,10 @@
 // written, and reading cached ones back into packed rows.
 //
 // Both kernels move every byte once.  Reading is bound by DRAM: 282 thousand rows of 4 heads, d = 128, 869 MB, in 133 us, 6.5 TB/s
-// (98% of a copy's rate).  Writing is bound by instructions, about 650 for the 2048 values of a block, and by the chain of dependent loads
+// (98% of a copy's rate).  Writing is bound by instructions, about 580 for the 2048 values of a block, and by the chain of dependent loads
 // that a warp makes for one unit (offsets, lengths, rows): 16384 tokens of 8 heads, 101 MB, in 20 us, 5.1 TB/s.
 // A warp that took several units after one search was slower (more registers, fewer warps).  Short calls are
-// launch and that chain: 256 single tokens 5.1 us, 23 chunks 5.1.  The position-aligned pieces of the requests are numbered so
+// launch and that chain: 256 single tokens 4.9 us, 23 chunks 5.0.  The position-aligned pieces of the requests are numbered so
 // that a warp finds its request with one search of the offsets, 32 of them at a time.
 #include "attn_quant.h"
 
@@ -20,7 +20,7 @@ __device__ __forceinline__ int request_of(const int32_t* cu, int N, int shift, i
   int lo = 0, n = N;
   while (n > 1) {
     const int step = (n + 31) >> 5, i = lo + lane * step;
-    const bool at = lane * step < n && (cu[i] >> shift) + (int64_t)gap * i <= (int64_t)w;
+    const bool at = lane * step < n && (uint32_t)(cu[i] >> shift) + (uint32_t)(gap * i) <= w;
     const uint32_t m = __ballot_sync(0xffffffffu, at) | 1u;
     const int k = (31 - __clz(m)) * step;
     lo += k;
@@ -28,6 +28,8 @@ __device__ __forceinline__ int request_of(const int32_t* cu, int N, int shift, i
   }
   return lo;
 }
+
+__device__ __forceinline__ uint32_t divide(uint32_t n, Divide d) { return __umulhi(n, d.mul) >> d.shift; }
 
 // A piece of a request: `1 << shift` positions from `first` on.
 struct Piece {
@@ -58,7 +60,7 @@ __device__ __forceinline__ Piece piece_of(const QuantRows& a, int shift, uint32_
   p.begin = fits ? (uint32_t)(len - rows) : 0u;  // if not, numbered as if its rows began at position 0
   const uint32_t end = fits ? (uint32_t)len : (uint32_t)rows;
   p.on = c0 >= 0 && c1 > c0 && c1 <= a.T;
-  const int64_t at = (int64_t)w - ((c0 >> s) + (int64_t)gap * p.n);  // row or piece of the request
+  const int at = (int)(w - ((uint32_t)(c0 >> s) + (uint32_t)(gap * p.n)));  // row or piece of the request; both are below 2^31
   const uint32_t mask = (1u << shift) - 1u;
   if (a.by_token) {
     const uint32_t pos = p.begin + (uint32_t)at;
@@ -235,10 +237,11 @@ __global__ void __launch_bounds__(kThreads) k_quant_append(const QuantRows a) {
   }
   const QuantCache& c = a.c;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, B = 1 << c.block_shift;
-  const int each = B / kGranule, part = warp % each;  // warps of a unit, this one's rows of it
+  const int each_shift = c.block_shift - kGranuleShift, each = 1 << each_shift;  // warps of a unit
+  const int part = warp & (each - 1);                                            // this one's rows of it
   const uint32_t pieces = a.by_token ? (uint32_t)a.T : (uint32_t)(a.T >> c.block_shift) + 2u * (uint32_t)a.N;
-  const uint32_t all = 2u * (uint32_t)c.hkv, unit = (blockIdx.x - 1) * (uint32_t)(kWarps / each) + (uint32_t)(warp / each);
-  const uint32_t w = unit / all, rest = unit - w * all;
+  const uint32_t all = 2u * (uint32_t)c.hkv, unit = ((blockIdx.x - 1) * (uint32_t)kWarps + (uint32_t)warp) >> each_shift;
+  const uint32_t w = divide(unit, a.heads), rest = unit - w * all;
   const int h = (int)(rest >> 1);
   const bool is_v = rest & 1;
   Piece p{};
@@ -353,7 +356,7 @@ __global__ void __launch_bounds__(kThreads) k_quant_read(const QuantRows a) {
   const uint32_t units = (a.by_token ? (uint32_t)a.T : (uint32_t)(a.T / kGranule) + 2u * (uint32_t)a.N) * 2u * (uint32_t)c.hkv;
   const uint32_t unit = (blockIdx.x - 1) * (uint32_t)kWarps + (threadIdx.x >> 5);
   if (unit < units) {
-    const uint32_t w = unit / (2u * (uint32_t)c.hkv), rest = unit - w * 2u * (uint32_t)c.hkv;
+    const uint32_t w = divide(unit, a.heads), rest = unit - w * 2u * (uint32_t)c.hkv;
     const int h = (int)(rest >> 1);
     const bool is_v = rest & 1;
     const Piece p = piece_of(a, kGranuleShift, w, lane);
@@ -454,6 +457,7 @@ template <int D, typename T>
 int append_t(QuantRows a, cudaStream_t st) {
   const int per = kWarps / ((1 << a.c.block_shift) / kGranule);  // units of a CTA
   a.by_token = quant_by_token(a.N, a.T, a.c.block_shift);
+  a.heads = divide_by(2u * (uint32_t)a.c.hkv);
   const int64_t units = (a.by_token ? a.T : quant_pieces(a.N, a.T, a.c.block_shift)) * 2 * a.c.hkv;
   return launch(k_quant_append<D, T>, a, (units + per - 1) / per, st);
 }
@@ -461,6 +465,7 @@ int append_t(QuantRows a, cudaStream_t st) {
 template <int D, typename T, typename TO>
 int read_t(QuantRows a, cudaStream_t st) {
   a.by_token = quant_by_token(a.N, a.T, kGranuleShift);
+  a.heads = divide_by(2u * (uint32_t)a.c.hkv);
   const int64_t units = (a.by_token ? a.T : quant_pieces(a.N, a.T, kGranuleShift)) * 2 * a.c.hkv;
   return launch(k_quant_read<D, T, TO>, a, (units + kWarps - 1) / kWarps, st);
 }
