@@ -5,15 +5,19 @@
 // (98% of a copy's rate).  Writing is bound by instructions, about 580 for the 2048 values of a block, and by the chain of dependent loads
 // that a warp makes for one unit (offsets, lengths, rows): 16384 tokens of 8 heads, 101 MB, in 20 us, 5.1 TB/s.
 // A warp that took several units after one search was slower (more registers, fewer warps).  Short calls are
-// launch and that chain: 256 single tokens 4.9 us, 23 chunks 5.0.  The position-aligned pieces of the requests are numbered so
+// launch and that chain: 256 single tokens 4.7 us, 23 chunks 4.9.  The position-aligned pieces of the requests are numbered so
 // that a warp finds its request with one search of the offsets, 32 of them at a time.
+#include <algorithm>
+
 #include "attn_quant.h"
 
 namespace gdn {
 
 namespace {
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
+// Threads of a CTA.  Four warps start and end sooner than eight (256 rows read 3.4 against 3.7 us, 10 thousand granules 6.6
+// against 6.9; long reads the same); a block of 128 tokens takes eight.
+constexpr int kThreads = 128, kMostThreads = 256, kMostWarps = kMostThreads / 32;
 
 // The last n < N with (cu[n] >> shift) + gap n <= w: the request that piece w belongs to.  All lanes take part.
 __device__ __forceinline__ int request_of(const int32_t* cu, int N, int shift, int gap, uint32_t w, int lane) {
@@ -85,7 +89,7 @@ __device__ __forceinline__ void report(WsHeader* h, int code) {
 template <bool APPEND>
 __device__ void check_requests(const QuantRows& a) {
   int bad = 0;
-  for (int n = threadIdx.x; n < a.N; n += kThreads) {
+  for (int n = threadIdx.x; n < a.N; n += blockDim.x) {
     const int c0 = a.cu[n], c1 = a.cu[n + 1];
     const int first = n == 0 ? 0 : c0, last = n == a.N - 1 ? a.T : c1;
     if (c0 != first || c1 != last || c0 < 0 || c1 < c0 || c1 > a.T) {
@@ -103,12 +107,13 @@ __device__ void check_requests(const QuantRows& a) {
 }
 
 // ------------------------------------------------------------------------- rounding ----
-// Codes of an int8 block: the quotient 127 x / m is rounded as it is in exact arithmetic.  inv is 127 / m rounded up, so that x inv
-// is the quotient or up to 2^-23 of it more (in magnitude), and one fma rounds it to a whole number.  In bf16 that is right as it
-// stands, in three cases, with X and M the 8-bit significands of x and m.  A quotient that is no half lies 2^-16 of itself or more away from
-// one, 254 X 2^t and odd M 2^u being whole numbers of 16 bits.  One that is a half, 254 x = odd m, has a 127 in odd or in M: 63.5 goes
-// up to 64, which is even; M = 254 makes 127 / m a power of two, and a half goes to even by itself.  In fp32 one that rounds up from next to a
-// half can be wrong: there the sign of 254 x - (2 k + 1) m decides, which the two products and what their rounding lost give exactly.
+// Codes of an int8 block: the quotient 127 x / m is rounded as it is in exact arithmetic.  inv is 127 / m rounded up, so that x
+// inv is the quotient or up to 2^-23 of it more (in magnitude), and one fma rounds it to a whole number.  In bf16 that is right
+// as it stands, in three cases, with X and M the 8-bit significands of x and m.  A quotient that is no half lies 2^-16 of
+// itself or more away from one, 254 X 2^t and odd M 2^u being whole numbers of 16 bits.  One that is a half, 254 x = odd m, has
+// a 127 in odd or in M: 63.5 goes up to 64, which is even; M = 254 makes 127 / m a power of two, and a half goes to even by
+// itself.  In fp32 one that rounds up from next to a half can be wrong: there the sign of 254 x - (2 k + 1) m decides, which
+// the two products and what their rounding lost give exactly.
 struct Rounder {
   float inv, m, scale;  // scale: what the block stores; m == 0: its codes are zeros
   float down;           // keeps the products of the exact comparison finite
@@ -218,7 +223,8 @@ struct Vec<float> {
   template <bool E4M3>
   __device__ __forceinline__ static void store(const Rounder& r, const uint4& u, uint8_t* to) {
     *reinterpret_cast<uint32_t*>(to) =
-        r.four<E4M3, false>({make_float2(__uint_as_float(u.x), __uint_as_float(u.y)), make_float2(__uint_as_float(u.z), __uint_as_float(u.w))});
+        r.four<E4M3, false>({make_float2(__uint_as_float(u.x), __uint_as_float(u.y)),
+                             make_float2(__uint_as_float(u.z), __uint_as_float(u.w))});
   }
 };
 
@@ -227,9 +233,9 @@ struct Vec<float> {
 // meet in shared memory.  The request's first block also takes care of its tail: a first block that is completed has the tail's
 // rows in registers before the rows of a later, unfinished one replace them.
 template <int D, typename T>
-__global__ void __launch_bounds__(kThreads) k_quant_append(const QuantRows a) {
+__global__ void __launch_bounds__(kMostThreads) k_quant_append(const QuantRows a) {
   constexpr int VEC = Vec<T>::N, LPR = D / VEC, RPP = 32 / LPR, PASSES = kGranule / RPP;
-  __shared__ uint32_t most[kWarps];
+  __shared__ uint32_t most[kMostWarps];
   if (blockIdx.x == 0) {
     if (a.hdr) check_requests<true>(a);
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -240,7 +246,7 @@ __global__ void __launch_bounds__(kThreads) k_quant_append(const QuantRows a) {
   const int each_shift = c.block_shift - kGranuleShift, each = 1 << each_shift;  // warps of a unit
   const int part = warp & (each - 1);                                            // this one's rows of it
   const uint32_t pieces = a.by_token ? (uint32_t)a.T : (uint32_t)(a.T >> c.block_shift) + 2u * (uint32_t)a.N;
-  const uint32_t all = 2u * (uint32_t)c.hkv, unit = ((blockIdx.x - 1) * (uint32_t)kWarps + (uint32_t)warp) >> each_shift;
+  const uint32_t all = 2u * (uint32_t)c.hkv, unit = (blockIdx.x - 1) * (blockDim.x >> (5 + each_shift)) + (uint32_t)(warp >> each_shift);
   const uint32_t w = divide(unit, a.heads), rest = unit - w * all;
   const int h = (int)(rest >> 1);
   const bool is_v = rest & 1;
@@ -354,7 +360,7 @@ __global__ void __launch_bounds__(kThreads) k_quant_read(const QuantRows a) {
   const QuantCache& c = a.c;
   const int lane = threadIdx.x & 31;
   const uint32_t units = (a.by_token ? (uint32_t)a.T : (uint32_t)(a.T / kGranule) + 2u * (uint32_t)a.N) * 2u * (uint32_t)c.hkv;
-  const uint32_t unit = (blockIdx.x - 1) * (uint32_t)kWarps + (threadIdx.x >> 5);
+  const uint32_t unit = (blockIdx.x - 1) * (uint32_t)(kThreads / 32) + (threadIdx.x >> 5);
   if (unit < units) {
     const uint32_t w = divide(unit, a.heads), rest = unit - w * 2u * (uint32_t)c.hkv;
     const int h = (int)(rest >> 1);
@@ -438,7 +444,7 @@ __global__ void k_quant_clear(WsHeader* hdr) {
 }
 
 template <typename K>
-int launch(K* kernel, const QuantRows& a, int64_t ctas, cudaStream_t st) {
+int launch(K* kernel, const QuantRows& a, int64_t warps, int threads, cudaStream_t st) {
   if (a.hdr) k_quant_clear<<<1, 1, 0, st>>>(a.hdr);
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -447,19 +453,19 @@ int launch(K* kernel, const QuantRows& a, int64_t ctas, cudaStream_t st) {
   c.stream = st;
   c.attrs = &attr;
   c.numAttrs = a.hdr ? 1 : 0;
-  c.gridDim = dim3((unsigned)(1 + ctas));
-  c.blockDim = dim3(kThreads);
+  c.gridDim = dim3((unsigned)(1 + (warps + threads / 32 - 1) / (threads / 32)));
+  c.blockDim = dim3(threads);
   cudaLaunchKernelEx(&c, kernel, a);
   return a.hdr ? 2 : 1;
 }
 
 template <int D, typename T>
 int append_t(QuantRows a, cudaStream_t st) {
-  const int per = kWarps / ((1 << a.c.block_shift) / kGranule);  // units of a CTA
+  const int each = (1 << a.c.block_shift) / kGranule;  // warps of a unit
   a.by_token = quant_by_token(a.N, a.T, a.c.block_shift);
   a.heads = divide_by(2u * (uint32_t)a.c.hkv);
   const int64_t units = (a.by_token ? a.T : quant_pieces(a.N, a.T, a.c.block_shift)) * 2 * a.c.hkv;
-  return launch(k_quant_append<D, T>, a, (units + per - 1) / per, st);
+  return launch(k_quant_append<D, T>, a, units * each, std::max(kThreads, 32 * each), st);
 }
 
 template <int D, typename T, typename TO>
@@ -467,7 +473,7 @@ int read_t(QuantRows a, cudaStream_t st) {
   a.by_token = quant_by_token(a.N, a.T, kGranuleShift);
   a.heads = divide_by(2u * (uint32_t)a.c.hkv);
   const int64_t units = (a.by_token ? a.T : quant_pieces(a.N, a.T, kGranuleShift)) * 2 * a.c.hkv;
-  return launch(k_quant_read<D, T, TO>, a, (units + kWarps - 1) / kWarps, st);
+  return launch(k_quant_read<D, T, TO>, a, units, kThreads, st);
 }
 
 template <int D>
