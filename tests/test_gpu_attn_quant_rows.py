@@ -163,6 +163,28 @@ def test_ties_go_to_even(attn, gdn, dtype, code):
         assert torch.equal(k[0], ref) and torch.equal(v[0], -ref)
 
 
+def test_every_bf16_value_under_every_largest(attn, gdn):
+    """Quotients depend on the two significands and the gap of the exponents: 128 largest values, 128 values and 10 gaps, after
+    which all of them round to 0; the codes themselves are compared."""
+    sig = torch.arange(128, 256, dtype=R.D)
+    x = torch.zeros((128, 16, 128), dtype=R.D)
+    for i, m in enumerate(sig):
+        v = torch.cat([sig * 2.0 ** -gap for gap in range(10)])
+        v = v[v <= m]
+        x[i].view(-1)[:len(v)] = v
+        x[i].view(-1)[-1] = m
+    x = x.view(-1, 1, 128)
+    assert torch.equal(x.to(BF).to(R.D), x)
+    for scale in (1.0, 2.0 ** -100, 2.0 ** 119):
+        b = (x * scale).to(BF)
+        s = Store(attn, gdn, [len(b)], 1, 128, 64, 16, "int8", BF)
+        s.append([b], [-b], [len(b)])
+        pages = s.table[0, :len(b) // 64].long()
+        c, _ = R.quantise(b.view(128, 1, 16, 128), "int8")
+        assert torch.equal(s.cache.k[pages].cpu().view(-1).to(R.D), c.view(-1))
+        assert torch.equal(s.cache.v[pages].cpu().view(-1).to(R.D), -c.view(-1))
+
+
 @pytest.mark.parametrize("code", ["int8", "e4m3"])
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_extreme_blocks(attn, gdn, dtype, code):
