@@ -8,7 +8,9 @@
 // in f16 with the keys as rows (scores^T = K q^T, out^T += V^T P^T), so that up to 8 heads cost one column tile and nothing
 // is computed for heads that are not there.  Codes are exact in f16: int8 as 1024 + (c + 128), less 1152;
 // e4m3 by conversion.  q is scaled by a power of two so that its largest entry lies in [2^14, 2^15), P by 2^14, so that f16
-// holds them with 11 bits down to 2^-28 of the largest; fp32 calls split both into two f16, 22 bits.  Scales multiply the
+// holds them with 11 bits down to 2^-28 of the largest; fp32 calls split both into two f16, 22 bits.  P's 2^14 is in the
+// operand alone and goes with the codes or their scale: put into what is taken off a score, it would be lost where
+// fp32 has no such bits (scores of 2^25 and more), and leave rounding of its own in any other.  Scales multiply the
 // scores, and the sums of one granule's 16 values, in fp32.
 //
 // Half the bytes of a bf16 cache leave half the time for the same products, so that instructions bound this kernel
@@ -25,7 +27,8 @@ namespace gdn {
 
 namespace {
 
-constexpr int kShiftP = 14;  // probabilities are held as p 2^14
+constexpr float kUpP = 0x1p14f, kDownP = 0x1p-14f;  // probabilities are p 2^14 in f16
+constexpr float kLowest = -3.402823466e38f;         // the maximum before any score: no score is less, and taken off it stays finite
 
 // What a warp needs to know of a request.
 struct QuantRequest {
@@ -145,11 +148,12 @@ __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)
 // it is below 2^-110).
 __device__ __forceinline__ int f16_exponent(float m) { return max((int)(__float_as_uint(m) >> 23) - 127, -110) - 14; }
 
-// Two pairs of f16 from four codes: of codes (0, 1) and (2, 3), or, APART, of (0, 2) and (1, 3).
-template <bool E4M3, bool APART>
+// Two pairs of f16 from four codes: of keys' codes (0, 1) and (2, 3), or of VALUES' (0, 2) and (1, 3).  Values in int8 come
+// times 2^-14, which is exact: as 2^-4 + (c + 128) 2^-14, less 2^-4 + 2^-7.
+template <bool E4M3, bool VALUES>
 __device__ __forceinline__ void widen16(uint32_t four, uint32_t& first, uint32_t& second) {
   if constexpr (E4M3) {
-    if constexpr (APART) four = __byte_perm(four, 0u, 0x3120);
+    if constexpr (VALUES) four = __byte_perm(four, 0u, 0x3120);
     asm("{.reg .b16 l, h;\n\t"
         "mov.b32 {l, h}, %2;\n\t"
         "cvt.rn.f16x2.e4m3x2 %0, l;\n\t"
@@ -158,9 +162,11 @@ __device__ __forceinline__ void widen16(uint32_t four, uint32_t& first, uint32_t
         : "r"(four));
   } else {
     const uint32_t u = four ^ 0x80808080u;
-    const uint32_t a = __byte_perm(u, 0x64646464u, APART ? 0x4240 : 0x4140);
-    const uint32_t b = __byte_perm(u, 0x64646464u, APART ? 0x4341 : 0x4342);
-    const __half2 bias = __floats2half2_rn(1152.f, 1152.f);
+    const uint32_t high = VALUES ? 0x2c2c2c2cu : 0x64646464u;
+    const uint32_t a = __byte_perm(u, high, VALUES ? 0x4240 : 0x4140);
+    const uint32_t b = __byte_perm(u, high, VALUES ? 0x4341 : 0x4342);
+    const float off = VALUES ? 1152.f * kDownP : 1152.f;
+    const __half2 bias = __floats2half2_rn(off, off);
     const __half2 x = __hsub2(*reinterpret_cast<const __half2*>(&a), bias), y = __hsub2(*reinterpret_cast<const __half2*>(&b), bias);
     first = *reinterpret_cast<const uint32_t*>(&x);
     second = *reinterpret_cast<const uint32_t*>(&y);
@@ -202,7 +208,7 @@ struct QuantEngine : Quant {
 
   uint32_t q[P][KS][NH][2];
   float qs[NH][2];  // scale of the scores
-  float m[NH][2], base[NH][2], l[NH][2], o[KS][NH][4];  // base: what is taken off a score, m - 14 or 0
+  float m[NH][2], l[NH][2], o[KS][NH][4];
 
   // place of 16-byte piece c of row r: 8 rows of a matrix load lie in 8 bank groups
   __device__ __forceinline__ static uint32_t place(int r, int c) {
@@ -249,8 +255,8 @@ struct QuantEngine : Quant {
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
         qs[h][b] = __shfl_sync(0xffffffffu, f, 4 * (2 * t + b));
-        m[h][b] = -INFINITY;
-        base[h][b] = l[h][b] = 0.f;
+        m[h][b] = kLowest;
+        l[h][b] = 0.f;
       }
     }
 #pragma unroll
@@ -261,7 +267,7 @@ struct QuantEngine : Quant {
         for (int e = 0; e < 4; ++e) o[j][h][e] = 0.f;
   }
 
-  // Products x of G granules with their keys, the first `rows` from key[i] on, to probabilities p 2^14, with the running
+  // Products x of G granules with their keys, the first `rows` from key[i] on, to probabilities, with the running
   // maximum and sum.
   template <int G>
   __device__ __forceinline__ void softmax(const QuantDecode& a, const float (&ks)[G], bool full, const int (&key)[G],
@@ -306,9 +312,8 @@ struct QuantEngine : Quant {
 #pragma unroll
           for (int w = 4; w < 32; w <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, w));
           y = fmaxf(y, m[h][e]);
-          f[e] = m[h][e] == -INFINITY ? 0.f : exp2_approx(__fsub_rn(m[h][e], y));
+          f[e] = exp2_approx(__fsub_rn(m[h][e], y));
           m[h][e] = y;
-          base[h][e] = y == -INFINITY ? 0.f : __fsub_rn(y, (float)kShiftP);
           l[h][e] = __fmul_rn(l[h][e], f[e]);
         }
 #pragma unroll
@@ -323,20 +328,21 @@ struct QuantEngine : Quant {
       for (int e = 0; e < 2; ++e) {
 #pragma unroll
         for (int i = 0; i < G; ++i) {
-          x[i][h][e] = exp2_approx(__fsub_rn(x[i][h][e], base[h][e]));
-          x[i][h][e + 2] = exp2_approx(__fsub_rn(x[i][h][e + 2], base[h][e]));
+          x[i][h][e] = exp2_approx(__fsub_rn(x[i][h][e], m[h][e]));
+          x[i][h][e + 2] = exp2_approx(__fsub_rn(x[i][h][e + 2], m[h][e]));
           l[h][e] = __fadd_rn(l[h][e], __fadd_rn(x[i][h][e], x[i][h][e + 2]));
         }
       }
   }
-  // P^T of a granule as the MMA's right operand: keys 2 t, 2 t + 1 (+ 8) of head g
+  // P^T 2^14 of a granule as the MMA's right operand: keys 2 t, 2 t + 1 (+ 8) of head g
   __device__ __forceinline__ static void operand(const float (&p)[4], uint32_t (&b)[P][2]) {
-    const uint32_t lo = pack_f16(p[0], p[1]), hi = pack_f16(p[2], p[3]);
+    const float2 up = make_float2(kUpP, kUpP), x = mul2(make_float2(p[0], p[1]), up), y = mul2(make_float2(p[2], p[3]), up);
+    const uint32_t lo = pack_f16(x.x, x.y), hi = pack_f16(y.x, y.y);
     b[0][0] = transposed(lo);
     b[0][1] = transposed(hi);
     if constexpr (SPLIT) {
-      b[P - 1][0] = transposed(pack_f16_rest(p[0], p[1], lo));
-      b[P - 1][1] = transposed(pack_f16_rest(p[2], p[3], hi));
+      b[P - 1][0] = transposed(pack_f16_rest(x.x, x.y, lo));
+      b[P - 1][1] = transposed(pack_f16_rest(y.x, y.y, hi));
     }
   }
   __device__ __forceinline__ void add(int j, int h, const float (&c)[4], float scale) {
@@ -384,7 +390,7 @@ struct QuantEngine : Quant {
 #pragma unroll
         for (int e = 0; e < 4; ++e) x[b][h][e] = __fadd_rn(x[b][h][e], y[b][h][e]);
       ks[b] = meta.ks[i + b];
-      vs[b] = meta.vs[i + b];
+      vs[b] = E4M3 ? __fmul_rn(meta.vs[i + b], kDownP) : meta.vs[i + b];
       key[b] = meta.key + ((i + b) << kGranuleShift) + (i + b >= meta.skip_from ? meta.skip : 0);
     }
     softmax<G>(a, ks, full, key, kGranule, len, x, lane);
@@ -568,7 +574,7 @@ struct QuantEngine : Quant {
         mma_f16_from0(rest, v[0], b[h][P - 1][0], b[h][P - 1][1]);
         mma_f16(rest, v[1], b[h][0][0], b[h][0][1]);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) c[e] = __fadd_rn(c[e], rest[e]);
+        for (int e = 0; e < 4; ++e) c[e] = __fmul_rn(__fadd_rn(c[e], rest[e]), kDownP);
         add(j, h, c, vs);
       }
     }
@@ -586,7 +592,7 @@ struct QuantEngine : Quant {
         if (bad) s = __builtin_nanf("");
         const int head = 8 * h + 2 * t + e;
         if (head >= k.heads) continue;
-        if (g == 0) k.stats(head, __fsub_rn(m[h][e], (float)kShiftP), s);
+        if (g == 0) k.stats(head, m[h][e], s);
         if (k.acc) {
           float* to = k.acc + head * k.acc_step + 2 * g;
 #pragma unroll

@@ -1,0 +1,89 @@
+"""Decode attention over the 8-bit cache at the ends of its range, against plain attention in 64 bits over what the cache
+holds."""
+import pytest
+import torch
+
+import attn_ref as A
+from test_gpu_attn_quant_rows import BF, F32, Store, attn, expect, ints, rows  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+LOG2E = 1.4426950408889634
+
+
+def decode(attn, gdn, q, ks, vs, block, code, dtype, page=32, **kw):
+    """(store, out, lse) of a cache that holds the rows ks and vs, error word checked."""
+    lens = [len(k) for k in ks]
+    s = Store(attn, gdn, lens, ks[0].shape[1], ks[0].shape[2], max(page, block), block, code, dtype)
+    s.append(ks, vs, lens)
+    ws = gdn.alloc_workspace(64 << 20, "cuda")
+    out, lse = attn.quant_decode(q.to(dtype).cuda(), s.cache, s.table, ints(lens), slots=s.slots, want_lse=True, ws=ws, **kw)
+    assert gdn.device_error(ws) == 0
+    return s, out, lse
+
+
+def along(signs, c, dtype):
+    """Keys c[j] times a row of signs: their products with a multiple of it are whole numbers, exact in any order."""
+    return (c[:, None, None] * signs).to(dtype)
+
+
+def tolerance(r, v, dtype):
+    """One key has all of the weight, or several share it equally, so that sums of p and p v are exact but for the product
+    with a scale, a tail's two f16 parts (2^-22 of a value, 2^-36 of the largest beside it), the division and the output's
+    rounding.  A score is off by the roundings of four factors, its log-sum-exp by three more: 2^-20 of it."""
+    u = 2.0 ** -8 if dtype == BF else 2.0 ** -24
+    return (u + 2.0 ** -20) * r["out"].abs() + 2.0 ** -36 * float(v.abs().max()), 2.0 ** -20 * r["lse"].abs() + 1e-30
+
+
+@pytest.mark.parametrize("power", [24, 25, 26, 27, 29])
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("code", ["int8", "e4m3"])
+@pytest.mark.parametrize("dtype,d", [(BF, 128), (F32, 64)])
+def test_scores_of_any_size(attn, gdn, dtype, d, code, sign, power):
+    """Largest scores (times log2 e) of 2^power to 1.75 2^power of either sign: the largest wins outright, and equal ones
+    share.  One key or many, in pages, in a tail or both, in one run or several."""
+    g = torch.Generator().manual_seed(power)
+    hk, group, lens = 2, 4, [1, 16, 17, 40, 300, 1031]
+    signs = torch.randint(0, 2, (hk, d), generator=g) * 2.0 - 1
+    top, low, high = (127, 1, 97) if sign > 0 else (20, 40, 128)
+    ks, vs = [], rows(lens, hk, d, dtype, power)
+    for n, L in enumerate(lens):
+        c = torch.randint(low, high, (L,), generator=g).double()
+        c[(7 * n) % L] = top
+        if sign > 0 and L >= 300:  # the same key in another block, where its scale is the same
+            c[L // 32 * 16 + 3] = top
+        ks.append(along(signs, c, dtype))
+        vs[n][:, :, ::3] = 0  # codes of 0, and
+        vs[n][:, 0, 1] *= 300  # many small ones
+    scale = 2.0 ** power / (LOG2E * d * top)
+    q = sign * signs.repeat_interleave(group, 0) * torch.tensor([1.0, 1.25, 1.5, 1.75]).repeat(hk)[:, None]
+    q = q.expand(len(lens), -1, -1)
+    for window in (0, 1):
+        _, out, lse = decode(attn, gdn, q, ks, vs, 16, code, dtype, scale=scale, window=window)
+        for i, L in enumerate(lens):
+            k, v = expect(ks[i], 16, code, F32), expect(vs[i], 16, code, F32)
+            r = A.attention(q[i:i + 1], k, v, torch.tensor([L - 1]), window, 0, scale)
+            to, tl = tolerance(r, v, dtype)
+            assert A.worst(out[i:i + 1], r["out"], to) <= 1, (i, L, window)
+            assert A.worst(lse[i:i + 1], r["lse"], tl) <= 1, (i, L, window)
+
+
+@pytest.mark.parametrize("code", ["int8", "e4m3"])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_log_sum_of_one_key_is_its_score(attn, gdn, dtype, code):
+    """Near 0 as well, where nothing of another size may be added to it and taken off again; in a page and in a tail."""
+    d, hk, group = 64, 1, 16
+    g = torch.Generator().manual_seed(3)
+    signs = torch.randint(0, 2, (hk, d), generator=g) * 2.0 - 1
+    lens = [1] * 16 + [16] * 16
+    ks = [along(signs, torch.tensor([1.0 + n % 16] * L), dtype) for n, L in enumerate(lens)]
+    vs = rows(lens, hk, d, dtype, 4)
+    q = signs.expand(group, d) * ((torch.arange(group) % 8 + 1) / 8 * (1 - 2.0 * (torch.arange(group) // 8)))[:, None]
+    q = q.expand(len(lens), -1, -1)
+    for top in (0.01, 0.1, 1.0):
+        scale = top / (16 * d)
+        _, out, lse = decode(attn, gdn, q, ks, vs, 16, code, dtype, scale=scale, window=1)
+        for i, L in enumerate(lens):
+            k, v = expect(ks[i], 16, code, F32), expect(vs[i], 16, code, F32)
+            r = A.attention(q[i:i + 1], k, v, torch.tensor([L - 1]), 1, 0, scale)
+            to, tl = tolerance(r, v, dtype)
+            assert A.worst(out[i:i + 1], r["out"], to) <= 1 and A.worst(lse[i:i + 1], r["lse"], tl) <= 1, (i, top)
