@@ -70,6 +70,7 @@ struct Paged {
     }
     return lost ? GDN_DEVERR_PAGES : 0;
   }
+  __device__ __forceinline__ static float divisor(const gdn::Request&, float l) { return l; }
 };
 
 // ---------------------------------------------------------------------------- SIMT ----

@@ -1,7 +1,7 @@
 // attn_decode.cuh -- what decode attention over the paged cache and over the 8-bit one share: a warp takes a run of a
 // request's visible keys and leaves (m, l, a) or the output, and k_decode_join adds a request's runs in ascending
-// order.  An engine E has a Kind with the types Args (the call) and Request (of a length: its runs) and check(), what
-// is wrong with a request's pages, and a type Run.
+// order.  An engine E has a Kind with the types Args (the call) and Request (of a length: its runs), check(), what
+// is wrong with a request's pages, and divisor(), the sum of its probabilities on the scale of its records' a; and a type Run.
 #pragma once
 
 #include "attn.h"
@@ -147,8 +147,9 @@ __global__ void __launch_bounds__(SPLIT ? 256 : 128) k_decode_join(const typenam
       }
     }
     if (g == 0 || !SPLIT) {
+      const float by = Kind::divisor(rq, l);
       store4(static_cast<T*>(a.out) + row * D + c,
-             make_float4(__fdiv_rn(o.x, l), __fdiv_rn(o.y, l), __fdiv_rn(o.z, l), __fdiv_rn(o.w, l)));
+             make_float4(__fdiv_rn(o.x, by), __fdiv_rn(o.y, by), __fdiv_rn(o.z, by), __fdiv_rn(o.w, by)));
       if (a.lse && c == 0) a.lse[row] = __fmul_rn(__fadd_rn(m, log2f(l)), kLn2);
     }
   }

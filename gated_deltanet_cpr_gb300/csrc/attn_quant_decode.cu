@@ -30,6 +30,11 @@ namespace {
 constexpr float kUpP = 0x1p14f, kDownP = 0x1p-14f;  // probabilities are p 2^14 in f16
 constexpr float kLowest = -3.402823466e38f;         // the maximum before any score: no score is less, and taken off it stays finite
 
+// Sums of p v are held times 2^-s, 2^s being above twice the request's length: they and their runs' cannot overflow, whatever
+// the values are (a mean of finite values is finite, their sum need not be).  Scales carry it, so that it costs a product a
+// granule; it is exact for values of 2^-100, the least that a block holds as more than zeros, up to 262144 tokens.
+__device__ __forceinline__ float sums_down(int len) { return __uint_as_float((uint32_t)(127 - (33 - __clz(len))) << 23); }
+
 // What a warp needs to know of a request.
 struct QuantRequest {
   int len;         // tokens (0 if the length is not valid)
@@ -85,6 +90,8 @@ struct Quant {
     }
     return wrong;
   }
+  // what the sums of p v are divided by
+  __device__ __forceinline__ static float divisor(const QuantRequest& rq, float l) { return __fmul_rn(l, sums_down(rq.len)); }
 };
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -209,6 +216,7 @@ struct QuantEngine : Quant {
   uint32_t q[P][KS][NH][2];
   float qs[NH][2];  // scale of the scores
   float m[NH][2], l[NH][2], o[KS][NH][4];
+  float down;  // o is held times this
 
   // place of 16-byte piece c of row r: 8 rows of a matrix load lie in 8 bank groups
   __device__ __forceinline__ static uint32_t place(int r, int c) {
@@ -220,7 +228,8 @@ struct QuantEngine : Quant {
     return r * TAILB + ((c ^ ((r / PER) & MASK)) << 4);
   }
 
-  __device__ __forceinline__ void start(const QuantDecode& a, int64_t row, int heads, int lane) {
+  __device__ __forceinline__ void start(const QuantDecode& a, int64_t row, int heads, int len, int lane) {
+    down = sums_down(len);
     const int g = lane >> 2, t = lane & 3;
     const float scale = __fmul_rn(a.scale, kLog2e);
 #pragma unroll
@@ -390,7 +399,7 @@ struct QuantEngine : Quant {
 #pragma unroll
         for (int e = 0; e < 4; ++e) x[b][h][e] = __fadd_rn(x[b][h][e], y[b][h][e]);
       ks[b] = meta.ks[i + b];
-      vs[b] = E4M3 ? __fmul_rn(meta.vs[i + b], kDownP) : meta.vs[i + b];
+      vs[b] = __fmul_rn(meta.vs[i + b], E4M3 ? __fmul_rn(down, kDownP) : down);
       key[b] = meta.key + ((i + b) << kGranuleShift) + (i + b >= meta.skip_from ? meta.skip : 0);
     }
     softmax<G>(a, ks, full, key, kGranule, len, x, lane);
@@ -467,6 +476,10 @@ struct QuantEngine : Quant {
 #pragma unroll
       for (int e = 0; e < 4; ++e) x[h][e] = __fmaf_rn(x[h][e], 0.f, x[h][e]);
     softmax<1>(a, {1.f}, false, {key}, TAIL_ROWS, len, xs, lane);
+#pragma unroll
+    for (int h = 0; h < NH; ++h)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[h][e] = __fmul_rn(x[h][e], down);
     uint32_t b[NH][2][2];
 #pragma unroll
     for (int h = 0; h < NH; ++h)
@@ -517,7 +530,7 @@ struct QuantEngine : Quant {
     const float km = tail_max(stage, lane), vm = tail_max(stage + SIDE, lane);
     const int ke = f16_exponent(km), ve = f16_exponent(vm);
     const float kd = km == km ? pow2(-ke) : 0.f, vd = vm == vm ? pow2(-ve) : 0.f;
-    const float vs = vm == vm ? pow2(ve) : vm;
+    const float vs = vm == vm ? __fmul_rn(pow2(ve), down) : vm;
     float xs[1][NH][4], ys[NH][4];
     float(&x)[NH][4] = xs[0];
 #pragma unroll
@@ -599,7 +612,7 @@ struct QuantEngine : Quant {
           for (int j = 0; j < KS; ++j) *reinterpret_cast<float2*>(to + 16 * j) = make_float2(o[j][h][e], o[j][h][2 + e]);
         } else {
           Elem* to = static_cast<Elem*>(k.out) + head * D + 2 * g;
-          const float f = __fdiv_rn(1.f, s);
+          const float f = __fdiv_rn(1.f, __fmul_rn(s, down));
 #pragma unroll
           for (int j = 0; j < KS; ++j) {
             const float y0 = __fmul_rn(o[j][h][e], f), y1 = __fmul_rn(o[j][h][2 + e], f);
@@ -840,7 +853,7 @@ __global__ void __launch_bounds__(32 * DecodeSmem<E>::WARPS, 1) k_quant_decode(c
     const int len = r.len;
     {
       const int g0 = (r.y % parts) * kHeadsPerRun;
-      eng.start(a, (int64_t)r.i * a.hq + (r.y / parts) * group + g0, min(kHeadsPerRun, group - g0), lane);
+      eng.start(a, (int64_t)r.i * a.hq + (r.y / parts) * group + g0, min(kHeadsPerRun, group - g0), len, lane);
     }
     int what;
     do {

@@ -1,9 +1,10 @@
 """Decode attention over the 8-bit cache at the ends of its range, against plain attention in 64 bits over what the cache
-holds."""
+holds: scores that leave no fraction in fp32, values up to the type's largest."""
 import pytest
 import torch
 
 import attn_ref as A
+from test_gpu_attn_quant_decode import reference
 from test_gpu_attn_quant_rows import BF, F32, Store, attn, expect, ints, rows  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -87,3 +88,49 @@ def test_log_sum_of_one_key_is_its_score(attn, gdn, dtype, code):
             r = A.attention(q[i:i + 1], k, v, torch.tensor([L - 1]), 1, 0, scale)
             to, tl = tolerance(r, v, dtype)
             assert A.worst(out[i:i + 1], r["out"], to) <= 1 and A.worst(lse[i:i + 1], r["lse"], tl) <= 1, (i, top)
+
+
+@pytest.mark.parametrize("code", ["int8", "e4m3"])
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("block", [16, 128])
+def test_values_up_to_the_largest(attn, gdn, block, dtype, code):
+    """Sums over keys of equal weights pass the type's largest value, the outputs do not.  (In fp32 2^-10 is left for roundings;
+    e4m3 holds 240 2^120 exactly, and the type's largest as 2^128.)"""
+    top = 240 * 2.0 ** 120 if code == "e4m3" else torch.finfo(dtype).max * (1 if dtype == BF else 1 - 2.0 ** -10)
+    hk, hq, d, lens = 2, 6, 64, [1, 16, 17, 100, 128, 130, 1031, 20000]
+    g = torch.Generator().manual_seed(5)
+    ks = rows(lens, hk, d, dtype, 6)
+    for kind in range(3):
+        q = rows([len(lens)], hq, d, dtype, 7)[0].float() * (0.0 if kind < 2 else 0.3)
+        vs = []
+        for L in lens:
+            v = torch.full((L, hk, d), top, dtype=torch.float64)
+            if kind:
+                v *= 1 - torch.rand((L, hk, d), generator=g, dtype=torch.float64) / 2
+            v[:, 1] *= -1
+            if kind == 2:
+                v[::2] *= -1
+            vs.append(v.to(dtype))
+        _, out, lse = decode(attn, gdn, q, ks, vs, block, code, dtype)
+        for i, L in enumerate(lens):
+            k, v = expect(ks[i], block, code, F32), expect(vs[i], block, code, F32)
+            assert v.isfinite().all()
+            r = reference(q[i:i + 1].to(dtype), k, v, L, dtype)
+            assert A.worst(out[i:i + 1], r["out"], r["tol"]["out"]) <= 1, (kind, i, L)
+            assert A.worst(lse[i:i + 1], r["lse"], r["tol"]["lse"]) <= 1, (kind, i, L)
+
+
+@pytest.mark.parametrize("code", ["int8", "e4m3"])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_small_values_keep_their_bits(attn, gdn, dtype, code):
+    """Down to what the cache holds as more than zeros, 2^-100, over many keys."""
+    hk, hq, d, lens = 1, 3, 64, [1, 16, 100, 3000, 20000]
+    ks, q = rows(lens, hk, d, dtype, 6), rows([len(lens)], hq, d, dtype, 7)[0]
+    for size in (2.0 ** -100, 2.0 ** -96, 2.0 ** -80):
+        vs = [(size * (1 + x.float().abs())).to(dtype) for x in rows(lens, hk, d, dtype, 8)]
+        _, out, _ = decode(attn, gdn, q, ks, vs, 16, code, dtype)
+        for i, L in enumerate(lens):
+            k, v = (expect(x[i], 16, code, F32) for x in (ks, vs))
+            # in units of 2^-60, beside which what is added to a bound for sums of 0 is nothing
+            r = reference(q[i:i + 1], k, v.double() * 2.0 ** 60, L, dtype)
+            assert A.worst(out[i:i + 1].double() * 2.0 ** 60, r["out"], r["tol"]["out"]) <= 1, (size, i, L)
