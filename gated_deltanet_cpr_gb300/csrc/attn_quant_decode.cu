@@ -145,10 +145,6 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 x = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&x);
 }
-__device__ __forceinline__ uint32_t f16_to_bf16(uint32_t x) {
-  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&x));
-  return pack_bf16(f.x, f.y);
-}
 // 2^e
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 // For values of largest magnitude m: e so that they times 2^-e stay below 2^15 and the largest reaches 2^14 (unless
@@ -252,12 +248,12 @@ struct QuantEngine : Quant {
       const uint32_t which = __ballot_sync(0xffffffffu, odd);
       const bool any = (which >> (4 * g)) & 15u;  // an infinity or a NaN in this head's row
       const int e = any ? 0 : f16_exponent(mx);
-      const float down = pow2(-e), f = any ? __builtin_nanf("") : __fmul_rn(scale, pow2(e));
+      const float by = pow2(-e), f = any ? __builtin_nanf("") : __fmul_rn(scale, pow2(e));
 #pragma unroll
       for (int s = 0; s < KS; ++s)
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
-          const float lo = any ? 0.f : __fmul_rn(x[s][2 * b], down), hi = any ? 0.f : __fmul_rn(x[s][2 * b + 1], down);
+          const float lo = any ? 0.f : __fmul_rn(x[s][2 * b], by), hi = any ? 0.f : __fmul_rn(x[s][2 * b + 1], by);
           q[0][s][h][b] = pack_f16(lo, hi);
           if constexpr (SPLIT) q[1][s][h][b] = pack_f16_rest(lo, hi, q[0][s][h][b]);
         }
@@ -276,19 +272,21 @@ struct QuantEngine : Quant {
         for (int e = 0; e < 4; ++e) o[j][h][e] = 0.f;
   }
 
-  // Products x of G granules with their keys, the first `rows` from key[i] on, to probabilities, with the running
-  // maximum and sum.
+  // Products of a granule's keys, whose scale is ks, to scores.
+  __device__ __forceinline__ void scores(float ks, float (&x)[NH][4]) const {
+#pragma unroll
+    for (int h = 0; h < NH; ++h) {
+      const float f[2] = {__fmul_rn(ks, qs[h][0]), __fmul_rn(ks, qs[h][1])};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[h][e] = __fmul_rn(x[h][e], f[e & 1]);
+    }
+  }
+  // Scores x of G granules, the first `rows` of each from key[i] on, to probabilities, with the running maximum and sum.
   template <int G>
-  __device__ __forceinline__ void softmax(const QuantDecode& a, const float (&ks)[G], bool full, const int (&key)[G],
-                                          int rows, int len, float (&x)[G][NH][4], int lane) {
+  __device__ __forceinline__ void softmax(const QuantDecode& a, bool full, const int (&key)[G], int rows, int len,
+                                          float (&x)[G][NH][4], int lane) {
 #pragma unroll
     for (int i = 0; i < G; ++i) {
-#pragma unroll
-      for (int h = 0; h < NH; ++h) {
-        const float f[2] = {__fmul_rn(ks[i], qs[h][0]), __fmul_rn(ks[i], qs[h][1])};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[i][h][e] = __fmul_rn(x[i][h][e], f[e & 1]);
-      }
       if (!full) {  // some may not be visible
         const int lo = a.window > 0 ? len - a.window : 0;
 #pragma unroll
@@ -390,7 +388,7 @@ struct QuantEngine : Quant {
         }
       }
     load_all<G, true, SIDE>(at, r);
-    float ks[G], vs[G];
+    float vs[G];
     int key[G];
 #pragma unroll
     for (int b = 0; b < G; ++b) {
@@ -398,11 +396,11 @@ struct QuantEngine : Quant {
       for (int h = 0; h < NH; ++h)
 #pragma unroll
         for (int e = 0; e < 4; ++e) x[b][h][e] = __fadd_rn(x[b][h][e], y[b][h][e]);
-      ks[b] = meta.ks[i + b];
+      scores(meta.ks[i + b], x[b]);
       vs[b] = __fmul_rn(meta.vs[i + b], E4M3 ? __fmul_rn(down, kDownP) : down);
       key[b] = meta.key + ((i + b) << kGranuleShift) + (i + b >= meta.skip_from ? meta.skip : 0);
     }
-    softmax<G>(a, ks, full, key, kGranule, len, x, lane);
+    softmax<G>(a, full, key, kGranule, len, x, lane);
     uint32_t p[G][NH][P][2];
 #pragma unroll
     for (int b = 0; b < G; ++b)
@@ -447,12 +445,16 @@ struct QuantEngine : Quant {
     }
   }
 
-  // Keys key .. key + TAIL_ROWS - 1 of the tail.  bf16 rows are operands as they are, with q in bf16 (its f16 form has
-  // no more bits) and P as the sum of two bf16.
-  __device__ __forceinline__ void tail_bf16(const QuantDecode& a, const unsigned char* stage, int key, int len, int lane) {
+  // Keys key .. key + TAIL_ROWS - 1 of the tail.  bf16 rows are operands as they are, with the rows of q (read again: scaled
+  // to f16's range they would overflow with keys of 2^106) and with P as the sum of two bf16.
+  __device__ __forceinline__ void tail_bf16(const QuantDecode& a, const unsigned char* stage, int key, int len, int64_t row,
+                                            int heads, int lane) {
     const int g = lane >> 2, t = lane & 3;
+    const float scale = __fmul_rn(a.scale, kLog2e);
     float xs[1][NH][4];
     float(&x)[NH][4] = xs[0];
+    const Elem* src = static_cast<const Elem*>(a.q) + (row + g) * D + 4 * t;
+    uint32_t odd = 0;  // an exponent of ones in either half carries into its upper bit
 #pragma unroll
     for (int s = 0; s < KS; ++s) {
       uint32_t k[4] = {0, 0, 0, 0};
@@ -462,20 +464,23 @@ struct QuantEngine : Quant {
         const uint2 u = *reinterpret_cast<const uint2*>(stage + place_tail(g + 8 * r, at >> 4) + (at & 15));
         k[r] = u.x;
         k[r + 2] = u.y;
+        odd |= ((u.x & 0x7fff7fffu) + 0x00800080u) | ((u.y & 0x7fff7fffu) + 0x00800080u);
       }
 #pragma unroll
       for (int h = 0; h < NH; ++h) {
-        const uint32_t b0 = f16_to_bf16(q[0][s][h][0]), b1 = f16_to_bf16(q[0][s][h][1]);
+        uint2 u = make_uint2(0u, 0u);
+        if (g + 8 * h < heads) u = *reinterpret_cast<const uint2*>(src + (8 * h) * D + 16 * s);
         if (s == 0) x[h][0] = x[h][1] = x[h][2] = x[h][3] = 0.f;
-        tc::mma16816(x[h], k, b0, b1);
+        tc::mma16816(x[h], k, u.x, u.y);
       }
     }
-    // a key that is not finite gives NaN, not a weight of 0
+    // a key that is not finite gives NaN, not a weight of 0, and so does a query
+    const float by = __any_sync(0xffffffffu, odd & 0x80008000u) ? __builtin_nanf("") : scale;
 #pragma unroll
     for (int h = 0; h < NH; ++h)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) x[h][e] = __fmaf_rn(x[h][e], 0.f, x[h][e]);
-    softmax<1>(a, {1.f}, false, {key}, TAIL_ROWS, len, xs, lane);
+      for (int e = 0; e < 4; ++e) x[h][e] = __fmul_rn(x[h][e], qs[h][e & 1] == qs[h][e & 1] ? by : qs[h][e & 1]);
+    softmax<1>(a, false, {key}, TAIL_ROWS, len, xs, lane);
 #pragma unroll
     for (int h = 0; h < NH; ++h)
 #pragma unroll
@@ -557,7 +562,8 @@ struct QuantEngine : Quant {
     for (int h = 0; h < NH; ++h)
 #pragma unroll
       for (int e = 0; e < 4; ++e) x[h][e] = __fadd_rn(x[h][e], ys[h][e]);
-    softmax<1>(a, {km == km ? pow2(ke) : km}, false, {key}, TAIL_ROWS, len, xs, lane);
+    scores(km == km ? pow2(ke) : km, x);
+    softmax<1>(a, false, {key}, TAIL_ROWS, len, xs, lane);
     uint32_t b[NH][P][2];
 #pragma unroll
     for (int h = 0; h < NH; ++h) operand(x[h], b[h]);
@@ -879,7 +885,10 @@ __global__ void __launch_bounds__(32 * DecodeSmem<E>::WARPS, 1) k_quant_decode(c
         }
       } else {
         if constexpr (E::SPLIT) eng.tail_f32(a, stage, meta.key, len, lane);
-        else eng.tail_bf16(a, stage, meta.key, len, lane);
+        else {
+          const int g0 = (r.y % parts) * kHeadsPerRun;
+          eng.tail_bf16(a, stage, meta.key, len, (int64_t)r.i * a.hq + (r.y / parts) * group + g0, min(kHeadsPerRun, group - g0), lane);
+        }
       }
       get = get + 1 == E::RING ? 0 : get + 1;
       __syncwarp();

@@ -1,5 +1,6 @@
 """Decode attention over the 8-bit cache at the ends of its range, against plain attention in 64 bits over what the cache
-holds: scores that leave no fraction in fp32, values up to the type's largest."""
+holds: scores that leave no fraction in fp32, values up to the type's largest, keys far from 1 in an unfinished
+block."""
 import pytest
 import torch
 
@@ -134,3 +135,37 @@ def test_small_values_keep_their_bits(attn, gdn, dtype, code):
             # in units of 2^-60, beside which what is added to a bound for sums of 0 is nothing
             r = reference(q[i:i + 1], k, v.double() * 2.0 ** 60, L, dtype)
             assert A.worst(out[i:i + 1].double() * 2.0 ** 60, r["out"], r["tol"]["out"]) <= 1, (size, i, L)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("block", [16, 128])
+def test_keys_of_any_size(attn, gdn, block, dtype):
+    """Keys far from 1 with queries that make up for it, in an unfinished block and, a token later, in a whole one."""
+    hk, hq, d = 2, 6, 64
+    lens = [1, 7, 15, 16, 100, 127, 128, 300]
+    for fq, fk in ((1e-36, 1e36), (1e-33, 3e33), (1e34, 1e-34), (1e-35, 3e35)):
+        q = (rows([len(lens)], hq, d, dtype, 9)[0].float() * fq).to(dtype)
+        ks = [(x.float() * fk).to(dtype) for x in rows(lens, hk, d, dtype, 1)]
+        vs = rows(lens, hk, d, dtype, 2)
+        assert all(k.isfinite().all() for k in ks)
+        for code in ("int8", "e4m3"):
+            s, out, lse = decode(attn, gdn, q, ks, vs, block, code, dtype, page=64)
+            for i, L in enumerate(lens):
+                r = reference(q[i:i + 1], expect(ks[i], block, code, F32), expect(vs[i], block, code, F32), L, dtype)
+                assert A.worst(out[i:i + 1], r["out"], r["tol"]["out"]) <= 1, (fq, code, i, L)
+                assert A.worst(lse[i:i + 1], r["lse"], r["tol"]["lse"]) <= 1, (fq, code, i, L)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_a_key_that_is_not_finite_gives_nan_in_a_tail(attn, gdn, dtype):
+    """Of either sign and whatever its weight would be: its request's rows, and none of the others'."""
+    lens, hk, hq, d = [9, 40, 23], 2, 6, 64
+    ks, vs, q = rows(lens, hk, d, dtype, 1), rows(lens, hk, d, dtype, 2), rows([3], hq, d, dtype, 3)[0]
+    _, ref, _ = decode(attn, gdn, q, ks, vs, 16, "int8", dtype)
+    for bad in (float("inf"), -float("inf"), float("nan")):
+        for at in ([8], [2, 5]):
+            bent = [k.clone() for k in ks]
+            for j in at:
+                bent[0][j, 1, 11] = bad
+            _, out, _ = decode(attn, gdn, q, bent, vs, 16, "int8", dtype)
+            assert out[0, 3:].isnan().all() and torch.equal(out[0, :3], ref[0, :3]) and torch.equal(out[1:], ref[1:])
