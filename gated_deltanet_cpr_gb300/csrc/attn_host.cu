@@ -198,8 +198,8 @@ gdn_status quant_rows_args(const gdn_cpr_quant_cache* c, int32_t N, int32_t T, c
   if (rc != GDN_OK) return rc;
   if (N > 65535) return GDN_ERR_UNSUPPORTED;
   const QuantCache q = quant_view(c);
-  // a warp or more for each piece (a block to append, a granule to read) of each head of k and v, in 31 bits
-  if ((double)quant_pieces(N, T, by_block ? q.block_shift : kGranuleShift) * 2 * c->h_kv >= 2147483648.0) return GDN_ERR_UNSUPPORTED;
+  // a piece is a block to append, a granule to read
+  if (!quant_units_fit(N, T, by_block ? q.block_shift : kGranuleShift, c->h_kv)) return GDN_ERR_UNSUPPORTED;
   if (N > 0 && (!ok_ptr(cu, 4) || !ok_ptr(seq_lens, 4) || !aligned(slot, 4))) return GDN_ERR_INVALID_ARG;
   if (N > 0 && max_blocks > 0 && !ok_ptr(block_table, 4)) return GDN_ERR_INVALID_ARG;
   if (ws && !ok_ws(ws, ws_bytes, GDN_CPR_ATTN_HEADER_BYTES)) return GDN_ERR_WORKSPACE;

@@ -28,6 +28,13 @@ inline Divide divide_by(uint32_t d) {
   while ((uint64_t)1 << l < d) ++l;
   return {(uint32_t)(((uint64_t)1 << (31 + l)) / d + 1), l - 1};
 }
+__host__ __device__ inline uint32_t divide(uint32_t n, Divide d) {
+#ifdef __CUDA_ARCH__
+  return __umulhi(n, d.mul) >> d.shift;
+#else
+  return (uint32_t)((uint64_t)n * d.mul >> 32) >> d.shift;
+#endif
+}
 
 // What append and read share: request n has rows cu[n] .. cu[n + 1] of the packed tensors, which are the last
 // ones of its seq_lens[n] positions.
@@ -47,6 +54,18 @@ struct QuantRows {
 inline int64_t quant_pieces(int N, int T, int shift) { return (int64_t)(T >> shift) + 2 * (int64_t)N; }
 // With few rows a request it is fewer to number every row, and to leave out those that do not begin a piece.
 inline bool quant_by_token(int N, int T, int shift) { return T < quant_pieces(N, T, shift); }
+// A unit is a piece of one head of k or v, one warp's or, in append, block / 16 warps'; units are numbered in 31 bits, a piece's
+// side by side.  Calls of more are refused.
+inline bool quant_units_fit(int N, int T, int shift, int hkv) { return quant_pieces(N, T, shift) * 2 * hkv < (int64_t)1 << 31; }
+inline int64_t quant_units(int N, int T, int shift, int hkv) {
+  return (quant_by_token(N, T, shift) ? T : quant_pieces(N, T, shift)) * 2 * hkv;
+}
+// CTAs of `threads` for them, where a unit takes `each` warps, and one before them that checks the call
+inline int64_t quant_blocks(int64_t units, int each, int threads) { return 1 + (units * each + threads / 32 - 1) / (threads / 32); }
+// the unit that a warp of CTA `block` (not counting the first) takes; units and more of them behind the last have no piece
+__host__ __device__ inline uint32_t quant_unit(uint32_t block, int threads, int warp, int each_shift) {
+  return block * (uint32_t)(threads >> (5 + each_shift)) + (uint32_t)(warp >> each_shift);
+}
 
 // Decode attention: a request's visible keys are counted in granules that hold any.
 struct QuantDecode : PagedDecode {

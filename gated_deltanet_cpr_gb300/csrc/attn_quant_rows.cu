@@ -33,8 +33,6 @@ __device__ __forceinline__ int request_of(const int32_t* cu, int N, int shift, i
   return lo;
 }
 
-__device__ __forceinline__ uint32_t divide(uint32_t n, Divide d) { return __umulhi(n, d.mul) >> d.shift; }
-
 // A piece of a request: `1 << shift` positions from `first` on.
 struct Piece {
   int n, j;             // request, number of the piece in it
@@ -246,7 +244,7 @@ __global__ void __launch_bounds__(kMostThreads) k_quant_append(const QuantRows a
   const int each_shift = c.block_shift - kGranuleShift, each = 1 << each_shift;  // warps of a unit
   const int part = warp & (each - 1);                                            // this one's rows of it
   const uint32_t pieces = a.by_token ? (uint32_t)a.T : (uint32_t)(a.T >> c.block_shift) + 2u * (uint32_t)a.N;
-  const uint32_t all = 2u * (uint32_t)c.hkv, unit = (blockIdx.x - 1) * (blockDim.x >> (5 + each_shift)) + (uint32_t)(warp >> each_shift);
+  const uint32_t all = 2u * (uint32_t)c.hkv, unit = quant_unit(blockIdx.x - 1, (int)blockDim.x, warp, each_shift);
   const uint32_t w = divide(unit, a.heads), rest = unit - w * all;
   const int h = (int)(rest >> 1);
   const bool is_v = rest & 1;
@@ -360,7 +358,7 @@ __global__ void __launch_bounds__(kThreads) k_quant_read(const QuantRows a) {
   const QuantCache& c = a.c;
   const int lane = threadIdx.x & 31;
   const uint32_t units = (a.by_token ? (uint32_t)a.T : (uint32_t)(a.T / kGranule) + 2u * (uint32_t)a.N) * 2u * (uint32_t)c.hkv;
-  const uint32_t unit = (blockIdx.x - 1) * (uint32_t)(kThreads / 32) + (threadIdx.x >> 5);
+  const uint32_t unit = quant_unit(blockIdx.x - 1, kThreads, (int)(threadIdx.x >> 5), 0);
   if (unit < units) {
     const uint32_t w = divide(unit, a.heads), rest = unit - w * 2u * (uint32_t)c.hkv;
     const int h = (int)(rest >> 1);
@@ -444,7 +442,7 @@ __global__ void k_quant_clear(WsHeader* hdr) {
 }
 
 template <typename K>
-int launch(K* kernel, const QuantRows& a, int64_t warps, int threads, cudaStream_t st) {
+int launch(K* kernel, const QuantRows& a, int64_t units, int each, int threads, cudaStream_t st) {
   if (a.hdr) k_quant_clear<<<1, 1, 0, st>>>(a.hdr);
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -453,7 +451,7 @@ int launch(K* kernel, const QuantRows& a, int64_t warps, int threads, cudaStream
   c.stream = st;
   c.attrs = &attr;
   c.numAttrs = a.hdr ? 1 : 0;
-  c.gridDim = dim3((unsigned)(1 + (warps + threads / 32 - 1) / (threads / 32)));
+  c.gridDim = dim3((unsigned)quant_blocks(units, each, threads));
   c.blockDim = dim3(threads);
   cudaLaunchKernelEx(&c, kernel, a);
   return a.hdr ? 2 : 1;
@@ -464,16 +462,16 @@ int append_t(QuantRows a, cudaStream_t st) {
   const int each = (1 << a.c.block_shift) / kGranule;  // warps of a unit
   a.by_token = quant_by_token(a.N, a.T, a.c.block_shift);
   a.heads = divide_by(2u * (uint32_t)a.c.hkv);
-  const int64_t units = (a.by_token ? a.T : quant_pieces(a.N, a.T, a.c.block_shift)) * 2 * a.c.hkv;
-  return launch(k_quant_append<D, T>, a, units * each, std::max(kThreads, 32 * each), st);
+  const int64_t units = quant_units(a.N, a.T, a.c.block_shift, a.c.hkv);
+  return launch(k_quant_append<D, T>, a, units, each, std::max(kThreads, 32 * each), st);
 }
 
 template <int D, typename T, typename TO>
 int read_t(QuantRows a, cudaStream_t st) {
   a.by_token = quant_by_token(a.N, a.T, kGranuleShift);
   a.heads = divide_by(2u * (uint32_t)a.c.hkv);
-  const int64_t units = (a.by_token ? a.T : quant_pieces(a.N, a.T, kGranuleShift)) * 2 * a.c.hkv;
-  return launch(k_quant_read<D, T, TO>, a, units, kThreads, st);
+  const int64_t units = quant_units(a.N, a.T, kGranuleShift, a.c.hkv);
+  return launch(k_quant_read<D, T, TO>, a, units, 1, kThreads, st);
 }
 
 template <int D>
