@@ -281,7 +281,7 @@ __global__ void __launch_bounds__(kMostThreads) k_quant_append(const QuantRows a
     const T* s = src + (int64_t)(p.cu0 + (int)(p.first + (uint32_t)r0 - p.begin)) * stride;
 #pragma unroll
     for (int i = 0; i < PASSES; ++i) x[i] = *reinterpret_cast<const uint4*>(s + i * RPP * stride);
-  } else if (p.on) {
+  } else if (whole || (p.on && p.j == 0)) {  // an unfinished block that is not the first is the first one's unit's to write, below
     load(p.first, whole);
   }
   if (whole) {
