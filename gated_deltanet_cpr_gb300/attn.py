@@ -22,6 +22,7 @@ LAYOUTS = {"half": 0, "interleaved": 1}
 CODES = {"int8": torch.int8, "e4m3": torch.float8_e4m3fn}
 _CODE_OF = {torch.int8: 0, torch.float8_e4m3fn: 1}
 HEADER_BYTES = 256
+_PLAIN = frozenset((int, float, type(None)))
 
 
 class NormRopeStruct(ctypes.Structure):
@@ -150,6 +151,11 @@ def _opt(x, shape, dtype, name):
     return None if x is None else _want(x, shape, dtype, name)
 
 
+def _value(x):
+    """A number by value: descriptions are kept by their numbers, and a tensor is equal to itself whatever it holds now."""
+    return x if type(x) in _PLAIN or not hasattr(x, "item") else x.item()
+
+
 def _clip(x):
     """A window, a count of first tokens or a bound on lengths, in 32 bits: lengths have no more, so anything
     past them means the same; negative ones stay so, for the library to refuse."""
@@ -199,7 +205,7 @@ def _norm_rope_struct(q, k, v, norm, eps, cos, sin, positions, layout, out_dtype
     vp, vs = (None, hk * d) if v is None else _rows(v, hk, d, "v")
     if v is not None and v.shape[0] != T:
         raise ValueError("q, k and v have the same tokens and dtype")
-    return _norm_rope_desc(T, hq, hk, d, rot, rows, norm, layout, eps, q.dtype, out_dtype, grad_dtype, qs, ks, vs), \
+    return _norm_rope_desc(T, hq, hk, d, rot, rows, norm, layout, _value(eps), q.dtype, out_dtype, grad_dtype, qs, ks, vs), \
         qp, kp, vp, cp, sp, pp
 
 
@@ -319,9 +325,10 @@ def paged_decode(q, cache: PagedCache, block_table, seq_lens, *, window=0, sinks
     blocks = table[1]
     if max_len is None:
         max_len = blocks * cache.page_size
+    max_len = _value(max_len)
     if not 0 <= max_len < 2 ** 31:
         max_len = _clip(max_len)
-    desc = (hq, cache.h_kv, d, window, sinks, scale, dtype)
+    desc = (hq, cache.h_kv, d, _value(window), _value(sinks), _value(scale), dtype)
     qp = _want(q, shape, dtype, "q")
     if out is None:
         out = torch.empty_like(q)
@@ -424,9 +431,10 @@ def quant_decode(q, cache: QuantCache, block_table, seq_lens, *, slots=None, win
         raise ValueError("q has a row and seq_lens a length for every request")
     if max_len is None:
         max_len = width * cache.page_size
+    max_len = _value(max_len)
     if not 0 <= max_len < 2 ** 31:
         max_len = _clip(max_len)
-    desc, nbytes = _quant_desc(N, max_len, hq, cache.h_kv, d, window, sinks, scale, dtype)
+    desc, nbytes = _quant_desc(N, max_len, hq, cache.h_kv, d, _value(window), _value(sinks), _value(scale), dtype)
     if out is None:
         out = torch.empty_like(q)
         op = out.data_ptr()
@@ -449,7 +457,7 @@ def _window_setup(q, k, v, cu_q, cu_k, window, sinks, scale, backward, ws):
     N = cu_q.numel() - 1
     cu_k = cu_q if cu_k is None else cu_k
     dtype, shape = q.dtype, (Tk, hkv, d)
-    desc = (hq, hkv, d, window, sinks, scale, dtype)
+    desc = (hq, hkv, d, _value(window), _value(sinks), _value(scale), dtype)
     offsets = _want(cu_q, (N + 1,), torch.int32, "cu_seqlens")
     args = (ctypes.byref(_attn_struct(*desc)), N, Tq, Tk, offsets,
             offsets if cu_k is cu_q else _want(cu_k, (N + 1,), torch.int32, "cu_seqlens_k"),
