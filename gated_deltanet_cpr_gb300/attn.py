@@ -179,6 +179,13 @@ def _bytes(fn, *args):
     return n.value
 
 
+def _given(ws, device):
+    """(pointer, bytes) of a workspace that the caller gives: the kernels write to it."""
+    if ws.device != device or not ws.is_contiguous():
+        raise ValueError(f"ws is on {ws.device}{'' if ws.is_contiguous() else ', not contiguous'}; expected on {device}")
+    return ws.data_ptr(), ws.numel()
+
+
 def _workspace(x, nbytes):
     return torch.empty(nbytes, dtype=torch.uint8, device=x.device)
 
@@ -259,7 +266,7 @@ def qk_norm_rope_bwd(q, k, dq_out, dk_out, *, norm="rms", q_weight=None, k_weigh
         dwq, dwk = out["dq_weight"].data_ptr(), out["dk_weight"].data_ptr()
         if ws is None:
             ws = _workspace(q, _bytes("gdn_cpr_qk_norm_rope_workspace_size", ctypes.byref(st)))
-        wp, nbytes = ws.data_ptr(), ws.numel()
+        wp, nbytes = _given(ws, dev)
     _check("gdn_cpr_qk_norm_rope_bwd", api.load().gdn_cpr_qk_norm_rope_bwd(
         ctypes.byref(st), qp, kp, _opt(q_weight, (d,), torch.float32, "q_weight"),
         _opt(k_weight, (d,), torch.float32, "k_weight"), cp, sp, pp, _want(dq_out, (T, hq, d), gd, "dq_out"),
@@ -343,7 +350,7 @@ def paged_decode(q, cache: PagedCache, block_table, seq_lens, *, window=0, sinks
         ctypes.byref(_attn_struct(*desc)), N, max_len, qp, kp, vp, cache.pages, cache.page_size,
         _want(block_table, table, torch.int32, "block_table"), blocks,
         _want(seq_lens, (N,), torch.int32, "seq_lens"), op,
-        None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.numel(), _raw_stream(device.index)))
+        None if lse is None else lse.data_ptr(), *_given(ws, device), _raw_stream(device.index)))
     return (out, lse) if want_lse else out
 
 
@@ -383,7 +390,7 @@ def quant_append(k, v, cache: QuantCache, block_table, seq_lens, cu_seqlens, *, 
     N, table, width, lens, slot = _quant_requests(cache, block_table, seq_lens, slots)
     kp, ks = _rows(k, hkv, cache.d, "k")
     vp, vs = _rows(v, hkv, cache.d, "v")
-    wp, nbytes = (None, 0) if ws is None else (ws.data_ptr(), ws.numel())
+    wp, nbytes = (None, 0) if ws is None else _given(ws, device)
     _check("gdn_cpr_quant_append", api.load().gdn_cpr_quant_append(
         cache._ref, N, T, kp, vp, ks, vs, _at(cu_seqlens, (N + 1,), torch.int32, "cu_seqlens", device), lens, table,
         width, slot, wp, nbytes, _raw_stream(device.index)))
@@ -411,7 +418,7 @@ def quant_read(cache: QuantCache, block_table, seq_lens, cu_seqlens, total_token
         vp = v_out.data_ptr()
     else:
         vp = _at(v_out, shape, od, "v_out", device)
-    wp, nbytes = (None, 0) if ws is None else (ws.data_ptr(), ws.numel())
+    wp, nbytes = (None, 0) if ws is None else _given(ws, device)
     _check("gdn_cpr_quant_read", api.load().gdn_cpr_quant_read(
         cache._ref, N, T, _at(cu_seqlens, (N + 1,), torch.int32, "cu_seqlens", device), lens, table, width, slot,
         _dt(od), kp, vp, wp, nbytes, _raw_stream(device.index)))
@@ -443,11 +450,12 @@ def quant_decode(q, cache: QuantCache, block_table, seq_lens, *, slots=None, win
     lse = torch.empty((N, hq), dtype=torch.float32, device=device) if want_lse else None
     if ws is None:
         ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        wp = ws.data_ptr()
     else:
-        nbytes = ws.numel()
+        wp, nbytes = _given(ws, device)
     _check("gdn_cpr_quant_decode", api.load().gdn_cpr_quant_decode(
         desc, cache._ref, N, max_len, qp, table, width, lens, slot, op, None if lse is None else lse.data_ptr(),
-        ws.data_ptr(), nbytes, _raw_stream(device.index)))
+        wp, nbytes, _raw_stream(device.index)))
     return (out, lse) if want_lse else out
 
 
@@ -478,8 +486,8 @@ def window_attn(q, k, v, cu_seqlens, *, cu_seqlens_k=None, window=0, sinks=0, sc
     if lse is None:
         lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
     _check("gdn_cpr_window_attn", api.load().gdn_cpr_window_attn(
-        *args, _want(out, q.shape, q.dtype, "out"), _want(lse, q.shape[:2], torch.float32, "lse"), ws.data_ptr(),
-        ws.numel(), _raw_stream(q.device.index)))
+        *args, _want(out, q.shape, q.dtype, "out"), _want(lse, q.shape[:2], torch.float32, "lse"),
+        *_given(ws, q.device), _raw_stream(q.device.index)))
     return out, lse
 
 
@@ -490,5 +498,5 @@ def window_attn_bwd(q, k, v, out, lse, dout, cu_seqlens, *, cu_seqlens_k=None, w
     _check("gdn_cpr_window_attn_bwd", api.load().gdn_cpr_window_attn_bwd(
         *args, _want(out, q.shape, q.dtype, "out"), _want(lse, q.shape[:2], torch.float32, "lse"),
         _want(dout, q.shape, q.dtype, "dout"), g["dq"].data_ptr(), g["dk"].data_ptr(), g["dv"].data_ptr(),
-        ws.data_ptr(), ws.numel(), _raw_stream(q.device.index)))
+        *_given(ws, q.device), _raw_stream(q.device.index)))
     return g

@@ -1,0 +1,13 @@
+"""The attention-layer binding without a GPU: what a caller gives beside the tensors that the kernels read."""
+import pytest
+import torch
+
+from gated_deltanet_cpr_gb300 import attn
+
+
+def test_a_workspace_is_memory_of_the_calls_device():
+    host = torch.empty(512, dtype=torch.uint8)
+    assert attn._given(host, host.device) == (host.data_ptr(), 512)
+    for ws, device in ((host, torch.device("cuda", 0)), (host[:1].expand(512), host.device), (host.view(2, 256).t(), host.device)):
+        with pytest.raises(ValueError, match="ws is on"):
+            attn._given(ws, device)

@@ -34,3 +34,26 @@ def test_numbers_given_as_tensors_count_as_they_are_now(attn, gdn):
             at[name].fill_(x)
         for a, b in zip(calls(**at), calls(scale=scale, window=window, sinks=sinks, max_len=bound)):
             assert torch.equal(a, b)
+
+
+def test_workspaces_that_the_kernels_could_not_write_are_refused(attn, gdn):
+    """On the host, or one byte repeated: refused before anything is queued, by every call that takes one."""
+    lens, hq, hk, d = [20, 33], 4, 2, 64
+    q, k, v = (torch.cat(rows(lens, h, d, BF, h)).cuda() for h in (hq, hk, hk))
+    s = Store(attn, gdn, lens, hk, d, 32, 16, "int8", BF)
+    p = attn.PagedCache(s.cache.pages, 32, hk, d)
+    cu, n, w = offsets(lens), ints(lens), torch.ones(d, device="cuda")
+    out, lse = attn.window_attn(q, k, v, cu)
+    calls = [lambda ws: attn.quant_append(k, v, s.cache, s.table, n, cu, slots=s.slots, ws=ws),
+             lambda ws: attn.quant_read(s.cache, s.table, n, cu, sum(lens), slots=s.slots, ws=ws),
+             lambda ws: attn.quant_decode(q[:2], s.cache, s.table, n, slots=s.slots, ws=ws),
+             lambda ws: attn.paged_decode(q[:2], p, s.table, n, ws=ws),
+             lambda ws: attn.window_attn(q, k, v, cu, ws=ws),
+             lambda ws: attn.window_attn_bwd(q, k, v, out, lse, out, cu, ws=ws),
+             lambda ws: attn.qk_norm_rope_bwd(q, k, q, k, q_weight=w, k_weight=w, ws=ws)]
+    before = s.state()
+    for ws in (torch.empty(1 << 20, dtype=torch.uint8), torch.empty(1, dtype=torch.uint8, device="cuda").expand(1 << 20)):
+        for i, call in enumerate(calls):
+            with pytest.raises(ValueError, match="ws is on"):
+                call(ws)
+    assert all(torch.equal(a, b) for a, b in zip(before, s.state()))
