@@ -72,7 +72,10 @@ class QuantCache:
     """Key-value cache in 8 bits: k, v [pages, H_kv, page_size, d] codes (int8 or float8_e4m3fn), k_scale, v_scale
     [pages, H_kv, page_size / block] fp32, one scale for `block` tokens of a head, and k_tail, v_tail [slots, H_kv,
     block, d] in dtype, where a request's last tokens wait, as they came, until they fill a block.  A request keeps
-    its slot while it lives, as in api.Cache; the tensors stay those that the cache was made with."""
+    its slot while it lives, as in api.Cache; the tensors stay those that the cache was made with: calls go to their
+    memory, so that they cannot be replaced."""
+
+    k, v, k_scale, v_scale, k_tail, v_tail = (property(lambda self, i=i: self._tensors[i]) for i in range(6))
 
     def __init__(self, pages, page_size, h_kv, d, slots, *, code="int8", block=16, dtype=torch.bfloat16, device="cuda"):
         if block <= 0 or page_size % block:
@@ -99,7 +102,7 @@ class QuantCache:
         if code is None or block <= 0 or page_size % block or tail_heads != hkv or tail_d != d:
             raise ValueError("pages hold int8 or float8_e4m3fn codes of whole blocks of the tails' heads and size")
         self.pages, self.h_kv, self.page_size, self.d, self.slots, self.block = n, hkv, page_size, d, slots, block
-        self.k, self.v, self.k_scale, self.v_scale, self.k_tail, self.v_tail = k, v, k_scale, v_scale, k_tail, v_tail
+        self._tensors = k, v, k_scale, v_scale, k_tail, v_tail
         self.dtype, self.device = dtype, at
         scales, f32 = (n, hkv, page_size // block), torch.float32
         self.struct = QuantCacheStruct(
