@@ -515,37 +515,45 @@ struct QuantEngine : Quant {
     }
   }
 
-  // Largest magnitude of a tail tile's keys or values: NaN where one of them is not finite.
-  __device__ __forceinline__ static float tail_max(const unsigned char* side, int lane) {
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < TAIL_ROWS * TAILB / 512; ++i) {
-      const uint4 u = *reinterpret_cast<const uint4*>(side + 512 * i + 16 * lane);
-      m = max(max(max(m, u.x & 0x7fffffffu), max(u.y & 0x7fffffffu, u.z & 0x7fffffffu)), u.w & 0x7fffffffu);
-    }
-    m = __reduce_max_sync(0xffffffffu, m);
-    return m >= 0x7f800000u ? __builtin_nanf("") : __uint_as_float(m);
+  // f16_exponent of a row of A, from the bits of its four lanes' largest magnitudes.
+  __device__ __forceinline__ static int row_exponent(uint32_t m) {
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    return f16_exponent(__uint_as_float(m));
   }
-  // 0 where the tile is not finite: its scale says so
-  __device__ __forceinline__ static float scaled(float x, float down) { return down == 0.f ? 0.f : __fmul_rn(x, down); }
+  __device__ __forceinline__ static uint32_t magnitude(float x) { return __float_as_uint(x) & 0x7fffffffu; }
 
-  // The same of fp32 rows, which are scaled by powers of two to sums of two f16.
+  // The same of fp32 rows, as sums of two f16: a key's row is scaled by a power of two of its own, and so is a column of the
+  // values, so that small ones beside large ones keep their bits.  An infinity's second part is NaN, so that all that it
+  // would reach is.
   __device__ __forceinline__ void tail_f32(const QuantDecode& a, const unsigned char* stage, int key, int len, int lane) {
     const int g = lane >> 2, t = lane & 3;
-    const float km = tail_max(stage, lane), vm = tail_max(stage + SIDE, lane);
-    const int ke = f16_exponent(km), ve = f16_exponent(vm);
-    const float kd = km == km ? pow2(-ke) : 0.f, vd = vm == vm ? pow2(-ve) : 0.f;
-    const float vs = vm == vm ? __fmul_rn(pow2(ve), down) : vm;
-    float xs[1][NH][4], ys[NH][4];
+    float xs[1][NH][4], ys[NH][4], kd[2], ks[2];
     float(&x)[NH][4] = xs[0];
+    auto row_of = [&](int r, int s) {
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (g + 8 * r < TAIL_ROWS) v = *reinterpret_cast<const float4*>(stage + place_tail(g + 8 * r, 4 * s + t));
+      return v;
+    };
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      uint32_t most = 0;
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        const float4 v = row_of(r, s);
+        most = max(max(max(most, magnitude(v.x)), max(magnitude(v.y), magnitude(v.z))), magnitude(v.w));
+      }
+      const int e = row_exponent(most);
+      kd[r] = pow2(-e);
+      ks[r] = pow2(e);
+    }
 #pragma unroll
     for (int s = 0; s < KS; ++s) {
       uint32_t k[2][4];
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (g + 8 * r < TAIL_ROWS) v = *reinterpret_cast<const float4*>(stage + place_tail(g + 8 * r, 4 * s + t));
-        const float y[4] = {scaled(v.x, kd), scaled(v.y, kd), scaled(v.z, kd), scaled(v.w, kd)};
+        const float4 v = row_of(r, s);
+        const float y[4] = {__fmul_rn(v.x, kd[r]), __fmul_rn(v.y, kd[r]), __fmul_rn(v.z, kd[r]), __fmul_rn(v.w, kd[r])};
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
           k[0][r + 2 * b] = pack_f16(y[2 * b], y[2 * b + 1]);
@@ -561,8 +569,7 @@ struct QuantEngine : Quant {
 #pragma unroll
     for (int h = 0; h < NH; ++h)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) x[h][e] = __fadd_rn(x[h][e], ys[h][e]);
-    scores(km == km ? pow2(ke) : km, x);
+      for (int e = 0; e < 4; ++e) x[h][e] = __fmul_rn(__fadd_rn(x[h][e], ys[h][e]), __fmul_rn(ks[e >> 1], qs[h][e & 1]));
     softmax<1>(a, false, {key}, TAIL_ROWS, len, xs, lane);
     uint32_t b[NH][P][2];
 #pragma unroll
@@ -571,20 +578,33 @@ struct QuantEngine : Quant {
     for (int j = 0; j < KS; ++j) {
       uint32_t v[2][4];
       const int at = (16 * j + 2 * g) * 4;
+      float2 y[2][2];  // keys 2 t, 2 t + 1 and those + 8, of two columns
+      uint32_t most[2] = {0, 0};
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {  // keys 2 t, 2 t + 1 and those + 8
-        float2 y[2];
+      for (int r = 0; r < 2; ++r)
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
           const int row = 8 * r + 2 * t + w;
-          y[w] = make_float2(0.f, 0.f);
-          if (row < TAIL_ROWS) y[w] = *reinterpret_cast<const float2*>(stage + SIDE + place_tail(row, at >> 4) + (at & 15));
-          y[w] = make_float2(scaled(y[w].x, vd), scaled(y[w].y, vd));
+          y[r][w] = make_float2(0.f, 0.f);
+          if (row < TAIL_ROWS) y[r][w] = *reinterpret_cast<const float2*>(stage + SIDE + place_tail(row, at >> 4) + (at & 15));
+          most[0] = max(most[0], magnitude(y[r][w].x));
+          most[1] = max(most[1], magnitude(y[r][w].y));
         }
-        v[0][2 * r] = pack_f16(y[0].x, y[1].x);
-        v[0][2 * r + 1] = pack_f16(y[0].y, y[1].y);
-        v[1][2 * r] = pack_f16_rest(y[0].x, y[1].x, v[0][2 * r]);
-        v[1][2 * r + 1] = pack_f16_rest(y[0].y, y[1].y, v[0][2 * r + 1]);
+      float vd[2], vs[2];
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int e = row_exponent(most[c]);
+        vd[c] = pow2(-e);
+        vs[c] = __fmul_rn(pow2(e), down);
+      }
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const float2 lo = make_float2(__fmul_rn(y[r][0].x, vd[0]), __fmul_rn(y[r][1].x, vd[0]));
+        const float2 hi = make_float2(__fmul_rn(y[r][0].y, vd[1]), __fmul_rn(y[r][1].y, vd[1]));
+        v[0][2 * r] = pack_f16(lo.x, lo.y);
+        v[0][2 * r + 1] = pack_f16(hi.x, hi.y);
+        v[1][2 * r] = pack_f16_rest(lo.x, lo.y, v[0][2 * r]);
+        v[1][2 * r + 1] = pack_f16_rest(hi.x, hi.y, v[0][2 * r + 1]);
       }
 #pragma unroll
       for (int h = 0; h < NH; ++h) {
@@ -593,8 +613,8 @@ struct QuantEngine : Quant {
         mma_f16_from0(rest, v[0], b[h][P - 1][0], b[h][P - 1][1]);
         mma_f16(rest, v[1], b[h][0][0], b[h][0][1]);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) c[e] = __fmul_rn(__fadd_rn(c[e], rest[e]), kDownP);
-        add(j, h, c, vs);
+        for (int e = 0; e < 4; ++e)
+          o[j][h][e] = __fmaf_rn(__fmul_rn(__fadd_rn(c[e], rest[e]), kDownP), vs[e >> 1], o[j][h][e]);
       }
     }
   }

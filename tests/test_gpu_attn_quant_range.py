@@ -169,3 +169,30 @@ def test_a_key_that_is_not_finite_gives_nan_in_a_tail(attn, gdn, dtype):
                 bent[0][j, 1, 11] = bad
             _, out, _ = decode(attn, gdn, q, bent, vs, 16, "int8", dtype)
             assert out[0, 3:].isnan().all() and torch.equal(out[0, :3], ref[0, :3]) and torch.equal(out[1:], ref[1:])
+
+
+def test_small_entries_beside_large_ones_in_an_fp32_tail(attn, gdn):
+    """Columns of a value from 1e-9 to 1e9: one key's output is the value, off by the two f16 parts' 2^-22 and three roundings.  A key
+    of 1e9 that has no weight: what the others give is off by their own sizes alone."""
+    hk, hq, d, lens = 2, 6, 128, [1, 4, 15, 16 + 9]
+    size = 10.0 ** (torch.arange(d) % 19 - 9)
+    ks, vs = rows(lens, hk, d, F32, 1), [x * size for x in rows(lens, hk, d, F32, 2)]
+    q = rows([len(lens)], hq, d, F32, 3)[0]
+    _, out, _ = decode(attn, gdn, q, ks, vs, 16, "int8", F32, window=1)
+    for i, x in enumerate(vs):
+        want = x[-1].double().repeat_interleave(hq // hk, 0)
+        assert A.worst(out[i], want, 2.0 ** -21 * want.abs()) <= 1, i
+    q[:, :, 0] = 1.0  # the only column where the last key is not 0, and the others are
+    for far in (0.0, 1e9):
+        for k in ks:
+            k[:, :, 0], k[-1] = 0, 0
+            k[-1, :, 0] = -far
+        _, out, lse = decode(attn, gdn, q, ks, vs, 16, "int8", F32)
+        for i, L in enumerate(lens):
+            if far and L == 1:
+                continue
+            keep = L - 1 if far else L
+            k, v = (expect(x[i], 16, "int8", F32)[:keep] for x in (ks, vs))
+            r = reference(q[i:i + 1], k, v, keep, F32)
+            assert A.worst(out[i:i + 1], r["out"], r["tol"]["out"]) <= 1, (far, i)
+            assert A.worst(lse[i:i + 1], r["lse"], r["tol"]["lse"]) <= 1, (far, i)
