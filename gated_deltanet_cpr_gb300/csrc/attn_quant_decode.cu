@@ -15,9 +15,9 @@
 //
 // Half the bytes of a bf16 cache leave half the time for the same products, so that instructions bound this kernel
 // where DRAM bounds attn_decode.cu: widening a code to f16 is 2.5 of them a pair of codes in int8 (1 to 1.5 in e4m3) and a
-// third of all.  256 requests of about 2112 tokens, 32 / 8 heads, d = 128: 193 us in int8, 188 in e4m3, where the bytes take 167
+// third of all.  256 requests of about 2112 tokens, 32 / 8 heads, d = 128: 194 us in int8, 191 in e4m3, where the bytes take 167
 // and 169 at a copy's rate (bf16 pages: 325).  Scores as rows of the MMA (16 heads, of which 4 are there) took 220.  Few
-// requests are bound by the chain of one run, launch and join: 4 of about 700 tokens take 10.4 us.
+// requests are bound by the chain of one run, launch and join: 4 of about 700 tokens take 10.3 us.
 #include <cuda_fp16.h>
 
 #include "attn_decode.cuh"
@@ -200,10 +200,12 @@ struct QuantEngine : Quant {
   };
   static_assert(sizeof(Meta) <= 128 && (2 * SIDE) % 128 == 0 && STAGE % 128 == 0, "key is stored with the three behind it, 16 bytes");
   static constexpr int kLast = 64, kEdge = 128;  // the run's last tile; some keys may not be visible
-  // Granules are gone through one by one: the instructions of two at a time (198 us for 256 requests of about 2112 tokens
-  // against 193, fp32 window case 32.7 against 27.3) overflow the nearest cache.  Two column tiles have more in flight
-  // by themselves and gain from pairs (48.7 against 49.8), but need more registers than 12 warps leave.  12 warps with a tile on its way take
-  // those 256 requests in 193 us, 8 with two 206, 16 with tiles of one granule 209.
+  // Granules are gone through one by one: the instructions of two at a time (197 us for 256 requests of about 2112 tokens
+  // against 194, fp32 window case 32.1 against 26.7) overflow the nearest cache.  Two column tiles need more registers than 12
+  // warps leave, and go in pairs: with d = 64 these 256 requests take 111.5 us with 12 heads a key head, one by one 115.6 (e4m3
+  // 106.3 and 110.8); with d = 128, where a pair is a whole tile, 33 requests of 500 to 15619 take 49.2 either way, but 256 of
+  // about 2112 with 16 heads a key head 165.7 against 152.7.  12 warps with a tile on its way take the first 256 requests in
+  // 194 us, 8 with two 207, 16 with tiles of one granule 209 (of 193 then).
   static constexpr bool PAIRS = NH == 2 && !SPLIT;
   static constexpr int MOST_WARPS = NH == 2 ? 8 : 12, RING = NH == 2 ? 3 : 2;
   static_assert(RING <= 3, "the queue holds four runs: the computed one, those of RING - 1 tiles ahead and the next");

@@ -531,7 +531,8 @@ gdn_status gdn_cpr_window_attn_workspace_size(const gdn_cpr_attn *attn, int32_t 
  *   GDN_E4M3  s = the least power of two 2^e with max|x| <= 448 2^e, c = x / s to the nearest e4m3
  *             value, ties to even
  * A block whose max|x| lies below 2^-100 is held as zeros with s = 0; one that holds an infinity or
- * a NaN as zeros with s = NaN, so that all of it reads as NaN.
+ * a NaN as zeros with s = NaN, so that all of it reads as NaN.  (In e4m3 a value of 1.9375 2^127 or
+ * more rounds to 2^128, which reads as an infinity.)
  *
  * Only whole blocks are held in 8 bits.  The rows of a request's unfinished block wait, as they
  * came, in its tail: of seq_len tokens the first seq_len / block * block are in the pages, the
