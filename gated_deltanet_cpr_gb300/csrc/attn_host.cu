@@ -569,6 +569,8 @@ gdn_status gdn_cpr_quant_decode(const gdn_cpr_attn* attn, const gdn_cpr_quant_ca
   a.max_splits = splits;
   a.hdr = static_cast<WsHeader*>(ws);
   a.c = quant_view(cache);
+  // copies of no bytes, of rows that are not there, name the tails' address all the same; without tails there is none
+  if (cache->slots == 0) a.c.k_tail = a.c.v_tail = ws;
   a.slot = slot;
   Stages stg(stream, kQuantDecodeStages);
   stg.mark(launch_quant_decode(a, attn->dtype == GDN_BF16, stream));

@@ -196,3 +196,23 @@ def test_small_entries_beside_large_ones_in_an_fp32_tail(attn, gdn):
             r = reference(q[i:i + 1], k, v, keep, F32)
             assert A.worst(out[i:i + 1], r["out"], r["tol"]["out"]) <= 1, (far, i)
             assert A.worst(lse[i:i + 1], r["lse"], r["tol"]["lse"]) <= 1, (far, i)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_a_cache_without_tails_serves_whole_blocks(attn, gdn, dtype):
+    """Requests of whole blocks, with no slot; one with an unfinished block gives NaN, and its append and its rows are reported."""
+    lens, hk, hq, d = [32, 48, 64], 2, 6, 64
+    ks, vs, q = rows(lens, hk, d, dtype, 1), rows(lens, hk, d, dtype, 2), rows([3], hq, d, dtype, 3)[0].cuda()
+    s, ref, _ = decode(attn, gdn, q.cpu(), ks, vs, 16, "int8", dtype)
+    c = attn.QuantCache.wrap(s.cache.k, s.cache.v, s.cache.k_scale, s.cache.v_scale, s.cache.k_tail[:0], s.cache.v_tail[:0])
+    ws = gdn.alloc_workspace(1 << 20, "cuda")
+    none = ints([0, 0, 0])
+    assert torch.equal(attn.quant_decode(q, c, s.table, ints(lens), slots=none, ws=ws), ref) and gdn.device_error(ws) == 0
+    out = attn.quant_decode(q, c, s.table, ints([32, 47, 64]), slots=none, ws=ws)
+    assert gdn.device_error(ws) == 2 and out[1].isnan().all() and torch.equal(out[::2], ref[::2])
+    k, _ = attn.quant_read(c, s.table, ints([32, 47, 64]), ints([0, 32, 79, 143]), 143, slots=none, ws=ws)
+    assert gdn.device_error(ws) == 2 and k[32:64].isfinite().all() and k[64:79].isnan().all() and k[79:].isfinite().all()
+    before = s.state()
+    new = torch.zeros((3, hk, d), dtype=dtype, device="cuda")
+    attn.quant_append(new, new, c, s.table, ints([33, 49, 65]), ints([0, 1, 2, 3]), slots=none, ws=ws)
+    assert gdn.device_error(ws) == 2 and all(torch.equal(a, b) for a, b in zip(before, s.state()))
